@@ -685,3 +685,9 @@ def q4_gemv_affine_x8(codes, scales, zeros, q1, q2, d, y=None, stream=None):
     if st != Q4_OK:
         raise Q4Error(st, "q4_gemv_affine_x8")
     return y
+
+
+from .experts import (q4_gemm_grouped, q4_gemm_grouped_ws_bytes, q4_moe_combine, q4_route_topk,  # noqa: E402
+                      q4_route_topk_ws_bytes)
+from .lora import (q4_gemm_lora, q4_gemm_lora_backward, q4_gemm_lora_backward_ws_bytes,  # noqa: E402
+                   q4_gemm_lora_ws_bytes)

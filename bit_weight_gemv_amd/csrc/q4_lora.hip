@@ -1,0 +1,765 @@
+// q4_lora.hip -- low-rank adapters beside a packed projection: the first
+// product t = s A x, and the backward pass.
+//
+// Forward: t[n] = s_a A_a X[n] here, then the packed product with the term
+// sum_j t[n][j] B_a[m][j] in its epilogue (q4_ragged.hip).
+// Backward, with the packed matrix frozen:
+//   u[n]  = s_a B_a^T dY[n]                            (the first product, on B transposed)
+//   dX[n] = What^T dY[n] + A_a^T u[n]
+//   dA_a  = sum u[n] x[n]^T,  dB_a = sum dY[n] t[n]^T  over the tokens of a
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "q4_lora.h"
+#include "q4_ragged.h"
+#include "q4_ragged_device.h"
+
+namespace q4 {
+
+namespace {
+
+// ---------------------------------------------------------------------------
+// t[n][j] = scaling[a] * sum_k Z[a][j][k] x[n][k], a = ids[n]; rows of tokens
+// without an adapter are not written.  Z is bf16 [L][r][pitch].
+// ---------------------------------------------------------------------------
+struct ShrinkArgs {
+    const uint16_t *X, *Z;
+    const float *scaling;
+    const int32_t *ids;
+    int N, K, pitch, r, L;
+    float *t;
+};
+
+// Eight bf16 of a row at column k; zeros past its end.  VEC: rows start on 16
+// bytes and have whole pieces.
+template <bool VEC>
+__device__ __forceinline__ u32x4_t row_piece(const uint16_t *row, int k, int K) {
+    u32x4_t v = {0u, 0u, 0u, 0u};
+    if constexpr (VEC) {
+        if (k < K) v = *reinterpret_cast<const u32x4_t *>(row + k);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (k + i < K) v[i >> 1] |= (uint32_t)row[k + i] << (16 * (i & 1));
+    }
+    return v;
+}
+
+__device__ __forceinline__ float dot8(const u32x4_t &x, const u32x4_t &z, float s) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        s = fmaf(bf16_lo(x[c]), bf16_lo(z[c]), s);
+        s = fmaf(bf16_hi(x[c]), bf16_hi(z[c]), s);
+    }
+    return s;
+}
+
+// Few tokens: a workgroup takes one token and 4 ranks, a wave a rank.
+template <bool VEC>
+__global__ __launch_bounds__(256) void lora_shrink_token_kernel(const ShrinkArgs a) {
+    const int n = blockIdx.x, j = blockIdx.y * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
+    const int id = a.ids[n];
+    if (id < 0 || id >= a.L || j >= a.r) return;
+    const uint16_t *x = a.X + (int64_t)n * a.K, *z = a.Z + ((int64_t)id * a.r + j) * a.pitch;
+    float s = 0.0f;
+#pragma unroll 4
+    for (int k = lane * 8; k < a.K; k += 512)
+        s = dot8(row_piece<VEC>(x, k, a.K), *reinterpret_cast<const u32x4_t *>(z + k), s);
+    s = wave_sum(s);
+    if (lane == 0) a.t[(int64_t)n * a.r + j] = s * a.scaling[id];
+}
+
+// Many tokens: a workgroup takes 32, its 8 waves split K in 64-blocks dealt
+// round; the adapters among the 32 tokens come one after the other.
+template <bool VEC, int JT>
+__global__ __launch_bounds__(512) void lora_shrink_kernel(const ShrinkArgs a) {
+    __shared__ float red[8][32 * 32];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int col = lane & 31, g = lane >> 5;
+    const int n0 = blockIdx.x * 32, n = n0 + col;
+    int id = n < a.N ? a.ids[n] : -1;
+    if (id >= a.L) id = -1;
+    const uint16_t *x = a.X + (int64_t)min(n, a.N - 1) * a.K;
+    const int nb = (a.K + 63) >> 6;
+    int pending = id;
+    while (true) {
+        const uint64_t left = __builtin_amdgcn_ballot_w64(pending >= 0);
+        if (!left) return;
+        const int now = __builtin_amdgcn_readlane(pending, __builtin_ctzll(left));
+        if (pending == now) pending = -1;
+        const float scale = a.scaling[now];
+        float16_t acc[JT];
+#pragma unroll
+        for (int q = 0; q < JT; ++q) acc[q] = float16_t{};
+        const uint16_t *z = a.Z + (int64_t)now * a.r * a.pitch;
+        for (int b = wave; b < nb; b += 8) {
+            const int k = 64 * b + 32 * g;
+            u32x4_t xv[4], zv[JT][4];
+#pragma unroll
+            for (int s = 0; s < 4; ++s) xv[s] = row_piece<VEC>(x, k + 8 * s, a.K);
+#pragma unroll
+            for (int q = 0; q < JT; ++q)
+#pragma unroll
+                for (int s = 0; s < 4; ++s) {
+                    zv[q][s] = u32x4_t{0u, 0u, 0u, 0u};
+                    if (32 * q + col < a.r && k + 8 * s < a.pitch)
+                        zv[q][s] = *reinterpret_cast<const u32x4_t *>(z + (int64_t)(32 * q + col) * a.pitch + k + 8 * s);
+                }
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+#pragma unroll
+                for (int q = 0; q < JT; ++q)
+                    acc[q] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, xv[s]),
+                                                                     __builtin_bit_cast(bf16x8_t, zv[q][s]), acc[q], 0,
+                                                                     0, 0);
+        }
+#pragma unroll
+        for (int q = 0; q < JT; ++q) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) red[wave][tile_row(i, lane) * 32 + col] = acc[q][i];
+            __syncthreads();
+            for (int o = threadIdx.x; o < 1024; o += 512) {
+                const int row = o >> 5, j = 32 * q + (o & 31);
+                if (n0 + row < a.N && j < a.r && a.ids[n0 + row] == now) {
+                    float s = red[0][o];
+#pragma unroll
+                    for (int w = 1; w < 8; ++w) s += red[w][o];
+                    a.t[(int64_t)(n0 + row) * a.r + j] = s * scale;
+                }
+            }
+            __syncthreads();
+        }
+    }
+}
+
+hipError_t launch_shrink(const ShrinkArgs &s, hipStream_t stream) {
+    ShrinkArgs a = s;
+    void *args[] = {&a};
+    const bool vec = a.K % 8 == 0;
+    // A token of its own workgroups reads its adapter alone; 32 tokens that
+    // share a workgroup read it once for all that use it, but one adapter
+    // after the other.
+    if (a.N <= 64)
+        return hipLaunchKernel(vec ? reinterpret_cast<const void *>(&lora_shrink_token_kernel<true>)
+                                   : reinterpret_cast<const void *>(&lora_shrink_token_kernel<false>),
+                               dim3((unsigned)a.N, (unsigned)((a.r + 3) / 4)), dim3(256), args, 0, stream);
+    const void *fn;
+    if (a.r <= 32)
+        fn = vec ? reinterpret_cast<const void *>(&lora_shrink_kernel<true, 1>)
+                 : reinterpret_cast<const void *>(&lora_shrink_kernel<false, 1>);
+    else if (a.r <= 64)
+        fn = vec ? reinterpret_cast<const void *>(&lora_shrink_kernel<true, 2>)
+                 : reinterpret_cast<const void *>(&lora_shrink_kernel<false, 2>);
+    else
+        fn = vec ? reinterpret_cast<const void *>(&lora_shrink_kernel<true, 4>)
+                 : reinterpret_cast<const void *>(&lora_shrink_kernel<false, 4>);
+    return hipLaunchKernel(fn, dim3((unsigned)((a.N + 31) / 32)), dim3(512), args, 0, stream);
+}
+
+// ---------------------------------------------------------------------------
+// Backward: what is prepared.
+// ---------------------------------------------------------------------------
+
+// Exponent of each packed row's largest scale (16 lanes a row), and behind
+// those workgroups B transposed: bt[a][j][m], rows of `pitch` with zeros past
+// M (a workgroup takes 64 m of one adapter).
+__global__ __launch_bounds__(256) void lora_rows_kernel(const uint16_t *__restrict__ scales, int M, int nb,
+                                                        int8_t *__restrict__ rowexp, int rowblocks,
+                                                        const uint16_t *__restrict__ B, int r, int pitch,
+                                                        uint16_t *__restrict__ bt) {
+    __shared__ uint16_t tile[64][130];
+    if ((int)blockIdx.x < rowblocks) {
+        const int row = blockIdx.x * 16 + (threadIdx.x >> 4);
+        if (row >= M) return;
+        int m = 0;
+        for (int b = threadIdx.x & 15; b < nb; b += 16) m = max(m, (int)(scales[(int64_t)row * nb + b] & 0x7FFF));
+#pragma unroll
+        for (int d = 8; d >= 1; d >>= 1) m = max(m, __shfl_xor(m, d));
+        const float f = f16_bits_to_f32((uint32_t)m);
+        const int e = m == 0 ? 0 : (int)(__builtin_bit_cast(uint32_t, f) >> 23) - 127;
+        if ((threadIdx.x & 15) == 0) rowexp[row] = (int8_t)min(e, 16);
+        return;
+    }
+    const int per = pitch / 64, w = blockIdx.x - rowblocks;
+    const int l = w / per, m0 = (w % per) * 64;
+    for (int i = threadIdx.x; i < 64 * r; i += 256) {
+        const int m = m0 + i / r, j = i % r;
+        tile[i / r][j] = m < M ? B[((int64_t)l * M + m) * r + j] : 0;
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < 64 * r; i += 256)
+        bt[((int64_t)l * r + i / 64) * pitch + m0 + i % 64] = tile[i % 64][i / 64];
+}
+
+// dY[n][m] 2^(rowexp[m] + shift[n]) as fp16, rows of `pitch` with zeros past
+// M: the power of two of each packed row goes to this side, so that the
+// weights' fp16 values keep their full precision, and the token's brings the
+// largest to [2^14, 2^15).
+__global__ __launch_bounds__(256) void lora_dy_kernel(const uint16_t *__restrict__ dY, int M, int pitch,
+                                                      const int8_t *__restrict__ rowexp, uint16_t *__restrict__ out,
+                                                      int32_t *__restrict__ exps) {
+    __shared__ int wmax[4];
+    const int n = blockIdx.x;
+    const uint16_t *src = dY + (int64_t)n * M;
+    int best = -1000;
+    for (int m = threadIdx.x; m < M; m += 256) {
+        const int mag = src[m] & 0x7FFF;
+        if (mag) best = max(best, min(mag >> 7, 254) + rowexp[m]);
+    }
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1) best = max(best, __shfl_xor(best, d));
+    if ((threadIdx.x & 63) == 0) wmax[threadIdx.x >> 6] = best;
+    __syncthreads();
+    best = max(max(wmax[0], wmax[1]), max(wmax[2], wmax[3]));
+    const int shift = best == -1000 ? 0 : 141 - best;
+    for (int m = threadIdx.x; m < pitch; m += 256) {
+        uint16_t v = 0;
+        if (m < M) v = __builtin_bit_cast(uint16_t, (_Float16)ldexpf(bf16_f32(src[m]), shift + rowexp[m]));
+        out[(int64_t)n * pitch + m] = v;
+    }
+    if (threadIdx.x == 0) exps[n] = -shift;
+}
+
+// ---------------------------------------------------------------------------
+// dX[n][k] = sum_m What[m,k] dY[n][m] + sum_j u[n][j] A_a[j][k].
+// ---------------------------------------------------------------------------
+struct DxArgs {
+    const uint16_t *dy16;   // fp16 [N][pitch]
+    const int32_t *exps;
+    const int8_t *rowexp;
+    const uint8_t *codes;
+    const uint16_t *scales;
+    int N, M, K, pitch, ktiles, splits;
+    float *part;            // [splits][N][K], or null
+    uint16_t *dX;
+    const uint16_t *A;
+    const float *u;
+    const int32_t *ids;
+    int r, L;
+};
+
+// A workgroup computes 64 MT tokens (2 waves of MT tiles of 32) by 256 k (4
+// waves of 64: one block of the packed rows, whose 32 code bytes are the 32
+// lanes' columns; a lane's two weights of a byte are the columns 2c and 2c+1
+// of two tiles).  The contraction runs over 64 packed rows a step: their code
+// bytes are transposed into LDS so that a lane reads its column's bytes of 32
+// rows as two 16-byte pieces.
+template <int MT>
+__global__ __launch_bounds__(512) void lora_dx_kernel(const DxArgs a) {
+    constexpr int TM = 64 * MT;
+    constexpr int kPieces = TM * 8 / 512;
+    __shared__ uint32_t lut[kLutDwords];
+    __shared__ uint4 ys[2][TM * 8];
+    __shared__ uint32_t ct[2][128 * 16];  // [column slot][64 rows' bytes]
+    __shared__ uint4 sl[2][4 * 8];        // [block of 64 k][64 rows] fp16 scales
+    __shared__ int xe[TM];
+    __shared__ int sid[TM];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int col = lane & 31, g = lane >> 5;
+    const int wt = wave & 1, wk = wave >> 1;
+    const int tile = blockIdx.x / a.ktiles, kt = blockIdx.x % a.ktiles;
+    const int n0 = tile * TM, count = min(TM, a.N - n0);
+    const int nb = a.K >> 6;
+    const int steps = a.pitch >> 6;
+    const int st0 = (int)((int64_t)steps * blockIdx.y / a.splits), st1 = (int)((int64_t)steps * (blockIdx.y + 1) / a.splits);
+
+    for (int i = threadIdx.x; i < TM; i += 512) {
+        xe[i] = i < count ? a.exps[n0 + i] : 0;
+        const int id = a.L > 0 && i < count ? a.ids[n0 + i] : -1;
+        sid[i] = id >= 0 && id < a.L ? id : -1;
+    }
+    const uint4 *ysrc[kPieces];
+#pragma unroll
+    for (int j = 0; j < kPieces; ++j) {
+        const int i = (threadIdx.x >> 3) + 64 * j;
+        const int piece = (threadIdx.x & 7) ^ (i & 7);
+        ysrc[j] = i < count ? reinterpret_cast<const uint4 *>(a.dy16 + (int64_t)(n0 + i) * a.pitch) + piece : nullptr;
+    }
+    // Codes: lane bits 0..3 pick four rows, the rest a dword of the 128 bytes.
+    const int m4 = threadIdx.x & 15, dc = threadIdx.x >> 4;
+    const int dbyte = kt * 128 + dc * 4;
+    const bool dlive = dbyte < (a.K >> 1);
+    const int skb = threadIdx.x >> 6, sm = threadIdx.x & 63;  // scales: first 256 threads
+
+    uint4 yv[kPieces];
+    uint32_t cv[4];
+    uint32_t sv = 0;
+    int se = 0;
+    auto load = [&](int st) {
+#pragma unroll
+        for (int j = 0; j < kPieces; ++j) yv[j] = ysrc[j] ? ysrc[j][8 * st] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int m = min(64 * st + 4 * m4 + i, a.M - 1);
+            cv[i] = dlive ? *reinterpret_cast<const uint32_t *>(a.codes + (int64_t)m * (a.K >> 1) + dbyte) : 0;
+        }
+        if (threadIdx.x < 256) {
+            const int m = 64 * st + sm, kb = kt * 4 + skb;
+            sv = 0;
+            se = 0;
+            if (m < a.M && kb < nb) {
+                sv = a.scales[(int64_t)m * nb + kb];
+                se = a.rowexp[m];
+            }
+        }
+    };
+    load(st0);
+    fill_lut(lut);
+
+    float16_t acc[MT][2];
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int q = 0; q < 2; ++q) acc[i][q] = float16_t{};
+    const uint32_t laneoff = (uint32_t)lane << 2;
+    // Column slot of byte 4 d + j: j * 32 + d, so that both the transposing
+    // writes and the reads meet every bank; 16-byte pieces under an exchange
+    // by j.
+    const int mycol = (col & 3) * 32 + wk * 8 + (col >> 2);
+
+    for (int st = st0; st < st1; ++st) {
+        const int bi = st & 1;
+#pragma unroll
+        for (int j = 0; j < kPieces; ++j) ys[bi][threadIdx.x + 512 * j] = yv[j];
+        {
+            const uint32_t p0 = __builtin_amdgcn_perm(cv[1], cv[0], 0x05010400u);  // r0.b0 r1.b0 r0.b1 r1.b1
+            const uint32_t p1 = __builtin_amdgcn_perm(cv[1], cv[0], 0x07030602u);  // r0.b2 r1.b2 r0.b3 r1.b3
+            const uint32_t p2 = __builtin_amdgcn_perm(cv[3], cv[2], 0x05010400u);
+            const uint32_t p3 = __builtin_amdgcn_perm(cv[3], cv[2], 0x07030602u);
+            const uint32_t o[4] = {__builtin_amdgcn_perm(p2, p0, 0x05040100u), __builtin_amdgcn_perm(p2, p0, 0x07060302u),
+                                   __builtin_amdgcn_perm(p3, p1, 0x05040100u), __builtin_amdgcn_perm(p3, p1, 0x07060302u)};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) ct[bi][(j * 32 + dc) * 16 + (((m4 >> 2) ^ j) << 2) + (m4 & 3)] = o[j];
+        }
+        if (threadIdx.x < 256)
+            reinterpret_cast<_Float16 *>(sl[bi])[skb * 64 + sm] = (_Float16)ldexpf(f16_bits_to_f32(sv), 14 - se);
+        __syncthreads();
+        if (st + 1 < st1) load(st + 1);
+
+        // This lane's column: the bytes of rows 32 g .. 32 g + 31.
+        u32x4_t by[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            by[h] = *reinterpret_cast<const u32x4_t *>(&ct[bi][mycol * 16 + (((2 * g + h) ^ (col & 3)) << 2)]);
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            // Rows 32 g + 8 s + (0..7): two dwords of bytes, eight scales.
+            const uint32_t w0 = by[s >> 1][2 * (s & 1)], w1 = by[s >> 1][2 * (s & 1) + 1];
+            half2_t v[8];
+            v[0] = lut_pair<0>(lut, w0, laneoff);
+            v[1] = lut_pair<1>(lut, w0, laneoff);
+            v[2] = lut_pair<2>(lut, w0, laneoff);
+            v[3] = lut_pair<3>(lut, w0, laneoff);
+            v[4] = lut_pair<0>(lut, w1, laneoff);
+            v[5] = lut_pair<1>(lut, w1, laneoff);
+            v[6] = lut_pair<2>(lut, w1, laneoff);
+            v[7] = lut_pair<3>(lut, w1, laneoff);
+            const uint4 sc = sl[bi][wk * 8 + 4 * g + s];
+            const uint32_t scd[4] = {sc.x, sc.y, sc.z, sc.w};
+            half2_t even[4], odd[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t x = __builtin_bit_cast(uint32_t, v[2 * i]), y = __builtin_bit_cast(uint32_t, v[2 * i + 1]);
+                const half2_t s2 = __builtin_bit_cast(half2_t, scd[i]);
+                even[i] = __builtin_bit_cast(half2_t, __builtin_amdgcn_perm(y, x, 0x05040100u)) * s2;
+                odd[i] = __builtin_bit_cast(half2_t, __builtin_amdgcn_perm(y, x, 0x07060302u)) * s2;
+            }
+            const half8_t b0 = join8(even), b1 = join8(odd);
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+                const int row = wt * 32 * MT + 32 * i + col;
+                const half8_t ya = __builtin_bit_cast(half8_t, ys[bi][row * 8 + ((4 * g + s) ^ (row & 7))]);
+                acc[i][0] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ya, b0, acc[i][0], 0, 0, 0);
+                acc[i][1] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ya, b1, acc[i][1], 0, 0, 0);
+            }
+        }
+    }
+
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            const int x = xe[wt * 32 * MT + 32 * i + tile_row(j, lane)] - 14;
+            acc[i][0][j] = ldexpf(acc[i][0][j], x);
+            acc[i][1][j] = ldexpf(acc[i][1][j], x);
+        }
+    const int k = kt * 256 + wk * 64 + 2 * col;  // this lane's two columns
+
+    if (!a.part) {
+        int mine[2] = {-1, -1};
+        const int w0 = wt * 32 * MT;
+        mine[0] = sid[w0 + (lane & (32 * MT - 1))];
+        if (MT == 4) mine[1] = sid[w0 + 64 + lane];
+        while (true) {
+            const uint64_t p0 = __builtin_amdgcn_ballot_w64(mine[0] >= 0);
+            const uint64_t p1 = __builtin_amdgcn_ballot_w64(mine[1] >= 0);
+            if (!(p0 | p1)) break;
+            const int id = p0 ? __builtin_amdgcn_readlane(mine[0], __builtin_ctzll(p0))
+                              : __builtin_amdgcn_readlane(mine[1], __builtin_ctzll(p1));
+            if (mine[0] == id) mine[0] = -1;
+            if (mine[1] == id) mine[1] = -1;
+            for (int j0 = 0; j0 < a.r; j0 += 16) {
+                const bool live = j0 + 8 * g < a.r;
+                uint32_t d[8];
+#pragma unroll
+                for (int x = 0; x < 8; ++x)
+                    d[x] = live && k < a.K ? *reinterpret_cast<const uint32_t *>(
+                                                 a.A + ((int64_t)id * a.r + j0 + 8 * g + x) * a.K + k)
+                                           : 0;
+                u32x4_t e, o;
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    e[x] = __builtin_amdgcn_perm(d[2 * x + 1], d[2 * x], 0x05040100u);
+                    o[x] = __builtin_amdgcn_perm(d[2 * x + 1], d[2 * x], 0x07060302u);
+                }
+                const bf16x8_t be = __builtin_bit_cast(bf16x8_t, e), bo = __builtin_bit_cast(bf16x8_t, o);
+#pragma unroll
+                for (int i = 0; i < MT; ++i) {
+                    const int row = w0 + 32 * i + col;
+                    const bool use = sid[row] == id;
+                    if (__builtin_amdgcn_ballot_w64(use) == 0) continue;
+                    float t[8];
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) t[x] = 0.0f;
+                    if (use && live) {
+                        const float *src = a.u + (int64_t)(n0 + row) * a.r + j0 + 8 * g;
+#pragma unroll
+                        for (int x = 0; x < 8; ++x) t[x] = src[x];
+                    }
+                    bf16x8_t hi, lo;
+                    split2(t, hi, lo);
+                    acc[i][0] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(hi, be, acc[i][0], 0, 0, 0);
+                    acc[i][0] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(lo, be, acc[i][0], 0, 0, 0);
+                    acc[i][1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(hi, bo, acc[i][1], 0, 0, 0);
+                    acc[i][1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(lo, bo, acc[i][1], 0, 0, 0);
+                }
+            }
+        }
+    }
+    if (k >= a.K) return;
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            const int row = wt * 32 * MT + 32 * i + tile_row(j, lane);
+            if (row >= count) continue;
+            const int64_t at = (int64_t)(n0 + row) * a.K + k;
+            if (a.part) {
+                float2 *o = reinterpret_cast<float2 *>(a.part + (int64_t)blockIdx.y * a.N * a.K + at);
+                *o = make_float2(acc[i][0][j], acc[i][1][j]);
+            } else {
+                *reinterpret_cast<uint32_t *>(a.dX + at) =
+                    (uint32_t)f32_bf16(acc[i][0][j]) | (uint32_t)f32_bf16(acc[i][1][j]) << 16;
+            }
+        }
+}
+
+// Adds the partial planes in order, and the adapter's term; two columns a lane.
+__global__ __launch_bounds__(256) void lora_dx_finish_kernel(const DxArgs a) {
+    const int per = (a.K + 511) >> 9;
+    const int n = blockIdx.x / per, k = ((blockIdx.x % per) * 256 + threadIdx.x) * 2;
+    if (k >= a.K) return;
+    const int64_t at = (int64_t)n * a.K + k, plane = (int64_t)a.N * a.K;
+    float2 v = *reinterpret_cast<const float2 *>(a.part + at);
+    for (int z = 1; z < a.splits; ++z) {
+        const float2 o = *reinterpret_cast<const float2 *>(a.part + z * plane + at);
+        v.x += o.x;
+        v.y += o.y;
+    }
+    const int id = a.L > 0 ? a.ids[n] : -1;
+    if (id >= 0 && id < a.L) {
+        float s0 = 0.0f, s1 = 0.0f;
+        for (int j = 0; j < a.r; ++j) {
+            const uint32_t d = *reinterpret_cast<const uint32_t *>(a.A + ((int64_t)id * a.r + j) * a.K + k);
+            const float t = a.u[(int64_t)n * a.r + j];
+            s0 = fmaf(t, bf16_lo(d), s0);
+            s1 = fmaf(t, bf16_hi(d), s1);
+        }
+        v.x += s0;
+        v.y += s1;
+    }
+    *reinterpret_cast<uint32_t *>(a.dX + at) = (uint32_t)f32_bf16(v.x) | (uint32_t)f32_bf16(v.y) << 16;
+}
+
+// ---------------------------------------------------------------------------
+// Gradients of the adapters: for pieces of at most kPieceTokens tokens of one
+// adapter (in the order of the tokens), g[j][c] = sum_n t[n][j] Z[n][c], one
+// lane a pair of columns, the t of a token uniform over the workgroup.
+// ---------------------------------------------------------------------------
+constexpr int kPieceTokens = 128;
+
+struct GradArgs {
+    const uint16_t *Z[2];    // X [N][K] and dY [N][M]
+    const float *t[2];       // u and t
+    int cols[2];
+    float *part[2];          // [pieces][r][cols]
+    float *out[2];           // dA [L][r][K], dB [L][M][r]
+    const int32_t *offsets, *rows;
+    int N, L, r, blocks0;
+};
+
+template <int J>
+__global__ __launch_bounds__(256) void lora_grad_kernel(const GradArgs a) {
+    const int q = (int)blockIdx.x >= a.blocks0 ? 1 : 0;
+    const Chunk ck = find_chunk(a.offsets, a.L, a.N, blockIdx.y, kPieceTokens);
+    if (ck.count == 0) return;
+    const int cols = a.cols[q];
+    const int c = ((int)(blockIdx.x - (q ? a.blocks0 : 0)) * 256 + threadIdx.x) * 2;
+    const int j0 = blockIdx.z * J;
+    if (c >= cols) return;
+    float s[J][2];
+#pragma unroll
+    for (int j = 0; j < J; ++j) s[j][0] = s[j][1] = 0.0f;
+    const bool pair = (cols & 1) == 0;
+    for (int i = 0; i < ck.count; ++i) {
+        const int n = __builtin_amdgcn_readfirstlane(a.rows[ck.start + i]);
+        const uint16_t *z = a.Z[q] + (int64_t)n * cols + c;
+        float z0, z1;
+        if (pair) {
+            const uint32_t d = *reinterpret_cast<const uint32_t *>(z);
+            z0 = bf16_lo(d);
+            z1 = bf16_hi(d);
+        } else {
+            z0 = bf16_f32(z[0]);
+            z1 = c + 1 < cols ? bf16_f32(z[1]) : 0.0f;
+        }
+        const float *t = a.t[q] + (int64_t)n * a.r + j0;
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            const float tj = t[j];
+            s[j][0] = fmaf(tj, z0, s[j][0]);
+            s[j][1] = fmaf(tj, z1, s[j][1]);
+        }
+    }
+    float *o = a.part[q] + ((int64_t)blockIdx.y * a.r + j0) * cols + c;
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+        o[(int64_t)j * cols] = s[j][0];
+        if (c + 1 < cols) o[(int64_t)j * cols + 1] = s[j][1];
+    }
+}
+
+// Adds the pieces of each adapter in order (none: zeros).
+__global__ __launch_bounds__(256) void lora_grad_sum_kernel(const GradArgs a) {
+    const int q = (int)blockIdx.x >= a.blocks0 ? 1 : 0;
+    const int l = blockIdx.y, j = blockIdx.z;
+    const int cols = a.cols[q];
+    const int c = (int)(blockIdx.x - (q ? a.blocks0 : 0)) * 256 + threadIdx.x;
+    // The pieces before those of adapter l, and its own.
+    int first = 0;
+    for (int e0 = 0; e0 < l; e0 += 64) {
+        const int e = e0 + (threadIdx.x & 63);
+        int n = 0;
+        if (e < l) n = (a.offsets[e + 1] - a.offsets[e] + kPieceTokens - 1) / kPieceTokens;
+#pragma unroll
+        for (int d = 32; d >= 1; d >>= 1) n += __shfl_xor(n, d);
+        first += n;
+    }
+    const int n = (a.offsets[l + 1] - a.offsets[l] + kPieceTokens - 1) / kPieceTokens;
+    if (c >= cols) return;
+    float s = 0.0f;
+    for (int i = 0; i < n; ++i) s += a.part[q][((int64_t)(first + i) * a.r + j) * cols + c];
+    if (q == 0) a.out[0][((int64_t)l * a.r + j) * cols + c] = s;
+    else a.out[1][((int64_t)l * cols + c) * a.r + j] = s;
+}
+
+int64_t pieces_bound(int64_t N, int64_t L) {
+    const int64_t p = N / kPieceTokens + L;
+    return p < N ? p : N;
+}
+
+struct DxPlan {
+    int mt, ktiles, splits;
+    int64_t tiles;
+};
+
+DxPlan dx_plan(int64_t M, int64_t K, int64_t N) {
+    DxPlan p = {};
+    p.mt = N > 1024 ? 4 : N > 64 ? 2 : 1;
+    p.tiles = (N + 64 * p.mt - 1) / (64 * p.mt);
+    p.ktiles = (int)((K + 255) / 256);
+    // Packed rows are split while there are fewer workgroups than compute
+    // units, into parts of 128 rows at least.
+    const int64_t steps = (M + 63) / 64, have = p.tiles * p.ktiles, cus = 256;
+    int64_t s = have >= cus || have == 0 ? 1 : (cus + have - 1) / have;
+    if (s > (steps + 1) / 2) s = (steps + 1) / 2;
+    p.splits = (int)(s < 1 ? 1 : s);
+    return p;
+}
+
+struct BackwardLayout {
+    size_t t, u, bt, dy16, exps, rowexp, offsets, rows, sort, part, grad[2], total;
+    int64_t pitch;
+};
+
+BackwardLayout backward_layout(int64_t M, int64_t K, int64_t N, int64_t r, int64_t L) {
+    BackwardLayout b = {};
+    size_t at = 0;
+    auto take = [&](size_t n) {
+        const size_t was = at;
+        at += round16(n);
+        return was;
+    };
+    b.pitch = (M + 63) / 64 * 64;
+    const DxPlan p = dx_plan(M, K, N);
+    b.t = take((size_t)N * r * 4);
+    b.u = take((size_t)N * r * 4);
+    b.bt = take((size_t)L * r * b.pitch * 2);
+    b.dy16 = take((size_t)N * b.pitch * 2);
+    b.exps = take((size_t)N * 4);
+    b.rowexp = take((size_t)M);
+    b.offsets = take((size_t)(L + 1) * 4);
+    b.rows = take((size_t)N * 4);
+    b.sort = take(sort_ws_bytes(N, L));
+    b.part = take(p.splits > 1 ? (size_t)p.splits * N * K * 4 : 0);
+    b.grad[0] = take((size_t)pieces_bound(N, L) * r * K * 4);
+    b.grad[1] = take((size_t)pieces_bound(N, L) * r * M * 4);
+    b.total = at;
+    return b;
+}
+
+}  // namespace
+
+bool lora_backward_fits(int64_t M, int64_t K, int64_t N, int64_t L) {
+    const DxPlan p = dx_plan(M, K, N);
+    const int64_t most = INT64_C(1) << 32;  // threads of one launch
+    return ((M + 15) / 16 + L * ((M + 63) / 64)) * 256 < most && p.tiles * p.ktiles * 512 < most &&
+           pieces_bound(N, L) < 65536;
+}
+
+size_t lora_ws_bytes(int64_t M, int64_t K, int64_t N, int64_t r, int64_t L) {
+    return (L > 0 ? round16((size_t)N * r * 4) : 0) + ragged_ws_bytes(1, M, K, N, N, false);
+}
+
+hipError_t launch_lora(const LoraCall &c, bool bf16, void *Y, void *workspace, hipStream_t stream) {
+    RaggedProduct p = {};
+    p.codes = c.codes;
+    p.scales = c.scales;
+    p.E = 1;
+    p.M = c.M;
+    p.K = c.K;
+    p.X = c.X;
+    p.T = p.R = c.N;
+    p.bf16 = bf16;
+    p.Y = Y;
+    char *w = static_cast<char *>(workspace);
+    if (c.L > 0) {
+        ShrinkArgs s = {c.X,      c.A, c.scaling, c.ids, (int)c.N, (int)c.K, (int)c.K, (int)c.r, (int)c.L,
+                        reinterpret_cast<float *>(w)};
+        const hipError_t e = launch_shrink(s, stream);
+        if (e != hipSuccess) return e;
+        p.B = c.B;
+        p.t = s.t;
+        p.ids = c.ids;
+        p.r = c.r;
+        p.L = c.L;
+        w += round16((size_t)c.N * c.r * 4);
+    }
+    return launch_ragged(p, w, stream);
+}
+
+size_t lora_backward_ws_bytes(int64_t M, int64_t K, int64_t N, int64_t r, int64_t L) {
+    return backward_layout(M, K, N, r, L).total;
+}
+
+hipError_t launch_lora_backward(const LoraCall &c, const uint16_t *dY, uint16_t *dX, float *dA, float *dB,
+                                void *workspace, hipStream_t stream) {
+    const BackwardLayout b = backward_layout(c.M, c.K, c.N, c.r, c.L);
+    char *w = static_cast<char *>(workspace);
+    float *t = reinterpret_cast<float *>(w + b.t), *u = reinterpret_cast<float *>(w + b.u);
+    uint16_t *bt = reinterpret_cast<uint16_t *>(w + b.bt), *dy16 = reinterpret_cast<uint16_t *>(w + b.dy16);
+    int32_t *exps = reinterpret_cast<int32_t *>(w + b.exps);
+    int8_t *rowexp = reinterpret_cast<int8_t *>(w + b.rowexp);
+    int32_t *offsets = reinterpret_cast<int32_t *>(w + b.offsets), *rows = reinterpret_cast<int32_t *>(w + b.rows);
+    hipError_t e;
+    if (c.N > 0) {
+        const uint16_t *scales = c.scales, *B = c.B;
+        int M = (int)c.M, nb = (int)(c.K / 64), rowblocks = dX ? (int)((c.M + 15) / 16) : 0, r = (int)c.r;
+        int pitch = (int)b.pitch;
+        void *rargs[] = {&scales, &M, &nb, &rowexp, &rowblocks, &B, &r, &pitch, &bt};
+        e = hipLaunchKernel(reinterpret_cast<const void *>(&lora_rows_kernel),
+                            dim3((unsigned)(rowblocks + c.L * (b.pitch / 64))), dim3(256), rargs, 0, stream);
+        if (e != hipSuccess) return e;
+        if (c.L > 0) {
+            ShrinkArgs su = {dY, bt, c.scaling, c.ids, (int)c.N, (int)c.M, (int)b.pitch, (int)c.r, (int)c.L, u};
+            if ((e = launch_shrink(su, stream)) != hipSuccess) return e;
+        }
+        if (dX) {
+            void *yargs[] = {&dY, &M, &pitch, &rowexp, &dy16, &exps};
+            e = hipLaunchKernel(reinterpret_cast<const void *>(&lora_dy_kernel), dim3((unsigned)c.N), dim3(256), yargs,
+                                0, stream);
+            if (e != hipSuccess) return e;
+            const DxPlan p = dx_plan(c.M, c.K, c.N);
+            DxArgs d = {};
+            d.dy16 = dy16;
+            d.exps = exps;
+            d.rowexp = rowexp;
+            d.codes = c.codes;
+            d.scales = c.scales;
+            d.N = (int)c.N;
+            d.M = M;
+            d.K = (int)c.K;
+            d.pitch = pitch;
+            d.ktiles = p.ktiles;
+            d.splits = p.splits;
+            d.part = p.splits > 1 ? reinterpret_cast<float *>(w + b.part) : nullptr;
+            d.dX = dX;
+            d.A = c.A;
+            d.u = u;
+            d.ids = c.ids;
+            d.r = r;
+            d.L = (int)c.L;
+            void *dargs[] = {&d};
+            const void *fn = p.mt == 4   ? reinterpret_cast<const void *>(&lora_dx_kernel<4>)
+                             : p.mt == 2 ? reinterpret_cast<const void *>(&lora_dx_kernel<2>)
+                                         : reinterpret_cast<const void *>(&lora_dx_kernel<1>);
+            e = hipLaunchKernel(fn, dim3((unsigned)(p.tiles * p.ktiles), (unsigned)p.splits), dim3(512), dargs, 0,
+                                stream);
+            if (e != hipSuccess) return e;
+            if (p.splits > 1) {
+                e = hipLaunchKernel(reinterpret_cast<const void *>(&lora_dx_finish_kernel),
+                                    dim3((unsigned)(c.N * ((c.K + 511) / 512))), dim3(256), dargs, 0, stream);
+                if (e != hipSuccess) return e;
+            }
+        }
+    }
+    if (!dA || c.L == 0) return hipSuccess;
+    if (c.N > 0) {
+        ShrinkArgs st = {c.X, c.A, c.scaling, c.ids, (int)c.N, (int)c.K, (int)c.K, (int)c.r, (int)c.L, t};
+        if ((e = launch_shrink(st, stream)) != hipSuccess) return e;
+    }
+    if ((e = launch_sort(c.ids, c.N, c.L, 1, offsets, rows, nullptr, w + b.sort, stream)) != hipSuccess) return e;
+    GradArgs g = {};
+    g.Z[0] = c.X;
+    g.Z[1] = dY;
+    g.t[0] = u;
+    g.t[1] = t;
+    g.cols[0] = (int)c.K;
+    g.cols[1] = (int)c.M;
+    g.part[0] = reinterpret_cast<float *>(w + b.grad[0]);
+    g.part[1] = reinterpret_cast<float *>(w + b.grad[1]);
+    g.out[0] = dA;
+    g.out[1] = dB;
+    g.offsets = offsets;
+    g.rows = rows;
+    g.N = (int)c.N;
+    g.L = (int)c.L;
+    g.r = (int)c.r;
+    void *gargs[] = {&g};
+    if (c.N > 0) {
+        g.blocks0 = (int)((c.K + 511) / 512);
+        const int J = c.r % 16 == 0 ? 16 : 8;
+        e = hipLaunchKernel(J == 16 ? reinterpret_cast<const void *>(&lora_grad_kernel<16>)
+                                    : reinterpret_cast<const void *>(&lora_grad_kernel<8>),
+                            dim3((unsigned)(g.blocks0 + (c.M + 511) / 512), (unsigned)pieces_bound(c.N, c.L),
+                                 (unsigned)(c.r / J)),
+                            dim3(256), gargs, 0, stream);
+        if (e != hipSuccess) return e;
+    }
+    g.blocks0 = (int)((c.K + 255) / 256);
+    return hipLaunchKernel(reinterpret_cast<const void *>(&lora_grad_sum_kernel),
+                           dim3((unsigned)(g.blocks0 + (c.M + 255) / 256), (unsigned)c.L, (unsigned)c.r), dim3(256),
+                           gargs, 0, stream);
+}
+
+}  // namespace q4

@@ -1,0 +1,614 @@
+// q4_ragged.hip -- the packed product of ragged groups of rows:
+//   Y[p][m] = sum_k What_e[m,k] x_p[k]            (plain)
+//   Y[p][m] = silu(What_e x_p) * (Up_e x_p)       (gate and up together)
+//   Y[p][m] = What x_p + sum_j t[p][j] B_a[m][j]  (beside an adapter)
+// where e is the group of position p and x_p the row of X that it names.
+// Two kernels: one for few rows a group (the weights' bytes bound it) and one
+// for many (the matrix cores bound it).
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "q4_internal.h"
+#include "q4_ragged.h"
+#include "q4_ragged_device.h"
+
+namespace q4 {
+
+namespace {
+
+struct Args {
+    const uint8_t *codes[2];
+    const uint16_t *scales[2];
+    const int8_t *rowexp[2];   // tile kernel: exponent of each row's largest scale
+    int M, K, E, R;
+    const uint16_t *X;         // bf16 (chunk kernel) or fp16 under 2^-xexp (tile kernel)
+    const int32_t *xexp;       // tile kernel: the power of two of each row of X
+    int T;
+    const int32_t *offsets, *rows;
+    void *Y;
+    int bf16;
+    float *part;               // chunk kernel: partial planes [mats][ranges][R][M], or null
+    int tiles_per_wg;
+    int ranges;
+    int rowtiles, chunks;      // tile kernel: grid shape
+    const uint16_t *B;
+    const float *t;
+    const int32_t *ids;
+    int r, L;
+};
+
+__device__ __forceinline__ int source_row(const Args &a, int p) {
+    const int row = a.rows ? a.rows[p] : p;
+    return row >= 0 && row < a.T ? row : -1;
+}
+
+// The adapter's part of output (p, m).
+__device__ __forceinline__ float adapter_term(const Args &a, int p, int m) {
+    const int id = a.ids[p];
+    if (id < 0 || id >= a.L) return 0.0f;
+    const uint16_t *b = a.B + ((int64_t)id * a.M + m) * a.r;
+    const float *t = a.t + (int64_t)p * a.r;
+    float s = 0.0f;
+    for (int j = 0; j < a.r; j += 8) {
+        const uint4 v = *reinterpret_cast<const uint4 *>(b + j);
+        const float4 t0 = *reinterpret_cast<const float4 *>(t + j), t1 = *reinterpret_cast<const float4 *>(t + j + 4);
+        s = fmaf(bf16_lo(v.x), t0.x, s);
+        s = fmaf(bf16_hi(v.x), t0.y, s);
+        s = fmaf(bf16_lo(v.y), t0.z, s);
+        s = fmaf(bf16_hi(v.y), t0.w, s);
+        s = fmaf(bf16_lo(v.z), t1.x, s);
+        s = fmaf(bf16_hi(v.z), t1.y, s);
+        s = fmaf(bf16_lo(v.w), t1.z, s);
+        s = fmaf(bf16_hi(v.w), t1.w, s);
+    }
+    return s;
+}
+
+// ---------------------------------------------------------------------------
+// Few rows a group: chunks of at most CAP rows (8 or 32).
+//
+// A workgroup holds one chunk, one range of at most 2048 weights along K and
+// a few 32-row tiles of the matrix.  Its 8 waves split the range; a wave's
+// part (at most four 64-blocks) of the chunk's activations is converted to
+// fp16 once (a power of two per row and wave) and stays in registers.  A lane
+// of v_mfma_f32_32x32x16_f16 holds 32 weights of one block of one row, 16
+// bytes of codes, so that both lanes of a row lie in the same block: the
+// block's scale multiplies the fp32 result of the block's four MFMAs and
+// nothing of it is rounded.  The waves' tiles are added through LDS.
+// ---------------------------------------------------------------------------
+constexpr int kChunkWaves = 8;
+constexpr int kRangeBlocks = 32;  // 64-blocks of one range: four a wave
+
+template <int CAP, int MATS, bool PART, bool LORA>
+__global__ __launch_bounds__(kChunkWaves * 64) void ragged_chunk_kernel(const Args a) {
+    constexpr int kRegs = CAP / 2;  // accumulator registers that hold rows below CAP
+    __shared__ uint32_t lut[kLutDwords];
+    __shared__ float red[MATS][kChunkWaves][CAP * 32];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int col = lane & 31, g = lane >> 5;
+
+    const Chunk ck = find_chunk(a.offsets, a.E, a.R, blockIdx.y, CAP);
+    if (ck.count == 0) return;
+    const int nb = a.K >> 6;
+    const int b0 = (int)((int64_t)nb * blockIdx.z / a.ranges), b1 = (int)((int64_t)nb * (blockIdx.z + 1) / a.ranges);
+    const int lo = b0 + (b1 - b0) * wave / kChunkWaves, nblk = b0 + (b1 - b0) * (wave + 1) / kChunkWaves - lo;
+
+    // This wave's activations: lane (row, g) holds k = 64 b + 32 g + (0..31).
+    u32x4_t x[4][4];
+    {
+        int row = -1;
+        if (col < ck.count) row = source_row(a, ck.start + col);
+        const uint16_t *src = a.X + (int64_t)max(row, 0) * a.K + 64 * lo + 32 * g;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+                x[i][s] = row >= 0 && i < nblk ? *reinterpret_cast<const u32x4_t *>(src + 64 * i + 8 * s)
+                                               : u32x4_t{0u, 0u, 0u, 0u};
+    }
+    fill_lut(lut);
+
+    int shift;  // of this lane's row
+    {
+        u16x2_t mx = {0, 0};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    mx = __builtin_elementwise_max(mx, __builtin_bit_cast(u16x2_t, x[i][s][c] & 0x7FFF7FFFu));
+        int m = max((int)mx.x, (int)mx.y);
+        m = max(m, __shfl_xor(m, 32));
+        shift = fp16_shift((uint32_t)m);
+        const float f = exp2i(shift);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) x[i][s][c] = bf16x2_to_f16x2(x[i][s][c], f);
+    }
+    int back[kRegs];  // the inverse power of two of each register's row
+#pragma unroll
+    for (int i = 0; i < kRegs; ++i) back[i] = -__shfl(shift, tile_row(i, lane));
+    __syncthreads();
+
+    const int ntiles = (a.M + 31) >> 5;
+    const int t0 = blockIdx.x * a.tiles_per_wg, t1 = min(t0 + a.tiles_per_wg, ntiles);
+    const uint32_t laneoff = (uint32_t)lane << 2;
+    for (int t = t0; t < t1; ++t) {
+        const int m = min(t * 32 + col, a.M - 1);
+        const int64_t mrow = (int64_t)ck.e * a.M + m;
+        u32x4_t cw[MATS][4];
+        float sc[MATS][4];
+#pragma unroll
+        for (int q = 0; q < MATS; ++q)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int b = min(lo + i, nb - 1);
+                cw[q][i] = *reinterpret_cast<const u32x4_t *>(a.codes[q] + mrow * (a.K >> 1) + 32 * b + 16 * g);
+                sc[q][i] = f16_bits_to_f32(a.scales[q][mrow * nb + b]);
+            }
+#pragma unroll
+        for (int q = 0; q < MATS; ++q) {
+            float acc[kRegs];
+#pragma unroll
+            for (int i = 0; i < kRegs; ++i) acc[i] = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (i < nblk) {
+                    float16_t d = {};
+#pragma unroll
+                    for (int s = 0; s < 4; ++s) {
+                        half2_t w[4];
+                        lut8(lut, cw[q][i][s], laneoff, w);
+                        d = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(half8_t, x[i][s]), join8(w), d, 0,
+                                                                   0, 0);
+                    }
+#pragma unroll
+                    for (int j = 0; j < kRegs; ++j) acc[j] = fmaf(sc[q][i], d[j], acc[j]);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kRegs; ++i)
+                red[q][wave][tile_row(i, lane) * 32 + col] = ldexpf(acc[i], back[i]);
+        }
+        __syncthreads();
+        for (int o = threadIdx.x; o < CAP * 32; o += kChunkWaves * 64) {
+            const int row = o >> 5, mo = t * 32 + (o & 31);
+            if (row >= ck.count || mo >= a.M) continue;
+            float v[MATS];
+#pragma unroll
+            for (int q = 0; q < MATS; ++q) {
+                v[q] = red[q][0][o];
+#pragma unroll
+                for (int w = 1; w < kChunkWaves; ++w) v[q] += red[q][w][o];
+            }
+            const int p = ck.start + row;
+            const int64_t at = (int64_t)p * a.M + mo;
+            if constexpr (PART) {
+#pragma unroll
+                for (int q = 0; q < MATS; ++q)
+                    a.part[((int64_t)q * a.ranges + blockIdx.z) * a.R * a.M + at] = v[q];
+            } else {
+                float y = MATS == 2 ? swiglu(v[0], v[MATS - 1]) : v[0];
+                if constexpr (LORA) y += adapter_term(a, p, mo);
+                store_out(a.Y, a.bf16, at, y);
+            }
+        }
+        __syncthreads();
+    }
+}
+
+// Adds the partial planes in range order and finishes the outputs.
+template <int MATS, bool LORA>
+__global__ __launch_bounds__(256) void ragged_finish_kernel(const Args a) {
+    const int per = (a.M + 255) >> 8;
+    const int p = blockIdx.x / per, m = (blockIdx.x % per) * 256 + threadIdx.x;
+    if (a.offsets) {
+        // A position outside every group has no planes, and keeps its row.
+        bool in = false;
+        for (int e = threadIdx.x & 63; e < a.E; e += 64)
+            in = in || (p >= min(max(a.offsets[e], 0), a.R) && p < min(max(a.offsets[e + 1], 0), a.R));
+        if (__builtin_amdgcn_ballot_w64(in) == 0) return;
+    }
+    if (m >= a.M) return;
+    const int64_t at = (int64_t)p * a.M + m, plane = (int64_t)a.R * a.M;
+    float v[MATS];
+#pragma unroll
+    for (int q = 0; q < MATS; ++q) {
+        const float *s = a.part + (int64_t)q * a.ranges * plane + at;
+        v[q] = s[0];
+        for (int z = 1; z < a.ranges; ++z) v[q] += s[z * plane];
+    }
+    float y = MATS == 2 ? swiglu(v[0], v[MATS - 1]) : v[0];
+    if constexpr (LORA) y += adapter_term(a, p, m);
+    store_out(a.Y, a.bf16, at, y);
+}
+
+// ---------------------------------------------------------------------------
+// Many rows a group.
+// ---------------------------------------------------------------------------
+
+// One workgroup a row of X: fp16 under a power of two (the row's largest
+// magnitude goes to [2^14, 2^15)), and that power of two.  The workgroups
+// behind them: the exponent of each packed row's largest scale.
+__global__ __launch_bounds__(256) void ragged_prepare_kernel(const uint16_t *__restrict__ X, int T, int K,
+                                                             uint16_t *__restrict__ x16, int32_t *__restrict__ xexp,
+                                                             const uint16_t *__restrict__ s0,
+                                                             const uint16_t *__restrict__ s1, int64_t nrows,
+                                                             int8_t *__restrict__ e0, int8_t *__restrict__ e1) {
+    __shared__ uint32_t wmax[4];
+    if ((int)blockIdx.x < T) {
+        const u32x4_t *src = reinterpret_cast<const u32x4_t *>(X + (int64_t)blockIdx.x * K);
+        u32x4_t *dst = reinterpret_cast<u32x4_t *>(x16 + (int64_t)blockIdx.x * K);
+        const int n = K / 8;
+        u16x2_t mx = {0, 0};
+        for (int i = threadIdx.x; i < n; i += 256) {
+            const u32x4_t v = src[i];
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                mx = __builtin_elementwise_max(mx, __builtin_bit_cast(u16x2_t, v[c] & 0x7FFF7FFFu));
+        }
+        const uint32_t m = wave_max_u32(mx.x > mx.y ? mx.x : mx.y);
+        if ((threadIdx.x & 63) == 0) wmax[threadIdx.x >> 6] = m;
+        __syncthreads();
+        const int shift = fp16_shift(max(max(wmax[0], wmax[1]), max(wmax[2], wmax[3])));
+        const float f = exp2i(shift);
+        for (int i = threadIdx.x; i < n; i += 256) {
+            u32x4_t v = src[i];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) v[c] = bf16x2_to_f16x2(v[c], f);
+            dst[i] = v;
+        }
+        if (threadIdx.x == 0) xexp[blockIdx.x] = -shift;
+        return;
+    }
+    // 16 lanes a packed row.
+    const int64_t row = ((int64_t)blockIdx.x - T) * 16 + (threadIdx.x >> 4);
+    if (row >= nrows) return;
+    const int nb = K >> 6;
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        const uint16_t *s = (q ? s1 : s0);
+        if (!s) continue;
+        int m = 0;
+        for (int b = threadIdx.x & 15; b < nb; b += 16) m = max(m, (int)(s[row * nb + b] & 0x7FFF));
+#pragma unroll
+        for (int d = 8; d >= 1; d >>= 1) m = max(m, __shfl_xor(m, d));
+        // floor(log2) of the scale, subnormal ones included; 0 for a row of zeros
+        const float f = f16_bits_to_f32((uint32_t)m);
+        const int e = m == 0 ? 0 : (int)(__builtin_bit_cast(uint32_t, f) >> 23) - 127;
+        if ((threadIdx.x & 15) == 0) (q ? e1 : e0)[row] = (int8_t)min(e, 16);
+    }
+}
+
+constexpr int kTileWaves = 8;
+
+// A workgroup computes 64 MT rows of X (2 waves of MT tiles of 32) by 256
+// packed rows (4 waves of two 32-row tiles; with MATS == 2 each wave's tiles
+// are the gate's and the up's same 32 rows).
+template <int MT, int MATS, bool LORA>
+__global__ __launch_bounds__(kTileWaves * 64) void ragged_tile_kernel(const Args a) {
+    constexpr int TM = 64 * MT;
+    constexpr int kRowsWg = MATS == 2 ? 128 : 256;
+    constexpr int kPieces = TM * 8 / (kTileWaves * 64);  // 16-byte pieces of X a thread stages
+    __shared__ uint32_t lut[kLutDwords];
+    __shared__ uint4 xs[2][TM * 8];
+    __shared__ int xe[TM];
+    __shared__ int sid[LORA ? TM : 1];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int col = lane & 31, g = lane >> 5;
+    const int wt = wave & 1, wr = wave >> 1;
+
+    const int c = blockIdx.x / a.rowtiles, rt0 = blockIdx.x % a.rowtiles;
+    const Chunk ck = find_chunk(a.offsets, a.E, a.R, c, TM);
+    if (ck.count == 0) return;
+
+    for (int i = threadIdx.x; i < TM; i += kTileWaves * 64) {
+        const int row = i < ck.count ? source_row(a, ck.start + i) : -1;
+        xe[i] = row >= 0 ? a.xexp[row] : 0;
+        if constexpr (LORA) {
+            const int id = i < ck.count ? a.ids[ck.start + i] : -1;
+            sid[i] = id >= 0 && id < a.L ? id : -1;
+        }
+    }
+    // Staging of X: piece j of this thread is row threadIdx / 8 + 64 j, slot
+    // threadIdx % 8, which holds the row's 16-byte piece slot ^ (row % 8).
+    const uint4 *xsrc[kPieces];
+#pragma unroll
+    for (int j = 0; j < kPieces; ++j) {
+        const int i = (threadIdx.x >> 3) + 64 * j;
+        const int row = i < ck.count ? source_row(a, ck.start + i) : -1;
+        const int piece = (threadIdx.x & 7) ^ (i & 7);
+        xsrc[j] = row >= 0 ? reinterpret_cast<const uint4 *>(a.X + (int64_t)row * a.K) + piece : nullptr;
+    }
+
+    int m[2];
+    const u32x4_t *csrc[2];
+    const uint16_t *ssrc[2];
+    int e[2];
+    const int nb = a.K >> 6;
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        const int mat = MATS == 2 ? q : 0;
+        m[q] = rt0 * kRowsWg + (MATS == 2 ? wr * 32 : wr * 64 + q * 32) + col;
+        const int64_t mrow = (int64_t)ck.e * a.M + min(m[q], a.M - 1);
+        csrc[q] = reinterpret_cast<const u32x4_t *>(a.codes[mat] + mrow * (a.K >> 1)) + g;
+        ssrc[q] = a.scales[mat] + mrow * nb;
+        e[q] = a.rowexp[mat][mrow];
+    }
+
+    uint4 xv[kPieces];
+    u32x4_t cw[2];
+    uint32_t sv[2];
+    auto load = [&](int b) {
+#pragma unroll
+        for (int j = 0; j < kPieces; ++j) xv[j] = xsrc[j] ? xsrc[j][8 * b] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            cw[q] = csrc[q][2 * b];
+            sv[q] = ssrc[q][b];
+        }
+    };
+    load(0);
+    fill_lut(lut);
+
+    float16_t acc[MT][2];
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int q = 0; q < 2; ++q) acc[i][q] = float16_t{};
+    const uint32_t laneoff = (uint32_t)lane << 2;
+
+    for (int b = 0; b < nb; ++b) {
+        uint4 *buf = xs[b & 1];
+#pragma unroll
+        for (int j = 0; j < kPieces; ++j) buf[threadIdx.x + 512 * j] = xv[j];
+        __syncthreads();
+        u32x4_t cc[2];
+        half2_t s2[2];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            cc[q] = cw[q];
+            const _Float16 h = (_Float16)ldexpf(f16_bits_to_f32(sv[q]), 14 - e[q]);
+            s2[q] = half2_t{h, h};
+        }
+        if (b + 1 < nb) load(b + 1);
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            half8_t w[2];
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                half2_t v[4];
+                lut8(lut, cc[q][s], laneoff, v);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] *= s2[q];
+                w[q] = join8(v);
+            }
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+                const int row = wt * 32 * MT + 32 * i + col;
+                const uint4 xr = buf[row * 8 + ((4 * g + s) ^ (row & 7))];
+                const half8_t xa = __builtin_bit_cast(half8_t, xr);
+                acc[i][0] = __builtin_amdgcn_mfma_f32_32x32x16_f16(xa, w[0], acc[i][0], 0, 0, 0);
+                acc[i][1] = __builtin_amdgcn_mfma_f32_32x32x16_f16(xa, w[1], acc[i][1], 0, 0, 0);
+            }
+        }
+    }
+
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            const int x = xe[wt * 32 * MT + 32 * i + tile_row(j, lane)] - 14;
+            acc[i][0][j] = ldexpf(acc[i][0][j], x + e[0]);
+            acc[i][1][j] = ldexpf(acc[i][1][j], x + e[1]);
+        }
+
+    if constexpr (LORA) {
+        // The adapters among this wave's rows, one after the other; the rows
+        // of others enter as zeros.
+        int mine[2] = {-1, -1};
+        const int w0 = wt * 32 * MT;
+        if (lane < 32 * MT) mine[0] = sid[w0 + lane];
+        if (MT == 4) mine[1] = sid[w0 + 64 + lane];
+        while (true) {
+            const uint64_t p0 = __builtin_amdgcn_ballot_w64(mine[0] >= 0);
+            const uint64_t p1 = __builtin_amdgcn_ballot_w64(mine[1] >= 0);
+            if (!(p0 | p1)) break;
+            const int id = p0 ? __builtin_amdgcn_readlane(mine[0], __builtin_ctzll(p0))
+                              : __builtin_amdgcn_readlane(mine[1], __builtin_ctzll(p1));
+            if (mine[0] == id) mine[0] = -1;
+            if (mine[1] == id) mine[1] = -1;
+            for (int j0 = 0; j0 < a.r; j0 += 16) {
+                const bool live = j0 + 8 * g < a.r;
+                bf16x8_t bb[2];
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    u32x4_t v = {0u, 0u, 0u, 0u};
+                    if (live && m[q] < a.M)
+                        v = *reinterpret_cast<const u32x4_t *>(a.B + ((int64_t)id * a.M + m[q]) * a.r + j0 + 8 * g);
+                    bb[q] = __builtin_bit_cast(bf16x8_t, v);
+                }
+#pragma unroll
+                for (int i = 0; i < MT; ++i) {
+                    const int row = w0 + 32 * i + col;
+                    const bool use = sid[row] == id;
+                    if (__builtin_amdgcn_ballot_w64(use) == 0) continue;
+                    float t[8];
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) t[x] = 0.0f;
+                    if (use && live) {
+                        const float *src = a.t + (int64_t)(ck.start + row) * a.r + j0 + 8 * g;
+#pragma unroll
+                        for (int x = 0; x < 8; ++x) t[x] = src[x];
+                    }
+                    bf16x8_t hi, lo;
+                    split2(t, hi, lo);
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        acc[i][q] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(hi, bb[q], acc[i][q], 0, 0, 0);
+                        acc[i][q] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(lo, bb[q], acc[i][q], 0, 0, 0);
+                    }
+                }
+            }
+        }
+    }
+
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            const int row = wt * 32 * MT + 32 * i + tile_row(j, lane);
+            if (row >= ck.count) continue;
+            const int64_t at = (int64_t)(ck.start + row) * a.M;
+            if constexpr (MATS == 2) {
+                if (m[0] < a.M) store_out(a.Y, a.bf16, at + m[0], swiglu(acc[i][0][j], acc[i][1][j]));
+            } else {
+                if (m[0] < a.M) store_out(a.Y, a.bf16, at + m[0], acc[i][0][j]);
+                if (m[1] < a.M) store_out(a.Y, a.bf16, at + m[1], acc[i][1][j]);
+            }
+        }
+}
+
+// How a call runs.
+struct Plan {
+    bool tiles;   // tile kernel (else chunk kernel)
+    int mt;       // tile kernel: 32-row tiles a wave
+    int cap;      // chunk kernel: rows a chunk
+    int ranges;   // chunk kernel: ranges of K
+};
+
+Plan plan_of(int64_t E, int64_t M, int64_t K, int64_t R) {
+    Plan p = {};
+    // Rows a group, were all groups in use equally full.
+    const int64_t groups = E < R ? E : R;
+    const int64_t avg = groups ? (R + groups - 1) / groups : 0;
+    p.tiles = avg > 64;
+    p.mt = avg > 160 ? 4 : 2;
+    p.cap = R <= 8 || avg <= 6 ? 8 : 32;
+    p.ranges = (int)((K / 64 + kRangeBlocks - 1) / kRangeBlocks);
+    return p;
+}
+
+// Chunks of `most` rows that R rows in E groups can make at most.
+int64_t chunk_bound(int64_t E, int64_t R, int64_t most) {
+    const int64_t a = R / most + E;
+    return a < R ? a : R;
+}
+
+}  // namespace
+
+int compute_units() {
+    int dev = 0, n = 0;
+    if (hipGetDevice(&dev) != hipSuccess ||
+        hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || n < 1)
+        return 256;
+    return n;
+}
+
+bool ragged_fits(int64_t E, int64_t M, int64_t K, int64_t T, int64_t R, bool up) {
+    const Plan p = plan_of(E, M, K, R);
+    const int64_t most = INT64_C(1) << 32;  // threads of one launch
+    if (p.tiles) {
+        const int64_t rowtiles = (M + (up ? 127 : 255)) / (up ? 128 : 256);
+        return (T + (E * M + 15) / 16) * 256 < most && rowtiles * chunk_bound(E, R, 64 * p.mt) * 512 < most;
+    }
+    return ((M + 255) / 256) * R * 256 < most && chunk_bound(E, R, p.cap) < 65536;
+}
+
+size_t ragged_ws_bytes(int64_t E, int64_t M, int64_t K, int64_t T, int64_t R, bool up) {
+    const Plan p = plan_of(E, M, K, R);
+    const size_t mats = up ? 2 : 1;
+    if (p.tiles)
+        return round16((size_t)T * K * 2) + round16((size_t)T * 4) + mats * round16((size_t)E * M);
+    return p.ranges > 1 ? mats * p.ranges * (size_t)R * M * 4 : 0;
+}
+
+template <int MT>
+static const void *tile_fn(bool up, bool lora) {
+    if (up) return reinterpret_cast<const void *>(&ragged_tile_kernel<MT, 2, false>);
+    return lora ? reinterpret_cast<const void *>(&ragged_tile_kernel<MT, 1, true>)
+                : reinterpret_cast<const void *>(&ragged_tile_kernel<MT, 1, false>);
+}
+
+template <int CAP>
+static const void *chunk_fn(bool up, bool part, bool lora) {
+    if (up)
+        return part ? reinterpret_cast<const void *>(&ragged_chunk_kernel<CAP, 2, true, false>)
+                    : reinterpret_cast<const void *>(&ragged_chunk_kernel<CAP, 2, false, false>);
+    if (part) return reinterpret_cast<const void *>(&ragged_chunk_kernel<CAP, 1, true, false>);
+    return lora ? reinterpret_cast<const void *>(&ragged_chunk_kernel<CAP, 1, false, true>)
+                : reinterpret_cast<const void *>(&ragged_chunk_kernel<CAP, 1, false, false>);
+}
+
+hipError_t launch_ragged(const RaggedProduct &p, void *workspace, hipStream_t stream) {
+    const Plan pl = plan_of(p.E, p.M, p.K, p.R);
+    const bool up = p.up_codes != nullptr, lora = p.B != nullptr;
+    Args a = {};
+    a.codes[0] = p.codes;
+    a.codes[1] = p.up_codes;
+    a.scales[0] = p.scales;
+    a.scales[1] = p.up_scales;
+    a.M = (int)p.M;
+    a.K = (int)p.K;
+    a.E = (int)p.E;
+    a.R = (int)p.R;
+    a.X = p.X;
+    a.T = (int)p.T;
+    a.offsets = p.offsets;
+    a.rows = p.rows;
+    a.Y = p.Y;
+    a.bf16 = p.bf16;
+    a.B = p.B;
+    a.t = p.t;
+    a.ids = p.ids;
+    a.r = (int)p.r;
+    a.L = (int)p.L;
+    void *args[] = {&a};
+    if (pl.tiles) {
+        char *w = static_cast<char *>(workspace);
+        uint16_t *x16 = reinterpret_cast<uint16_t *>(w);
+        w += round16((size_t)p.T * p.K * 2);
+        int32_t *xexp = reinterpret_cast<int32_t *>(w);
+        w += round16((size_t)p.T * 4);
+        int8_t *re0 = reinterpret_cast<int8_t *>(w), *re1 = up ? re0 + round16((size_t)p.E * p.M) : nullptr;
+        int64_t nrows = p.E * p.M;
+        int T = a.T, K = a.K;
+        const uint16_t *X = p.X, *s0 = p.scales, *s1 = p.up_scales;
+        void *pargs[] = {&X, &T, &K, &x16, &xexp, &s0, &s1, &nrows, &re0, &re1};
+        const int64_t blocks = p.T + (nrows + 15) / 16;
+        hipError_t e = hipLaunchKernel(reinterpret_cast<const void *>(&ragged_prepare_kernel), dim3((unsigned)blocks),
+                                       dim3(256), pargs, 0, stream);
+        if (e != hipSuccess) return e;
+        a.X = x16;
+        a.xexp = xexp;
+        a.rowexp[0] = re0;
+        a.rowexp[1] = re1;
+        const int rows_wg = up ? 128 : 256;
+        a.rowtiles = (int)((p.M + rows_wg - 1) / rows_wg);
+        a.chunks = (int)chunk_bound(p.E, p.R, 64 * pl.mt);
+        const void *fn = pl.mt == 4 ? tile_fn<4>(up, lora) : tile_fn<2>(up, lora);
+        return hipLaunchKernel(fn, dim3((unsigned)((int64_t)a.rowtiles * a.chunks)), dim3(kTileWaves * 64), args, 0,
+                               stream);
+    }
+    a.ranges = pl.ranges;
+    const bool part = pl.ranges > 1;
+    a.part = part ? static_cast<float *>(workspace) : nullptr;
+    const int64_t ntiles = (p.M + 31) / 32, chunks = chunk_bound(p.E, p.R, pl.cap);
+    // Two workgroups a compute unit at least, and as few more as it takes.
+    int64_t per = ntiles * chunks * pl.ranges / (2 * compute_units());
+    a.tiles_per_wg = (int)(per < 1 ? 1 : per > 8 ? 8 : per);
+    const dim3 grid((unsigned)((ntiles + a.tiles_per_wg - 1) / a.tiles_per_wg), (unsigned)chunks, (unsigned)pl.ranges);
+    hipError_t e = hipLaunchKernel(pl.cap == 8 ? chunk_fn<8>(up, part, lora) : chunk_fn<32>(up, part, lora), grid,
+                                   dim3(kChunkWaves * 64), args, 0, stream);
+    if (e != hipSuccess || !part) return e;
+    const void *fin = up     ? reinterpret_cast<const void *>(&ragged_finish_kernel<2, false>)
+                      : lora ? reinterpret_cast<const void *>(&ragged_finish_kernel<1, true>)
+                             : reinterpret_cast<const void *>(&ragged_finish_kernel<1, false>);
+    return hipLaunchKernel(fin, dim3((unsigned)((p.M + 255) / 256 * p.R)), dim3(256), args, 0, stream);
+}
+
+}  // namespace q4

@@ -1,0 +1,119 @@
+// q4_ragged_device.h -- pieces shared by the ragged products, the router and
+// the adapters' kernels (gfx950).
+#pragma once
+
+#include "q4_device.h"
+#include "q4_lut.h"
+
+namespace q4 {
+
+typedef _Float16 half8_t __attribute__((ext_vector_type(8)));
+
+__device__ __forceinline__ float bf16_lo(uint32_t d) { return __builtin_bit_cast(float, d << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t d) { return __builtin_bit_cast(float, d & 0xFFFF0000u); }
+__device__ __forceinline__ float bf16_f32(uint16_t b) { return __builtin_bit_cast(float, (uint32_t)b << 16); }
+// Nearest even.
+__device__ __forceinline__ uint16_t f32_bf16(float v) { return __builtin_bit_cast(uint16_t, (__bf16)v); }
+
+__device__ __forceinline__ void store_out(void *Y, bool bf16, int64_t at, float v) {
+    if (bf16) static_cast<uint16_t *>(Y)[at] = f32_bf16(v);
+    else static_cast<float *>(Y)[at] = v;
+}
+
+// silu(g) * u; for g below -88 e^-g overflows to infinity and the quotient is -0.
+__device__ __forceinline__ float swiglu(float g, float u) { return g / (1.0f + __expf(-g)) * u; }
+
+// A piece of at most `most` rows of one group.
+struct Chunk {
+    int e;      // group
+    int start;  // first position
+    int count;  // rows (0: no such chunk)
+};
+
+// Chunk c of the groups cut into pieces of `most` rows, in order.  Every lane
+// of the wave returns the same values.  Offsets are held to 0 .. R.
+__device__ __forceinline__ Chunk find_chunk(const int32_t *__restrict__ offsets, int E, int R, int c, int most) {
+    if (!offsets) {
+        const int64_t s = (int64_t)c * most;
+        if (s >= R) return {0, 0, 0};
+        return {0, (int)s, min(most, R - (int)s)};
+    }
+    const int lane = threadIdx.x & 63;
+    int base = 0;
+    for (int e0 = 0; e0 < E; e0 += 64) {
+        const int e = e0 + lane;
+        int lo = 0, hi = 0;
+        if (e < E) {
+            lo = min(max(offsets[e], 0), R);
+            hi = min(max(offsets[e + 1], 0), R);
+        }
+        const int n = max(hi - lo, 0);
+        const int pieces = (n + most - 1) / most;
+        int incl = pieces;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int o = __shfl_up(incl, d);
+            if (lane >= d) incl += o;
+        }
+        const int first = base + incl - pieces;
+        const uint64_t hit = __builtin_amdgcn_ballot_w64(c >= first && c < first + pieces);
+        if (hit) {
+            const int src = __builtin_ctzll(hit);
+            const int s = lo + (c - first) * most;
+            Chunk k;
+            k.e = __builtin_amdgcn_readlane(e, src);
+            k.start = __builtin_amdgcn_readlane(s, src);
+            k.count = __builtin_amdgcn_readlane(min(most, hi - s), src);
+            return k;
+        }
+        base += __shfl(incl, 63);
+    }
+    return {0, 0, 0};
+}
+
+// Shift that puts a bf16 row's largest magnitude (given as its bits) into
+// fp16's upper range [2^14, 2^15); held to what one fp32 power of two can do
+// (a row below 2^-113 then stays smaller), and taken as for the largest
+// finite exponent where the row holds an infinity or a NaN.
+__device__ __forceinline__ int fp16_shift(uint32_t maxbits) {
+    const int E = min((int)(maxbits >> 7), 254);
+    return min(141 - E, 127);
+}
+
+// Two bf16 of a dword, each times 2^shift (f), as two fp16.  Exact where the
+// result is an fp16 normal number, towards zero below that.
+__device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t d, float f) {
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(bf16_lo(d) * f, bf16_hi(d) * f));
+}
+
+// Eight weights of four code bytes, as fp16 table entries.
+__device__ __forceinline__ void lut8(const uint32_t *lut, uint32_t word, uint32_t laneoff, half2_t (&w)[4]) {
+    w[0] = lut_pair<0>(lut, word, laneoff);
+    w[1] = lut_pair<1>(lut, word, laneoff);
+    w[2] = lut_pair<2>(lut, word, laneoff);
+    w[3] = lut_pair<3>(lut, word, laneoff);
+}
+
+__device__ __forceinline__ half8_t join8(const half2_t (&w)[4]) {
+    const u32x4_t v = {__builtin_bit_cast(uint32_t, w[0]), __builtin_bit_cast(uint32_t, w[1]),
+                       __builtin_bit_cast(uint32_t, w[2]), __builtin_bit_cast(uint32_t, w[3])};
+    return __builtin_bit_cast(half8_t, v);
+}
+
+// A 32 x 32 tile of v_mfma_f32_32x32x16: lane l holds column l % 32 and, in
+// register i, row 8 (i / 4) + 4 (l / 32) + i % 4.
+__device__ __forceinline__ int tile_row(int i, int lane) { return 8 * (i >> 2) + 4 * (lane >> 5) + (i & 3); }
+
+// v as the sum of two bf16: the nearest one and the nearest to what it leaves
+// (2^-17 of v at most is lost).  An infinity or a NaN stands alone.
+__device__ __forceinline__ void split2(const float (&v)[8], bf16x8_t &hi, bf16x8_t &lo) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const __bf16 h = (__bf16)v[i];
+        const float rest = v[i] - (float)h;
+        hi[i] = h;
+        lo[i] = (__bf16)(fabsf(rest) < __builtin_inff() ? rest : 0.0f);
+    }
+}
+
+}  // namespace q4

@@ -1,0 +1,432 @@
+// q4_route.hip -- which experts a token goes to, the order that groups the
+// tokens by expert, and the weighted sum of the experts' outputs.
+//
+// Top k: one wave a token, the logits spread over its lanes; k times the
+// largest key wins, where a key is the logit's bits in an order that compares
+// as unsigned (the upper half) and the complement of the index (the lower
+// half), so that equal logits fall to the lowest index.
+//
+// Grouping is a counting sort that keeps the slots' order: workgroups take
+// consecutive runs of slots; the first launch leaves each run's count of
+// every expert, the second adds up the counts before its run and ranks its
+// own slots (a wave at a time, by ballots over the expert's bits).  A run
+// that holds every slot needs one launch.  No atomics on memory: the same
+// input gives the same plan.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "q4_experts.h"
+#include "q4_ragged.h"
+#include "q4_ragged_device.h"
+
+namespace q4 {
+
+namespace {
+
+constexpr int kRouteThreads = 512;
+constexpr int kRouteWaves = kRouteThreads / 64;
+constexpr int kMaxRuns = 256;    // runs of the counting sort at most
+constexpr int kRunTokens = 64;   // tokens of a run at least (slots, for a plain sort: 512)
+
+struct RouteArgs {
+    const void *logits;
+    int bf16, T, E, k, all;
+    int32_t *experts;
+    float *weights;
+    int32_t *hist;    // [runs][E], or null: one run, sorted in the same launch
+    int run;          // tokens of a run
+    int32_t *offsets, *rows, *pos;
+};
+
+struct SortArgs {
+    const int32_t *bins;
+    int slots, E, per, run;  // run: slots of a run
+    const int32_t *hist;     // [runs][E], or null: one run
+    int32_t *offsets, *rows, *pos;
+};
+
+__device__ __forceinline__ uint64_t key_of(float v, int index) {
+    v = v != v ? -__builtin_inff() : v + 0.0f;  // NaN as -infinity, -0 as 0
+    const uint32_t b = __builtin_bit_cast(uint32_t, v);
+    const uint32_t order = b & 0x80000000u ? ~b : b | 0x80000000u;
+    return (uint64_t)order << 32 | (uint32_t)~index;
+}
+
+__device__ __forceinline__ uint64_t wave_max_u64(uint64_t v) {
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1) {
+        const uint32_t lo = __shfl_xor((uint32_t)v, d), hi = __shfl_xor((uint32_t)(v >> 32), d);
+        const uint64_t o = (uint64_t)hi << 32 | lo;
+        v = o > v ? o : v;
+    }
+    return v;
+}
+
+// The choice of token t by this wave.
+template <int EPL>
+__device__ __forceinline__ void choose(const RouteArgs &a, int t) {
+    const int lane = threadIdx.x & 63;
+    float l[EPL];
+    uint64_t key[EPL];
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+        const int e = lane + 64 * i;
+        l[i] = -__builtin_inff();
+        key[i] = 0;  // below every logit's
+        if (e < a.E) {
+            const int64_t at = (int64_t)t * a.E + e;
+            const float v = a.bf16 ? bf16_f32(static_cast<const uint16_t *>(a.logits)[at])
+                                   : static_cast<const float *>(a.logits)[at];
+            l[i] = v != v ? -__builtin_inff() : v;
+            key[i] = key_of(v, e);
+        }
+    }
+    float largest = 0.0f, total = 0.0f, mine = 0.0f;
+    int chosen = 0;
+    for (int j = 0; j < a.k; ++j) {
+        uint64_t best = key[0];
+#pragma unroll
+        for (int i = 1; i < EPL; ++i) best = key[i] > best ? key[i] : best;
+        best = wave_max_u64(best);
+#pragma unroll
+        for (int i = 0; i < EPL; ++i)
+            if (key[i] == best) key[i] = 0;
+        const uint32_t order = (uint32_t)(best >> 32);
+        const float v = __builtin_bit_cast(float, order & 0x80000000u ? order & 0x7FFFFFFFu : ~order);
+        if (j == 0) largest = v;
+        const float p = v == largest ? 1.0f : expf(v - largest);
+        total += p;
+        if (lane == j) {
+            mine = p;
+            chosen = (int)~(uint32_t)best;
+        }
+    }
+    if (a.all) {
+        float s = 0.0f;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i)
+            if (lane + 64 * i < a.E) s += l[i] == largest ? 1.0f : expf(l[i] - largest);
+        total = wave_sum(s);
+    }
+    if (lane < a.k) {
+        a.experts[(int64_t)t * a.k + lane] = chosen;
+        a.weights[(int64_t)t * a.k + lane] = largest == -__builtin_inff() ? 0.0f : mine / total;
+    }
+}
+
+// Ranks slots s0 .. s1 - 1; next[e] is the position that the next slot of bin
+// e takes (bin E: none).  Whole workgroup.
+__device__ __forceinline__ void rank_run(const int32_t *bins, int s0, int s1, int E, int per, int32_t *next,
+                                         int32_t *rows, int32_t *pos) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    int bits = 1;
+    while ((1 << bits) <= E) ++bits;
+    for (int base = s0; base < s1; base += kRouteThreads) {
+        const int s = base + threadIdx.x;
+        const bool live = s < s1;
+        int e = live ? bins[s] : E;
+        if (e < 0 || e > E) e = E;
+        uint64_t same = __builtin_amdgcn_ballot_w64(live);
+        for (int b = 0; b < bits; ++b) {
+            const uint64_t with = __builtin_amdgcn_ballot_w64((e >> b) & 1);
+            same &= (e >> b) & 1 ? with : ~with;
+        }
+        const int before = __builtin_popcountll(same & ((1ull << lane) - 1));
+        const int waves = min(kRouteWaves, (s1 - base + 63) >> 6);
+        for (int w = 0; w < waves; ++w) {
+            if (wave == w && live) {
+                const int p = next[e] + before;
+                if (before == 0) next[e] += __builtin_popcountll(same);
+                rows[p] = s / per;
+                if (pos) pos[s] = p;
+            }
+            __syncthreads();
+        }
+    }
+}
+
+// From counts[e] (this run's first slot of each bin comes after `before[e]`
+// earlier ones, `total[e]` in all): offsets and the first positions.  LDS
+// arrays of E + 1; whole workgroup.
+__device__ __forceinline__ void first_positions(int E, int slots, const int32_t *total, int32_t *next, int32_t *sum,
+                                                int32_t *offsets, bool write) {
+    // Exclusive sums over the bins: each wave's lanes take runs of bins.
+    const int n = (E + kRouteThreads - 1) / kRouteThreads;
+    const int e0 = threadIdx.x * n;
+    int s = 0;
+    for (int i = 0; i < n; ++i)
+        if (e0 + i < E) s += total[e0 + i];
+    int incl = s;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int o = __shfl_up(incl, d);
+        if (lane >= d) incl += o;
+    }
+    if (lane == 63) sum[wave] = incl;
+    __syncthreads();
+    int at = incl - s;
+    for (int w = 0; w < wave; ++w) at += sum[w];
+    for (int i = 0; i < n; ++i) {
+        const int e = e0 + i;
+        if (e < E) {
+            if (write) offsets[e] = at;
+            next[e] += at;
+            at += total[e];
+        }
+    }
+    int all = 0;
+    for (int w = 0; w < kRouteWaves; ++w) all += sum[w];
+    if (threadIdx.x == 0) {
+        if (write) offsets[E] = all;
+        next[E] += all;  // slots of no bin
+    }
+    __syncthreads();
+    (void)slots;
+}
+
+template <int EPL>
+__global__ __launch_bounds__(kRouteThreads) void route_kernel(const RouteArgs a) {
+    __shared__ int32_t total[Q4_MAX_EXPERTS + 1], next[Q4_MAX_EXPERTS + 1], sum[kRouteWaves];
+    const int t0 = blockIdx.x * a.run, t1 = min(t0 + a.run, a.T);
+    for (int e = threadIdx.x; e <= a.E; e += kRouteThreads) total[e] = next[e] = 0;
+    for (int t = t0 + (threadIdx.x >> 6); t < t1; t += kRouteWaves) choose<EPL>(a, t);
+    __threadfence_block();
+    __syncthreads();
+    const int s0 = t0 * a.k, s1 = t1 * a.k;
+    for (int s = s0 + threadIdx.x; s < s1; s += kRouteThreads) atomicAdd(&total[a.experts[s]], 1);
+    __syncthreads();
+    if (a.hist) {
+        for (int e = threadIdx.x; e < a.E; e += kRouteThreads) a.hist[(int64_t)blockIdx.x * a.E + e] = total[e];
+        return;
+    }
+    first_positions(a.E, s1, total, next, sum, a.offsets, true);
+    rank_run(a.experts, s0, s1, a.E, a.k, next, a.rows, a.pos);
+}
+
+// Counts of each run, for a plain sort.
+__global__ __launch_bounds__(kRouteThreads) void sort_count_kernel(const SortArgs a, int32_t *hist) {
+    __shared__ int32_t total[Q4_MAX_EXPERTS + 1];
+    for (int e = threadIdx.x; e <= a.E; e += kRouteThreads) total[e] = 0;
+    __syncthreads();
+    const int s0 = blockIdx.x * a.run, s1 = min(s0 + a.run, a.slots);
+    for (int s = s0 + threadIdx.x; s < s1; s += kRouteThreads) {
+        const int e = a.bins[s];
+        if (e >= 0 && e < a.E) atomicAdd(&total[e], 1);
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < a.E; e += kRouteThreads) hist[(int64_t)blockIdx.x * a.E + e] = total[e];
+}
+
+__global__ __launch_bounds__(kRouteThreads) void sort_kernel(const SortArgs a) {
+    __shared__ int32_t total[Q4_MAX_EXPERTS + 1], next[Q4_MAX_EXPERTS + 1], sum[kRouteWaves];
+    const int s0 = blockIdx.x * a.run, s1 = min(s0 + a.run, a.slots);
+    for (int e = threadIdx.x; e <= a.E; e += kRouteThreads) total[e] = next[e] = 0;
+    __syncthreads();
+    if (a.hist) {
+        int before_all = 0;
+        for (int e = threadIdx.x; e < a.E; e += kRouteThreads) {
+            int before = 0, all = 0;
+#pragma unroll 8
+            for (int b = 0; b < (int)gridDim.x; ++b) {
+                const int n = a.hist[(int64_t)b * a.E + e];
+                if (b < (int)blockIdx.x) before += n;
+                all += n;
+            }
+            total[e] = all;
+            next[e] = before;
+            before_all += before;
+        }
+        // Slots of no bin before this run: those that the bins do not count.
+        atomicAdd(&total[a.E], before_all);
+        __syncthreads();
+        if (threadIdx.x == 0) next[a.E] = s0 - total[a.E];
+        __syncthreads();
+    } else {
+        for (int s = s0 + threadIdx.x; s < s1; s += kRouteThreads) {
+            const int e = a.bins[s];
+            if (e >= 0 && e < a.E) atomicAdd(&total[e], 1);
+        }
+        __syncthreads();
+    }
+    first_positions(a.E, a.slots, total, next, sum, a.offsets, blockIdx.x == 0);
+    rank_run(a.bins, s0, s1, a.E, a.per, next, a.rows, a.pos);
+}
+
+struct CombineArgs {
+    const void *Y;
+    int y_bf16, R, M;
+    const float *weights;
+    const int32_t *pos;
+    int T, k, out_bf16, per;  // per: workgroups a token
+    void *out;
+};
+
+// A lane adds 8 neighbouring columns (VEC: rows of whole 16-byte pieces) or
+// one.
+template <bool VEC>
+__global__ __launch_bounds__(256) void combine_kernel(const CombineArgs a) {
+    constexpr int W = VEC ? 8 : 1;
+    const int t = blockIdx.x / a.per;
+    const int m = ((blockIdx.x % a.per) * 256 + threadIdx.x) * W;
+    if (m >= a.M) return;
+    float s[W];
+#pragma unroll
+    for (int i = 0; i < W; ++i) s[i] = 0.0f;
+    for (int j = 0; j < a.k; ++j) {
+        const int p = a.pos[(int64_t)t * a.k + j];
+        if (p < 0 || p >= a.R) continue;
+        const float w = a.weights[(int64_t)t * a.k + j];
+        const int64_t at = (int64_t)p * a.M + m;
+        if constexpr (VEC) {
+            if (a.y_bf16) {
+                const uint4 v = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.Y) + at);
+                const uint32_t d[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    s[2 * i] = fmaf(w, bf16_lo(d[i]), s[2 * i]);
+                    s[2 * i + 1] = fmaf(w, bf16_hi(d[i]), s[2 * i + 1]);
+                }
+            } else {
+                const float4 *y = reinterpret_cast<const float4 *>(static_cast<const float *>(a.Y) + at);
+                const float4 u = y[0], v = y[1];
+                const float d[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int i = 0; i < 8; ++i) s[i] = fmaf(w, d[i], s[i]);
+            }
+        } else {
+            const float y = a.y_bf16 ? bf16_f32(static_cast<const uint16_t *>(a.Y)[at])
+                                     : static_cast<const float *>(a.Y)[at];
+            s[0] = fmaf(w, y, s[0]);
+        }
+    }
+    const int64_t at = (int64_t)t * a.M + m;
+    if constexpr (VEC) {
+        if (a.out_bf16) {
+            uint32_t d[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                d[i] = (uint32_t)f32_bf16(s[2 * i]) | (uint32_t)f32_bf16(s[2 * i + 1]) << 16;
+            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + at) = make_uint4(d[0], d[1], d[2], d[3]);
+        } else {
+            float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(a.out) + at);
+            o[0] = make_float4(s[0], s[1], s[2], s[3]);
+            o[1] = make_float4(s[4], s[5], s[6], s[7]);
+        }
+    } else {
+        store_out(a.out, a.out_bf16, at, s[0]);
+    }
+}
+
+// Items of a run, so that at most kMaxRuns runs of whole `least` cover n.
+int64_t run_of(int64_t n, int64_t least) {
+    const int64_t per = (n + kMaxRuns - 1) / kMaxRuns;
+    return per <= least ? least : (per + least - 1) / least * least;
+}
+
+const void *route_fn(int64_t E) {
+    if (E <= 64) return reinterpret_cast<const void *>(&route_kernel<1>);
+    if (E <= 128) return reinterpret_cast<const void *>(&route_kernel<2>);
+    if (E <= 256) return reinterpret_cast<const void *>(&route_kernel<4>);
+    if (E <= 512) return reinterpret_cast<const void *>(&route_kernel<8>);
+    return reinterpret_cast<const void *>(&route_kernel<16>);
+}
+
+}  // namespace
+
+size_t sort_ws_bytes(int64_t slots, int64_t E) {
+    const int64_t run = run_of(slots, kRouteThreads), runs = (slots + run - 1) / run;
+    return runs > 1 ? (size_t)runs * E * 4 : 0;
+}
+
+hipError_t launch_sort(const int32_t *bins, int64_t slots, int64_t E, int64_t per, int32_t *offsets, int32_t *rows,
+                       int32_t *pos, void *workspace, hipStream_t stream) {
+    SortArgs a = {};
+    a.bins = bins;
+    a.slots = (int)slots;
+    a.E = (int)E;
+    a.per = (int)per;
+    a.run = (int)run_of(slots, kRouteThreads);
+    a.offsets = offsets;
+    a.rows = rows;
+    a.pos = pos;
+    int64_t runs = (slots + a.run - 1) / a.run;
+    if (runs < 1) runs = 1;  // offsets are still written
+    if (runs > 1) {
+        int32_t *hist = static_cast<int32_t *>(workspace);
+        void *cargs[] = {&a, &hist};
+        const hipError_t e = hipLaunchKernel(reinterpret_cast<const void *>(&sort_count_kernel), dim3((unsigned)runs),
+                                             dim3(kRouteThreads), cargs, 0, stream);
+        if (e != hipSuccess) return e;
+        a.hist = hist;
+    }
+    void *args[] = {&a};
+    return hipLaunchKernel(reinterpret_cast<const void *>(&sort_kernel), dim3((unsigned)runs), dim3(kRouteThreads),
+                           args, 0, stream);
+}
+
+size_t route_ws_bytes(int64_t T, int64_t E, int64_t k) {
+    const int64_t run = run_of(T, kRunTokens), runs = (T + run - 1) / run;
+    (void)k;
+    return runs > 1 ? (size_t)runs * E * 4 : 0;
+}
+
+hipError_t launch_route(const void *logits, bool bf16, int64_t T, int64_t E, int64_t k, bool all, int32_t *experts,
+                        float *weights, int32_t *offsets, int32_t *rows, int32_t *pos, void *workspace,
+                        hipStream_t stream) {
+    RouteArgs a = {};
+    a.logits = logits;
+    a.bf16 = bf16;
+    a.T = (int)T;
+    a.E = (int)E;
+    a.k = (int)k;
+    a.all = all;
+    a.experts = experts;
+    a.weights = weights;
+    a.run = (int)run_of(T, kRunTokens);
+    a.offsets = offsets;
+    a.rows = rows;
+    a.pos = pos;
+    int64_t runs = (T + a.run - 1) / a.run;
+    if (runs < 1) runs = 1;
+    if (runs > 1) a.hist = static_cast<int32_t *>(workspace);
+    void *args[] = {&a};
+    const hipError_t e = hipLaunchKernel(route_fn(E), dim3((unsigned)runs), dim3(kRouteThreads), args, 0, stream);
+    if (e != hipSuccess || runs == 1) return e;
+    SortArgs b = {};
+    b.bins = experts;
+    b.slots = (int)(T * k);
+    b.E = (int)E;
+    b.per = (int)k;
+    b.run = (int)(a.run * k);
+    b.hist = a.hist;
+    b.offsets = offsets;
+    b.rows = rows;
+    b.pos = pos;
+    void *sargs[] = {&b};
+    return hipLaunchKernel(reinterpret_cast<const void *>(&sort_kernel), dim3((unsigned)runs), dim3(kRouteThreads),
+                           sargs, 0, stream);
+}
+
+hipError_t launch_combine(const void *Y, bool y_bf16, int64_t R, int64_t M, const float *weights, const int32_t *pos,
+                          int64_t T, int64_t k, bool out_bf16, void *out, hipStream_t stream) {
+    CombineArgs a = {};
+    a.Y = Y;
+    a.y_bf16 = y_bf16;
+    a.R = (int)R;
+    a.M = (int)M;
+    a.weights = weights;
+    a.pos = pos;
+    a.T = (int)T;
+    a.k = (int)k;
+    a.out_bf16 = out_bf16;
+    a.out = out;
+    const bool vec = M % 8 == 0;  // every row starts on 16 bytes
+    a.per = (int)((M + (vec ? 2047 : 255)) / (vec ? 2048 : 256));
+    void *args[] = {&a};
+    return hipLaunchKernel(vec ? reinterpret_cast<const void *>(&combine_kernel<true>)
+                               : reinterpret_cast<const void *>(&combine_kernel<false>),
+                           dim3((unsigned)(T * a.per)), dim3(256), args, 0, stream);
+}
+
+}  // namespace q4
