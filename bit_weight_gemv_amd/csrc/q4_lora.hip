@@ -30,6 +30,8 @@ struct ShrinkArgs {
     float *t;
 };
 
+constexpr int64_t kTokenBytes = 32 << 20;  // adapters' bytes that tokens on their own may read
+
 // Eight bf16 of a row at column k; zeros past its end.  VEC: rows start on 16
 // bytes and have whole pieces.
 template <bool VEC>
@@ -69,14 +71,17 @@ __global__ __launch_bounds__(256) void lora_shrink_token_kernel(const ShrinkArgs
     if (lane == 0) a.t[(int64_t)n * a.r + j] = s * a.scaling[id];
 }
 
-// Many tokens: a workgroup takes 32, its 8 waves split K in 64-blocks dealt
-// round; the adapters among the 32 tokens come one after the other.
+// Many tokens: a workgroup takes 16, its 8 waves split K in 64-blocks dealt
+// round; the adapters among the 16 tokens come one after the other.  Lane
+// (row, g) of v_mfma_f32_16x16x32_bf16 holds k = 64 b + 16 g + (0..15) of a
+// block in two steps, so a row's four lanes read 128 neighbouring bytes.
+// Bound by the bytes of X: one adapter's rows stay in the cache.
 template <bool VEC, int JT>
 __global__ __launch_bounds__(512) void lora_shrink_kernel(const ShrinkArgs a) {
-    __shared__ float red[8][32 * 32];
+    __shared__ float red[8][16 * 16 * JT];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int col = lane & 31, g = lane >> 5;
-    const int n0 = blockIdx.x * 32, n = n0 + col;
+    const int col = lane & 15, g = lane >> 4;
+    const int n0 = blockIdx.x * 16, n = n0 + col;
     int id = n < a.N ? a.ids[n] : -1;
     if (id >= a.L) id = -1;
     const uint16_t *x = a.X + (int64_t)min(n, a.N - 1) * a.K;
@@ -88,47 +93,47 @@ __global__ __launch_bounds__(512) void lora_shrink_kernel(const ShrinkArgs a) {
         const int now = __builtin_amdgcn_readlane(pending, __builtin_ctzll(left));
         if (pending == now) pending = -1;
         const float scale = a.scaling[now];
-        float16_t acc[JT];
+        float4_t acc[JT];
 #pragma unroll
-        for (int q = 0; q < JT; ++q) acc[q] = float16_t{};
+        for (int q = 0; q < JT; ++q) acc[q] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
         const uint16_t *z = a.Z + (int64_t)now * a.r * a.pitch;
         for (int b = wave; b < nb; b += 8) {
-            const int k = 64 * b + 32 * g;
-            u32x4_t xv[4], zv[JT][4];
+            const int k = 64 * b + 16 * g;
+            u32x4_t xv[2], zv[JT][2];
 #pragma unroll
-            for (int s = 0; s < 4; ++s) xv[s] = row_piece<VEC>(x, k + 8 * s, a.K);
+            for (int s = 0; s < 2; ++s) xv[s] = row_piece<VEC>(x, k + 8 * s, a.K);
 #pragma unroll
             for (int q = 0; q < JT; ++q)
 #pragma unroll
-                for (int s = 0; s < 4; ++s) {
+                for (int s = 0; s < 2; ++s) {
                     zv[q][s] = u32x4_t{0u, 0u, 0u, 0u};
-                    if (32 * q + col < a.r && k + 8 * s < a.pitch)
-                        zv[q][s] = *reinterpret_cast<const u32x4_t *>(z + (int64_t)(32 * q + col) * a.pitch + k + 8 * s);
+                    if (16 * q + col < a.r)
+                        zv[q][s] = *reinterpret_cast<const u32x4_t *>(z + (int64_t)(16 * q + col) * a.pitch + k + 8 * s);
                 }
 #pragma unroll
-            for (int s = 0; s < 4; ++s)
+            for (int s = 0; s < 2; ++s)
 #pragma unroll
                 for (int q = 0; q < JT; ++q)
-                    acc[q] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, xv[s]),
+                    acc[q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, xv[s]),
                                                                      __builtin_bit_cast(bf16x8_t, zv[q][s]), acc[q], 0,
                                                                      0, 0);
         }
+        // Register i: token 4 g + i, rank 16 q + col.
 #pragma unroll
-        for (int q = 0; q < JT; ++q) {
+        for (int q = 0; q < JT; ++q)
 #pragma unroll
-            for (int i = 0; i < 16; ++i) red[wave][tile_row(i, lane) * 32 + col] = acc[q][i];
-            __syncthreads();
-            for (int o = threadIdx.x; o < 1024; o += 512) {
-                const int row = o >> 5, j = 32 * q + (o & 31);
-                if (n0 + row < a.N && j < a.r && a.ids[n0 + row] == now) {
-                    float s = red[0][o];
+            for (int i = 0; i < 4; ++i) red[wave][(4 * g + i) * 16 * JT + 16 * q + col] = acc[q][i];
+        __syncthreads();
+        for (int o = threadIdx.x; o < 256 * JT; o += 512) {
+            const int row = o / (16 * JT), j = o % (16 * JT);
+            if (n0 + row < a.N && j < a.r && a.ids[n0 + row] == now) {
+                float s = red[0][o];
 #pragma unroll
-                    for (int w = 1; w < 8; ++w) s += red[w][o];
-                    a.t[(int64_t)(n0 + row) * a.r + j] = s * scale;
-                }
+                for (int w = 1; w < 8; ++w) s += red[w][o];
+                a.t[(int64_t)(n0 + row) * a.r + j] = s * scale;
             }
-            __syncthreads();
         }
+        __syncthreads();
     }
 }
 
@@ -136,24 +141,27 @@ hipError_t launch_shrink(const ShrinkArgs &s, hipStream_t stream) {
     ShrinkArgs a = s;
     void *args[] = {&a};
     const bool vec = a.K % 8 == 0;
-    // A token of its own workgroups reads its adapter alone; 32 tokens that
-    // share a workgroup read it once for all that use it, but one adapter
-    // after the other.
-    if (a.N <= 64)
+    // A token of its own workgroups reads its adapter alone: many short waits
+    // at once, but an adapter's bytes for every token; 16 tokens that share a
+    // workgroup read it once for all that use it, one adapter after the other.
+    if (a.N <= 64 || (int64_t)a.N * a.r * a.pitch * 2 <= kTokenBytes)
         return hipLaunchKernel(vec ? reinterpret_cast<const void *>(&lora_shrink_token_kernel<true>)
                                    : reinterpret_cast<const void *>(&lora_shrink_token_kernel<false>),
                                dim3((unsigned)a.N, (unsigned)((a.r + 3) / 4)), dim3(256), args, 0, stream);
     const void *fn;
-    if (a.r <= 32)
+    if (a.r <= 16)
         fn = vec ? reinterpret_cast<const void *>(&lora_shrink_kernel<true, 1>)
                  : reinterpret_cast<const void *>(&lora_shrink_kernel<false, 1>);
-    else if (a.r <= 64)
+    else if (a.r <= 32)
         fn = vec ? reinterpret_cast<const void *>(&lora_shrink_kernel<true, 2>)
                  : reinterpret_cast<const void *>(&lora_shrink_kernel<false, 2>);
-    else
+    else if (a.r <= 64)
         fn = vec ? reinterpret_cast<const void *>(&lora_shrink_kernel<true, 4>)
                  : reinterpret_cast<const void *>(&lora_shrink_kernel<false, 4>);
-    return hipLaunchKernel(fn, dim3((unsigned)((a.N + 31) / 32)), dim3(512), args, 0, stream);
+    else
+        fn = vec ? reinterpret_cast<const void *>(&lora_shrink_kernel<true, 8>)
+                 : reinterpret_cast<const void *>(&lora_shrink_kernel<false, 8>);
+    return hipLaunchKernel(fn, dim3((unsigned)((a.N + 15) / 16)), dim3(512), args, 0, stream);
 }
 
 // ---------------------------------------------------------------------------
@@ -195,6 +203,7 @@ __global__ __launch_bounds__(256) void lora_rows_kernel(const uint16_t *__restri
 // M: the power of two of each packed row goes to this side, so that the
 // weights' fp16 values keep their full precision, and the token's brings the
 // largest to [2^14, 2^15).
+template <bool VEC>
 __global__ __launch_bounds__(256) void lora_dy_kernel(const uint16_t *__restrict__ dY, int M, int pitch,
                                                       const int8_t *__restrict__ rowexp, uint16_t *__restrict__ out,
                                                       int32_t *__restrict__ exps) {
@@ -202,9 +211,14 @@ __global__ __launch_bounds__(256) void lora_dy_kernel(const uint16_t *__restrict
     const int n = blockIdx.x;
     const uint16_t *src = dY + (int64_t)n * M;
     int best = -1000;
-    for (int m = threadIdx.x; m < M; m += 256) {
-        const int mag = src[m] & 0x7FFF;
-        if (mag) best = max(best, min(mag >> 7, 254) + rowexp[m]);
+    for (int m = threadIdx.x * 8; m < M; m += 2048) {
+        const u32x4_t v = row_piece<VEC>(src, m, M);
+        const uint64_t e = *reinterpret_cast<const uint64_t *>(rowexp + m);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int mag = (v[i >> 1] >> (16 * (i & 1))) & 0x7FFF;
+            if (mag) best = max(best, min(mag >> 7, 254) + (int)(int8_t)(e >> (8 * i)));
+        }
     }
 #pragma unroll
     for (int d = 32; d >= 1; d >>= 1) best = max(best, __shfl_xor(best, d));
@@ -212,10 +226,16 @@ __global__ __launch_bounds__(256) void lora_dy_kernel(const uint16_t *__restrict
     __syncthreads();
     best = max(max(wmax[0], wmax[1]), max(wmax[2], wmax[3]));
     const int shift = best == -1000 ? 0 : 141 - best;
-    for (int m = threadIdx.x; m < pitch; m += 256) {
-        uint16_t v = 0;
-        if (m < M) v = __builtin_bit_cast(uint16_t, (_Float16)ldexpf(bf16_f32(src[m]), shift + rowexp[m]));
-        out[(int64_t)n * pitch + m] = v;
+    for (int m = threadIdx.x * 8; m < pitch; m += 2048) {
+        const u32x4_t v = row_piece<VEC>(src, m, M);
+        const uint64_t e = *reinterpret_cast<const uint64_t *>(rowexp + m);
+        half2_t h[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            h[i].x = (_Float16)ldexpf(bf16_lo(v[i]), shift + (int)(int8_t)(e >> (16 * i)));
+            h[i].y = (_Float16)ldexpf(bf16_hi(v[i]), shift + (int)(int8_t)(e >> (16 * i + 8)));
+        }
+        *reinterpret_cast<half8_t *>(out + (int64_t)n * pitch + m) = join8(h);
     }
     if (threadIdx.x == 0) exps[n] = -shift;
 }
@@ -483,8 +503,13 @@ __global__ __launch_bounds__(256) void lora_dx_finish_kernel(const DxArgs a) {
 
 // ---------------------------------------------------------------------------
 // Gradients of the adapters: for pieces of at most kPieceTokens tokens of one
-// adapter (in the order of the tokens), g[j][c] = sum_n t[n][j] Z[n][c], one
-// lane a pair of columns, the t of a token uniform over the workgroup.
+// adapter (in the order of the tokens), g[j][c] = sum_n t[n][j] Z[n][c].
+//
+// v_mfma_f32_16x16x4_f32 adds four tokens' products of 16 ranks and 16
+// columns, exact products of fp32 operands: lane (i, g) holds t[n + g][j0 + i]
+// and one column of Z's row n + g, both as they lie in memory, so nothing is
+// transposed and nothing rounded.  A lane's 16 bytes of a row are 8 columns,
+// one for each of 8 such products.  A wave takes 128 columns.
 // ---------------------------------------------------------------------------
 constexpr int kPieceTokens = 128;
 
@@ -498,45 +523,70 @@ struct GradArgs {
     int N, L, r, blocks0;
 };
 
-template <int J>
+// VEC: both matrices' rows start on 16 bytes.  JT: tiles of 16 ranks at once.
+template <bool VEC, int JT>
 __global__ __launch_bounds__(256) void lora_grad_kernel(const GradArgs a) {
+    constexpr int U = 4;  // steps of four tokens whose loads go together
     const int q = (int)blockIdx.x >= a.blocks0 ? 1 : 0;
     const Chunk ck = find_chunk(a.offsets, a.L, a.N, blockIdx.y, kPieceTokens);
     if (ck.count == 0) return;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i16 = lane & 15, g = lane >> 4;
     const int cols = a.cols[q];
-    const int c = ((int)(blockIdx.x - (q ? a.blocks0 : 0)) * 256 + threadIdx.x) * 2;
-    const int j0 = blockIdx.z * J;
-    if (c >= cols) return;
-    float s[J][2];
+    const int c = (int)(blockIdx.x - (q ? a.blocks0 : 0)) * 512 + wave * 128 + 8 * i16;
+    const int j0 = blockIdx.z * 16 * JT;
+    const uint16_t *Z = a.Z[q];
+    const float *T = a.t[q];
+    float4_t acc[JT][8];
 #pragma unroll
-    for (int j = 0; j < J; ++j) s[j][0] = s[j][1] = 0.0f;
-    const bool pair = (cols & 1) == 0;
-    for (int i = 0; i < ck.count; ++i) {
-        const int n = __builtin_amdgcn_readfirstlane(a.rows[ck.start + i]);
-        const uint16_t *z = a.Z[q] + (int64_t)n * cols + c;
-        float z0, z1;
-        if (pair) {
-            const uint32_t d = *reinterpret_cast<const uint32_t *>(z);
-            z0 = bf16_lo(d);
-            z1 = bf16_hi(d);
-        } else {
-            z0 = bf16_f32(z[0]);
-            z1 = c + 1 < cols ? bf16_f32(z[1]) : 0.0f;
+    for (int p = 0; p < JT; ++p)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[p][i] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int s = 0; s < ck.count; s += 4 * U) {
+        u32x4_t z[U];
+        float t[U][JT];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int at = s + 4 * u + g;
+            z[u] = u32x4_t{0u, 0u, 0u, 0u};
+#pragma unroll
+            for (int p = 0; p < JT; ++p) t[u][p] = 0.0f;
+            if (at < ck.count) {
+                const int n = a.rows[ck.start + at];
+                z[u] = row_piece<VEC>(Z + (int64_t)n * cols, c, cols);
+#pragma unroll
+                for (int p = 0; p < JT; ++p)
+                    if (j0 + 16 * p + i16 < a.r) t[u][p] = T[(int64_t)n * a.r + j0 + 16 * p + i16];
+            }
         }
-        const float *t = a.t[q] + (int64_t)n * a.r + j0;
 #pragma unroll
-        for (int j = 0; j < J; ++j) {
-            const float tj = t[j];
-            s[j][0] = fmaf(tj, z0, s[j][0]);
-            s[j][1] = fmaf(tj, z1, s[j][1]);
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float v = i & 1 ? bf16_hi(z[u][i >> 1]) : bf16_lo(z[u][i >> 1]);
+#pragma unroll
+                for (int p = 0; p < JT; ++p)
+                    acc[p][i] = __builtin_amdgcn_mfma_f32_16x16x4f32(t[u][p], v, acc[p][i], 0, 0, 0);
+            }
+    }
+    // Register x of tile (p, i): rank j0 + 16 p + 4 g + x, column c + i.
+#pragma unroll
+    for (int p = 0; p < JT; ++p)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            const int j = j0 + 16 * p + 4 * g + x;
+            if (j >= a.r) continue;
+            float *o = a.part[q] + ((int64_t)blockIdx.y * a.r + j) * cols + c;
+            if (VEC) {
+                if (c < cols) {
+                    *reinterpret_cast<float4 *>(o) = make_float4(acc[p][0][x], acc[p][1][x], acc[p][2][x], acc[p][3][x]);
+                    *reinterpret_cast<float4 *>(o + 4) = make_float4(acc[p][4][x], acc[p][5][x], acc[p][6][x], acc[p][7][x]);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (c + i < cols) o[i] = acc[p][i][x];
+            }
         }
-    }
-    float *o = a.part[q] + ((int64_t)blockIdx.y * a.r + j0) * cols + c;
-#pragma unroll
-    for (int j = 0; j < J; ++j) {
-        o[(int64_t)j * cols] = s[j][0];
-        if (c + 1 < cols) o[(int64_t)j * cols + 1] = s[j][1];
-    }
 }
 
 // Adds the pieces of each adapter in order (none: zeros).
@@ -607,7 +657,7 @@ BackwardLayout backward_layout(int64_t M, int64_t K, int64_t N, int64_t r, int64
     b.bt = take((size_t)L * r * b.pitch * 2);
     b.dy16 = take((size_t)N * b.pitch * 2);
     b.exps = take((size_t)N * 4);
-    b.rowexp = take((size_t)M);
+    b.rowexp = take((size_t)b.pitch);
     b.offsets = take((size_t)(L + 1) * 4);
     b.rows = take((size_t)N * 4);
     b.sort = take(sort_ws_bytes(N, L));
@@ -686,8 +736,9 @@ hipError_t launch_lora_backward(const LoraCall &c, const uint16_t *dY, uint16_t 
         }
         if (dX) {
             void *yargs[] = {&dY, &M, &pitch, &rowexp, &dy16, &exps};
-            e = hipLaunchKernel(reinterpret_cast<const void *>(&lora_dy_kernel), dim3((unsigned)c.N), dim3(256), yargs,
-                                0, stream);
+            e = hipLaunchKernel(c.M % 8 == 0 ? reinterpret_cast<const void *>(&lora_dy_kernel<true>)
+                                             : reinterpret_cast<const void *>(&lora_dy_kernel<false>),
+                                dim3((unsigned)c.N), dim3(256), yargs, 0, stream);
             if (e != hipSuccess) return e;
             const DxPlan p = dx_plan(c.M, c.K, c.N);
             DxArgs d = {};
@@ -748,11 +799,15 @@ hipError_t launch_lora_backward(const LoraCall &c, const uint16_t *dY, uint16_t 
     void *gargs[] = {&g};
     if (c.N > 0) {
         g.blocks0 = (int)((c.K + 511) / 512);
-        const int J = c.r % 16 == 0 ? 16 : 8;
-        e = hipLaunchKernel(J == 16 ? reinterpret_cast<const void *>(&lora_grad_kernel<16>)
-                                    : reinterpret_cast<const void *>(&lora_grad_kernel<8>),
+        const bool vec = c.M % 8 == 0;
+        const int jt = c.r > 16 ? 2 : 1;
+        const void *fn = vec ? jt == 2 ? reinterpret_cast<const void *>(&lora_grad_kernel<true, 2>)
+                                       : reinterpret_cast<const void *>(&lora_grad_kernel<true, 1>)
+                             : jt == 2 ? reinterpret_cast<const void *>(&lora_grad_kernel<false, 2>)
+                                       : reinterpret_cast<const void *>(&lora_grad_kernel<false, 1>);
+        e = hipLaunchKernel(fn,
                             dim3((unsigned)(g.blocks0 + (c.M + 511) / 512), (unsigned)pieces_bound(c.N, c.L),
-                                 (unsigned)(c.r / J)),
+                                 (unsigned)((c.r + 16 * jt - 1) / (16 * jt))),
                             dim3(256), gargs, 0, stream);
         if (e != hipSuccess) return e;
     }

@@ -65,125 +65,179 @@ __device__ __forceinline__ float adapter_term(const Args &a, int p, int m) {
 }
 
 // ---------------------------------------------------------------------------
-// Few rows a group: chunks of at most CAP rows (8 or 32).
+// Few rows a group: chunks of at most 16 NT rows.
 //
 // A workgroup holds one chunk, one range of at most 2048 weights along K and
-// a few 32-row tiles of the matrix.  Its 8 waves split the range; a wave's
-// part (at most four 64-blocks) of the chunk's activations is converted to
-// fp16 once (a power of two per row and wave) and stays in registers.  A lane
-// of v_mfma_f32_32x32x16_f16 holds 32 weights of one block of one row, 16
-// bytes of codes, so that both lanes of a row lie in the same block: the
-// block's scale multiplies the fp32 result of the block's four MFMAs and
-// nothing of it is rounded.  The waves' tiles are added through LDS.
+// a few 32-row tiles of the matrix.  Its 8 waves split the range into slices
+// of four 64-blocks; a wave's slice of the chunk's activations is converted
+// to fp16 once (a power of two per row and wave) and stays in registers.
+// v_mfma_f32_16x16x32_f16 takes k in any order that both operands share: lane
+// (r, g) holds block g of the slice for row r, so a lane's 64 weights have
+// one scale and come from 32 neighbouring bytes.  They are multiplied by the
+// scale in fp16, under a power of two that brings the largest of the row's
+// four scales to [2^14, 2^15).  The waves' tiles are added through LDS.
+//
+// Bytes and latency bound it: the codes of the first tile are asked for
+// before the activations are converted, those of the next before the sums go
+// through LDS, and registers (128) and LDS (80 KB) leave room for two
+// workgroups a compute unit.
 // ---------------------------------------------------------------------------
 constexpr int kChunkWaves = 8;
 constexpr int kRangeBlocks = 32;  // 64-blocks of one range: four a wave
 
-template <int CAP, int MATS, bool PART, bool LORA>
-__global__ __launch_bounds__(kChunkWaves * 64) void ragged_chunk_kernel(const Args a) {
-    constexpr int kRegs = CAP / 2;  // accumulator registers that hold rows below CAP
+template <int NT, int MATS, bool PART, bool LORA>
+__global__ __launch_bounds__(kChunkWaves * 64, NT * MATS > 2 ? 2 : 4) void ragged_chunk_kernel(const Args a) {
+    constexpr int CAP = 16 * NT;
+    constexpr int kOuts = CAP * 32 / (kChunkWaves * 64);
     __shared__ uint32_t lut[kLutDwords];
-    __shared__ float red[MATS][kChunkWaves][CAP * 32];
+    __shared__ float red[MATS][kChunkWaves / 2][CAP * 32];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int col = lane & 31, g = lane >> 5;
+    const int col = lane & 15, g = lane >> 4;
 
     const Chunk ck = find_chunk(a.offsets, a.E, a.R, blockIdx.y, CAP);
     if (ck.count == 0) return;
     const int nb = a.K >> 6;
     const int b0 = (int)((int64_t)nb * blockIdx.z / a.ranges), b1 = (int)((int64_t)nb * (blockIdx.z + 1) / a.ranges);
-    const int lo = b0 + (b1 - b0) * wave / kChunkWaves, nblk = b0 + (b1 - b0) * (wave + 1) / kChunkWaves - lo;
+    const int lo = b0 + (b1 - b0) * wave / kChunkWaves, hi = b0 + (b1 - b0) * (wave + 1) / kChunkWaves;
+    const bool live = lo + g < hi;      // this lane has a block
+    const int ntiles = (a.M + 31) >> 5;
+    const int t0 = blockIdx.x * a.tiles_per_wg, t1 = min(t0 + a.tiles_per_wg, ntiles);
 
-    // This wave's activations: lane (row, g) holds k = 64 b + 32 g + (0..31).
-    u32x4_t x[4][4];
+    u32x4_t cw[MATS][2][2];             // [matrix][16 rows][half a block]
+    uint32_t sc[MATS][2];
+    auto load_tile = [&](int q, int t) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int64_t mrow = (int64_t)ck.e * a.M + min(t * 32 + 16 * h + col, a.M - 1);
+            cw[q][h][0] = cw[q][h][1] = u32x4_t{0u, 0u, 0u, 0u};
+            sc[q][h] = 0;
+            if (live) {
+                const u32x4_t *c = reinterpret_cast<const u32x4_t *>(a.codes[q] + mrow * (a.K >> 1) + 32 * (lo + g));
+                cw[q][h][0] = c[0];
+                cw[q][h][1] = c[1];
+                sc[q][h] = a.scales[q][mrow * nb + lo + g];
+            }
+        }
+    };
+
+    u32x4_t x[NT][8];
     {
-        int row = -1;
-        if (col < ck.count) row = source_row(a, ck.start + col);
-        const uint16_t *src = a.X + (int64_t)max(row, 0) * a.K + 64 * lo + 32 * g;
+        int row[NT];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int n = 0; n < NT; ++n)
+            row[n] = 16 * n + col < ck.count ? source_row(a, ck.start + 16 * n + col) : -1;
 #pragma unroll
-            for (int s = 0; s < 4; ++s)
-                x[i][s] = row >= 0 && i < nblk ? *reinterpret_cast<const u32x4_t *>(src + 64 * i + 8 * s)
-                                               : u32x4_t{0u, 0u, 0u, 0u};
+        for (int q = 0; q < MATS; ++q) load_tile(q, t0);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const u32x4_t *src = reinterpret_cast<const u32x4_t *>(a.X + (int64_t)row[n] * a.K + 64 * (lo + g));
+#pragma unroll
+            for (int s = 0; s < 8; ++s) x[n][s] = u32x4_t{0u, 0u, 0u, 0u};
+            if (row[n] >= 0 && live) {
+#pragma unroll
+                for (int s = 0; s < 8; ++s) x[n][s] = src[s];
+            }
+        }
     }
     fill_lut(lut);
 
-    int shift;  // of this lane's row
-    {
+    int back[NT][4];  // the inverse power of two of each register's row
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
         u16x2_t mx = {0, 0};
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int s = 0; s < 8; ++s)
 #pragma unroll
-            for (int s = 0; s < 4; ++s)
-#pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    mx = __builtin_elementwise_max(mx, __builtin_bit_cast(u16x2_t, x[i][s][c] & 0x7FFF7FFFu));
+            for (int c = 0; c < 4; ++c)
+                mx = __builtin_elementwise_max(mx, __builtin_bit_cast(u16x2_t, x[n][s][c] & 0x7FFF7FFFu));
         int m = max((int)mx.x, (int)mx.y);
+        m = max(m, __shfl_xor(m, 16));
         m = max(m, __shfl_xor(m, 32));
-        shift = fp16_shift((uint32_t)m);
+        const int shift = fp16_shift((uint32_t)m);
         const float f = exp2i(shift);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int s = 0; s < 8; ++s)
 #pragma unroll
-            for (int s = 0; s < 4; ++s)
+            for (int c = 0; c < 4; ++c) x[n][s][c] = bf16x2_to_f16x2(x[n][s][c], f);
 #pragma unroll
-                for (int c = 0; c < 4; ++c) x[i][s][c] = bf16x2_to_f16x2(x[i][s][c], f);
+        for (int i = 0; i < 4; ++i) back[n][i] = -14 - __shfl(shift, 4 * g + i);
     }
-    int back[kRegs];  // the inverse power of two of each register's row
-#pragma unroll
-    for (int i = 0; i < kRegs; ++i) back[i] = -__shfl(shift, tile_row(i, lane));
     __syncthreads();
 
-    const int ntiles = (a.M + 31) >> 5;
-    const int t0 = blockIdx.x * a.tiles_per_wg, t1 = min(t0 + a.tiles_per_wg, ntiles);
     const uint32_t laneoff = (uint32_t)lane << 2;
     for (int t = t0; t < t1; ++t) {
-        const int m = min(t * 32 + col, a.M - 1);
-        const int64_t mrow = (int64_t)ck.e * a.M + m;
-        u32x4_t cw[MATS][4];
-        float sc[MATS][4];
+        float4_t d[MATS][2][NT];
+        int e[MATS][2];
+#pragma unroll
+        for (int q = 0; q < MATS; ++q) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                int m = (int)(sc[q][h] & 0x7FFFu);
+                m = max(m, __shfl_xor(m, 16));
+                m = max(m, __shfl_xor(m, 32));
+                e[q][h] = m ? (int)(__builtin_bit_cast(uint32_t, f16_bits_to_f32((uint32_t)m)) >> 23) - 127 : 0;
+                const _Float16 sh = (_Float16)ldexpf(f16_bits_to_f32(sc[q][h]), 14 - e[q][h]);
+                const half2_t s2 = {sh, sh};
+#pragma unroll
+                for (int n = 0; n < NT; ++n) d[q][h][n] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int s = 0; s < 8; ++s) {
+                    half2_t w[4];
+                    lut8(lut, cw[q][h][s >> 2][s & 3], laneoff, w);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) w[c] *= s2;
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+                        d[q][h][n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, x[n][s]),
+                                                                            join8(w), d[q][h][n], 0, 0, 0);
+                }
+            }
+            if (t + 1 < t1) load_tile(q, t + 1);
+        }
+        // Register i of token tile n: row 16 n + 4 g + i, column 16 h + col.
 #pragma unroll
         for (int q = 0; q < MATS; ++q)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int b = min(lo + i, nb - 1);
-                cw[q][i] = *reinterpret_cast<const u32x4_t *>(a.codes[q] + mrow * (a.K >> 1) + 32 * b + 16 * g);
-                sc[q][i] = f16_bits_to_f32(a.scales[q][mrow * nb + b]);
-            }
+            for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int q = 0; q < MATS; ++q) {
-            float acc[kRegs];
+                for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int i = 0; i < kRegs; ++i) acc[i] = 0.0f;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (i < nblk) {
-                    float16_t d = {};
-#pragma unroll
-                    for (int s = 0; s < 4; ++s) {
-                        half2_t w[4];
-                        lut8(lut, cw[q][i][s], laneoff, w);
-                        d = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(half8_t, x[i][s]), join8(w), d, 0,
-                                                                   0, 0);
+                    for (int i = 0; i < 4; ++i) {
+                        d[q][h][n][i] = ldexpf(d[q][h][n][i], e[q][h] + back[n][i]);
+                        if (wave >= kChunkWaves / 2)
+                            red[q][wave - kChunkWaves / 2][(16 * n + 4 * g + i) * 32 + 16 * h + col] = d[q][h][n][i];
                     }
+        float term[kOuts];
+        if constexpr (LORA) {
 #pragma unroll
-                    for (int j = 0; j < kRegs; ++j) acc[j] = fmaf(sc[q][i], d[j], acc[j]);
-                }
+            for (int n = 0; n < kOuts; ++n) {
+                const int o = threadIdx.x + n * kChunkWaves * 64, row = o >> 5, mo = t * 32 + (o & 31);
+                term[n] = row < ck.count && mo < a.M ? adapter_term(a, ck.start + row, mo) : 0.0f;
             }
-#pragma unroll
-            for (int i = 0; i < kRegs; ++i)
-                red[q][wave][tile_row(i, lane) * 32 + col] = ldexpf(acc[i], back[i]);
         }
         __syncthreads();
-        for (int o = threadIdx.x; o < CAP * 32; o += kChunkWaves * 64) {
-            const int row = o >> 5, mo = t * 32 + (o & 31);
+        if (wave < kChunkWaves / 2) {
+#pragma unroll
+            for (int q = 0; q < MATS; ++q)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            red[q][wave][(16 * n + 4 * g + i) * 32 + 16 * h + col] += d[q][h][n][i];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int n = 0; n < kOuts; ++n) {
+            const int o = threadIdx.x + n * kChunkWaves * 64, row = o >> 5, mo = t * 32 + (o & 31);
             if (row >= ck.count || mo >= a.M) continue;
             float v[MATS];
 #pragma unroll
             for (int q = 0; q < MATS; ++q) {
                 v[q] = red[q][0][o];
 #pragma unroll
-                for (int w = 1; w < kChunkWaves; ++w) v[q] += red[q][w][o];
+                for (int w = 1; w < kChunkWaves / 2; ++w) v[q] += red[q][w][o];
             }
             const int p = ck.start + row;
             const int64_t at = (int64_t)p * a.M + mo;
@@ -193,11 +247,11 @@ __global__ __launch_bounds__(kChunkWaves * 64) void ragged_chunk_kernel(const Ar
                     a.part[((int64_t)q * a.ranges + blockIdx.z) * a.R * a.M + at] = v[q];
             } else {
                 float y = MATS == 2 ? swiglu(v[0], v[MATS - 1]) : v[0];
-                if constexpr (LORA) y += adapter_term(a, p, mo);
+                if constexpr (LORA) y += term[n];
                 store_out(a.Y, a.bf16, at, y);
             }
         }
-        __syncthreads();
+        if (t + 1 < t1) __syncthreads();
     }
 }
 
@@ -488,7 +542,7 @@ Plan plan_of(int64_t E, int64_t M, int64_t K, int64_t R) {
     const int64_t avg = groups ? (R + groups - 1) / groups : 0;
     p.tiles = avg > 64;
     p.mt = avg > 160 ? 4 : 2;
-    p.cap = R <= 8 || avg <= 6 ? 8 : 32;
+    p.cap = R <= 16 || avg <= 12 ? 16 : 32;
     p.ranges = (int)((K / 64 + kRangeBlocks - 1) / kRangeBlocks);
     return p;
 }
@@ -534,14 +588,14 @@ static const void *tile_fn(bool up, bool lora) {
                 : reinterpret_cast<const void *>(&ragged_tile_kernel<MT, 1, false>);
 }
 
-template <int CAP>
+template <int NT>
 static const void *chunk_fn(bool up, bool part, bool lora) {
     if (up)
-        return part ? reinterpret_cast<const void *>(&ragged_chunk_kernel<CAP, 2, true, false>)
-                    : reinterpret_cast<const void *>(&ragged_chunk_kernel<CAP, 2, false, false>);
-    if (part) return reinterpret_cast<const void *>(&ragged_chunk_kernel<CAP, 1, true, false>);
-    return lora ? reinterpret_cast<const void *>(&ragged_chunk_kernel<CAP, 1, false, true>)
-                : reinterpret_cast<const void *>(&ragged_chunk_kernel<CAP, 1, false, false>);
+        return part ? reinterpret_cast<const void *>(&ragged_chunk_kernel<NT, 2, true, false>)
+                    : reinterpret_cast<const void *>(&ragged_chunk_kernel<NT, 2, false, false>);
+    if (part) return reinterpret_cast<const void *>(&ragged_chunk_kernel<NT, 1, true, false>);
+    return lora ? reinterpret_cast<const void *>(&ragged_chunk_kernel<NT, 1, false, true>)
+                : reinterpret_cast<const void *>(&ragged_chunk_kernel<NT, 1, false, false>);
 }
 
 hipError_t launch_ragged(const RaggedProduct &p, void *workspace, hipStream_t stream) {
@@ -602,7 +656,7 @@ hipError_t launch_ragged(const RaggedProduct &p, void *workspace, hipStream_t st
     int64_t per = ntiles * chunks * pl.ranges / (2 * compute_units());
     a.tiles_per_wg = (int)(per < 1 ? 1 : per > 8 ? 8 : per);
     const dim3 grid((unsigned)((ntiles + a.tiles_per_wg - 1) / a.tiles_per_wg), (unsigned)chunks, (unsigned)pl.ranges);
-    hipError_t e = hipLaunchKernel(pl.cap == 8 ? chunk_fn<8>(up, part, lora) : chunk_fn<32>(up, part, lora), grid,
+    hipError_t e = hipLaunchKernel(pl.cap == 16 ? chunk_fn<1>(up, part, lora) : chunk_fn<2>(up, part, lora), grid,
                                    dim3(kChunkWaves * 64), args, 0, stream);
     if (e != hipSuccess || !part) return e;
     const void *fin = up     ? reinterpret_cast<const void *>(&ragged_finish_kernel<2, false>)

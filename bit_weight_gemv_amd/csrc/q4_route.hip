@@ -1,10 +1,11 @@
 // q4_route.hip -- which experts a token goes to, the order that groups the
 // tokens by expert, and the weighted sum of the experts' outputs.
 //
-// Top k: one wave a token, the logits spread over its lanes; k times the
-// largest key wins, where a key is the logit's bits in an order that compares
-// as unsigned (the upper half) and the complement of the index (the lower
-// half), so that equal logits fall to the lowest index.
+// Top k: one wave a token, the logits spread over its lanes as bits in an
+// order that compares as unsigned; k times the largest of them (maxima over
+// lanes by DPP) goes to the lowest index that holds it (the first lane of the
+// first ballot that is not empty).  The next token's logits are on their way
+// meanwhile.
 //
 // Grouping is a counting sort that keeps the slots' order: workgroups take
 // consecutive runs of slots; the first launch leaves each run's count of
@@ -45,67 +46,73 @@ struct SortArgs {
     int32_t *offsets, *rows, *pos;
 };
 
-__device__ __forceinline__ uint64_t key_of(float v, int index) {
-    v = v != v ? -__builtin_inff() : v + 0.0f;  // NaN as -infinity, -0 as 0
+// A logit's bits in an order that compares as unsigned; every logit's is
+// above 0.  NaN as -infinity, -0 as 0.
+__device__ __forceinline__ uint32_t order_of(float v) {
+    v = v != v ? -__builtin_inff() : v + 0.0f;
     const uint32_t b = __builtin_bit_cast(uint32_t, v);
-    const uint32_t order = b & 0x80000000u ? ~b : b | 0x80000000u;
-    return (uint64_t)order << 32 | (uint32_t)~index;
+    return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
-__device__ __forceinline__ uint64_t wave_max_u64(uint64_t v) {
+__device__ __forceinline__ float value_of(uint32_t order) {
+    return __builtin_bit_cast(float, order & 0x80000000u ? order & 0x7FFFFFFFu : ~order);
+}
+
+// This lane's logits of token t, in the order above (0: no such expert).
+template <int EPL>
+__device__ __forceinline__ void load_logits(const RouteArgs &a, int t, uint32_t (&o)[EPL]) {
 #pragma unroll
-    for (int d = 32; d >= 1; d >>= 1) {
-        const uint32_t lo = __shfl_xor((uint32_t)v, d), hi = __shfl_xor((uint32_t)(v >> 32), d);
-        const uint64_t o = (uint64_t)hi << 32 | lo;
-        v = o > v ? o : v;
+    for (int i = 0; i < EPL; ++i) {
+        const int e = (threadIdx.x & 63) + 64 * i;
+        o[i] = 0;
+        if (e < a.E) {
+            const int64_t at = (int64_t)t * a.E + e;
+            o[i] = order_of(a.bf16 ? bf16_f32(static_cast<const uint16_t *>(a.logits)[at])
+                                   : static_cast<const float *>(a.logits)[at]);
+        }
     }
-    return v;
 }
 
 // The choice of token t by this wave.
 template <int EPL>
-__device__ __forceinline__ void choose(const RouteArgs &a, int t) {
+__device__ __forceinline__ void choose(const RouteArgs &a, int t, uint32_t (&o)[EPL]) {
     const int lane = threadIdx.x & 63;
-    float l[EPL];
-    uint64_t key[EPL];
+    uint32_t key[EPL];
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-        const int e = lane + 64 * i;
-        l[i] = -__builtin_inff();
-        key[i] = 0;  // below every logit's
-        if (e < a.E) {
-            const int64_t at = (int64_t)t * a.E + e;
-            const float v = a.bf16 ? bf16_f32(static_cast<const uint16_t *>(a.logits)[at])
-                                   : static_cast<const float *>(a.logits)[at];
-            l[i] = v != v ? -__builtin_inff() : v;
-            key[i] = key_of(v, e);
-        }
-    }
+    for (int i = 0; i < EPL; ++i) key[i] = o[i];
     float largest = 0.0f, total = 0.0f, mine = 0.0f;
     int chosen = 0;
     for (int j = 0; j < a.k; ++j) {
-        uint64_t best = key[0];
+        uint32_t best = key[0];
 #pragma unroll
-        for (int i = 1; i < EPL; ++i) best = key[i] > best ? key[i] : best;
-        best = wave_max_u64(best);
+        for (int i = 1; i < EPL; ++i) best = max(best, key[i]);
+        best = wave_max_u32(best);
+        int at = -1;  // the lowest index that holds it
 #pragma unroll
-        for (int i = 0; i < EPL; ++i)
-            if (key[i] == best) key[i] = 0;
-        const uint32_t order = (uint32_t)(best >> 32);
-        const float v = __builtin_bit_cast(float, order & 0x80000000u ? order & 0x7FFFFFFFu : ~order);
+        for (int i = 0; i < EPL; ++i) {
+            const uint64_t has = __builtin_amdgcn_ballot_w64(key[i] == best);
+            if (at < 0 && has) {
+                const int l = __builtin_ctzll(has);
+                at = 64 * i + l;
+                if (lane == l) key[i] = 0;
+            }
+        }
+        const float v = value_of(best);
         if (j == 0) largest = v;
         const float p = v == largest ? 1.0f : expf(v - largest);
         total += p;
         if (lane == j) {
             mine = p;
-            chosen = (int)~(uint32_t)best;
+            chosen = at;
         }
     }
     if (a.all) {
         float s = 0.0f;
 #pragma unroll
-        for (int i = 0; i < EPL; ++i)
-            if (lane + 64 * i < a.E) s += l[i] == largest ? 1.0f : expf(l[i] - largest);
+        for (int i = 0; i < EPL; ++i) {
+            const float v = value_of(o[i]);
+            if (o[i]) s += v == largest ? 1.0f : expf(v - largest);
+        }
         total = wave_sum(s);
     }
     if (lane < a.k) {
@@ -190,7 +197,17 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(const RouteArgs a)
     __shared__ int32_t total[Q4_MAX_EXPERTS + 1], next[Q4_MAX_EXPERTS + 1], sum[kRouteWaves];
     const int t0 = blockIdx.x * a.run, t1 = min(t0 + a.run, a.T);
     for (int e = threadIdx.x; e <= a.E; e += kRouteThreads) total[e] = next[e] = 0;
-    for (int t = t0 + (threadIdx.x >> 6); t < t1; t += kRouteWaves) choose<EPL>(a, t);
+    {
+        uint32_t now[EPL], next_o[EPL];
+        int t = t0 + (threadIdx.x >> 6);
+        if (t < t1) load_logits<EPL>(a, t, now);
+        for (; t < t1; t += kRouteWaves) {
+            if (t + kRouteWaves < t1) load_logits<EPL>(a, t + kRouteWaves, next_o);
+            choose<EPL>(a, t, now);
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) now[i] = next_o[i];
+        }
+    }
     __threadfence_block();
     __syncthreads();
     const int s0 = t0 * a.k, s1 = t1 * a.k;
@@ -224,21 +241,22 @@ __global__ __launch_bounds__(kRouteThreads) void sort_kernel(const SortArgs a) {
     for (int e = threadIdx.x; e <= a.E; e += kRouteThreads) total[e] = next[e] = 0;
     __syncthreads();
     if (a.hist) {
-        int before_all = 0;
-        for (int e = threadIdx.x; e < a.E; e += kRouteThreads) {
+        // Threads beyond the bins take runs of their own.
+        const int parts = a.E < kRouteThreads ? kRouteThreads / a.E : 1;
+        for (int i = threadIdx.x; i < a.E * parts; i += kRouteThreads) {
+            const int e = i % a.E;
             int before = 0, all = 0;
 #pragma unroll 8
-            for (int b = 0; b < (int)gridDim.x; ++b) {
+            for (int b = i / a.E; b < (int)gridDim.x; b += parts) {
                 const int n = a.hist[(int64_t)b * a.E + e];
                 if (b < (int)blockIdx.x) before += n;
                 all += n;
             }
-            total[e] = all;
-            next[e] = before;
-            before_all += before;
+            atomicAdd(&total[e], all);
+            atomicAdd(&next[e], before);
+            // Slots of no bin before this run: those that the bins do not count.
+            atomicAdd(&total[a.E], before);
         }
-        // Slots of no bin before this run: those that the bins do not count.
-        atomicAdd(&total[a.E], before_all);
         __syncthreads();
         if (threadIdx.x == 0) next[a.E] = s0 - total[a.E];
         __syncthreads();
