@@ -56,10 +56,15 @@ __device__ __forceinline__ float dot8(const u32x4_t &x, const u32x4_t &z, float 
     return s;
 }
 
-// Few tokens: a workgroup takes one token and 4 ranks, a wave a rank.
+// Few tokens: a workgroup takes one token and 4 ranks, a wave a rank.  The
+// workgroups behind those write the packed product's activations as pieces.
 template <bool VEC>
-__global__ __launch_bounds__(256) void lora_shrink_token_kernel(const ShrinkArgs a) {
-    const int n = blockIdx.x, j = blockIdx.y * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
+__global__ __launch_bounds__(256) void lora_shrink_token_kernel(const ShrinkArgs a, const Pieces pieces, int shrinks) {
+    if ((int)blockIdx.x >= shrinks) {
+        write_pieces(a.X, nullptr, a.K, a.N, a.N, pieces, blockIdx.x - shrinks);
+        return;
+    }
+    const int n = blockIdx.x % a.N, j = blockIdx.x / a.N * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int id = a.ids[n];
     if (id < 0 || id >= a.L || j >= a.r) return;
     const uint16_t *x = a.X + (int64_t)n * a.K, *z = a.Z + ((int64_t)id * a.r + j) * a.pitch;
@@ -137,17 +142,21 @@ __global__ __launch_bounds__(512) void lora_shrink_kernel(const ShrinkArgs a) {
     }
 }
 
-hipError_t launch_shrink(const ShrinkArgs &s, hipStream_t stream) {
+hipError_t launch_shrink(const ShrinkArgs &s, Pieces pieces, hipStream_t stream) {
     ShrinkArgs a = s;
     void *args[] = {&a};
     const bool vec = a.K % 8 == 0;
     // A token of its own workgroups reads its adapter alone: many short waits
     // at once, but an adapter's bytes for every token; 16 tokens that share a
     // workgroup read it once for all that use it, one adapter after the other.
-    if (a.N <= 64 || (int64_t)a.N * a.r * a.pitch * 2 <= kTokenBytes)
+    if (a.N <= 64 || pieces.x16 || (int64_t)a.N * a.r * a.pitch * 2 <= kTokenBytes) {
+        int shrinks = a.N * ((a.r + 3) / 4);
+        void *targs[] = {&a, &pieces, &shrinks};
         return hipLaunchKernel(vec ? reinterpret_cast<const void *>(&lora_shrink_token_kernel<true>)
                                    : reinterpret_cast<const void *>(&lora_shrink_token_kernel<false>),
-                               dim3((unsigned)a.N, (unsigned)((a.r + 3) / 4)), dim3(256), args, 0, stream);
+                               dim3((unsigned)(shrinks + (pieces.x16 ? pieces_blocks(a.K, a.N) : 0))), dim3(256),
+                               targs, 0, stream);
+    }
     const void *fn;
     if (a.r <= 16)
         fn = vec ? reinterpret_cast<const void *>(&lora_shrink_kernel<true, 1>)
@@ -678,7 +687,7 @@ bool lora_backward_fits(int64_t M, int64_t K, int64_t N, int64_t L) {
 }
 
 size_t lora_ws_bytes(int64_t M, int64_t K, int64_t N, int64_t r, int64_t L) {
-    return (L > 0 ? round16((size_t)N * r * 4) : 0) + ragged_ws_bytes(1, M, K, N, N, false);
+    return (L > 0 ? round16((size_t)N * r * 4) : 0) + ragged_ws_bytes(1, M, K, N, N, false, L > 0);
 }
 
 hipError_t launch_lora(const LoraCall &c, bool bf16, void *Y, void *workspace, hipStream_t stream) {
@@ -696,7 +705,10 @@ hipError_t launch_lora(const LoraCall &c, bool bf16, void *Y, void *workspace, h
     if (c.L > 0) {
         ShrinkArgs s = {c.X,      c.A, c.scaling, c.ids, (int)c.N, (int)c.K, (int)c.K, (int)c.r, (int)c.L,
                         reinterpret_cast<float *>(w)};
-        const hipError_t e = launch_shrink(s, stream);
+        Pieces pieces = {};
+        if (ragged_takes_pieces(1, c.M, c.K, c.N, true))
+            pieces = pieces_at(c.K, c.N, w + round16((size_t)c.N * c.r * 4));
+        const hipError_t e = launch_shrink(s, pieces, stream);
         if (e != hipSuccess) return e;
         p.B = c.B;
         p.t = s.t;
@@ -732,7 +744,7 @@ hipError_t launch_lora_backward(const LoraCall &c, const uint16_t *dY, uint16_t 
         if (e != hipSuccess) return e;
         if (c.L > 0) {
             ShrinkArgs su = {dY, bt, c.scaling, c.ids, (int)c.N, (int)c.M, (int)b.pitch, (int)c.r, (int)c.L, u};
-            if ((e = launch_shrink(su, stream)) != hipSuccess) return e;
+            if ((e = launch_shrink(su, Pieces{}, stream)) != hipSuccess) return e;
         }
         if (dX) {
             void *yargs[] = {&dY, &M, &pitch, &rowexp, &dy16, &exps};
@@ -777,7 +789,7 @@ hipError_t launch_lora_backward(const LoraCall &c, const uint16_t *dY, uint16_t 
     if (!dA || c.L == 0) return hipSuccess;
     if (c.N > 0) {
         ShrinkArgs st = {c.X, c.A, c.scaling, c.ids, (int)c.N, (int)c.K, (int)c.K, (int)c.r, (int)c.L, t};
-        if ((e = launch_shrink(st, stream)) != hipSuccess) return e;
+        if ((e = launch_shrink(st, Pieces{}, stream)) != hipSuccess) return e;
     }
     if ((e = launch_sort(c.ids, c.N, c.L, 1, offsets, rows, nullptr, w + b.sort, stream)) != hipSuccess) return e;
     GradArgs g = {};

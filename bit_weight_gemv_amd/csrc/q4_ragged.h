@@ -30,10 +30,30 @@ struct RaggedProduct {
 
 // Whether the launches of this shape stay within what a grid can hold.
 bool ragged_fits(int64_t E, int64_t M, int64_t K, int64_t T, int64_t R, bool up);
-size_t ragged_ws_bytes(int64_t E, int64_t M, int64_t K, int64_t T, int64_t R, bool up);
+size_t ragged_ws_bytes(int64_t E, int64_t M, int64_t K, int64_t T, int64_t R, bool up, bool lora);
 hipError_t launch_ragged(const RaggedProduct &p, void *workspace, hipStream_t stream);
 
 inline size_t round16(size_t n) { return (n + 15) & ~(size_t)15; }
+
+// The activations of R positions as the few-rows kernel reads them: fp16
+// times 2^exps[slice of 256 k][position], in pieces of 8 k, [K / 8][R][8].
+// They lie at the start of the product's workspace; where
+// ragged_takes_pieces holds beside an adapter (lora), the adapters' first
+// launch writes them.
+struct Pieces {
+    uint16_t *x16;
+    int32_t *exps;
+};
+inline size_t pieces_bytes(int64_t K, int64_t R) {
+    return round16((size_t)K * R * 2) + round16((size_t)((K + 255) / 256) * R * 4);
+}
+inline Pieces pieces_at(int64_t K, int64_t R, void *workspace) {
+    char *w = static_cast<char *>(workspace);
+    return {reinterpret_cast<uint16_t *>(w), reinterpret_cast<int32_t *>(w + round16((size_t)K * R * 2))};
+}
+// Workgroups that write them: a wave takes a slice of two positions.
+inline int64_t pieces_blocks(int64_t K, int64_t R) { return ((K + 255) / 256 * ((R + 1) / 2) + 3) / 4; }
+bool ragged_takes_pieces(int64_t E, int64_t M, int64_t K, int64_t R, bool lora);
 
 // The current device's number of compute units (256 where it cannot be read).
 int compute_units();

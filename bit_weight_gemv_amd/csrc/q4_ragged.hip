@@ -21,15 +21,14 @@ struct Args {
     const uint16_t *scales[2];
     const int8_t *rowexp[2];   // tile kernel: exponent of each row's largest scale
     int M, K, E, R;
-    const uint16_t *X;         // bf16 (chunk kernel) or fp16 under 2^-xexp (tile kernel)
-    const int32_t *xexp;       // tile kernel: the power of two of each row of X
+    const uint16_t *X;         // bf16 [T][K]; fp16 [T][K] (tile kernel) or [K/8][R][8] (chunk kernel, PRE) times 2^-xexp
+    const int32_t *xexp;       // the power of two of each row of X (tile kernel) or slice and position (chunk kernel)
     int T;
     const int32_t *offsets, *rows;
     void *Y;
     int bf16;
     float *part;               // chunk kernel: partial planes [mats][ranges][R][M], or null
-    int tiles_per_wg;
-    int ranges;
+    int ranges, slices_each, slices_more;  // chunk kernel: ranges of K, slices of each, and how many have one more
     int rowtiles, chunks;      // tile kernel: grid shape
     const uint16_t *B;
     const float *t;
@@ -67,192 +66,240 @@ __device__ __forceinline__ float adapter_term(const Args &a, int p, int m) {
 // ---------------------------------------------------------------------------
 // Few rows a group: chunks of at most 16 NT rows.
 //
-// A workgroup holds one chunk, one range of at most 2048 weights along K and
-// a few 32-row tiles of the matrix.  Its 8 waves split the range into slices
-// of four 64-blocks; a wave's slice of the chunk's activations is converted
-// to fp16 once (a power of two per row and wave) and stays in registers.
+// K is cut into slices of four 64-blocks, and slices into ranges of at most
+// 8.  A workgroup holds one chunk, one range and a few tiles of 32 rows
+// (16 where NT is 2) of the matrix, with a wave for each slice; the wave's slice of the chunk's
+// activations, in fp16 under a power of two a row, stays in registers.
 // v_mfma_f32_16x16x32_f16 takes k in any order that both operands share: lane
 // (r, g) holds block g of the slice for row r, so a lane's 64 weights have
 // one scale and come from 32 neighbouring bytes.  They are multiplied by the
 // scale in fp16, under a power of two that brings the largest of the row's
 // four scales to [2^14, 2^15).  The waves' tiles are added through LDS.
 //
-// Bytes and latency bound it: the codes of the first tile are asked for
-// before the activations are converted, those of the next before the sums go
-// through LDS, and registers (128) and LDS (80 KB) leave room for two
-// workgroups a compute unit.
+// Such calls are bound by their waits and by the instructions of a wave (four
+// cycles each, 16 waves a compute unit) more than by their bytes: nothing is
+// cleared that a clamped address or a scale of 0 makes harmless, the codes of
+// a tile are asked for before anything else and those of the next before the
+// sums go through LDS, and registers (128) and LDS (80 KB) leave room for two
+// workgroups a compute unit.  PRE: the activations were converted by an
+// earlier launch, and lie in the order of the loads.
 // ---------------------------------------------------------------------------
 constexpr int kChunkWaves = 8;
-constexpr int kRangeBlocks = 32;  // 64-blocks of one range: four a wave
+constexpr int kSliceK = 256;
 
-template <int NT, int MATS, bool PART, bool LORA>
-__global__ __launch_bounds__(kChunkWaves * 64, NT * MATS > 2 ? 2 : 4) void ragged_chunk_kernel(const Args a) {
+template <int NT, int MATS, bool PART, bool LORA, bool PRE>
+__global__ __launch_bounds__(kChunkWaves * 64, 4) void ragged_chunk_kernel(const Args a) {
     constexpr int CAP = 16 * NT;
-    constexpr int kOuts = CAP * 32 / (kChunkWaves * 64);
+    constexpr int H = NT == 2 ? 1 : 2;  // 16-row pieces of a tile: what 128 registers hold
+    constexpr int ROWS = 16 * H;
+    // Where all waves' tiles would leave room for one workgroup only, the
+    // upper half of the waves comes first and the lower adds to it.
+    constexpr bool kFold = MATS > 1;
+    constexpr int kRed = kFold ? kChunkWaves / 2 : kChunkWaves;
+    static_assert(CAP * ROWS == kChunkWaves * 64, "an output a thread");
     __shared__ uint32_t lut[kLutDwords];
-    __shared__ float red[MATS][kChunkWaves / 2][CAP * 32];
+    __shared__ float red[MATS][kRed][CAP * ROWS];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int col = lane & 15, g = lane >> 4;
 
     const Chunk ck = find_chunk(a.offsets, a.E, a.R, blockIdx.y, CAP);
     if (ck.count == 0) return;
     const int nb = a.K >> 6;
-    const int b0 = (int)((int64_t)nb * blockIdx.z / a.ranges), b1 = (int)((int64_t)nb * (blockIdx.z + 1) / a.ranges);
-    const int lo = b0 + (b1 - b0) * wave / kChunkWaves, hi = b0 + (b1 - b0) * (wave + 1) / kChunkWaves;
-    const bool live = lo + g < hi;      // this lane has a block
-    const int ntiles = (a.M + 31) >> 5;
-    const int t0 = blockIdx.x * a.tiles_per_wg, t1 = min(t0 + a.tiles_per_wg, ntiles);
+    // Ranges take slices dealt evenly, the longer ones first.
+    const int z = blockIdx.z;
+    const int s0 = z * a.slices_each + min(z, a.slices_more), ns = a.slices_each + (z < a.slices_more ? 1 : 0);
+    const int b = 4 * (s0 + wave) + g;       // this lane's block
+    const bool live = b < nb;
+    const int bc = min(b, nb - 1);
+    const int ntiles = (a.M + ROWS - 1) / ROWS;
+    const int t0 = (int)((uint32_t)ntiles * blockIdx.x / gridDim.x), t1 = (int)((uint32_t)ntiles * (blockIdx.x + 1) / gridDim.x);
 
-    u32x4_t cw[MATS][2][2];             // [matrix][16 rows][half a block]
-    uint32_t sc[MATS][2];
+    u32x4_t cw[MATS][H][2];                  // [matrix][16 rows][half a block]
+    uint32_t sc[MATS][H];
     auto load_tile = [&](int q, int t) {
+        const int64_t m0 = (int64_t)ck.e * a.M + t * ROWS;
+        const uint8_t *cbase = a.codes[q] + m0 * (a.K >> 1);
+        const uint16_t *sbase = a.scales[q] + m0 * nb;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int64_t mrow = (int64_t)ck.e * a.M + min(t * 32 + 16 * h + col, a.M - 1);
-            cw[q][h][0] = cw[q][h][1] = u32x4_t{0u, 0u, 0u, 0u};
-            sc[q][h] = 0;
-            if (live) {
-                const u32x4_t *c = reinterpret_cast<const u32x4_t *>(a.codes[q] + mrow * (a.K >> 1) + 32 * (lo + g));
-                cw[q][h][0] = c[0];
-                cw[q][h][1] = c[1];
-                sc[q][h] = a.scales[q][mrow * nb + lo + g];
-            }
+        for (int h = 0; h < H; ++h) {
+            const uint32_t m = min(16 * h + col, a.M - 1 - t * ROWS);
+            const u32x4_t *c = reinterpret_cast<const u32x4_t *>(cbase + (m * (uint32_t)(a.K >> 1) + 32 * bc));
+            cw[q][h][0] = c[0];
+            cw[q][h][1] = c[1];
+            sc[q][h] = sbase[m * (uint32_t)nb + bc];
         }
     };
 
     u32x4_t x[NT][8];
-    {
+    int back[NT][4];                         // the inverse power of two of each register's row, less 14
+    if constexpr (PRE) {
+#pragma unroll
+        for (int q = 0; q < MATS; ++q) load_tile(q, t0);
+        // [piece of 8 k][position]: 16 lanes read 256 neighbouring bytes.
+        const u32x4_t *src = reinterpret_cast<const u32x4_t *>(a.X) + (int64_t)(8 * bc) * a.R + ck.start;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const int row = min(16 * n + col, ck.count - 1);
+#pragma unroll
+            for (int s = 0; s < 8; ++s) x[n][s] = src[(int64_t)s * a.R + row];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                back[n][i] = a.xexp[(int64_t)(bc >> 2) * a.R + ck.start + min(16 * n + 4 * g + i, ck.count - 1)] - 14;
+        }
+        fill_lut(lut);
+    } else {
         int row[NT];
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-            row[n] = 16 * n + col < ck.count ? source_row(a, ck.start + 16 * n + col) : -1;
+        for (int n = 0; n < NT; ++n) row[n] = max(source_row(a, ck.start + min(16 * n + col, ck.count - 1)), 0);
 #pragma unroll
         for (int q = 0; q < MATS; ++q) load_tile(q, t0);
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            const u32x4_t *src = reinterpret_cast<const u32x4_t *>(a.X + (int64_t)row[n] * a.K + 64 * (lo + g));
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int s = 0; s < 8; ++s) x[n][s] = u32x4_t{0u, 0u, 0u, 0u};
-            if (row[n] >= 0 && live) {
+        if (a.T > 0) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const u32x4_t *src = reinterpret_cast<const u32x4_t *>(a.X + (int64_t)row[n] * a.K + 64 * bc);
 #pragma unroll
                 for (int s = 0; s < 8; ++s) x[n][s] = src[s];
             }
         }
-    }
-    fill_lut(lut);
-
-    int back[NT][4];  // the inverse power of two of each register's row
+        fill_lut(lut);
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        u16x2_t mx = {0, 0};
+        for (int n = 0; n < NT; ++n) {
+            u16x2_t mx = {0, 0};
 #pragma unroll
-        for (int s = 0; s < 8; ++s)
+            for (int s = 0; s < 8; ++s)
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
-                mx = __builtin_elementwise_max(mx, __builtin_bit_cast(u16x2_t, x[n][s][c] & 0x7FFF7FFFu));
-        int m = max((int)mx.x, (int)mx.y);
-        m = max(m, __shfl_xor(m, 16));
-        m = max(m, __shfl_xor(m, 32));
-        const int shift = fp16_shift((uint32_t)m);
-        const float f = exp2i(shift);
+                for (int c = 0; c < 4; ++c)
+                    mx = __builtin_elementwise_max(mx, __builtin_bit_cast(u16x2_t, x[n][s][c] & 0x7FFF7FFFu));
+            int m = max((int)mx.x, (int)mx.y);
+            m = max(m, __shfl_xor(m, 16));
+            m = max(m, __shfl_xor(m, 32));
+            const int shift = fp16_shift((uint32_t)m);
+            const float f = exp2i(shift);
 #pragma unroll
-        for (int s = 0; s < 8; ++s)
+            for (int s = 0; s < 8; ++s)
 #pragma unroll
-            for (int c = 0; c < 4; ++c) x[n][s][c] = bf16x2_to_f16x2(x[n][s][c], f);
+                for (int c = 0; c < 4; ++c) x[n][s][c] = bf16x2_to_f16x2(x[n][s][c], f);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) back[n][i] = -14 - __shfl(shift, 4 * g + i);
+            for (int i = 0; i < 4; ++i) back[n][i] = -14 - __shfl(shift, 4 * g + i);
+        }
     }
     __syncthreads();
 
     const uint32_t laneoff = (uint32_t)lane << 2;
     for (int t = t0; t < t1; ++t) {
-        float4_t d[MATS][2][NT];
-        int e[MATS][2];
-#pragma unroll
-        for (int q = 0; q < MATS; ++q) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                int m = (int)(sc[q][h] & 0x7FFFu);
-                m = max(m, __shfl_xor(m, 16));
-                m = max(m, __shfl_xor(m, 32));
-                e[q][h] = m ? (int)(__builtin_bit_cast(uint32_t, f16_bits_to_f32((uint32_t)m)) >> 23) - 127 : 0;
-                const _Float16 sh = (_Float16)ldexpf(f16_bits_to_f32(sc[q][h]), 14 - e[q][h]);
-                const half2_t s2 = {sh, sh};
-#pragma unroll
-                for (int n = 0; n < NT; ++n) d[q][h][n] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                for (int s = 0; s < 8; ++s) {
-                    half2_t w[4];
-                    lut8(lut, cw[q][h][s >> 2][s & 3], laneoff, w);
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) w[c] *= s2;
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-                        d[q][h][n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, x[n][s]),
-                                                                            join8(w), d[q][h][n], 0, 0, 0);
-                }
-            }
-            if (t + 1 < t1) load_tile(q, t + 1);
-        }
-        // Register i of token tile n: row 16 n + 4 g + i, column 16 h + col.
-#pragma unroll
-        for (int q = 0; q < MATS; ++q)
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        d[q][h][n][i] = ldexpf(d[q][h][n][i], e[q][h] + back[n][i]);
-                        if (wave >= kChunkWaves / 2)
-                            red[q][wave - kChunkWaves / 2][(16 * n + 4 * g + i) * 32 + 16 * h + col] = d[q][h][n][i];
-                    }
-        float term[kOuts];
-        if constexpr (LORA) {
-#pragma unroll
-            for (int n = 0; n < kOuts; ++n) {
-                const int o = threadIdx.x + n * kChunkWaves * 64, row = o >> 5, mo = t * 32 + (o & 31);
-                term[n] = row < ck.count && mo < a.M ? adapter_term(a, ck.start + row, mo) : 0.0f;
-            }
-        }
-        __syncthreads();
-        if (wave < kChunkWaves / 2) {
+        // This thread's output.
+        const int o = threadIdx.x, row = o / ROWS, mo = t * ROWS + o % ROWS, p = ck.start + row;
+        const bool out = row < ck.count && mo < a.M;
+        float term = 0.0f;
+        if constexpr (LORA)
+            if (out) term = adapter_term(a, p, mo);
+        float4_t d[MATS][H][NT];
+        if (wave < ns) {
+            int e[MATS][H];
+            half2_t s2[MATS][H];
 #pragma unroll
             for (int q = 0; q < MATS; ++q)
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
+                for (int h = 0; h < H; ++h) {
+                    const uint32_t bits = live ? sc[q][h] : 0;
+                    int m = (int)(bits & 0x7FFFu);
+                    m = max(m, __shfl_xor(m, 16));
+                    m = max(m, __shfl_xor(m, 32));
+                    e[q][h] = m ? (int)(__builtin_bit_cast(uint32_t, f16_bits_to_f32((uint32_t)m)) >> 23) - 127 : 0;
+                    const _Float16 sh = (_Float16)ldexpf(f16_bits_to_f32(bits), 14 - e[q][h]);
+                    s2[q][h] = half2_t{sh, sh};
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) d[q][h][n] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
+                }
+            // A step of all matrices and pieces together: their lookups are
+            // in flight at once, and their products are chains of their own.
+#pragma unroll
+            for (int s = 0; s < 8; ++s) {
+                half2_t w[MATS][H][4];
+#pragma unroll
+                for (int q = 0; q < MATS; ++q)
+#pragma unroll
+                    for (int h = 0; h < H; ++h) lut8(lut, cw[q][h][s >> 2][s & 3], laneoff, w[q][h]);
+#pragma unroll
+                for (int q = 0; q < MATS; ++q)
+#pragma unroll
+                    for (int h = 0; h < H; ++h) {
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) w[q][h][c] *= s2[q][h];
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+                            d[q][h][n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+                                __builtin_bit_cast(half8_t, x[n][s]), join8(w[q][h]), d[q][h][n], 0, 0, 0);
+                    }
+            }
+#pragma unroll
+            for (int q = 0; q < MATS; ++q)
+                if (t + 1 < t1) load_tile(q, t + 1);
+#pragma unroll
+            for (int q = 0; q < MATS; ++q)
+#pragma unroll
+                for (int h = 0; h < H; ++h)
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            red[q][wave][(16 * n + 4 * g + i) * 32 + 16 * h + col] += d[q][h][n][i];
+                        for (int i = 0; i < 4; ++i) d[q][h][n][i] = ldexpf(d[q][h][n][i], e[q][h] + back[n][i]);
+        }
+        // Register i of row tile n: row 16 n + 4 g + i, column 16 h + col.
+        auto each = [&](auto f) {
+#pragma unroll
+            for (int q = 0; q < MATS; ++q)
+#pragma unroll
+                for (int h = 0; h < H; ++h)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) f(q, (16 * n + 4 * g + i) * ROWS + 16 * h + col, d[q][h][n][i]);
+        };
+        if constexpr (kFold) {
+            if (wave >= kRed && wave < ns) each([&](int q, int at, float v) { red[q][wave - kRed][at] = v; });
+            __syncthreads();
+            if (wave < kRed) {
+                if (wave + kRed < ns) each([&](int q, int at, float v) { red[q][wave][at] += v; });
+                else if (wave < ns) each([&](int q, int at, float v) { red[q][wave][at] = v; });
+            }
+        } else {
+            if (wave < ns) each([&](int q, int at, float v) { red[q][wave][at] = v; });
         }
         __syncthreads();
-#pragma unroll
-        for (int n = 0; n < kOuts; ++n) {
-            const int o = threadIdx.x + n * kChunkWaves * 64, row = o >> 5, mo = t * 32 + (o & 31);
-            if (row >= ck.count || mo >= a.M) continue;
+        const int nred = min(ns, kRed);
+        if (out) {
             float v[MATS];
 #pragma unroll
             for (int q = 0; q < MATS; ++q) {
                 v[q] = red[q][0][o];
 #pragma unroll
-                for (int w = 1; w < kChunkWaves / 2; ++w) v[q] += red[q][w][o];
+                for (int w = 1; w < kRed; ++w)
+                    if (w < nred) v[q] += red[q][w][o];
             }
-            const int p = ck.start + row;
+            if (!PRE && a.rows && source_row(a, p) < 0) {
+#pragma unroll
+                for (int q = 0; q < MATS; ++q) v[q] = 0.0f;
+            }
             const int64_t at = (int64_t)p * a.M + mo;
             if constexpr (PART) {
 #pragma unroll
-                for (int q = 0; q < MATS; ++q)
-                    a.part[((int64_t)q * a.ranges + blockIdx.z) * a.R * a.M + at] = v[q];
+                for (int q = 0; q < MATS; ++q) a.part[((int64_t)q * a.ranges + z) * a.R * a.M + at] = v[q];
             } else {
-                float y = MATS == 2 ? swiglu(v[0], v[MATS - 1]) : v[0];
-                if constexpr (LORA) y += term[n];
-                store_out(a.Y, a.bf16, at, y);
+                store_out(a.Y, a.bf16, at, (MATS == 2 ? swiglu(v[0], v[MATS - 1]) : v[0]) + term);
             }
         }
         if (t + 1 < t1) __syncthreads();
     }
+}
+
+__global__ __launch_bounds__(256) void ragged_pieces_kernel(const uint16_t *__restrict__ X,
+                                                            const int32_t *__restrict__ rows, int K, int T, int R,
+                                                            Pieces out) {
+    write_pieces(X, rows, K, T, R, out, blockIdx.x);
 }
 
 // Adds the partial planes in range order and finishes the outputs.
@@ -527,15 +574,18 @@ __global__ __launch_bounds__(kTileWaves * 64) void ragged_tile_kernel(const Args
         }
 }
 
+int64_t slices_of(int64_t K) { return (K + kSliceK - 1) / kSliceK; }
+
 // How a call runs.
 struct Plan {
     bool tiles;   // tile kernel (else chunk kernel)
     int mt;       // tile kernel: 32-row tiles a wave
     int cap;      // chunk kernel: rows a chunk
+    bool pre;     // chunk kernel: the activations are converted by a launch before
     int ranges;   // chunk kernel: ranges of K
 };
 
-Plan plan_of(int64_t E, int64_t M, int64_t K, int64_t R) {
+Plan plan_of(int64_t E, int64_t M, int64_t K, int64_t R, bool lora) {
     Plan p = {};
     // Rows a group, were all groups in use equally full.
     const int64_t groups = E < R ? E : R;
@@ -543,7 +593,8 @@ Plan plan_of(int64_t E, int64_t M, int64_t K, int64_t R) {
     p.tiles = avg > 64;
     p.mt = avg > 160 ? 4 : 2;
     p.cap = R <= 16 || avg <= 12 ? 16 : 32;
-    p.ranges = (int)((K / 64 + kRangeBlocks - 1) / kRangeBlocks);
+    p.pre = lora || R > 16;
+    p.ranges = (int)((slices_of(K) + kChunkWaves - 1) / kChunkWaves);
     return p;
 }
 
@@ -564,7 +615,7 @@ int compute_units() {
 }
 
 bool ragged_fits(int64_t E, int64_t M, int64_t K, int64_t T, int64_t R, bool up) {
-    const Plan p = plan_of(E, M, K, R);
+    const Plan p = plan_of(E, M, K, R, false);
     const int64_t most = INT64_C(1) << 32;  // threads of one launch
     if (p.tiles) {
         const int64_t rowtiles = (M + (up ? 127 : 255)) / (up ? 128 : 256);
@@ -573,12 +624,17 @@ bool ragged_fits(int64_t E, int64_t M, int64_t K, int64_t T, int64_t R, bool up)
     return ((M + 255) / 256) * R * 256 < most && chunk_bound(E, R, p.cap) < 65536;
 }
 
-size_t ragged_ws_bytes(int64_t E, int64_t M, int64_t K, int64_t T, int64_t R, bool up) {
-    const Plan p = plan_of(E, M, K, R);
+size_t ragged_ws_bytes(int64_t E, int64_t M, int64_t K, int64_t T, int64_t R, bool up, bool lora) {
+    const Plan p = plan_of(E, M, K, R, lora);
     const size_t mats = up ? 2 : 1;
     if (p.tiles)
         return round16((size_t)T * K * 2) + round16((size_t)T * 4) + mats * round16((size_t)E * M);
-    return p.ranges > 1 ? mats * p.ranges * (size_t)R * M * 4 : 0;
+    return (p.pre ? pieces_bytes(K, R) : 0) + (p.ranges > 1 ? mats * p.ranges * (size_t)R * M * 4 : 0);
+}
+
+bool ragged_takes_pieces(int64_t E, int64_t M, int64_t K, int64_t R, bool lora) {
+    const Plan p = plan_of(E, M, K, R, lora);
+    return !p.tiles && p.pre;
 }
 
 template <int MT>
@@ -588,19 +644,20 @@ static const void *tile_fn(bool up, bool lora) {
                 : reinterpret_cast<const void *>(&ragged_tile_kernel<MT, 1, false>);
 }
 
-template <int NT>
+template <int NT, bool PRE>
 static const void *chunk_fn(bool up, bool part, bool lora) {
     if (up)
-        return part ? reinterpret_cast<const void *>(&ragged_chunk_kernel<NT, 2, true, false>)
-                    : reinterpret_cast<const void *>(&ragged_chunk_kernel<NT, 2, false, false>);
-    if (part) return reinterpret_cast<const void *>(&ragged_chunk_kernel<NT, 1, true, false>);
-    return lora ? reinterpret_cast<const void *>(&ragged_chunk_kernel<NT, 1, false, true>)
-                : reinterpret_cast<const void *>(&ragged_chunk_kernel<NT, 1, false, false>);
+        return part ? reinterpret_cast<const void *>(&ragged_chunk_kernel<NT, 2, true, false, PRE>)
+                    : reinterpret_cast<const void *>(&ragged_chunk_kernel<NT, 2, false, false, PRE>);
+    if (part) return reinterpret_cast<const void *>(&ragged_chunk_kernel<NT, 1, true, false, PRE>);
+    if constexpr (PRE)
+        if (lora) return reinterpret_cast<const void *>(&ragged_chunk_kernel<NT, 1, false, true, true>);
+    return reinterpret_cast<const void *>(&ragged_chunk_kernel<NT, 1, false, false, PRE>);
 }
 
 hipError_t launch_ragged(const RaggedProduct &p, void *workspace, hipStream_t stream) {
-    const Plan pl = plan_of(p.E, p.M, p.K, p.R);
     const bool up = p.up_codes != nullptr, lora = p.B != nullptr;
+    const Plan pl = plan_of(p.E, p.M, p.K, p.R, lora);
     Args a = {};
     a.codes[0] = p.codes;
     a.codes[1] = p.up_codes;
@@ -649,15 +706,36 @@ hipError_t launch_ragged(const RaggedProduct &p, void *workspace, hipStream_t st
                                stream);
     }
     a.ranges = pl.ranges;
+    a.slices_each = (int)(slices_of(p.K) / pl.ranges);
+    a.slices_more = (int)(slices_of(p.K) % pl.ranges);
+    hipError_t e;
+    char *w = static_cast<char *>(workspace);
+    if (pl.pre) {
+        Pieces pc = pieces_at(p.K, p.R, w);
+        w += pieces_bytes(p.K, p.R);
+        if (!lora) {  // (the adapters' first launch writes them)
+            const uint16_t *X = p.X;
+            const int32_t *rows = p.rows;
+            int K = a.K, T = a.T, R = a.R;
+            void *pargs[] = {&X, &rows, &K, &T, &R, &pc};
+            e = hipLaunchKernel(reinterpret_cast<const void *>(&ragged_pieces_kernel), dim3((unsigned)pieces_blocks(p.K, p.R)),
+                                dim3(256), pargs, 0, stream);
+            if (e != hipSuccess) return e;
+        }
+        a.X = pc.x16;
+        a.xexp = pc.exps;
+    }
     const bool part = pl.ranges > 1;
-    a.part = part ? static_cast<float *>(workspace) : nullptr;
-    const int64_t ntiles = (p.M + 31) / 32, chunks = chunk_bound(p.E, p.R, pl.cap);
-    // Two workgroups a compute unit at least, and as few more as it takes.
-    int64_t per = ntiles * chunks * pl.ranges / (2 * compute_units());
-    a.tiles_per_wg = (int)(per < 1 ? 1 : per > 8 ? 8 : per);
-    const dim3 grid((unsigned)((ntiles + a.tiles_per_wg - 1) / a.tiles_per_wg), (unsigned)chunks, (unsigned)pl.ranges);
-    hipError_t e = hipLaunchKernel(pl.cap == 16 ? chunk_fn<1>(up, part, lora) : chunk_fn<2>(up, part, lora), grid,
-                                   dim3(kChunkWaves * 64), args, 0, stream);
+    a.part = part ? reinterpret_cast<float *>(w) : nullptr;
+    const int tile_rows = pl.cap == 16 ? 32 : 16;
+    const int64_t ntiles = (p.M + tile_rows - 1) / tile_rows, chunks = chunk_bound(p.E, p.R, pl.cap);
+    // Two workgroups a compute unit, the tiles dealt evenly over them.
+    int64_t wgs = 2 * compute_units() / (chunks * pl.ranges);
+    wgs = wgs < 1 ? 1 : wgs > ntiles ? ntiles : wgs;
+    const dim3 grid((unsigned)wgs, (unsigned)chunks, (unsigned)pl.ranges);
+    const void *fn = pl.cap == 16 ? pl.pre ? chunk_fn<1, true>(up, part, lora) : chunk_fn<1, false>(up, part, lora)
+                                  : pl.pre ? chunk_fn<2, true>(up, part, lora) : chunk_fn<2, false>(up, part, lora);
+    e = hipLaunchKernel(fn, grid, dim3(kChunkWaves * 64), args, 0, stream);
     if (e != hipSuccess || !part) return e;
     const void *fin = up     ? reinterpret_cast<const void *>(&ragged_finish_kernel<2, false>)
                       : lora ? reinterpret_cast<const void *>(&ragged_finish_kernel<1, true>)

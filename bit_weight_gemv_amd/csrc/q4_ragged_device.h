@@ -4,6 +4,7 @@
 
 #include "q4_device.h"
 #include "q4_lut.h"
+#include "q4_ragged.h"
 
 namespace q4 {
 
@@ -84,6 +85,36 @@ __device__ __forceinline__ int fp16_shift(uint32_t maxbits) {
 // result is an fp16 normal number, towards zero below that.
 __device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t d, float f) {
     return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(bf16_lo(d) * f, bf16_hi(d) * f));
+}
+
+// Workgroup `block` (of 256) of those that write the rows of X (bf16 [T][K];
+// position p takes rows[p], or row p; one outside [0, T): zeros) as pieces: a
+// lane converts one piece, the 32 lanes of a half-wave a slice of a position.
+__device__ __forceinline__ void write_pieces(const uint16_t *__restrict__ X, const int32_t *__restrict__ rows, int K,
+                                             int T, int R, const Pieces &out, int block) {
+    const int pairs = (R + 1) >> 1, slices = (K + 255) >> 8;
+    const int w = block * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
+    const int slice = w / pairs, p = (w % pairs) * 2 + (lane >> 5), piece = slice * 32 + (lane & 31);
+    const bool live = slice < slices && p < R && piece < K / 8;
+    u32x4_t v = {0u, 0u, 0u, 0u};
+    if (live) {
+        const int row = rows ? rows[p] : p;
+        if (row >= 0 && row < T) v = reinterpret_cast<const u32x4_t *>(X + (int64_t)row * K)[piece];
+    }
+    u16x2_t mx = {0, 0};
+#pragma unroll
+    for (int c = 0; c < 4; ++c) mx = __builtin_elementwise_max(mx, __builtin_bit_cast(u16x2_t, v[c] & 0x7FFF7FFFu));
+    int m = max((int)mx.x, (int)mx.y);
+#pragma unroll
+    for (int d = 16; d >= 1; d >>= 1) m = max(m, __shfl_xor(m, d));
+    const int shift = fp16_shift((uint32_t)m);
+    const float f = exp2i(shift);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) v[c] = bf16x2_to_f16x2(v[c], f);
+    if (live) {
+        reinterpret_cast<u32x4_t *>(out.x16)[(int64_t)piece * R + p] = v;
+        if ((lane & 31) == 0) out.exps[(int64_t)slice * R + p] = -shift;
+    }
 }
 
 // Eight weights of four code bytes, as fp16 table entries.
