@@ -41,14 +41,13 @@ __device__ __forceinline__ int source_row(const Args &a, int p) {
     return row >= 0 && row < a.T ? row : -1;
 }
 
-// The adapter's part of output (p, m).
-__device__ __forceinline__ float adapter_term(const Args &a, int p, int m) {
-    const int id = a.ids[p];
+// The part of adapter id in output (p, m), from rank j0 on.
+__device__ __forceinline__ float adapter_term(const Args &a, int id, int p, int m, int j0 = 0) {
     if (id < 0 || id >= a.L) return 0.0f;
     const uint16_t *b = a.B + ((int64_t)id * a.M + m) * a.r;
     const float *t = a.t + (int64_t)p * a.r;
     float s = 0.0f;
-    for (int j = 0; j < a.r; j += 8) {
+    for (int j = j0; j < a.r; j += 8) {
         const uint4 v = *reinterpret_cast<const uint4 *>(b + j);
         const float4 t0 = *reinterpret_cast<const float4 *>(t + j), t1 = *reinterpret_cast<const float4 *>(t + j + 4);
         s = fmaf(bf16_lo(v.x), t0.x, s);
@@ -71,88 +70,105 @@ __device__ __forceinline__ float adapter_term(const Args &a, int p, int m) {
 // (16 where NT is 2) of the matrix, with a wave for each slice; the wave's slice of the chunk's
 // activations, in fp16 under a power of two a row, stays in registers.
 // v_mfma_f32_16x16x32_f16 takes k in any order that both operands share: lane
-// (r, g) holds block g of the slice for row r, so a lane's 64 weights have
-// one scale and come from 32 neighbouring bytes.  They are multiplied by the
-// scale in fp16, under a power of two that brings the largest of the row's
-// four scales to [2^14, 2^15).  The waves' tiles are added through LDS.
+// (r, g) holds the pieces g and 4 + g of 32 weights of row r, so that a load
+// takes 64 neighbouring bytes of a row and a piece has one scale.  The weights
+// are multiplied by the scale in fp16, under a power of two that brings the
+// largest of the row's four scales to [2^14, 2^15).  The waves' tiles are
+// added through LDS.
 //
 // Such calls are bound by their waits and by the instructions of a wave (four
-// cycles each, 16 waves a compute unit) more than by their bytes: nothing is
-// cleared that a clamped address or a scale of 0 makes harmless, the codes of
-// a tile are asked for before anything else and those of the next before the
-// sums go through LDS, and registers (128) and LDS (80 KB) leave room for two
-// workgroups a compute unit.  PRE: the activations were converted by an
-// earlier launch, and lie in the order of the loads.
+// cycles each) more than by their bytes: nothing is cleared that a clamped
+// address or a scale of 0 makes harmless; the codes (and the adapters' rows)
+// of the first two tiles are asked for before anything else, and a tile's
+// registers take the tile after next.  PRE: the activations were converted by
+// an earlier launch, and lie in the order of the loads.
 // ---------------------------------------------------------------------------
 constexpr int kChunkWaves = 8;
 constexpr int kSliceK = 256;
 
 template <int NT, int MATS, bool PART, bool LORA, bool PRE>
-__global__ __launch_bounds__(kChunkWaves * 64, 4) void ragged_chunk_kernel(const Args a) {
+__global__ __launch_bounds__(kChunkWaves * 64, NT * MATS == 1 && !LORA ? 4 : 2) void ragged_chunk_kernel(const Args a) {
     constexpr int CAP = 16 * NT;
-    constexpr int H = NT == 2 ? 1 : 2;  // 16-row pieces of a tile: what 128 registers hold
+    constexpr int H = NT == 2 ? 1 : 2;  // 16-row pieces of a tile
     constexpr int ROWS = 16 * H;
-    // Where all waves' tiles would leave room for one workgroup only, the
-    // upper half of the waves comes first and the lower adds to it.
-    constexpr bool kFold = MATS > 1;
-    constexpr int kRed = kFold ? kChunkWaves / 2 : kChunkWaves;
+    constexpr int D = 2;                // tiles whose codes are held or on their way
     static_assert(CAP * ROWS == kChunkWaves * 64, "an output a thread");
     __shared__ uint32_t lut[kLutDwords];
-    __shared__ float red[MATS][kRed][CAP * ROWS];
+    __shared__ float red[MATS][kChunkWaves][CAP * ROWS];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int col = lane & 15, g = lane >> 4;
 
-    const Chunk ck = find_chunk(a.offsets, a.E, a.R, blockIdx.y, CAP);
-    if (ck.count == 0) return;
+    const Share share = find_share(a.offsets, a.E, a.R, CAP, blockIdx.x, gridDim.x);
+    const Chunk ck = share.chunk;
     const int nb = a.K >> 6;
     // Ranges take slices dealt evenly, the longer ones first.
-    const int z = blockIdx.z;
+    const int z = blockIdx.y;
     const int s0 = z * a.slices_each + min(z, a.slices_more), ns = a.slices_each + (z < a.slices_more ? 1 : 0);
-    const int b = 4 * (s0 + wave) + g;       // this lane's block
-    const bool live = b < nb;
-    const int bc = min(b, nb - 1);
+    // This lane's two pieces of 32 k, and whether they lie within the row.
+    const int pc[2] = {8 * (s0 + wave) + g, 8 * (s0 + wave) + 4 + g};
+    const bool live[2] = {pc[0] < 2 * nb, pc[1] < 2 * nb};
+    const int at[2] = {min(pc[0], 2 * nb - 1), min(pc[1], 2 * nb - 1)};
     const int ntiles = (a.M + ROWS - 1) / ROWS;
-    const int t0 = (int)((uint32_t)ntiles * blockIdx.x / gridDim.x), t1 = (int)((uint32_t)ntiles * (blockIdx.x + 1) / gridDim.x);
+    const int t0 = (int)((uint32_t)ntiles * share.part / share.nparts);
+    const int t1 = (int)((uint32_t)ntiles * (share.part + 1) / share.nparts);
+    if (ck.count == 0 || t0 == t1) return;
+    // This thread's output of each tile: row p of Y, packed row `om` of the tile.
+    const int orow = threadIdx.x / ROWS, om = threadIdx.x % ROWS, p = ck.start + min(orow, ck.count - 1);
 
-    u32x4_t cw[MATS][H][2];                  // [matrix][16 rows][half a block]
-    uint32_t sc[MATS][H];
-    auto load_tile = [&](int q, int t) {
-        const int64_t m0 = (int64_t)ck.e * a.M + t * ROWS;
-        const uint8_t *cbase = a.codes[q] + m0 * (a.K >> 1);
-        const uint16_t *sbase = a.scales[q] + m0 * nb;
+    u32x4_t cw[D][MATS][H][2];          // [matrix][16 rows][piece]
+    uint32_t sc[D][MATS][H][2];
+    u32x4_t bw[D][2];                   // the first 16 ranks of B for this thread's output
+    int id = -1;
+    const uint16_t *brow = nullptr;
+    if constexpr (LORA) {
+        id = a.ids[p];
+        if (id >= a.L) id = -1;
+        brow = a.B + (int64_t)max(id, 0) * a.M * a.r;
+    }
+    auto load_tile = [&](int u, int t) {
 #pragma unroll
-        for (int h = 0; h < H; ++h) {
-            const uint32_t m = min(16 * h + col, a.M - 1 - t * ROWS);
-            const u32x4_t *c = reinterpret_cast<const u32x4_t *>(cbase + (m * (uint32_t)(a.K >> 1) + 32 * bc));
-            cw[q][h][0] = c[0];
-            cw[q][h][1] = c[1];
-            sc[q][h] = sbase[m * (uint32_t)nb + bc];
+        for (int q = 0; q < MATS; ++q) {
+            const int64_t m0 = (int64_t)ck.e * a.M + t * ROWS;
+            const uint8_t *cbase = a.codes[q] + m0 * (a.K >> 1);
+            const uint16_t *sbase = a.scales[q] + m0 * nb;
+#pragma unroll
+            for (int h = 0; h < H; ++h) {
+                const uint32_t m = min(16 * h + col, a.M - 1 - t * ROWS);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    cw[u][q][h][j] = *reinterpret_cast<const u32x4_t *>(cbase + (m * (uint32_t)(a.K >> 1) + 16 * at[j]));
+                    sc[u][q][h][j] = sbase[m * (uint32_t)nb + (at[j] >> 1)];
+                }
+            }
+        }
+        if constexpr (LORA) {
+            const uint16_t *b = brow + (int64_t)min(t * ROWS + om, a.M - 1) * a.r;
+            bw[u][0] = *reinterpret_cast<const u32x4_t *>(b);
+            bw[u][1] = *reinterpret_cast<const u32x4_t *>(b + (a.r > 8 ? 8 : 0));
         }
     };
-
     u32x4_t x[NT][8];
-    int back[NT][4];                         // the inverse power of two of each register's row, less 14
+    int back[NT][4];                    // the inverse power of two of each register's row, less 14
     if constexpr (PRE) {
-#pragma unroll
-        for (int q = 0; q < MATS; ++q) load_tile(q, t0);
         // [piece of 8 k][position]: 16 lanes read 256 neighbouring bytes.
-        const u32x4_t *src = reinterpret_cast<const u32x4_t *>(a.X) + (int64_t)(8 * bc) * a.R + ck.start;
+        const u32x4_t *src = reinterpret_cast<const u32x4_t *>(a.X) + ck.start;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             const int row = min(16 * n + col, ck.count - 1);
 #pragma unroll
-            for (int s = 0; s < 8; ++s) x[n][s] = src[(int64_t)s * a.R + row];
+            for (int s = 0; s < 8; ++s) x[n][s] = src[(int64_t)(4 * at[s >> 2] + (s & 3)) * a.R + row];
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                back[n][i] = a.xexp[(int64_t)(bc >> 2) * a.R + ck.start + min(16 * n + 4 * g + i, ck.count - 1)] - 14;
+                back[n][i] = a.xexp[(int64_t)(at[0] >> 3) * a.R + ck.start + min(16 * n + 4 * g + i, ck.count - 1)] - 14;
         }
+#pragma unroll
+        for (int u = 0; u < D; ++u) load_tile(u, min(t0 + u, t1 - 1));
         fill_lut(lut);
     } else {
         int row[NT];
 #pragma unroll
         for (int n = 0; n < NT; ++n) row[n] = max(source_row(a, ck.start + min(16 * n + col, ck.count - 1)), 0);
-#pragma unroll
-        for (int q = 0; q < MATS; ++q) load_tile(q, t0);
+        load_tile(0, t0);
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -160,11 +176,13 @@ __global__ __launch_bounds__(kChunkWaves * 64, 4) void ragged_chunk_kernel(const
         if (a.T > 0) {
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                const u32x4_t *src = reinterpret_cast<const u32x4_t *>(a.X + (int64_t)row[n] * a.K + 64 * bc);
+                const u32x4_t *src = reinterpret_cast<const u32x4_t *>(a.X + (int64_t)row[n] * a.K);
 #pragma unroll
-                for (int s = 0; s < 8; ++s) x[n][s] = src[s];
+                for (int s = 0; s < 8; ++s) x[n][s] = src[4 * at[s >> 2] + (s & 3)];
             }
         }
+#pragma unroll
+        for (int u = 1; u < D; ++u) load_tile(u, min(t0 + u, t1 - 1));
         fill_lut(lut);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
@@ -187,31 +205,33 @@ __global__ __launch_bounds__(kChunkWaves * 64, 4) void ragged_chunk_kernel(const
             for (int i = 0; i < 4; ++i) back[n][i] = -14 - __shfl(shift, 4 * g + i);
         }
     }
+    float tv[16];                       // the first 16 of t for this thread's row
+    if constexpr (LORA) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) tv[i] = id >= 0 && i < a.r ? a.t[(int64_t)p * a.r + i] : 0.0f;
+    }
     __syncthreads();
 
     const uint32_t laneoff = (uint32_t)lane << 2;
-    for (int t = t0; t < t1; ++t) {
-        // This thread's output.
-        const int o = threadIdx.x, row = o / ROWS, mo = t * ROWS + o % ROWS, p = ck.start + row;
-        const bool out = row < ck.count && mo < a.M;
-        float term = 0.0f;
-        if constexpr (LORA)
-            if (out) term = adapter_term(a, p, mo);
+    auto tile = [&](int u, int t) {
         float4_t d[MATS][H][NT];
         if (wave < ns) {
             int e[MATS][H];
-            half2_t s2[MATS][H];
+            half2_t s2[MATS][H][2];
 #pragma unroll
             for (int q = 0; q < MATS; ++q)
 #pragma unroll
                 for (int h = 0; h < H; ++h) {
-                    const uint32_t bits = live ? sc[q][h] : 0;
-                    int m = (int)(bits & 0x7FFFu);
+                    const uint32_t bits[2] = {live[0] ? sc[u][q][h][0] : 0, live[1] ? sc[u][q][h][1] : 0};
+                    int m = (int)max(bits[0] & 0x7FFFu, bits[1] & 0x7FFFu);
                     m = max(m, __shfl_xor(m, 16));
                     m = max(m, __shfl_xor(m, 32));
                     e[q][h] = m ? (int)(__builtin_bit_cast(uint32_t, f16_bits_to_f32((uint32_t)m)) >> 23) - 127 : 0;
-                    const _Float16 sh = (_Float16)ldexpf(f16_bits_to_f32(bits), 14 - e[q][h]);
-                    s2[q][h] = half2_t{sh, sh};
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const _Float16 sh = (_Float16)ldexpf(f16_bits_to_f32(bits[j]), 14 - e[q][h]);
+                        s2[q][h][j] = half2_t{sh, sh};
+                    }
 #pragma unroll
                     for (int n = 0; n < NT; ++n) d[q][h][n] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
                 }
@@ -223,22 +243,20 @@ __global__ __launch_bounds__(kChunkWaves * 64, 4) void ragged_chunk_kernel(const
 #pragma unroll
                 for (int q = 0; q < MATS; ++q)
 #pragma unroll
-                    for (int h = 0; h < H; ++h) lut8(lut, cw[q][h][s >> 2][s & 3], laneoff, w[q][h]);
+                    for (int h = 0; h < H; ++h) lut8(lut, cw[u][q][h][s >> 2][s & 3], laneoff, w[q][h]);
 #pragma unroll
                 for (int q = 0; q < MATS; ++q)
 #pragma unroll
                     for (int h = 0; h < H; ++h) {
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) w[q][h][c] *= s2[q][h];
+                        for (int c = 0; c < 4; ++c) w[q][h][c] *= s2[q][h][s >> 2];
 #pragma unroll
                         for (int n = 0; n < NT; ++n)
                             d[q][h][n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
                                 __builtin_bit_cast(half8_t, x[n][s]), join8(w[q][h]), d[q][h][n], 0, 0, 0);
                     }
             }
-#pragma unroll
-            for (int q = 0; q < MATS; ++q)
-                if (t + 1 < t1) load_tile(q, t + 1);
+            // Register i of row tile n: row 16 n + 4 g + i, column 16 h + col.
 #pragma unroll
             for (int q = 0; q < MATS; ++q)
 #pragma unroll
@@ -246,53 +264,155 @@ __global__ __launch_bounds__(kChunkWaves * 64, 4) void ragged_chunk_kernel(const
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) d[q][h][n][i] = ldexpf(d[q][h][n][i], e[q][h] + back[n][i]);
+                        for (int i = 0; i < 4; ++i)
+                            red[q][wave][(16 * n + 4 * g + i) * ROWS + 16 * h + col] =
+                                ldexpf(d[q][h][n][i], e[q][h] + back[n][i]);
         }
-        // Register i of row tile n: row 16 n + 4 g + i, column 16 h + col.
-        auto each = [&](auto f) {
+        float term = 0.0f;
+        if constexpr (LORA) {
 #pragma unroll
-            for (int q = 0; q < MATS; ++q)
-#pragma unroll
-                for (int h = 0; h < H; ++h)
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) f(q, (16 * n + 4 * g + i) * ROWS + 16 * h + col, d[q][h][n][i]);
-        };
-        if constexpr (kFold) {
-            if (wave >= kRed && wave < ns) each([&](int q, int at, float v) { red[q][wave - kRed][at] = v; });
-            __syncthreads();
-            if (wave < kRed) {
-                if (wave + kRed < ns) each([&](int q, int at, float v) { red[q][wave][at] += v; });
-                else if (wave < ns) each([&](int q, int at, float v) { red[q][wave][at] = v; });
+            for (int c = 0; c < 8; ++c) {
+                term = fmaf(bf16_lo(bw[u][c >> 2][c & 3]), tv[2 * c], term);
+                term = fmaf(bf16_hi(bw[u][c >> 2][c & 3]), tv[2 * c + 1], term);
             }
-        } else {
-            if (wave < ns) each([&](int q, int at, float v) { red[q][wave][at] = v; });
         }
+        if (t + D < t1) load_tile(u, t + D);
         __syncthreads();
-        const int nred = min(ns, kRed);
-        if (out) {
+        const int mo = t * ROWS + om;
+        if (orow < ck.count && mo < a.M) {
             float v[MATS];
 #pragma unroll
             for (int q = 0; q < MATS; ++q) {
-                v[q] = red[q][0][o];
+                v[q] = red[q][0][threadIdx.x];
 #pragma unroll
-                for (int w = 1; w < kRed; ++w)
-                    if (w < nred) v[q] += red[q][w][o];
+                for (int w = 1; w < kChunkWaves; ++w)
+                    if (w < ns) v[q] += red[q][w][threadIdx.x];
             }
             if (!PRE && a.rows && source_row(a, p) < 0) {
 #pragma unroll
                 for (int q = 0; q < MATS; ++q) v[q] = 0.0f;
             }
-            const int64_t at = (int64_t)p * a.M + mo;
+            const int64_t o = (int64_t)p * a.M + mo;
             if constexpr (PART) {
 #pragma unroll
-                for (int q = 0; q < MATS; ++q) a.part[((int64_t)q * a.ranges + z) * a.R * a.M + at] = v[q];
+                for (int q = 0; q < MATS; ++q) a.part[((int64_t)q * a.ranges + z) * a.R * a.M + o] = v[q];
             } else {
-                store_out(a.Y, a.bf16, at, (MATS == 2 ? swiglu(v[0], v[MATS - 1]) : v[0]) + term);
+                float y = MATS == 2 ? swiglu(v[0], v[MATS - 1]) : v[0];
+                if constexpr (LORA) {
+                    if (id >= 0) y += term + adapter_term(a, id, p, mo, 16);
+                }
+                store_out(a.Y, a.bf16, o, y);
             }
         }
-        if (t + 1 < t1) __syncthreads();
+        __syncthreads();
+    };
+    for (int t = t0; t < t1; t += D) {
+#pragma unroll
+        for (int u = 0; u < D; ++u)
+            if (t + u < t1) tile(u, t + u);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// One row a group, mostly: every row of X by itself.
+//
+// A wave takes tiles of 8 packed rows (with MATS == 2 four of the gate and the
+// same four of the up matrix) of one range of at most 2048 weights; a lane
+// holds one piece of 32 weights of each row (1 KB of a row in one load) and
+// the same 32 activations, in fp16 under a power of two a range, in registers.
+// Table lookups feed v_dot2_f32_f16, the piece's scale multiplies its fp32
+// sum, and the 8 rows' sums are added over the lanes together.  Waves do not
+// wait for each other after the table is filled, and a row's registers take
+// the next tile's row as soon as it is used: bound by the bytes of the codes,
+// or by the launch and the waits before the first of them.
+// ---------------------------------------------------------------------------
+constexpr int kRowTile = 8;
+constexpr int kRowRangeK = 2048;
+
+template <int MATS, bool PART, bool LORA>
+__global__ __launch_bounds__(512, 4) void ragged_row_kernel(const Args a) {
+    constexpr int ROWS = kRowTile / MATS;
+    __shared__ uint32_t lut[kLutDwords];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int waves = blockDim.x >> 6;
+    const int nb = a.K >> 6;
+    const int z = blockIdx.y;
+    const int first = z * (kRowRangeK / 32) + lane;
+    const bool live = first < 2 * nb;
+    const int piece = min(first, 2 * nb - 1);
+    const int ntiles = (a.M * MATS + kRowTile - 1) / kRowTile;
+    const Share share = find_share(a.offsets, a.E, a.R, 1, blockIdx.x, gridDim.x);
+    const Chunk ck = share.chunk;
+    int t = share.part * waves + wave;
+    const int tstep = share.nparts * waves;
+    if (ck.count == 0) return;
+
+    u32x4_t cw[kRowTile];
+    uint32_t sc[kRowTile];
+    auto load = [&](int tile, int r) {
+        const int q = r / ROWS, m = min(tile * ROWS + r % ROWS, a.M - 1);
+        const int64_t mrow = (int64_t)ck.e * a.M + m;
+        cw[r] = *reinterpret_cast<const u32x4_t *>(a.codes[q] + mrow * (a.K >> 1) + 16 * (uint32_t)piece);
+        sc[r] = a.scales[q][mrow * nb + (piece >> 1)];
+    };
+    const int p = ck.start, row = source_row(a, p);
+#pragma unroll
+    for (int r = 0; r < kRowTile; ++r) load(min(t, ntiles - 1), r);
+    u32x4_t xr[4];
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+        xr[s] = u32x4_t{0u, 0u, 0u, 0u};
+        if (row >= 0) xr[s] = reinterpret_cast<const u32x4_t *>(a.X + (int64_t)row * a.K + 32 * piece)[s];
+    }
+    fill_lut(lut);
+    half2_t x[16];
+    u16x2_t mx = {0, 0};
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+            mx = __builtin_elementwise_max(mx, __builtin_bit_cast(u16x2_t, xr[s][c] & 0x7FFF7FFFu));
+    const int shift = fp16_shift(wave_max_u32(mx.x > mx.y ? mx.x : mx.y));
+    const float f = exp2i(shift);
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) x[4 * s + c] = __builtin_bit_cast(half2_t, bf16x2_to_f16x2(xr[s][c], f));
+    int id = -1;
+    if constexpr (LORA) id = a.ids[p];
+    __syncthreads();
+
+    const uint32_t laneoff = (uint32_t)lane << 2;
+    for (; t < ntiles; t += tstep) {
+        const int mo = t * ROWS + (lane & (ROWS - 1));
+        float term = 0.0f;
+        if constexpr (LORA)
+            if (lane < ROWS && mo < a.M) term = adapter_term(a, id, p, mo);
+        float v[kRowTile];
+#pragma unroll
+        for (int r = 0; r < kRowTile; ++r) {
+            float d0 = 0.0f, d1 = 0.0f;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                half2_t w[4];
+                lut8(lut, cw[r][c], laneoff, w);
+                d0 = __builtin_amdgcn_fdot2(w[0], x[4 * c], d0, false);
+                d1 = __builtin_amdgcn_fdot2(w[1], x[4 * c + 1], d1, false);
+                d0 = __builtin_amdgcn_fdot2(w[2], x[4 * c + 2], d0, false);
+                d1 = __builtin_amdgcn_fdot2(w[3], x[4 * c + 3], d1, false);
+            }
+            v[r] = live ? f16_bits_to_f32(sc[r]) * (d0 + d1) : 0.0f;
+            if (t + tstep < ntiles) load(t + tstep, r);
+        }
+        float total = ldexpf(reduce_rows<kRowTile>(v), -shift);  // of row lane % 8
+        const int64_t at = (int64_t)p * a.M + mo;
+        if constexpr (PART) {
+            const int q = (lane & (kRowTile - 1)) / ROWS;
+            if (lane < kRowTile && mo < a.M) a.part[((int64_t)q * a.ranges + z) * a.R * a.M + at] = total;
+        } else {
+            if constexpr (MATS == 2) total = swiglu(total, __shfl_xor(total, ROWS));
+            if (lane < ROWS && mo < a.M) store_out(a.Y, a.bf16, at, total + term);
+        }
     }
 }
 
@@ -324,7 +444,7 @@ __global__ __launch_bounds__(256) void ragged_finish_kernel(const Args a) {
         for (int z = 1; z < a.ranges; ++z) v[q] += s[z * plane];
     }
     float y = MATS == 2 ? swiglu(v[0], v[MATS - 1]) : v[0];
-    if constexpr (LORA) y += adapter_term(a, p, m);
+    if constexpr (LORA) y += adapter_term(a, a.ids[p], p, m);
     store_out(a.Y, a.bf16, at, y);
 }
 
@@ -578,6 +698,7 @@ int64_t slices_of(int64_t K) { return (K + kSliceK - 1) / kSliceK; }
 
 // How a call runs.
 struct Plan {
+    bool single;  // row kernel
     bool tiles;   // tile kernel (else chunk kernel)
     int mt;       // tile kernel: 32-row tiles a wave
     int cap;      // chunk kernel: rows a chunk
@@ -590,17 +711,19 @@ Plan plan_of(int64_t E, int64_t M, int64_t K, int64_t R, bool lora) {
     // Rows a group, were all groups in use equally full.
     const int64_t groups = E < R ? E : R;
     const int64_t avg = groups ? (R + groups - 1) / groups : 0;
+    p.single = R == 1 || R * 4 <= E;
     p.tiles = avg > 64;
     p.mt = avg > 160 ? 4 : 2;
     p.cap = R <= 16 || avg <= 12 ? 16 : 32;
-    p.pre = lora || R > 16;
-    p.ranges = (int)((slices_of(K) + kChunkWaves - 1) / kChunkWaves);
+    p.pre = !p.single && (lora || R > 16);
+    p.ranges = p.single ? (int)((K + kRowRangeK - 1) / kRowRangeK)
+                       : (int)((slices_of(K) + kChunkWaves - 1) / kChunkWaves);
     return p;
 }
 
 // Chunks of `most` rows that R rows in E groups can make at most.
 int64_t chunk_bound(int64_t E, int64_t R, int64_t most) {
-    const int64_t a = R / most + E;
+    const int64_t a = E == 1 ? (R + most - 1) / most : R / most + E;
     return a < R ? a : R;
 }
 
@@ -621,7 +744,7 @@ bool ragged_fits(int64_t E, int64_t M, int64_t K, int64_t T, int64_t R, bool up)
         const int64_t rowtiles = (M + (up ? 127 : 255)) / (up ? 128 : 256);
         return (T + (E * M + 15) / 16) * 256 < most && rowtiles * chunk_bound(E, R, 64 * p.mt) * 512 < most;
     }
-    return ((M + 255) / 256) * R * 256 < most && chunk_bound(E, R, p.cap) < 65536;
+    return ((M + 255) / 256) * R * 256 < most && chunk_bound(E, R, p.single ? 1 : p.cap) < 65536;
 }
 
 size_t ragged_ws_bytes(int64_t E, int64_t M, int64_t K, int64_t T, int64_t R, bool up, bool lora) {
@@ -642,6 +765,15 @@ static const void *tile_fn(bool up, bool lora) {
     if (up) return reinterpret_cast<const void *>(&ragged_tile_kernel<MT, 2, false>);
     return lora ? reinterpret_cast<const void *>(&ragged_tile_kernel<MT, 1, true>)
                 : reinterpret_cast<const void *>(&ragged_tile_kernel<MT, 1, false>);
+}
+
+static const void *row_fn(bool up, bool part, bool lora) {
+    if (up)
+        return part ? reinterpret_cast<const void *>(&ragged_row_kernel<2, true, false>)
+                    : reinterpret_cast<const void *>(&ragged_row_kernel<2, false, false>);
+    if (part) return reinterpret_cast<const void *>(&ragged_row_kernel<1, true, false>);
+    return lora ? reinterpret_cast<const void *>(&ragged_row_kernel<1, false, true>)
+                : reinterpret_cast<const void *>(&ragged_row_kernel<1, false, false>);
 }
 
 template <int NT, bool PRE>
@@ -727,15 +859,29 @@ hipError_t launch_ragged(const RaggedProduct &p, void *workspace, hipStream_t st
     }
     const bool part = pl.ranges > 1;
     a.part = part ? reinterpret_cast<float *>(w) : nullptr;
-    const int tile_rows = pl.cap == 16 ? 32 : 16;
-    const int64_t ntiles = (p.M + tile_rows - 1) / tile_rows, chunks = chunk_bound(p.E, p.R, pl.cap);
-    // Two workgroups a compute unit, the tiles dealt evenly over them.
-    int64_t wgs = 2 * compute_units() / (chunks * pl.ranges);
-    wgs = wgs < 1 ? 1 : wgs > ntiles ? ntiles : wgs;
-    const dim3 grid((unsigned)wgs, (unsigned)chunks, (unsigned)pl.ranges);
-    const void *fn = pl.cap == 16 ? pl.pre ? chunk_fn<1, true>(up, part, lora) : chunk_fn<1, false>(up, part, lora)
-                                  : pl.pre ? chunk_fn<2, true>(up, part, lora) : chunk_fn<2, false>(up, part, lora);
-    e = hipLaunchKernel(fn, grid, dim3(kChunkWaves * 64), args, 0, stream);
+    const int64_t chunks = chunk_bound(p.E, p.R, pl.single ? 1 : pl.cap);
+    // The workgroups that the compute units hold at once (two of 128 registers
+    // each, or one), the tiles dealt evenly over them.
+    const int at_once = pl.single || (pl.cap == 16 && !up && (!lora || pl.ranges > 1)) ? 2 : 1;
+    int64_t wgs = at_once * compute_units() / pl.ranges;
+    if (pl.single) {
+        const int64_t ntiles = (p.M * (up ? 2 : 1) + kRowTile - 1) / kRowTile * chunks;
+        // 4 waves a workgroup while 8 would leave compute units empty.
+        const int waves = ntiles * pl.ranges < 8 * compute_units() ? 4 : 8;
+        if (wgs * waves > ntiles) wgs = (ntiles + waves - 1) / waves;
+        if (wgs < chunks) wgs = chunks;
+        e = hipLaunchKernel(row_fn(up, part, lora), dim3((unsigned)wgs, (unsigned)pl.ranges), dim3(64 * waves), args, 0,
+                            stream);
+    } else {
+        const int tile_rows = pl.cap == 16 ? 32 : 16;
+        const int64_t ntiles = (p.M + tile_rows - 1) / tile_rows * chunks;
+        if (wgs > ntiles) wgs = ntiles;
+        if (wgs < chunks) wgs = chunks;
+        const void *fn = pl.cap == 16
+                             ? pl.pre ? chunk_fn<1, true>(up, part, lora) : chunk_fn<1, false>(up, part, lora)
+                             : pl.pre ? chunk_fn<2, true>(up, part, lora) : chunk_fn<2, false>(up, part, lora);
+        e = hipLaunchKernel(fn, dim3((unsigned)wgs, (unsigned)pl.ranges), dim3(kChunkWaves * 64), args, 0, stream);
+    }
     if (e != hipSuccess || !part) return e;
     const void *fin = up     ? reinterpret_cast<const void *>(&ragged_finish_kernel<2, false>)
                       : lora ? reinterpret_cast<const void *>(&ragged_finish_kernel<1, true>)

@@ -31,8 +31,16 @@ struct Chunk {
     int count;  // rows (0: no such chunk)
 };
 
+// Rows of group e, its offsets held to 0 .. R.
+__device__ __forceinline__ int group_rows(const int32_t *__restrict__ offsets, int E, int R, int e, int &lo) {
+    lo = 0;
+    if (e >= E) return 0;
+    lo = min(max(offsets[e], 0), R);
+    return max(min(max(offsets[e + 1], 0), R) - lo, 0);
+}
+
 // Chunk c of the groups cut into pieces of `most` rows, in order.  Every lane
-// of the wave returns the same values.  Offsets are held to 0 .. R.
+// of the wave returns the same values.
 __device__ __forceinline__ Chunk find_chunk(const int32_t *__restrict__ offsets, int E, int R, int c, int most) {
     if (!offsets) {
         const int64_t s = (int64_t)c * most;
@@ -43,12 +51,8 @@ __device__ __forceinline__ Chunk find_chunk(const int32_t *__restrict__ offsets,
     int base = 0;
     for (int e0 = 0; e0 < E; e0 += 64) {
         const int e = e0 + lane;
-        int lo = 0, hi = 0;
-        if (e < E) {
-            lo = min(max(offsets[e], 0), R);
-            hi = min(max(offsets[e + 1], 0), R);
-        }
-        const int n = max(hi - lo, 0);
+        int lo;
+        const int n = group_rows(offsets, E, R, e, lo);
         const int pieces = (n + most - 1) / most;
         int incl = pieces;
 #pragma unroll
@@ -60,16 +64,44 @@ __device__ __forceinline__ Chunk find_chunk(const int32_t *__restrict__ offsets,
         const uint64_t hit = __builtin_amdgcn_ballot_w64(c >= first && c < first + pieces);
         if (hit) {
             const int src = __builtin_ctzll(hit);
-            const int s = lo + (c - first) * most;
+            const int s = (c - first) * most;
             Chunk k;
             k.e = __builtin_amdgcn_readlane(e, src);
-            k.start = __builtin_amdgcn_readlane(s, src);
-            k.count = __builtin_amdgcn_readlane(min(most, hi - s), src);
+            k.start = __builtin_amdgcn_readlane(lo + s, src);
+            k.count = __builtin_amdgcn_readlane(min(most, n - s), src);
             return k;
         }
-        base += __shfl(incl, 63);
+        base += __builtin_amdgcn_readlane(incl, 63);
     }
     return {0, 0, 0};
+}
+
+// Number of chunks of at most `most` rows.
+__device__ __forceinline__ int count_chunks(const int32_t *__restrict__ offsets, int E, int R, int most) {
+    if (!offsets) return (R + most - 1) / most;
+    int total = 0;
+    for (int e = threadIdx.x & 63; e < E + 63; e += 64) {
+        int lo;
+        total += (group_rows(offsets, E, R, e, lo) + most - 1) / most;
+        if (e - (int)(threadIdx.x & 63) + 64 >= E) break;
+    }
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1) total += __shfl_xor(total, d);
+    return total;
+}
+
+// The share of workgroup `w` of `wgs` (at least as many as there are chunks):
+// a chunk, and the part'th of the nparts that its row tiles are dealt to.
+struct Share {
+    Chunk chunk;  // count 0: nothing
+    int part, nparts;
+};
+__device__ __forceinline__ Share find_share(const int32_t *__restrict__ offsets, int E, int R, int most, int w,
+                                            int wgs) {
+    const int n = __builtin_amdgcn_readfirstlane(count_chunks(offsets, E, R, most));
+    if (n == 0) return {{0, 0, 0}, 0, 1};
+    const int c = w % n;
+    return {find_chunk(offsets, E, R, c, most), w / n, (wgs - c - 1) / n + 1};
 }
 
 // Shift that puts a bf16 row's largest magnitude (given as its bits) into
