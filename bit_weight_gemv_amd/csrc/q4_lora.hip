@@ -32,30 +32,6 @@ struct ShrinkArgs {
 
 constexpr int64_t kTokenBytes = 32 << 20;  // adapters' bytes that tokens on their own may read
 
-// Eight bf16 of a row at column k; zeros past its end.  VEC: rows start on 16
-// bytes and have whole pieces.
-template <bool VEC>
-__device__ __forceinline__ u32x4_t row_piece(const uint16_t *row, int k, int K) {
-    u32x4_t v = {0u, 0u, 0u, 0u};
-    if constexpr (VEC) {
-        if (k < K) v = *reinterpret_cast<const u32x4_t *>(row + k);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (k + i < K) v[i >> 1] |= (uint32_t)row[k + i] << (16 * (i & 1));
-    }
-    return v;
-}
-
-__device__ __forceinline__ float dot8(const u32x4_t &x, const u32x4_t &z, float s) {
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        s = fmaf(bf16_lo(x[c]), bf16_lo(z[c]), s);
-        s = fmaf(bf16_hi(x[c]), bf16_hi(z[c]), s);
-    }
-    return s;
-}
-
 // Few tokens: a workgroup takes one token and 4 ranks, a wave a rank.  The
 // workgroups behind those write the packed product's activations as pieces.
 template <bool VEC>
@@ -64,16 +40,8 @@ __global__ __launch_bounds__(256) void lora_shrink_token_kernel(const ShrinkArgs
         write_pieces(a.X, nullptr, a.K, a.N, a.N, pieces, blockIdx.x - shrinks);
         return;
     }
-    const int n = blockIdx.x % a.N, j = blockIdx.x / a.N * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
-    const int id = a.ids[n];
-    if (id < 0 || id >= a.L || j >= a.r) return;
-    const uint16_t *x = a.X + (int64_t)n * a.K, *z = a.Z + ((int64_t)id * a.r + j) * a.pitch;
-    float s = 0.0f;
-#pragma unroll 4
-    for (int k = lane * 8; k < a.K; k += 512)
-        s = dot8(row_piece<VEC>(x, k, a.K), *reinterpret_cast<const u32x4_t *>(z + k), s);
-    s = wave_sum(s);
-    if (lane == 0) a.t[(int64_t)n * a.r + j] = s * a.scaling[id];
+    shrink_row<VEC>(a.X, a.Z, a.scaling, a.ids, a.K, a.pitch, a.r, a.L, blockIdx.x % a.N,
+                    blockIdx.x / a.N * 4 + (threadIdx.x >> 6), a.N, a.t);
 }
 
 // Many tokens: a workgroup takes 16, its 8 waves split K in 64-blocks dealt
@@ -702,7 +670,11 @@ hipError_t launch_lora(const LoraCall &c, bool bf16, void *Y, void *workspace, h
     p.bf16 = bf16;
     p.Y = Y;
     char *w = static_cast<char *>(workspace);
-    if (c.L > 0) {
+    if (c.L > 0 && ragged_shrinks(1, c.M, c.K, c.N)) {
+        p.A = c.A;
+        p.scaling = c.scaling;
+        p.t = reinterpret_cast<float *>(w);
+    } else if (c.L > 0) {
         ShrinkArgs s = {c.X,      c.A, c.scaling, c.ids, (int)c.N, (int)c.K, (int)c.K, (int)c.r, (int)c.L,
                         reinterpret_cast<float *>(w)};
         Pieces pieces = {};
@@ -710,8 +682,10 @@ hipError_t launch_lora(const LoraCall &c, bool bf16, void *Y, void *workspace, h
             pieces = pieces_at(c.K, c.N, w + round16((size_t)c.N * c.r * 4));
         const hipError_t e = launch_shrink(s, pieces, stream);
         if (e != hipSuccess) return e;
-        p.B = c.B;
         p.t = s.t;
+    }
+    if (c.L > 0) {
+        p.B = c.B;
         p.ids = c.ids;
         p.r = c.r;
         p.L = c.L;

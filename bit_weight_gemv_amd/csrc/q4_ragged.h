@@ -24,6 +24,8 @@ struct RaggedProduct {
     void *Y;
     const uint16_t *B;                  // bf16 [L][M][r], or null
     const float *t;                     // fp32 [R][r], the adapter's scaling in it
+    const uint16_t *A;                  // where ragged_shrinks holds: what t is made of
+    const float *scaling;
     const int32_t *ids;                 // [R]
     int64_t r, L;
 };
@@ -53,6 +55,8 @@ inline Pieces pieces_at(int64_t K, int64_t R, void *workspace) {
 }
 // Workgroups that write them: a wave takes a slice of two positions.
 inline int64_t pieces_blocks(int64_t K, int64_t R) { return ((K + 255) / 256 * ((R + 1) / 2) + 3) / 4; }
+// Whether the product itself makes t (written to p.t) beside its first launch.
+bool ragged_shrinks(int64_t E, int64_t M, int64_t K, int64_t R);
 bool ragged_takes_pieces(int64_t E, int64_t M, int64_t K, int64_t R, bool lora);
 
 // The current device's number of compute units (256 where it cannot be read).

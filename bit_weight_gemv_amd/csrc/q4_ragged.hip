@@ -34,6 +34,10 @@ struct Args {
     const float *t;
     const int32_t *ids;
     int r, L;
+    const uint16_t *A;         // row kernel, beside adapters: what t is made of, by the workgroups from `wgs` on
+    const float *scaling;
+    float *tout;
+    int wgs;
 };
 
 __device__ __forceinline__ int source_row(const Args &a, int p) {
@@ -329,9 +333,19 @@ __global__ __launch_bounds__(kChunkWaves * 64, NT * MATS == 1 && !LORA ? 4 : 2) 
 constexpr int kRowTile = 8;
 constexpr int kRowRangeK = 2048;
 
+// Beside adapters (LORA) the last workgroups make t = s A x meanwhile, a wave
+// a rank, and the launch that adds the planes has both.
 template <int MATS, bool PART, bool LORA>
 __global__ __launch_bounds__(512, 4) void ragged_row_kernel(const Args a) {
     constexpr int ROWS = kRowTile / MATS;
+    static_assert(!LORA || PART, "t is made by the same launch");
+    if constexpr (LORA) {
+        if ((int)blockIdx.x >= a.wgs) {
+            const int n = ((int)blockIdx.x - a.wgs) * ((int)blockDim.x >> 6) + ((int)threadIdx.x >> 6);
+            if (blockIdx.y == 0) shrink_row(a.X, a.A, a.scaling, a.ids, a.K, a.K, a.r, a.L, n / a.r, n % a.r, a.R, a.tout);
+            return;
+        }
+    }
     __shared__ uint32_t lut[kLutDwords];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int waves = blockDim.x >> 6;
@@ -341,7 +355,7 @@ __global__ __launch_bounds__(512, 4) void ragged_row_kernel(const Args a) {
     const bool live = first < 2 * nb;
     const int piece = min(first, 2 * nb - 1);
     const int ntiles = (a.M * MATS + kRowTile - 1) / kRowTile;
-    const Share share = find_share(a.offsets, a.E, a.R, 1, blockIdx.x, gridDim.x);
+    const Share share = find_share(a.offsets, a.E, a.R, 1, blockIdx.x, LORA ? a.wgs : (int)gridDim.x);
     const Chunk ck = share.chunk;
     int t = share.part * waves + wave;
     const int tstep = share.nparts * waves;
@@ -378,16 +392,11 @@ __global__ __launch_bounds__(512, 4) void ragged_row_kernel(const Args a) {
     for (int s = 0; s < 4; ++s)
 #pragma unroll
         for (int c = 0; c < 4; ++c) x[4 * s + c] = __builtin_bit_cast(half2_t, bf16x2_to_f16x2(xr[s][c], f));
-    int id = -1;
-    if constexpr (LORA) id = a.ids[p];
     __syncthreads();
 
     const uint32_t laneoff = (uint32_t)lane << 2;
     for (; t < ntiles; t += tstep) {
         const int mo = t * ROWS + (lane & (ROWS - 1));
-        float term = 0.0f;
-        if constexpr (LORA)
-            if (lane < ROWS && mo < a.M) term = adapter_term(a, id, p, mo);
         float v[kRowTile];
 #pragma unroll
         for (int r = 0; r < kRowTile; ++r) {
@@ -411,7 +420,7 @@ __global__ __launch_bounds__(512, 4) void ragged_row_kernel(const Args a) {
             if (lane < kRowTile && mo < a.M) a.part[((int64_t)q * a.ranges + z) * a.R * a.M + at] = total;
         } else {
             if constexpr (MATS == 2) total = swiglu(total, __shfl_xor(total, ROWS));
-            if (lane < ROWS && mo < a.M) store_out(a.Y, a.bf16, at, total + term);
+            if (lane < ROWS && mo < a.M) store_out(a.Y, a.bf16, at, total);
         }
     }
 }
@@ -752,13 +761,15 @@ size_t ragged_ws_bytes(int64_t E, int64_t M, int64_t K, int64_t T, int64_t R, bo
     const size_t mats = up ? 2 : 1;
     if (p.tiles)
         return round16((size_t)T * K * 2) + round16((size_t)T * 4) + mats * round16((size_t)E * M);
-    return (p.pre ? pieces_bytes(K, R) : 0) + (p.ranges > 1 ? mats * p.ranges * (size_t)R * M * 4 : 0);
+    return (p.pre ? pieces_bytes(K, R) : 0) + (p.ranges > 1 || (p.single && lora) ? mats * p.ranges * (size_t)R * M * 4 : 0);
 }
 
 bool ragged_takes_pieces(int64_t E, int64_t M, int64_t K, int64_t R, bool lora) {
     const Plan p = plan_of(E, M, K, R, lora);
     return !p.tiles && p.pre;
 }
+
+bool ragged_shrinks(int64_t E, int64_t M, int64_t K, int64_t R) { return plan_of(E, M, K, R, true).single; }
 
 template <int MT>
 static const void *tile_fn(bool up, bool lora) {
@@ -771,8 +782,8 @@ static const void *row_fn(bool up, bool part, bool lora) {
     if (up)
         return part ? reinterpret_cast<const void *>(&ragged_row_kernel<2, true, false>)
                     : reinterpret_cast<const void *>(&ragged_row_kernel<2, false, false>);
-    if (part) return reinterpret_cast<const void *>(&ragged_row_kernel<1, true, false>);
-    return lora ? reinterpret_cast<const void *>(&ragged_row_kernel<1, false, true>)
+    if (lora) return reinterpret_cast<const void *>(&ragged_row_kernel<1, true, true>);
+    return part ? reinterpret_cast<const void *>(&ragged_row_kernel<1, true, false>)
                 : reinterpret_cast<const void *>(&ragged_row_kernel<1, false, false>);
 }
 
@@ -810,6 +821,9 @@ hipError_t launch_ragged(const RaggedProduct &p, void *workspace, hipStream_t st
     a.ids = p.ids;
     a.r = (int)p.r;
     a.L = (int)p.L;
+    a.A = p.A;
+    a.scaling = p.scaling;
+    a.tout = const_cast<float *>(p.t);
     void *args[] = {&a};
     if (pl.tiles) {
         char *w = static_cast<char *>(workspace);
@@ -857,7 +871,7 @@ hipError_t launch_ragged(const RaggedProduct &p, void *workspace, hipStream_t st
         a.X = pc.x16;
         a.xexp = pc.exps;
     }
-    const bool part = pl.ranges > 1;
+    const bool part = pl.ranges > 1 || (pl.single && lora);
     a.part = part ? reinterpret_cast<float *>(w) : nullptr;
     const int64_t chunks = chunk_bound(p.E, p.R, pl.single ? 1 : pl.cap);
     // The workgroups that the compute units hold at once (two of 128 registers
@@ -870,6 +884,8 @@ hipError_t launch_ragged(const RaggedProduct &p, void *workspace, hipStream_t st
         const int waves = ntiles * pl.ranges < 8 * compute_units() ? 4 : 8;
         if (wgs * waves > ntiles) wgs = (ntiles + waves - 1) / waves;
         if (wgs < chunks) wgs = chunks;
+        a.wgs = (int)wgs;
+        if (lora) wgs += (p.R * p.r + waves - 1) / waves;
         e = hipLaunchKernel(row_fn(up, part, lora), dim3((unsigned)wgs, (unsigned)pl.ranges), dim3(64 * waves), args, 0,
                             stream);
     } else {

@@ -149,6 +149,49 @@ __device__ __forceinline__ void write_pieces(const uint16_t *__restrict__ X, con
     }
 }
 
+// Eight bf16 of a row at column k; zeros past its end.  VEC: rows start on 16
+// bytes and have whole pieces.
+template <bool VEC>
+__device__ __forceinline__ u32x4_t row_piece(const uint16_t *row, int k, int K) {
+    u32x4_t v = {0u, 0u, 0u, 0u};
+    if constexpr (VEC) {
+        if (k < K) v = *reinterpret_cast<const u32x4_t *>(row + k);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (k + i < K) v[i >> 1] |= (uint32_t)row[k + i] << (16 * (i & 1));
+    }
+    return v;
+}
+
+__device__ __forceinline__ float dot8(const u32x4_t &x, const u32x4_t &z, float s) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        s = fmaf(bf16_lo(x[c]), bf16_lo(z[c]), s);
+        s = fmaf(bf16_hi(x[c]), bf16_hi(z[c]), s);
+    }
+    return s;
+}
+
+// t[n][j] = scaling[a] * sum_k Z[a][j][k] x[n][k], a = ids[n], by one wave
+// (nothing where the token has no adapter).
+template <bool VEC = true>
+__device__ __forceinline__ void shrink_row(const uint16_t *X, const uint16_t *Z, const float *scaling,
+                                           const int32_t *ids, int K, int pitch, int r, int L, int n, int j, int N,
+                                           float *t) {
+    if (n >= N || j >= r) return;
+    const int id = ids[n];
+    if (id < 0 || id >= L) return;
+    const int lane = threadIdx.x & 63;
+    const uint16_t *x = X + (int64_t)n * K, *z = Z + ((int64_t)id * r + j) * pitch;
+    float s = 0.0f;
+#pragma unroll 4
+    for (int k = lane * 8; k < K; k += 512)
+        s = dot8(row_piece<VEC>(x, k, K), *reinterpret_cast<const u32x4_t *>(z + k), s);
+    s = wave_sum(s);
+    if (lane == 0) t[(int64_t)n * r + j] = s * scaling[id];
+}
+
 // Eight weights of four code bytes, as fp16 table entries.
 __device__ __forceinline__ void lut8(const uint32_t *lut, uint32_t word, uint32_t laneoff, half2_t (&w)[4]) {
     w[0] = lut_pair<0>(lut, word, laneoff);

@@ -1,11 +1,9 @@
 // q4_route.hip -- which experts a token goes to, the order that groups the
 // tokens by expert, and the weighted sum of the experts' outputs.
 //
-// Top k: one wave a token, the logits spread over its lanes as bits in an
-// order that compares as unsigned; k times the largest of them (maxima over
-// lanes by DPP) goes to the lowest index that holds it (the first lane of the
-// first ballot that is not empty).  The next token's logits are on their way
-// meanwhile.
+// Top k: 16 lanes a token (a wave, above 256 experts), the logits spread over
+// them as bits in an order that compares as unsigned; k times the largest of
+// them (maxima over lanes by DPP) goes to the lowest index that holds it.
 //
 // Grouping is a counting sort that keeps the slots' order: workgroups take
 // consecutive runs of slots; the first launch leaves each run's count of
@@ -27,14 +25,16 @@ namespace {
 constexpr int kRouteThreads = 512;
 constexpr int kRouteWaves = kRouteThreads / 64;
 constexpr int kMaxRuns = 256;    // runs of the counting sort at most
-constexpr int kRunTokens = 64;   // tokens of a run at least (slots, for a plain sort: 512)
+constexpr int kRunTokens = 32;   // tokens of a run at least (slots, for a plain sort: 512)
+
+__host__ __device__ constexpr int hist_pitch(int64_t E) { return (int)(E + 3) & ~3; }
 
 struct RouteArgs {
     const void *logits;
     int bf16, T, E, k, all;
     int32_t *experts;
     float *weights;
-    int32_t *hist;    // [runs][E], or null: one run, sorted in the same launch
+    int32_t *hist;    // [runs][hist_pitch(E)], or null: one run, sorted in the same launch
     int run;          // tokens of a run
     int32_t *offsets, *rows, *pos;
 };
@@ -42,7 +42,7 @@ struct RouteArgs {
 struct SortArgs {
     const int32_t *bins;
     int slots, E, per, run;  // run: slots of a run
-    const int32_t *hist;     // [runs][E], or null: one run
+    const int32_t *hist;     // [runs][hist_pitch(E)], or null: one run
     int32_t *offsets, *rows, *pos;
 };
 
@@ -58,66 +58,75 @@ __device__ __forceinline__ float value_of(uint32_t order) {
     return __builtin_bit_cast(float, order & 0x80000000u ? order & 0x7FFFFFFFu : ~order);
 }
 
-// This lane's logits of token t, in the order above (0: no such expert).
-template <int EPL>
-__device__ __forceinline__ void load_logits(const RouteArgs &a, int t, uint32_t (&o)[EPL]) {
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-        const int e = (threadIdx.x & 63) + 64 * i;
-        o[i] = 0;
-        if (e < a.E) {
-            const int64_t at = (int64_t)t * a.E + e;
-            o[i] = order_of(a.bf16 ? bf16_f32(static_cast<const uint16_t *>(a.logits)[at])
-                                   : static_cast<const float *>(a.logits)[at]);
-        }
-    }
+__device__ __forceinline__ uint32_t load_logit(const RouteArgs &a, int t, int e) {
+    if (t >= a.T || e >= a.E) return 0;  // below every logit's
+    const int64_t at = (int64_t)t * a.E + e;
+    return order_of(a.bf16 ? bf16_f32(static_cast<const uint16_t *>(a.logits)[at])
+                           : static_cast<const float *>(a.logits)[at]);
 }
 
-// The choice of token t by this wave.
-template <int EPL>
-__device__ __forceinline__ void choose(const RouteArgs &a, int t, uint32_t (&o)[EPL]) {
-    const int lane = threadIdx.x & 63;
+// Reductions over the LANES (16 or 64) lanes of a token; every one gets it.
+template <int LANES>
+__device__ __forceinline__ uint32_t lanes_max(uint32_t v) {
+    if constexpr (LANES == 64) return wave_max_u32(v);
+    v = dpp_max_u32<kDppQuadXor1>(v);
+    v = dpp_max_u32<kDppQuadXor2>(v);
+    v = dpp_max_u32<kDppRowHalfMirror>(v);
+    return dpp_max_u32<kDppRowMirror>(v);
+}
+template <int LANES>
+__device__ __forceinline__ float lanes_sum(float v) {
+    if constexpr (LANES == 64) return wave_sum(v);
+    v += dpp_f<kDppQuadXor1>(v);
+    v += dpp_f<kDppQuadXor2>(v);
+    v += dpp_f<kDppRowHalfMirror>(v);
+    return v + dpp_f<kDppRowMirror>(v);
+}
+
+// The choice of token t by LANES lanes, which hold logits e = lane + LANES i.
+// The lowest index among equals is the largest complement of an index.
+template <int EPL, int LANES>
+__device__ __forceinline__ void choose(const RouteArgs &a, int t, const uint32_t (&o)[EPL]) {
+    const int lane = threadIdx.x & (LANES - 1);
     uint32_t key[EPL];
 #pragma unroll
     for (int i = 0; i < EPL; ++i) key[i] = o[i];
-    float largest = 0.0f, total = 0.0f, mine = 0.0f;
+    float mine = 0.0f, largest = 0.0f;
     int chosen = 0;
     for (int j = 0; j < a.k; ++j) {
         uint32_t best = key[0];
 #pragma unroll
         for (int i = 1; i < EPL; ++i) best = max(best, key[i]);
-        best = wave_max_u32(best);
-        int at = -1;  // the lowest index that holds it
+        best = lanes_max<LANES>(best);
+        uint32_t index = 0;
 #pragma unroll
-        for (int i = 0; i < EPL; ++i) {
-            const uint64_t has = __builtin_amdgcn_ballot_w64(key[i] == best);
-            if (at < 0 && has) {
-                const int l = __builtin_ctzll(has);
-                at = 64 * i + l;
-                if (lane == l) key[i] = 0;
-            }
-        }
+        for (int i = EPL - 1; i >= 0; --i)
+            if (key[i] == best) index = ~(uint32_t)(lane + LANES * i);
+        const int at = (int)~lanes_max<LANES>(index);
+#pragma unroll
+        for (int i = 0; i < EPL; ++i)
+            if (at == lane + LANES * i) key[i] = 0;
         const float v = value_of(best);
         if (j == 0) largest = v;
-        const float p = v == largest ? 1.0f : expf(v - largest);
-        total += p;
         if (lane == j) {
-            mine = p;
+            mine = v;
             chosen = at;
         }
     }
+    const float p = lane >= a.k ? 0.0f : mine == largest ? 1.0f : expf(mine - largest);
+    float s = p;
     if (a.all) {
-        float s = 0.0f;
+        s = 0.0f;
 #pragma unroll
         for (int i = 0; i < EPL; ++i) {
             const float v = value_of(o[i]);
             if (o[i]) s += v == largest ? 1.0f : expf(v - largest);
         }
-        total = wave_sum(s);
     }
-    if (lane < a.k) {
+    const float total = lanes_sum<LANES>(s);
+    if (lane < a.k && t < a.T) {
         a.experts[(int64_t)t * a.k + lane] = chosen;
-        a.weights[(int64_t)t * a.k + lane] = largest == -__builtin_inff() ? 0.0f : mine / total;
+        a.weights[(int64_t)t * a.k + lane] = largest == -__builtin_inff() ? 0.0f : p / total;
     }
 }
 
@@ -192,21 +201,19 @@ __device__ __forceinline__ void first_positions(int E, int slots, const int32_t 
     (void)slots;
 }
 
-template <int EPL>
+template <int EPL, int LANES>
 __global__ __launch_bounds__(kRouteThreads) void route_kernel(const RouteArgs a) {
     __shared__ int32_t total[Q4_MAX_EXPERTS + 1], next[Q4_MAX_EXPERTS + 1], sum[kRouteWaves];
     const int t0 = blockIdx.x * a.run, t1 = min(t0 + a.run, a.T);
     for (int e = threadIdx.x; e <= a.E; e += kRouteThreads) total[e] = next[e] = 0;
-    {
-        uint32_t now[EPL], next_o[EPL];
-        int t = t0 + (threadIdx.x >> 6);
-        if (t < t1) load_logits<EPL>(a, t, now);
-        for (; t < t1; t += kRouteWaves) {
-            if (t + kRouteWaves < t1) load_logits<EPL>(a, t + kRouteWaves, next_o);
-            choose<EPL>(a, t, now);
+    for (int t = t0; t < t1; t += kRouteThreads / LANES) {
+        const int mine = t + (int)threadIdx.x / LANES;
+        if (mine - (int)(threadIdx.x & 63) / LANES >= t1) continue;  // the whole wave's are past the run
+        uint32_t o[EPL];
+        const int lt = mine < t1 ? mine : a.T;                       // (a.T: no token)
 #pragma unroll
-            for (int i = 0; i < EPL; ++i) now[i] = next_o[i];
-        }
+        for (int i = 0; i < EPL; ++i) o[i] = load_logit(a, lt, (threadIdx.x & (LANES - 1)) + LANES * i);
+        choose<EPL, LANES>(a, lt, o);
     }
     __threadfence_block();
     __syncthreads();
@@ -214,7 +221,8 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(const RouteArgs a)
     for (int s = s0 + threadIdx.x; s < s1; s += kRouteThreads) atomicAdd(&total[a.experts[s]], 1);
     __syncthreads();
     if (a.hist) {
-        for (int e = threadIdx.x; e < a.E; e += kRouteThreads) a.hist[(int64_t)blockIdx.x * a.E + e] = total[e];
+        for (int e = threadIdx.x; e < hist_pitch(a.E); e += kRouteThreads)
+            a.hist[(int64_t)blockIdx.x * hist_pitch(a.E) + e] = e < a.E ? total[e] : 0;
         return;
     }
     first_positions(a.E, s1, total, next, sum, a.offsets, true);
@@ -232,7 +240,8 @@ __global__ __launch_bounds__(kRouteThreads) void sort_count_kernel(const SortArg
         if (e >= 0 && e < a.E) atomicAdd(&total[e], 1);
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < a.E; e += kRouteThreads) hist[(int64_t)blockIdx.x * a.E + e] = total[e];
+    for (int e = threadIdx.x; e < hist_pitch(a.E); e += kRouteThreads)
+        hist[(int64_t)blockIdx.x * hist_pitch(a.E) + e] = e < a.E ? total[e] : 0;
 }
 
 __global__ __launch_bounds__(kRouteThreads) void sort_kernel(const SortArgs a) {
@@ -241,22 +250,33 @@ __global__ __launch_bounds__(kRouteThreads) void sort_kernel(const SortArgs a) {
     for (int e = threadIdx.x; e <= a.E; e += kRouteThreads) total[e] = next[e] = 0;
     __syncthreads();
     if (a.hist) {
-        // Threads beyond the bins take runs of their own.
-        const int parts = a.E < kRouteThreads ? kRouteThreads / a.E : 1;
-        for (int i = threadIdx.x; i < a.E * parts; i += kRouteThreads) {
-            const int e = i % a.E;
-            int before = 0, all = 0;
+        // A thread adds up four neighbouring bins of every parts'th run.
+        const int quads = hist_pitch(a.E) / 4, parts = max(kRouteThreads / quads, 1);
+        const int4 *h = reinterpret_cast<const int4 *>(a.hist);
+        int sum_before = 0;
+        for (int i = threadIdx.x; i < quads * parts; i += kRouteThreads) {
+            const int quad = i % quads;
+            int4 before = make_int4(0, 0, 0, 0), all = make_int4(0, 0, 0, 0);
 #pragma unroll 8
-            for (int b = i / a.E; b < (int)gridDim.x; b += parts) {
-                const int n = a.hist[(int64_t)b * a.E + e];
-                if (b < (int)blockIdx.x) before += n;
-                all += n;
+            for (int b = i / quads; b < (int)gridDim.x; b += parts) {
+                const int4 n = h[b * quads + quad];
+                const int w = b < (int)blockIdx.x ? 1 : 0;
+                before.x += n.x * w, before.y += n.y * w, before.z += n.z * w, before.w += n.w * w;
+                all.x += n.x, all.y += n.y, all.z += n.z, all.w += n.w;
             }
-            atomicAdd(&total[e], all);
-            atomicAdd(&next[e], before);
-            // Slots of no bin before this run: those that the bins do not count.
-            atomicAdd(&total[a.E], before);
+            const int be[4] = {before.x, before.y, before.z, before.w}, al[4] = {all.x, all.y, all.z, all.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if (4 * quad + e >= a.E) break;
+                atomicAdd(&total[4 * quad + e], al[e]);
+                atomicAdd(&next[4 * quad + e], be[e]);
+                sum_before += be[e];
+            }
         }
+        // Slots of no bin before this run: those that the bins do not count.
+#pragma unroll
+        for (int d = 32; d >= 1; d >>= 1) sum_before += __shfl_xor(sum_before, d);
+        if ((threadIdx.x & 63) == 0) atomicAdd(&total[a.E], sum_before);
         __syncthreads();
         if (threadIdx.x == 0) next[a.E] = s0 - total[a.E];
         __syncthreads();
@@ -343,18 +363,19 @@ int64_t run_of(int64_t n, int64_t least) {
 }
 
 const void *route_fn(int64_t E) {
-    if (E <= 64) return reinterpret_cast<const void *>(&route_kernel<1>);
-    if (E <= 128) return reinterpret_cast<const void *>(&route_kernel<2>);
-    if (E <= 256) return reinterpret_cast<const void *>(&route_kernel<4>);
-    if (E <= 512) return reinterpret_cast<const void *>(&route_kernel<8>);
-    return reinterpret_cast<const void *>(&route_kernel<16>);
+    if (E <= 16) return reinterpret_cast<const void *>(&route_kernel<1, 16>);
+    if (E <= 64) return reinterpret_cast<const void *>(&route_kernel<4, 16>);
+    if (E <= 128) return reinterpret_cast<const void *>(&route_kernel<8, 16>);
+    if (E <= 256) return reinterpret_cast<const void *>(&route_kernel<16, 16>);
+    if (E <= 512) return reinterpret_cast<const void *>(&route_kernel<8, 64>);
+    return reinterpret_cast<const void *>(&route_kernel<16, 64>);
 }
 
 }  // namespace
 
 size_t sort_ws_bytes(int64_t slots, int64_t E) {
     const int64_t run = run_of(slots, kRouteThreads), runs = (slots + run - 1) / run;
-    return runs > 1 ? (size_t)runs * E * 4 : 0;
+    return runs > 1 ? (size_t)runs * hist_pitch(E) * 4 : 0;
 }
 
 hipError_t launch_sort(const int32_t *bins, int64_t slots, int64_t E, int64_t per, int32_t *offsets, int32_t *rows,
@@ -386,7 +407,7 @@ hipError_t launch_sort(const int32_t *bins, int64_t slots, int64_t E, int64_t pe
 size_t route_ws_bytes(int64_t T, int64_t E, int64_t k) {
     const int64_t run = run_of(T, kRunTokens), runs = (T + run - 1) / run;
     (void)k;
-    return runs > 1 ? (size_t)runs * E * 4 : 0;
+    return runs > 1 ? (size_t)runs * hist_pitch(E) * 4 : 0;
 }
 
 hipError_t launch_route(const void *logits, bool bf16, int64_t T, int64_t E, int64_t k, bool all, int32_t *experts,

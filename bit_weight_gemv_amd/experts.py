@@ -32,6 +32,7 @@ _ARGS = {
 }
 
 
+@_base.sizes
 def q4_route_topk_ws_bytes(T: int, E: int, k: int) -> int:
     """Bytes of scratch q4_route_topk needs for this shape (0: none)."""
     return int(_base.function("q4_route_topk_ws_bytes", _ARGS)(T, E, k))
@@ -80,6 +81,7 @@ def _planes(codes, scales, what):
     return E, M, K
 
 
+@_base.sizes
 def q4_gemm_grouped_ws_bytes(E: int, M: int, K: int, T: int, R: int, has_up: bool) -> int:
     """Bytes of scratch q4_gemm_grouped needs for this shape (0: none)."""
     return int(_base.function("q4_gemm_grouped_ws_bytes", _ARGS)(E, M, K, T, R, int(bool(has_up))))

@@ -26,11 +26,13 @@ _ARGS = {
 }
 
 
+@_base.sizes
 def q4_gemm_lora_ws_bytes(M: int, K: int, N: int, r: int, L: int) -> int:
     """Bytes of scratch q4_gemm_lora needs for this shape (0: none)."""
     return int(_base.function("q4_gemm_lora_ws_bytes", _ARGS)(M, K, N, r, L))
 
 
+@_base.sizes
 def q4_gemm_lora_backward_ws_bytes(M: int, K: int, N: int, r: int, L: int) -> int:
     """Bytes of scratch q4_gemm_lora_backward needs for this shape."""
     return int(_base.function("q4_gemm_lora_backward_ws_bytes", _ARGS)(M, K, N, r, L))

@@ -62,7 +62,8 @@ def test_route_refusals(q4):
     p[2] = p[0] + 124                   # weights over the last logit
     assert _route(q4, p=p) == q4.Q4_ERR_OVERLAP
     need = q4.q4_route_topk_ws_bytes(65, 8, 2)
-    assert q4.q4_route_topk_ws_bytes(64, 8, 2) == 0 and need == 2 * 8 * 4
+    assert q4.q4_route_topk_ws_bytes(32, 8, 2) == 0 and need == 3 * 8 * 4
+    assert q4.q4_route_topk_ws_bytes(65, 9, 2) == 3 * 12 * 4
     assert _route(q4, T=65) == q4.Q4_ERR_WORKSPACE
     assert _route(q4, T=65, ws=P(9), nb=need - 1) == q4.Q4_ERR_WORKSPACE
     assert _route(q4, T=65, ws=P(9) + 4, nb=need) == q4.Q4_ERR_ALIGN
