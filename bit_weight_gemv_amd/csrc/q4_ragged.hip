@@ -518,27 +518,49 @@ constexpr int kTileWaves = 8;
 
 // A workgroup computes 64 MT rows of X (2 waves of MT tiles of 32) by 256
 // packed rows (4 waves of two 32-row tiles; with MATS == 2 each wave's tiles
-// are the gate's and the up's same 32 rows).
+// are the gate's and the up's same 32 rows), 64 k a step.  X goes through LDS
+// in two buffers; each wave looks its own weights up and multiplies them by
+// the block's scale in fp16.
+//
+// The matrix cores bound it where nothing of a step is waited for: a step's
+// rows of X go from registers to the free buffer while the step before it is
+// multiplied, the loads of the step after take their place, and the lookups of
+// a quarter step (16 k a lane group) are under way during the products of the
+// quarter before, the last quarter's across the barrier.
+template <int MT, bool LORA>
+struct TileShared {
+    uint32_t lut[kLutDwords];  // first: its address is 0, and a lookup's the code byte and the lane
+    u32x4_t xs[2][64 * MT * 8];
+    int xe[64 * MT];
+    int sid[LORA ? 64 * MT : 1];
+};
+
 template <int MT, int MATS, bool LORA>
 __global__ __launch_bounds__(kTileWaves * 64) void ragged_tile_kernel(const Args a) {
     constexpr int TM = 64 * MT;
     constexpr int kRowsWg = MATS == 2 ? 128 : 256;
     constexpr int kPieces = TM * 8 / (kTileWaves * 64);  // 16-byte pieces of X a thread stages
-    __shared__ uint32_t lut[kLutDwords];
-    __shared__ uint4 xs[2][TM * 8];
-    __shared__ int xe[TM];
-    __shared__ int sid[LORA ? TM : 1];
+    __shared__ TileShared<MT, LORA> sm;
+    int (&xe)[TM] = sm.xe;
+    auto &sid = sm.sid;
+    const uint32_t *lut = sm.lut;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int col = lane & 31, g = lane >> 5;
     const int wt = wave & 1, wr = wave >> 1;
 
-    const int c = blockIdx.x / a.rowtiles, rt0 = blockIdx.x % a.rowtiles;
-    const Chunk ck = find_chunk(a.offsets, a.E, a.R, c, TM);
-    if (ck.count == 0) return;
+    // Workgroups go round the 8 XCDs; each XCD takes a run of the (chunk, row
+    // tile) pairs, so that a chunk's rows stay in one L2.
+    const int total = __builtin_amdgcn_readfirstlane(count_chunks(a.offsets, a.E, a.R, TM)) * a.rowtiles;
+    const int each = (total + 7) >> 3, at = (int)(blockIdx.x & 7) * each + (int)(blockIdx.x >> 3);
+    if ((int)(blockIdx.x >> 3) >= each || at >= total) return;
+    const int rt0 = at % a.rowtiles;
+    const Chunk ck = find_chunk(a.offsets, a.E, a.R, at / a.rowtiles, TM);
 
+    // A row outside [0, T) reads row 0 and is put out as zeros (kNoRow).
+    constexpr int kNoRow = -1000000;
     for (int i = threadIdx.x; i < TM; i += kTileWaves * 64) {
         const int row = i < ck.count ? source_row(a, ck.start + i) : -1;
-        xe[i] = row >= 0 ? a.xexp[row] : 0;
+        xe[i] = row >= 0 ? a.xexp[row] : kNoRow;
         if constexpr (LORA) {
             const int id = i < ck.count ? a.ids[ck.start + i] : -1;
             sid[i] = id >= 0 && id < a.L ? id : -1;
@@ -546,13 +568,13 @@ __global__ __launch_bounds__(kTileWaves * 64) void ragged_tile_kernel(const Args
     }
     // Staging of X: piece j of this thread is row threadIdx / 8 + 64 j, slot
     // threadIdx % 8, which holds the row's 16-byte piece slot ^ (row % 8).
-    const uint4 *xsrc[kPieces];
+    const u32x4_t *xsrc[kPieces];
 #pragma unroll
     for (int j = 0; j < kPieces; ++j) {
         const int i = (threadIdx.x >> 3) + 64 * j;
-        const int row = i < ck.count ? source_row(a, ck.start + i) : -1;
+        const int row = max(source_row(a, ck.start + min(i, ck.count - 1)), 0);
         const int piece = (threadIdx.x & 7) ^ (i & 7);
-        xsrc[j] = row >= 0 ? reinterpret_cast<const uint4 *>(a.X + (int64_t)row * a.K) + piece : nullptr;
+        xsrc[j] = reinterpret_cast<const u32x4_t *>(a.X + (int64_t)row * a.K) + piece;
     }
 
     int m[2];
@@ -570,20 +592,33 @@ __global__ __launch_bounds__(kTileWaves * 64) void ragged_tile_kernel(const Args
         e[q] = a.rowexp[mat][mrow];
     }
 
-    uint4 xv[kPieces];
-    u32x4_t cw[2];
-    uint32_t sv[2];
-    auto load = [&](int b) {
+    // Codes and scales come for two steps at once (a row's 64 neighbouring
+    // bytes): those of the steps at hand, and of the two behind them.
+    u32x4_t xv[kPieces], cw[2][2], cn[2][2];
+    uint32_t sv[2][2], sn[2][2];
+    auto load_x = [&](int b) {
 #pragma unroll
-        for (int j = 0; j < kPieces; ++j) xv[j] = xsrc[j] ? xsrc[j][8 * b] : make_uint4(0, 0, 0, 0);
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            cw[q] = csrc[q][2 * b];
-            sv[q] = ssrc[q][b];
-        }
+        for (int j = 0; j < kPieces; ++j) xv[j] = __builtin_nontemporal_load(xsrc[j] + 8 * b);  // (read once)
     };
-    load(0);
-    fill_lut(lut);
+    auto load_codes = [&](int b, u32x4_t (&cd)[2][2], uint32_t (&sd)[2][2]) {
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                cd[h][q] = csrc[q][2 * min(b + h, nb - 1)];
+                sd[h][q] = ssrc[q][min(b + h, nb - 1)];
+            }
+    };
+    auto stage = [&](int b) {
+        u32x4_t *buf = sm.xs[b & 1];
+#pragma unroll
+        for (int j = 0; j < kPieces; ++j) buf[threadIdx.x + 512 * j] = xv[j];
+    };
+    load_x(0);
+    load_codes(0, cw, sv);
+    fill_lut(sm.lut);
+    stage(0);
+    load_x(min(1, nb - 1));
 
     float16_t acc[MT][2];
 #pragma unroll
@@ -592,49 +627,75 @@ __global__ __launch_bounds__(kTileWaves * 64) void ragged_tile_kernel(const Args
         for (int q = 0; q < 2; ++q) acc[i][q] = float16_t{};
     const uint32_t laneoff = (uint32_t)lane << 2;
 
-    for (int b = 0; b < nb; ++b) {
-        uint4 *buf = xs[b & 1];
+    // The weights of a quarter step: lookups, then the scale.
+    half2_t raw[2][4];
+    half2_t s2[2];
+    auto look = [&](const u32x4_t (&cd)[2], int s) {
 #pragma unroll
-        for (int j = 0; j < kPieces; ++j) buf[threadIdx.x + 512 * j] = xv[j];
-        __syncthreads();
-        u32x4_t cc[2];
-        half2_t s2[2];
+        for (int q = 0; q < 2; ++q) lut8(lut, cd[q][s], laneoff, raw[q]);
+    };
+    auto scale = [&](const uint32_t (&sd)[2]) {
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
-            cc[q] = cw[q];
-            const _Float16 h = (_Float16)ldexpf(f16_bits_to_f32(sv[q]), 14 - e[q]);
+            const _Float16 h = (_Float16)ldexpf(f16_bits_to_f32(sd[q]), 14 - e[q]);
             s2[q] = half2_t{h, h};
         }
-        if (b + 1 < nb) load(b + 1);
+    };
+    // Step b, whose first lookups were made by the step before; it makes those
+    // of the next, with codes cnext and scales snext.
+    auto step = [&](int b, const u32x4_t (&cd)[2], const u32x4_t (&cnext)[2], const uint32_t (&snext)[2]) {
+        const u32x4_t *buf = sm.xs[b & 1];
+        // (The last steps stage and load what is there already.)
+        stage(b + 1);
+        load_x(min(b + 2, nb - 1));
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
             half8_t w[2];
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-                half2_t v[4];
-                lut8(lut, cc[q][s], laneoff, v);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) v[i] *= s2[q];
-                w[q] = join8(v);
+                for (int i = 0; i < 4; ++i) raw[q][i] *= s2[q];
+                w[q] = join8(raw[q]);
+            }
+            if (s < 3) {
+                look(cd, s + 1);
+            } else {
+                scale(snext);
+                look(cnext, 0);
             }
 #pragma unroll
             for (int i = 0; i < MT; ++i) {
                 const int row = wt * 32 * MT + 32 * i + col;
-                const uint4 xr = buf[row * 8 + ((4 * g + s) ^ (row & 7))];
-                const half8_t xa = __builtin_bit_cast(half8_t, xr);
+                const half8_t xa = __builtin_bit_cast(half8_t, buf[row * 8 + ((4 * g + s) ^ (row & 7))]);
                 acc[i][0] = __builtin_amdgcn_mfma_f32_32x32x16_f16(xa, w[0], acc[i][0], 0, 0, 0);
                 acc[i][1] = __builtin_amdgcn_mfma_f32_32x32x16_f16(xa, w[1], acc[i][1], 0, 0, 0);
             }
         }
+        __syncthreads();
+    };
+    __syncthreads();
+    scale(sv[0]);
+    look(cw[0], 0);
+    for (int b = 0; b < nb; b += 2) {
+        load_codes(b + 2, cn, sn);
+        step(b, cw[0], cw[1], sv[1]);
+        if (b + 1 < nb) step(b + 1, cw[1], cn[0], sn[0]);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                cw[h][q] = cn[h][q];
+                sv[h][q] = sn[h][q];
+            }
     }
 
 #pragma unroll
     for (int i = 0; i < MT; ++i)
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
-            const int x = xe[wt * 32 * MT + 32 * i + tile_row(j, lane)] - 14;
-            acc[i][0][j] = ldexpf(acc[i][0][j], x + e[0]);
-            acc[i][1][j] = ldexpf(acc[i][1][j], x + e[1]);
+            const int x = xe[wt * 32 * MT + 32 * i + tile_row(j, lane)];
+            acc[i][0][j] = x == kNoRow ? 0.0f : ldexpf(acc[i][0][j], x - 14 + e[0]);
+            acc[i][1][j] = x == kNoRow ? 0.0f : ldexpf(acc[i][1][j], x - 14 + e[1]);
         }
 
     if constexpr (LORA) {
@@ -848,8 +909,8 @@ hipError_t launch_ragged(const RaggedProduct &p, void *workspace, hipStream_t st
         a.rowtiles = (int)((p.M + rows_wg - 1) / rows_wg);
         a.chunks = (int)chunk_bound(p.E, p.R, 64 * pl.mt);
         const void *fn = pl.mt == 4 ? tile_fn<4>(up, lora) : tile_fn<2>(up, lora);
-        return hipLaunchKernel(fn, dim3((unsigned)((int64_t)a.rowtiles * a.chunks)), dim3(kTileWaves * 64), args, 0,
-                               stream);
+        return hipLaunchKernel(fn, dim3((unsigned)(((int64_t)a.rowtiles * a.chunks + 7) / 8 * 8)), dim3(kTileWaves * 64),
+                               args, 0, stream);
     }
     a.ranges = pl.ranges;
     a.slices_each = (int)(slices_of(p.K) / pl.ranges);
