@@ -269,7 +269,7 @@ __global__ __launch_bounds__(512) void lora_dx_kernel(const DxArgs a) {
 #pragma unroll
     for (int j = 0; j < kPieces; ++j) {
         const int i = (threadIdx.x >> 3) + 64 * j;
-        const int piece = (threadIdx.x & 7) ^ (i & 7);
+        const int piece = (threadIdx.x & 7) ^ ((i >> 1) & 7);
         ysrc[j] = i < count ? reinterpret_cast<const uint4 *>(a.dy16 + (int64_t)(n0 + i) * a.pitch) + piece : nullptr;
     }
     // Codes: lane bits 0..3 pick four rows, the rest a dword of the 128 bytes.
@@ -365,7 +365,7 @@ __global__ __launch_bounds__(512) void lora_dx_kernel(const DxArgs a) {
 #pragma unroll
             for (int i = 0; i < MT; ++i) {
                 const int row = wt * 32 * MT + 32 * i + col;
-                const half8_t ya = __builtin_bit_cast(half8_t, ys[bi][row * 8 + ((4 * g + s) ^ (row & 7))]);
+                const half8_t ya = __builtin_bit_cast(half8_t, ys[bi][row * 8 + ((4 * g + s) ^ ((row >> 1) & 7))]);
                 acc[i][0] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ya, b0, acc[i][0], 0, 0, 0);
                 acc[i][1] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ya, b1, acc[i][1], 0, 0, 0);
             }

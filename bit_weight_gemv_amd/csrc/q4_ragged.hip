@@ -567,13 +567,14 @@ __global__ __launch_bounds__(kTileWaves * 64) void ragged_tile_kernel(const Args
         }
     }
     // Staging of X: piece j of this thread is row threadIdx / 8 + 64 j, slot
-    // threadIdx % 8, which holds the row's 16-byte piece slot ^ (row % 8).
+    // threadIdx % 8, which holds the row's 16-byte piece slot ^ (row / 2 % 8): the
+    // 16 rows that LDS serves at once then meet all 64 banks.
     const u32x4_t *xsrc[kPieces];
 #pragma unroll
     for (int j = 0; j < kPieces; ++j) {
         const int i = (threadIdx.x >> 3) + 64 * j;
         const int row = max(source_row(a, ck.start + min(i, ck.count - 1)), 0);
-        const int piece = (threadIdx.x & 7) ^ (i & 7);
+        const int piece = (threadIdx.x & 7) ^ ((i >> 1) & 7);
         xsrc[j] = reinterpret_cast<const u32x4_t *>(a.X + (int64_t)row * a.K) + piece;
     }
 
@@ -592,22 +593,21 @@ __global__ __launch_bounds__(kTileWaves * 64) void ragged_tile_kernel(const Args
         e[q] = a.rowexp[mat][mrow];
     }
 
-    // Codes and scales come for two steps at once (a row's 64 neighbouring
-    // bytes): those of the steps at hand, and of the two behind them.
-    u32x4_t xv[kPieces], cw[2][2], cn[2][2];
-    uint32_t sv[2][2], sn[2][2];
+    // Codes and scales of even and of odd steps: a set is loaded for the step
+    // after next as soon as it is used up (and never copied, which would wait
+    // for the loads).
+    u32x4_t xv[kPieces], c0[2], c1[2];
+    uint32_t v0[2], v1[2];
     auto load_x = [&](int b) {
 #pragma unroll
         for (int j = 0; j < kPieces; ++j) xv[j] = __builtin_nontemporal_load(xsrc[j] + 8 * b);  // (read once)
     };
-    auto load_codes = [&](int b, u32x4_t (&cd)[2][2], uint32_t (&sd)[2][2]) {
+    auto load_codes = [&](int b, u32x4_t (&cd)[2], uint32_t (&sd)[2]) {
 #pragma unroll
-        for (int q = 0; q < 2; ++q)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                cd[h][q] = csrc[q][2 * min(b + h, nb - 1)];
-                sd[h][q] = ssrc[q][min(b + h, nb - 1)];
-            }
+        for (int q = 0; q < 2; ++q) {
+            cd[q] = csrc[q][2 * b];
+            sd[q] = ssrc[q][b];
+        }
     };
     auto stage = [&](int b) {
         u32x4_t *buf = sm.xs[b & 1];
@@ -615,7 +615,8 @@ __global__ __launch_bounds__(kTileWaves * 64) void ragged_tile_kernel(const Args
         for (int j = 0; j < kPieces; ++j) buf[threadIdx.x + 512 * j] = xv[j];
     };
     load_x(0);
-    load_codes(0, cw, sv);
+    load_codes(0, c0, v0);
+    load_codes(min(1, nb - 1), c1, v1);
     fill_lut(sm.lut);
     stage(0);
     load_x(min(1, nb - 1));
@@ -627,67 +628,95 @@ __global__ __launch_bounds__(kTileWaves * 64) void ragged_tile_kernel(const Args
         for (int q = 0; q < 2; ++q) acc[i][q] = float16_t{};
     const uint32_t laneoff = (uint32_t)lane << 2;
 
-    // The weights of a quarter step: lookups, then the scale.
+    // A quarter step's weights (lookups, then the scale) and its rows of X.
     half2_t raw[2][4];
     half2_t s2[2];
+    u32x4_t xa[2][MT];
     auto look = [&](const u32x4_t (&cd)[2], int s) {
 #pragma unroll
         for (int q = 0; q < 2; ++q) lut8(lut, cd[q][s], laneoff, raw[q]);
     };
-    auto scale = [&](const uint32_t (&sd)[2]) {
+    auto scale = [&](int b, const uint32_t (&sd)[2]) {
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
-            const _Float16 h = (_Float16)ldexpf(f16_bits_to_f32(sd[q]), 14 - e[q]);
+            const _Float16 h = (_Float16)ldexpf(b < nb ? f16_bits_to_f32(sd[q]) : 0.0f, 14 - e[q]);
             s2[q] = half2_t{h, h};
         }
     };
-    // Step b, whose first lookups were made by the step before; it makes those
-    // of the next, with codes cnext and scales snext.
-    auto step = [&](int b, const u32x4_t (&cd)[2], const u32x4_t (&cnext)[2], const uint32_t (&snext)[2]) {
-        const u32x4_t *buf = sm.xs[b & 1];
+    auto rows = [&](int b, int s) {
+        const u32x4_t *buf = sm.xs[b & 1] + (wt * 32 * MT + col) * 8 + ((4 * g + s) ^ ((col >> 1) & 7));
+#pragma unroll
+        for (int i = 0; i < MT; ++i) xa[s & 1][i] = buf[32 * 8 * i];
+    };
+    half8_t w[2];
+    auto weigh = [&]() {
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) raw[q][i] *= s2[q];
+            w[q] = join8(raw[q]);
+        }
+    };
+    // Step b on the codes `cd`, with those of the next in `cnext`; its first
+    // weights and rows were made by the step before.
+    auto step = [&](int b, u32x4_t (&cd)[2], uint32_t (&sd)[2], const u32x4_t (&cnext)[2],
+                    const uint32_t (&snext)[2]) {
         // (The last steps stage and load what is there already.)
         stage(b + 1);
         load_x(min(b + 2, nb - 1));
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
-            half8_t w[2];
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) raw[q][i] *= s2[q];
-                w[q] = join8(raw[q]);
-            }
+            const half8_t wn[2] = {w[0], w[1]};
             if (s < 3) {
                 look(cd, s + 1);
+                rows(b, s + 1);
             } else {
-                scale(snext);
+                // Every wave has staged step b + 1, and has this step's last rows.
+                __syncthreads();
+                load_codes(min(b + 2, nb - 1), cd, sd);
+                scale(b + 1, snext);
                 look(cnext, 0);
+                rows(b + 1, 0);
             }
 #pragma unroll
             for (int i = 0; i < MT; ++i) {
-                const int row = wt * 32 * MT + 32 * i + col;
-                const half8_t xa = __builtin_bit_cast(half8_t, buf[row * 8 + ((4 * g + s) ^ (row & 7))]);
-                acc[i][0] = __builtin_amdgcn_mfma_f32_32x32x16_f16(xa, w[0], acc[i][0], 0, 0, 0);
-                acc[i][1] = __builtin_amdgcn_mfma_f32_32x32x16_f16(xa, w[1], acc[i][1], 0, 0, 0);
+                const half8_t x = __builtin_bit_cast(half8_t, xa[s & 1][i]);
+                acc[i][0] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x, wn[0], acc[i][0], 0, 0, 0);
+                acc[i][1] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x, wn[1], acc[i][1], 0, 0, 0);
+            }
+            weigh();
+            // In the shadow of each product: lookups and rows of the next
+            // quarter beside the first half of them, their scales beside the
+            // second.
+#pragma unroll
+            for (int k = 0; k < MT; ++k) {
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);            // a product
+                __builtin_amdgcn_sched_group_barrier(0x002, 8 / MT, 0);       // addresses
+                __builtin_amdgcn_sched_group_barrier(0x100, 8 / MT + 1, 0);   // LDS reads
+                if (s == 0) {
+                    __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);        // staging
+                    __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < MT; ++k) {
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                if (s == 3) __builtin_amdgcn_sched_group_barrier(0x002, 8 / MT + 2, 0);
+                else __builtin_amdgcn_sched_group_barrier(0x002, 8 / MT, 0);
             }
         }
-        __syncthreads();
     };
     __syncthreads();
-    scale(sv[0]);
-    look(cw[0], 0);
+    scale(0, v0);
+    look(c0, 0);
+    rows(0, 0);
+    weigh();
+    // (An odd last step runs with scales of 0.)
     for (int b = 0; b < nb; b += 2) {
-        load_codes(b + 2, cn, sn);
-        step(b, cw[0], cw[1], sv[1]);
-        if (b + 1 < nb) step(b + 1, cw[1], cn[0], sn[0]);
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                cw[h][q] = cn[h][q];
-                sv[h][q] = sn[h][q];
-            }
+        step(b, c0, v0, c1, v1);
+        step(b + 1, c1, v1, c0, v0);
     }
+    __syncthreads();
 
 #pragma unroll
     for (int i = 0; i < MT; ++i)
