@@ -145,24 +145,16 @@ hipError_t launch_shrink(const ShrinkArgs &s, Pieces pieces, hipStream_t stream)
 // Backward: what is prepared.
 // ---------------------------------------------------------------------------
 
-// Exponent of each packed row's largest scale (16 lanes a row), and behind
-// those workgroups B transposed: bt[a][j][m], rows of `pitch` with zeros past
-// M (a workgroup takes 64 m of one adapter).
+// The packed rows' exponents and scales (16 rows a workgroup), and behind those
+// workgroups B transposed: bt[a][j][m], rows of `pitch` with zeros past M (a
+// workgroup takes 64 m of one adapter).
 __global__ __launch_bounds__(256) void lora_rows_kernel(const uint16_t *__restrict__ scales, int M, int nb,
-                                                        int8_t *__restrict__ rowexp, int rowblocks,
-                                                        const uint16_t *__restrict__ B, int r, int pitch,
-                                                        uint16_t *__restrict__ bt) {
+                                                        int8_t *__restrict__ rowexp, uint16_t *__restrict__ tscale,
+                                                        int rowblocks, const uint16_t *__restrict__ B, int r,
+                                                        int pitch, uint16_t *__restrict__ bt) {
     __shared__ uint16_t tile[64][130];
     if ((int)blockIdx.x < rowblocks) {
-        const int row = blockIdx.x * 16 + (threadIdx.x >> 4);
-        if (row >= M) return;
-        int m = 0;
-        for (int b = threadIdx.x & 15; b < nb; b += 16) m = max(m, (int)(scales[(int64_t)row * nb + b] & 0x7FFF));
-#pragma unroll
-        for (int d = 8; d >= 1; d >>= 1) m = max(m, __shfl_xor(m, d));
-        const float f = f16_bits_to_f32((uint32_t)m);
-        const int e = m == 0 ? 0 : (int)(__builtin_bit_cast(uint32_t, f) >> 23) - 127;
-        if ((threadIdx.x & 15) == 0) rowexp[row] = (int8_t)min(e, 16);
+        prepare_scales(scales, (int64_t)blockIdx.x * 16, M, M, nb, rowexp, tscale);
         return;
     }
     const int per = pitch / 64, w = blockIdx.x - rowblocks;
@@ -223,9 +215,8 @@ __global__ __launch_bounds__(256) void lora_dy_kernel(const uint16_t *__restrict
 struct DxArgs {
     const uint16_t *dy16;   // fp16 [N][pitch]
     const int32_t *exps;
-    const int8_t *rowexp;
     const uint8_t *codes;
-    const uint16_t *scales;
+    const uint16_t *tscale; // the scales under each packed row's power of two, [K/64][M]
     int N, M, K, pitch, ktiles, splits;
     float *part;            // [splits][N][K], or null
     uint16_t *dX;
@@ -281,7 +272,6 @@ __global__ __launch_bounds__(512) void lora_dx_kernel(const DxArgs a) {
     uint4 yv[kPieces];
     uint32_t cv[4];
     uint32_t sv = 0;
-    int se = 0;
     auto load = [&](int st) {
 #pragma unroll
         for (int j = 0; j < kPieces; ++j) yv[j] = ysrc[j] ? ysrc[j][8 * st] : make_uint4(0, 0, 0, 0);
@@ -292,12 +282,7 @@ __global__ __launch_bounds__(512) void lora_dx_kernel(const DxArgs a) {
         }
         if (threadIdx.x < 256) {
             const int m = 64 * st + sm, kb = kt * 4 + skb;
-            sv = 0;
-            se = 0;
-            if (m < a.M && kb < nb) {
-                sv = a.scales[(int64_t)m * nb + kb];
-                se = a.rowexp[m];
-            }
+            sv = m < a.M && kb < nb ? a.tscale[(int64_t)kb * a.M + m] : 0;
         }
     };
     load(st0);
@@ -329,7 +314,7 @@ __global__ __launch_bounds__(512) void lora_dx_kernel(const DxArgs a) {
             for (int j = 0; j < 4; ++j) ct[bi][(j * 32 + dc) * 16 + (((m4 >> 2) ^ j) << 2) + (m4 & 3)] = o[j];
         }
         if (threadIdx.x < 256)
-            reinterpret_cast<_Float16 *>(sl[bi])[skb * 64 + sm] = (_Float16)ldexpf(f16_bits_to_f32(sv), 14 - se);
+            reinterpret_cast<uint16_t *>(sl[bi])[skb * 64 + sm] = (uint16_t)sv;
         __syncthreads();
         if (st + 1 < st1) load(st + 1);
 
@@ -615,7 +600,7 @@ DxPlan dx_plan(int64_t M, int64_t K, int64_t N) {
 }
 
 struct BackwardLayout {
-    size_t t, u, bt, dy16, exps, rowexp, offsets, rows, sort, part, grad[2], total;
+    size_t t, u, bt, dy16, exps, rowexp, tscale, offsets, rows, sort, part, grad[2], total;
     int64_t pitch;
 };
 
@@ -635,6 +620,7 @@ BackwardLayout backward_layout(int64_t M, int64_t K, int64_t N, int64_t r, int64
     b.dy16 = take((size_t)N * b.pitch * 2);
     b.exps = take((size_t)N * 4);
     b.rowexp = take((size_t)b.pitch);
+    b.tscale = take((size_t)M * (K / 64) * 2);
     b.offsets = take((size_t)(L + 1) * 4);
     b.rows = take((size_t)N * 4);
     b.sort = take(sort_ws_bytes(N, L));
@@ -706,13 +692,14 @@ hipError_t launch_lora_backward(const LoraCall &c, const uint16_t *dY, uint16_t 
     uint16_t *bt = reinterpret_cast<uint16_t *>(w + b.bt), *dy16 = reinterpret_cast<uint16_t *>(w + b.dy16);
     int32_t *exps = reinterpret_cast<int32_t *>(w + b.exps);
     int8_t *rowexp = reinterpret_cast<int8_t *>(w + b.rowexp);
+    uint16_t *tscale = reinterpret_cast<uint16_t *>(w + b.tscale);
     int32_t *offsets = reinterpret_cast<int32_t *>(w + b.offsets), *rows = reinterpret_cast<int32_t *>(w + b.rows);
     hipError_t e;
     if (c.N > 0) {
         const uint16_t *scales = c.scales, *B = c.B;
         int M = (int)c.M, nb = (int)(c.K / 64), rowblocks = dX ? (int)((c.M + 15) / 16) : 0, r = (int)c.r;
         int pitch = (int)b.pitch;
-        void *rargs[] = {&scales, &M, &nb, &rowexp, &rowblocks, &B, &r, &pitch, &bt};
+        void *rargs[] = {&scales, &M, &nb, &rowexp, &tscale, &rowblocks, &B, &r, &pitch, &bt};
         e = hipLaunchKernel(reinterpret_cast<const void *>(&lora_rows_kernel),
                             dim3((unsigned)(rowblocks + c.L * (b.pitch / 64))), dim3(256), rargs, 0, stream);
         if (e != hipSuccess) return e;
@@ -730,9 +717,8 @@ hipError_t launch_lora_backward(const LoraCall &c, const uint16_t *dY, uint16_t 
             DxArgs d = {};
             d.dy16 = dy16;
             d.exps = exps;
-            d.rowexp = rowexp;
             d.codes = c.codes;
-            d.scales = c.scales;
+            d.tscale = tscale;
             d.N = (int)c.N;
             d.M = M;
             d.K = (int)c.K;

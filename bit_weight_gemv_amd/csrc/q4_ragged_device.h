@@ -149,6 +149,38 @@ __device__ __forceinline__ void write_pieces(const uint16_t *__restrict__ X, con
     }
 }
 
+// A workgroup of 256 takes the 16 packed rows from row0 (below nrows; matrices
+// of M rows, nb blocks a row, one after the other): the exponent of each row's
+// largest scale (0 in a row of zeros), and scale 2^(14 - exponent) as fp16 at
+// [matrix][block][row].
+__device__ __forceinline__ void prepare_scales(const uint16_t *__restrict__ scales, int64_t row0, int64_t nrows, int M,
+                                               int nb, int8_t *__restrict__ rowexp, uint16_t *__restrict__ out) {
+    __shared__ int16_t exps[16];
+    __syncthreads();
+    {
+        const int64_t row = row0 + (threadIdx.x >> 4);
+        int m = 0;
+        if (row < nrows)
+            for (int b = threadIdx.x & 15; b < nb; b += 16) m = max(m, (int)(scales[row * nb + b] & 0x7FFF));
+#pragma unroll
+        for (int d = 8; d >= 1; d >>= 1) m = max(m, __shfl_xor(m, d));
+        const float f = f16_bits_to_f32((uint32_t)m);
+        const int e = m == 0 ? 0 : min((int)(__builtin_bit_cast(uint32_t, f) >> 23) - 127, 16);
+        if ((threadIdx.x & 15) == 0) {
+            exps[threadIdx.x >> 4] = (int16_t)e;
+            if (row < nrows) rowexp[row] = (int8_t)e;
+        }
+    }
+    __syncthreads();
+    const int64_t row = row0 + (threadIdx.x & 15);
+    if (row >= nrows) return;
+    const int e = exps[threadIdx.x & 15];
+    const int64_t mat = row / M;
+    for (int b = threadIdx.x >> 4; b < nb; b += 16)
+        out[(mat * nb + b) * M + (row - mat * M)] =
+            __builtin_bit_cast(uint16_t, (_Float16)ldexpf(f16_bits_to_f32(scales[row * nb + b]), 14 - e));
+}
+
 // Eight bf16 of a row at column k; zeros past its end.  VEC: rows start on 16
 // bytes and have whole pieces.
 template <bool VEC>
