@@ -70,26 +70,34 @@ __global__ __launch_bounds__(512) void lora_shrink_kernel(const ShrinkArgs a) {
 #pragma unroll
         for (int q = 0; q < JT; ++q) acc[q] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
         const uint16_t *z = a.Z + (int64_t)now * a.r * a.pitch;
-        for (int b = wave; b < nb; b += 8) {
-            const int k = 64 * b + 16 * g;
-            u32x4_t xv[2], zv[JT][2];
+        // U blocks' loads go together; blocks past the row are zeros.
+        constexpr int U = JT >= 4 ? 2 : 4;
+        for (int b = wave; b < nb; b += 8 * U) {
+            u32x4_t xv[U][2], zv[U][JT][2];
 #pragma unroll
-            for (int s = 0; s < 2; ++s) xv[s] = row_piece<VEC>(x, k + 8 * s, a.K);
+            for (int u = 0; u < U; ++u) {
+                const int k = 64 * (b + 8 * u) + 16 * g;
 #pragma unroll
-            for (int q = 0; q < JT; ++q)
-#pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    zv[q][s] = u32x4_t{0u, 0u, 0u, 0u};
-                    if (16 * q + col < a.r)
-                        zv[q][s] = *reinterpret_cast<const u32x4_t *>(z + (int64_t)(16 * q + col) * a.pitch + k + 8 * s);
-                }
-#pragma unroll
-            for (int s = 0; s < 2; ++s)
+                for (int s = 0; s < 2; ++s) xv[u][s] = row_piece<VEC>(x, k + 8 * s, a.K);
 #pragma unroll
                 for (int q = 0; q < JT; ++q)
-                    acc[q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, xv[s]),
-                                                                     __builtin_bit_cast(bf16x8_t, zv[q][s]), acc[q], 0,
-                                                                     0, 0);
+#pragma unroll
+                    for (int s = 0; s < 2; ++s) {
+                        zv[u][q][s] = u32x4_t{0u, 0u, 0u, 0u};
+                        if (16 * q + col < a.r && k < a.pitch)
+                            zv[u][q][s] =
+                                *reinterpret_cast<const u32x4_t *>(z + (int64_t)(16 * q + col) * a.pitch + k + 8 * s);
+                    }
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int s = 0; s < 2; ++s)
+#pragma unroll
+                    for (int q = 0; q < JT; ++q)
+                        acc[q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, xv[u][s]),
+                                                                         __builtin_bit_cast(bf16x8_t, zv[u][q][s]),
+                                                                         acc[q], 0, 0, 0);
         }
         // Register i: token 4 g + i, rank 16 q + col.
 #pragma unroll
@@ -149,7 +157,7 @@ hipError_t launch_shrink(const ShrinkArgs &s, Pieces pieces, hipStream_t stream)
 // workgroups B transposed: bt[a][j][m], rows of `pitch` with zeros past M (a
 // workgroup takes 64 m of one adapter).
 __global__ __launch_bounds__(256) void lora_rows_kernel(const uint16_t *__restrict__ scales, int M, int nb,
-                                                        int8_t *__restrict__ rowexp, uint16_t *__restrict__ tscale,
+                                                        int16_t *__restrict__ rowexp, uint16_t *__restrict__ tscale,
                                                         int rowblocks, const uint16_t *__restrict__ B, int r,
                                                         int pitch, uint16_t *__restrict__ bt) {
     __shared__ uint16_t tile[64][130];
@@ -172,40 +180,70 @@ __global__ __launch_bounds__(256) void lora_rows_kernel(const uint16_t *__restri
 // M: the power of two of each packed row goes to this side, so that the
 // weights' fp16 values keep their full precision, and the token's brings the
 // largest to [2^14, 2^15).
+// The exponents of two values are found at once in 16-bit halves; the first
+// kDyHeld pieces of a thread stay in registers between the two passes.
+typedef short s16x2_t __attribute__((ext_vector_type(2)));
+constexpr int kDyHeld = 6;
+
 template <bool VEC>
 __global__ __launch_bounds__(256) void lora_dy_kernel(const uint16_t *__restrict__ dY, int M, int pitch,
-                                                      const int8_t *__restrict__ rowexp, uint16_t *__restrict__ out,
+                                                      const int16_t *__restrict__ rowexp, uint16_t *__restrict__ out,
                                                       int32_t *__restrict__ exps) {
     __shared__ int wmax[4];
     const int n = blockIdx.x;
     const uint16_t *src = dY + (int64_t)n * M;
-    int best = -1000;
-    for (int m = threadIdx.x * 8; m < M; m += 2048) {
-        const u32x4_t v = row_piece<VEC>(src, m, M);
-        const uint64_t e = *reinterpret_cast<const uint64_t *>(rowexp + m);
+    s16x2_t best2 = {0, 0};
+    u32x4_t held[kDyHeld];
+    auto look = [&](const u32x4_t &v, int m) {
+        const u32x4_t e = *reinterpret_cast<const u32x4_t *>(rowexp + m);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int mag = (v[i >> 1] >> (16 * (i & 1))) & 0x7FFF;
-            if (mag) best = max(best, min(mag >> 7, 254) + (int)(int8_t)(e >> (8 * i)));
+        for (int c = 0; c < 4; ++c) {
+            const u16x2_t mag = __builtin_bit_cast(u16x2_t, v[c] & 0x7FFF7FFFu);
+            u16x2_t ex = mag >> 7;
+            ex = __builtin_elementwise_min(ex, u16x2_t{254, 254});
+            // 2048 more than the exponent, and 0 for a zero (whatever stands
+            // in the exponents behind the last packed row).
+            const s16x2_t nz = __builtin_bit_cast(s16x2_t, __builtin_elementwise_min(mag, u16x2_t{1, 1}));
+            const s16x2_t key = __builtin_bit_cast(s16x2_t, ex) + __builtin_bit_cast(s16x2_t, e[c]) + s16x2_t{2048, 2048};
+            best2 = __builtin_elementwise_max(best2, key & -nz);
         }
+    };
+    auto put = [&](const u32x4_t &v, int m, int shift) {
+        const u32x4_t e = *reinterpret_cast<const u32x4_t *>(rowexp + m);
+        u32x4_t h;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const int el = (int)(e[c] << 16) >> 16, eh = (int)e[c] >> 16;
+            h[c] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(ldexpf(bf16_lo(v[c]), shift + el),
+                                                                           ldexpf(bf16_hi(v[c]), shift + eh)));
+        }
+        *reinterpret_cast<u32x4_t *>(out + (int64_t)n * pitch + m) = h;
+    };
+#pragma unroll
+    for (int i = 0; i < kDyHeld; ++i) {
+        const int m = threadIdx.x * 8 + 2048 * i;
+        held[i] = m < M ? row_piece<VEC>(src, m, M) : u32x4_t{0u, 0u, 0u, 0u};
     }
+#pragma unroll
+    for (int i = 0; i < kDyHeld; ++i) {
+        const int m = threadIdx.x * 8 + 2048 * i;
+        if (m < M) look(held[i], m);
+    }
+    for (int m = threadIdx.x * 8 + 2048 * kDyHeld; m < M; m += 2048) look(row_piece<VEC>(src, m, M), m);
+    int best = max((int)best2.x, (int)best2.y);
 #pragma unroll
     for (int d = 32; d >= 1; d >>= 1) best = max(best, __shfl_xor(best, d));
     if ((threadIdx.x & 63) == 0) wmax[threadIdx.x >> 6] = best;
     __syncthreads();
-    best = max(max(wmax[0], wmax[1]), max(wmax[2], wmax[3]));
-    const int shift = best == -1000 ? 0 : 141 - best;
-    for (int m = threadIdx.x * 8; m < pitch; m += 2048) {
-        const u32x4_t v = row_piece<VEC>(src, m, M);
-        const uint64_t e = *reinterpret_cast<const uint64_t *>(rowexp + m);
-        half2_t h[4];
+    best = max(max(wmax[0], wmax[1]), max(wmax[2], wmax[3])) - 2048;
+    const int shift = best < -1024 ? 0 : 141 - best;  // (a row of zeros)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            h[i].x = (_Float16)ldexpf(bf16_lo(v[i]), shift + (int)(int8_t)(e >> (16 * i)));
-            h[i].y = (_Float16)ldexpf(bf16_hi(v[i]), shift + (int)(int8_t)(e >> (16 * i + 8)));
-        }
-        *reinterpret_cast<half8_t *>(out + (int64_t)n * pitch + m) = join8(h);
+    for (int i = 0; i < kDyHeld; ++i) {
+        const int m = threadIdx.x * 8 + 2048 * i;
+        if (m < pitch) put(held[i], m, shift);
     }
+    for (int m = threadIdx.x * 8 + 2048 * kDyHeld; m < pitch; m += 2048)
+        put(m < M ? row_piece<VEC>(src, m, M) : u32x4_t{0u, 0u, 0u, 0u}, m, shift);
     if (threadIdx.x == 0) exps[n] = -shift;
 }
 
@@ -488,7 +526,7 @@ struct GradArgs {
 // VEC: both matrices' rows start on 16 bytes.  JT: tiles of 16 ranks at once.
 template <bool VEC, int JT>
 __global__ __launch_bounds__(256) void lora_grad_kernel(const GradArgs a) {
-    constexpr int U = 4;  // steps of four tokens whose loads go together
+    constexpr int U = JT == 1 ? 8 : 4;  // steps of four tokens whose loads go together
     const int q = (int)blockIdx.x >= a.blocks0 ? 1 : 0;
     const Chunk ck = find_chunk(a.offsets, a.L, a.N, blockIdx.y, kPieceTokens);
     if (ck.count == 0) return;
@@ -498,6 +536,11 @@ __global__ __launch_bounds__(256) void lora_grad_kernel(const GradArgs a) {
     const int j0 = blockIdx.z * 16 * JT;
     const uint16_t *Z = a.Z[q];
     const float *T = a.t[q];
+    // The piece's tokens: two of them in a lane.
+    static_assert(kPieceTokens == 128, "two rows a lane");
+    int tok[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) tok[h] = a.rows[ck.start + min(64 * h + lane, ck.count - 1)];
     float4_t acc[JT][8];
 #pragma unroll
     for (int p = 0; p < JT; ++p)
@@ -509,11 +552,11 @@ __global__ __launch_bounds__(256) void lora_grad_kernel(const GradArgs a) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int at = s + 4 * u + g;
+            const int n = __shfl(s < 64 ? tok[0] : tok[1], at & 63);
             z[u] = u32x4_t{0u, 0u, 0u, 0u};
 #pragma unroll
             for (int p = 0; p < JT; ++p) t[u][p] = 0.0f;
             if (at < ck.count) {
-                const int n = a.rows[ck.start + at];
                 z[u] = row_piece<VEC>(Z + (int64_t)n * cols, c, cols);
 #pragma unroll
                 for (int p = 0; p < JT; ++p)
@@ -619,7 +662,7 @@ BackwardLayout backward_layout(int64_t M, int64_t K, int64_t N, int64_t r, int64
     b.bt = take((size_t)L * r * b.pitch * 2);
     b.dy16 = take((size_t)N * b.pitch * 2);
     b.exps = take((size_t)N * 4);
-    b.rowexp = take((size_t)b.pitch);
+    b.rowexp = take((size_t)b.pitch * 2);
     b.tscale = take((size_t)M * (K / 64) * 2);
     b.offsets = take((size_t)(L + 1) * 4);
     b.rows = take((size_t)N * 4);
@@ -691,7 +734,7 @@ hipError_t launch_lora_backward(const LoraCall &c, const uint16_t *dY, uint16_t 
     float *t = reinterpret_cast<float *>(w + b.t), *u = reinterpret_cast<float *>(w + b.u);
     uint16_t *bt = reinterpret_cast<uint16_t *>(w + b.bt), *dy16 = reinterpret_cast<uint16_t *>(w + b.dy16);
     int32_t *exps = reinterpret_cast<int32_t *>(w + b.exps);
-    int8_t *rowexp = reinterpret_cast<int8_t *>(w + b.rowexp);
+    int16_t *rowexp = reinterpret_cast<int16_t *>(w + b.rowexp);
     uint16_t *tscale = reinterpret_cast<uint16_t *>(w + b.tscale);
     int32_t *offsets = reinterpret_cast<int32_t *>(w + b.offsets), *rows = reinterpret_cast<int32_t *>(w + b.rows);
     hipError_t e;

@@ -153,8 +153,9 @@ __device__ __forceinline__ void write_pieces(const uint16_t *__restrict__ X, con
 // of M rows, nb blocks a row, one after the other): the exponent of each row's
 // largest scale (0 in a row of zeros), and scale 2^(14 - exponent) as fp16 at
 // [matrix][block][row].
+template <typename E>
 __device__ __forceinline__ void prepare_scales(const uint16_t *__restrict__ scales, int64_t row0, int64_t nrows, int M,
-                                               int nb, int8_t *__restrict__ rowexp, uint16_t *__restrict__ out) {
+                                               int nb, E *__restrict__ rowexp, uint16_t *__restrict__ out) {
     __shared__ int16_t exps[16];
     __syncthreads();
     {
@@ -168,7 +169,7 @@ __device__ __forceinline__ void prepare_scales(const uint16_t *__restrict__ scal
         const int e = m == 0 ? 0 : min((int)(__builtin_bit_cast(uint32_t, f) >> 23) - 127, 16);
         if ((threadIdx.x & 15) == 0) {
             exps[threadIdx.x >> 4] = (int16_t)e;
-            if (row < nrows) rowexp[row] = (int8_t)e;
+            if (row < nrows) rowexp[row] = (E)e;
         }
     }
     __syncthreads();
