@@ -818,6 +818,9 @@ int64_t chunk_bound(int64_t E, int64_t R, int64_t most) {
     return a < R ? a : R;
 }
 
+// The tile kernel's rows of X in fp16: one at least, which rows outside [0, T) read.
+size_t tile_rows_bytes(int64_t T, int64_t K) { return (size_t)(T > 0 ? T : 1) * K * 2; }
+
 }  // namespace
 
 int compute_units() {
@@ -842,7 +845,7 @@ size_t ragged_ws_bytes(int64_t E, int64_t M, int64_t K, int64_t T, int64_t R, bo
     const Plan p = plan_of(E, M, K, R, lora);
     const size_t mats = up ? 2 : 1;
     if (p.tiles)
-        return round16((size_t)T * K * 2) + round16((size_t)T * 4) +
+        return tile_rows_bytes(T, K) + round16((size_t)T * 4) +
                mats * (round16((size_t)E * M) + round16((size_t)E * M * (K / 64) * 2));
     return (p.pre ? pieces_bytes(K, R) : 0) + (p.ranges > 1 || (p.single && lora) ? mats * p.ranges * (size_t)R * M * 4 : 0);
 }
@@ -911,7 +914,7 @@ hipError_t launch_ragged(const RaggedProduct &p, void *workspace, hipStream_t st
     if (pl.tiles) {
         char *w = static_cast<char *>(workspace);
         uint16_t *x16 = reinterpret_cast<uint16_t *>(w);
-        w += round16((size_t)p.T * p.K * 2);
+        w += tile_rows_bytes(p.T, p.K);
         int32_t *xexp = reinterpret_cast<int32_t *>(w);
         w += round16((size_t)p.T * 4);
         const size_t eb = round16((size_t)p.E * p.M), sb = round16((size_t)p.E * p.M * (p.K / 64) * 2);

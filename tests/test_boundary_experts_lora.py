@@ -108,6 +108,14 @@ def test_grouped_refusals(q4):
     assert _grouped(q4, ws=P(4) + 1600, nb=need, **kw) == q4.Q4_ERR_OVERLAP
 
 
+def test_grouped_workspace_without_rows(q4):
+    """With no row of X every position reads as zeros; the tile kernel reads a
+    row of its workspace for them all the same, so one row is held."""
+    with_one = q4.q4_gemm_grouped_ws_bytes(1, 32, 131072 // 2, 1, 500, False)
+    without = q4.q4_gemm_grouped_ws_bytes(1, 32, 131072 // 2, 0, 500, False)
+    assert with_one - without == 16 and without >= 131072
+
+
 def _combine(q4, R=10, M=16, T=5, k=2, yk=1, ok=1, p=None):
     p = p or [P(i) for i in range(4)]
     return _call(q4, "experts", "q4_moe_combine", p[0], yk, R, M, p[1], p[2], T, k, ok, p[3], None)

@@ -208,6 +208,20 @@ def test_grouped_rows_outside_and_values_that_are_not_finite(env):
         assert torch.isfinite(y2).all()
 
 
+@pytest.mark.parametrize("R", [3, 20, 300])
+def test_grouped_without_rows(env, R):
+    """No row of X at all: every index is outside, every output is zero."""
+    torch, q4, dev = env
+    rng = np.random.default_rng(4)
+    codes, scales = (_dev(env, a) for a in _packed(rng, 2, 40, 4160))
+    off = _dev(env, _groups(rng, 2, [R // 2, R - R // 2]))
+    rows = torch.zeros(R, dtype=torch.int32, device=dev)
+    X = torch.empty((0, 4160), dtype=torch.bfloat16, device=dev)
+    for up in (None, (codes, scales)):
+        y = q4.q4_gemm_grouped(codes, scales, X, off, rows=rows, up=up, out_dtype=torch.float32)
+        assert torch.all(y == 0)
+
+
 def test_grouped_on_another_stream_and_captured(env):
     """The same bits from a call on a side stream, and from a captured call
     replayed with other work in between; two graphs with workspaces of their
