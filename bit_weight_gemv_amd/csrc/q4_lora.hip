@@ -44,14 +44,15 @@ __global__ __launch_bounds__(256) void lora_shrink_token_kernel(const ShrinkArgs
                     blockIdx.x / a.N * 4 + (threadIdx.x >> 6), a.N, a.t);
 }
 
-// Many tokens: a workgroup takes 16, its 8 waves split K in 64-blocks dealt
-// round; the adapters among the 16 tokens come one after the other.  Lane
-// (row, g) of v_mfma_f32_16x16x32_bf16 holds k = 64 b + 16 g + (0..15) of a
-// block in two steps, so a row's four lanes read 128 neighbouring bytes.
-// Bound by the bytes of X: one adapter's rows stay in the cache.
+// Many tokens: a workgroup takes 16, its W waves split K in 64-blocks dealt
+// round; the adapters among the 16 tokens come AD at a time.  Lane (row, g) of
+// v_mfma_f32_16x16x32_bf16 holds k = 64 b + 32 s + 8 g + (0..7) of a block
+// in step s, so a row's four lanes read 64 neighbouring bytes.  Bound by the
+// bytes of X: an adapter's rows stay in the cache.
 template <bool VEC, int JT>
-__global__ __launch_bounds__(512) void lora_shrink_kernel(const ShrinkArgs a) {
-    __shared__ float red[8][16 * 16 * JT];
+__global__ __launch_bounds__(JT >= 8 ? 512 : 1024) void lora_shrink_kernel(const ShrinkArgs a) {
+    constexpr int AD = JT == 1 ? 2 : 1, W = JT >= 8 ? 8 : 16;
+    __shared__ float red[W][AD][16 * 16 * JT];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int col = lane & 15, g = lane >> 4;
     const int n0 = blockIdx.x * 16, n = n0 + col;
@@ -61,57 +62,68 @@ __global__ __launch_bounds__(512) void lora_shrink_kernel(const ShrinkArgs a) {
     const int nb = (a.K + 63) >> 6;
     int pending = id;
     while (true) {
-        const uint64_t left = __builtin_amdgcn_ballot_w64(pending >= 0);
-        if (!left) return;
-        const int now = __builtin_amdgcn_readlane(pending, __builtin_ctzll(left));
-        if (pending == now) pending = -1;
-        const float scale = a.scaling[now];
-        float4_t acc[JT];
+        int now[AD];
 #pragma unroll
-        for (int q = 0; q < JT; ++q) acc[q] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
-        const uint16_t *z = a.Z + (int64_t)now * a.r * a.pitch;
+        for (int p = 0; p < AD; ++p) {
+            const uint64_t left = __builtin_amdgcn_ballot_w64(pending >= 0);
+            if (p == 0 && !left) return;
+            now[p] = left ? __builtin_amdgcn_readlane(pending, __builtin_ctzll(left)) : -1;
+            if (pending == now[p]) pending = -1;
+        }
+        float4_t acc[AD][JT];
+#pragma unroll
+        for (int p = 0; p < AD; ++p)
+#pragma unroll
+            for (int q = 0; q < JT; ++q) acc[p][q] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
         // U blocks' loads go together; blocks past the row are zeros.
         constexpr int U = JT >= 4 ? 2 : 4;
-        for (int b = wave; b < nb; b += 8 * U) {
-            u32x4_t xv[U][2], zv[U][JT][2];
+        for (int b = wave; b < nb; b += W * U) {
+            u32x4_t xv[U][2], zv[U][AD][JT][2];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int k = 64 * (b + 8 * u) + 16 * g;
+                const int k = 64 * (b + W * u) + 8 * g;
 #pragma unroll
-                for (int s = 0; s < 2; ++s) xv[u][s] = row_piece<VEC>(x, k + 8 * s, a.K);
+                for (int s = 0; s < 2; ++s) xv[u][s] = row_piece<VEC>(x, k + 32 * s, a.K);
 #pragma unroll
-                for (int q = 0; q < JT; ++q)
+                for (int p = 0; p < AD; ++p)
 #pragma unroll
-                    for (int s = 0; s < 2; ++s) {
-                        zv[u][q][s] = u32x4_t{0u, 0u, 0u, 0u};
-                        if (16 * q + col < a.r && k < a.pitch)
-                            zv[u][q][s] =
-                                *reinterpret_cast<const u32x4_t *>(z + (int64_t)(16 * q + col) * a.pitch + k + 8 * s);
-                    }
+                    for (int q = 0; q < JT; ++q)
+#pragma unroll
+                        for (int s = 0; s < 2; ++s) {
+                            zv[u][p][q][s] = u32x4_t{0u, 0u, 0u, 0u};
+                            if (now[p] >= 0 && 16 * q + col < a.r && k < a.pitch)
+                                zv[u][p][q][s] = *reinterpret_cast<const u32x4_t *>(
+                                    a.Z + ((int64_t)now[p] * a.r + 16 * q + col) * a.pitch + k + 32 * s);
+                        }
             }
 #pragma unroll
             for (int u = 0; u < U; ++u)
 #pragma unroll
                 for (int s = 0; s < 2; ++s)
 #pragma unroll
-                    for (int q = 0; q < JT; ++q)
-                        acc[q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, xv[u][s]),
-                                                                         __builtin_bit_cast(bf16x8_t, zv[u][q][s]),
-                                                                         acc[q], 0, 0, 0);
+                    for (int p = 0; p < AD; ++p)
+#pragma unroll
+                        for (int q = 0; q < JT; ++q)
+                            acc[p][q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                                __builtin_bit_cast(bf16x8_t, xv[u][s]), __builtin_bit_cast(bf16x8_t, zv[u][p][q][s]),
+                                acc[p][q], 0, 0, 0);
         }
         // Register i: token 4 g + i, rank 16 q + col.
 #pragma unroll
-        for (int q = 0; q < JT; ++q)
+        for (int p = 0; p < AD; ++p)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) red[wave][(4 * g + i) * 16 * JT + 16 * q + col] = acc[q][i];
+            for (int q = 0; q < JT; ++q)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) red[wave][p][(4 * g + i) * 16 * JT + 16 * q + col] = acc[p][q][i];
         __syncthreads();
-        for (int o = threadIdx.x; o < 256 * JT; o += 512) {
-            const int row = o / (16 * JT), j = o % (16 * JT);
-            if (n0 + row < a.N && j < a.r && a.ids[n0 + row] == now) {
-                float s = red[0][o];
+        for (int o = threadIdx.x; o < AD * 256 * JT; o += 64 * W) {
+            const int p = o / (256 * JT), at = o % (256 * JT), row = at / (16 * JT), j = at % (16 * JT);
+            const int adapter = p == 0 ? now[0] : now[AD - 1];
+            if (n0 + row < a.N && j < a.r && adapter >= 0 && a.ids[n0 + row] == adapter) {
+                float s = red[0][p][at];
 #pragma unroll
-                for (int w = 1; w < 8; ++w) s += red[w][o];
-                a.t[(int64_t)(n0 + row) * a.r + j] = s * scale;
+                for (int w = 1; w < W; ++w) s += red[w][p][at];
+                a.t[(int64_t)(n0 + row) * a.r + j] = s * a.scaling[adapter];
             }
         }
         __syncthreads();
@@ -146,7 +158,7 @@ hipError_t launch_shrink(const ShrinkArgs &s, Pieces pieces, hipStream_t stream)
     else
         fn = vec ? reinterpret_cast<const void *>(&lora_shrink_kernel<true, 8>)
                  : reinterpret_cast<const void *>(&lora_shrink_kernel<false, 8>);
-    return hipLaunchKernel(fn, dim3((unsigned)((a.N + 15) / 16)), dim3(512), args, 0, stream);
+    return hipLaunchKernel(fn, dim3((unsigned)((a.N + 15) / 16)), dim3(a.r > 64 ? 512 : 1024), args, 0, stream);
 }
 
 // ---------------------------------------------------------------------------
