@@ -30,7 +30,8 @@ struct ShrinkArgs {
     float *t;
 };
 
-constexpr int64_t kTokenBytes = 32 << 20;  // adapters' bytes that tokens on their own may read
+constexpr int64_t kTokens = 1024;           // tokens on their own at most,
+constexpr int64_t kTokenBytes = 256 << 20;  // and the adapters' bytes that they may read
 
 // Few tokens: a workgroup takes one token and 4 ranks, a wave a rank.  The
 // workgroups behind those write the packed product's activations as pieces.
@@ -136,14 +137,19 @@ hipError_t launch_shrink(const ShrinkArgs &s, Pieces pieces, hipStream_t stream)
     const bool vec = a.K % 8 == 0;
     // A token of its own workgroups reads its adapter alone: many short waits
     // at once, but an adapter's bytes for every token; 16 tokens that share a
-    // workgroup read it once for all that use it, one adapter after the other.
-    if (a.N <= 64 || pieces.x16 || (int64_t)a.N * a.r * a.pitch * 2 <= kTokenBytes) {
-        int shrinks = a.N * ((a.r + 3) / 4);
+    // workgroup read it once for all that use it.  With the product, K = 2048
+    // (tokens alone | 16 together): 512 tokens of rank 16 71.9 | 75.2 us, 4096
+    // 82.8 | 76.8, 512 of rank 64 85.9 | 96.1, 2048 108 | 103.
+    const bool alone = a.N <= 64 || (a.N <= kTokens && (int64_t)a.N * a.r * a.pitch * 2 <= kTokenBytes);
+    if (alone || pieces.x16) {
+        int shrinks = alone ? a.N * ((a.r + 3) / 4) : 0;
         void *targs[] = {&a, &pieces, &shrinks};
-        return hipLaunchKernel(vec ? reinterpret_cast<const void *>(&lora_shrink_token_kernel<true>)
-                                   : reinterpret_cast<const void *>(&lora_shrink_token_kernel<false>),
-                               dim3((unsigned)(shrinks + (pieces.x16 ? pieces_blocks(a.K, a.N) : 0))), dim3(256),
-                               targs, 0, stream);
+        const hipError_t e =
+            hipLaunchKernel(vec ? reinterpret_cast<const void *>(&lora_shrink_token_kernel<true>)
+                                : reinterpret_cast<const void *>(&lora_shrink_token_kernel<false>),
+                            dim3((unsigned)(shrinks + (pieces.x16 ? pieces_blocks(a.K, a.N) : 0))), dim3(256), targs, 0,
+                            stream);
+        if (alone || e != hipSuccess) return e;
     }
     const void *fn;
     if (a.r <= 16)
@@ -642,14 +648,18 @@ struct DxPlan {
 
 DxPlan dx_plan(int64_t M, int64_t K, int64_t N) {
     DxPlan p = {};
-    p.mt = N > 1024 ? 4 : N > 64 ? 2 : 1;
+    // 1 | 2 | 4 tiles a wave, the whole call in us: 2048 x 2048, N = 64 40.3 |
+    // 41.7 | 44.2, 512 64.5 | 64.1 | 72.4; 11008 x 2048, N = 512 146 | 125 |
+    // 126, 2048 341 | 262 | 244.
+    p.mt = N > 1024 ? 4 : N > 256 ? 2 : 1;
     p.tiles = (N + 64 * p.mt - 1) / (64 * p.mt);
     p.ktiles = (int)((K + 255) / 256);
     // Packed rows are split while there are fewer workgroups than compute
-    // units, into parts of 128 rows at least.
+    // units, into parts of 256 rows at least: 2048 x 2048, N = 64 in 1, 4, 8,
+    // 16 parts 71.5, 42.2, 38.5, 40.4 us; N = 128 in 4, 8, 16 48.3, 47.1, 52.9.
     const int64_t steps = (M + 63) / 64, have = p.tiles * p.ktiles, cus = 256;
     int64_t s = have >= cus || have == 0 ? 1 : (cus + have - 1) / have;
-    if (s > (steps + 1) / 2) s = (steps + 1) / 2;
+    if (s > (steps + 3) / 4) s = (steps + 3) / 4;
     p.splits = (int)(s < 1 ? 1 : s);
     return p;
 }

@@ -797,25 +797,58 @@ struct Plan {
     int ranges;   // chunk kernel: ranges of K
 };
 
-Plan plan_of(int64_t E, int64_t M, int64_t K, int64_t R, bool lora) {
-    Plan p = {};
-    // Rows a group, were all groups in use equally full.
-    const int64_t groups = E < R ? E : R;
-    const int64_t avg = groups ? (R + groups - 1) / groups : 0;
-    p.single = R == 1 || R * 4 <= E;
-    p.tiles = avg > 64;
-    p.mt = avg > 160 ? 4 : 2;
-    p.cap = R <= 16 || avg <= 12 ? 16 : 32;
-    p.pre = !p.single && (lora || R > 16);
-    p.ranges = p.single ? (int)((K + kRowRangeK - 1) / kRowRangeK)
-                       : (int)((slices_of(K) + kChunkWaves - 1) / kChunkWaves);
-    return p;
-}
-
 // Chunks of `most` rows that R rows in E groups can make at most.
 int64_t chunk_bound(int64_t E, int64_t R, int64_t most) {
     const int64_t a = E == 1 ? (R + most - 1) / most : R / most + E;
     return a < R ? a : R;
+}
+
+// The rules, with what both sides take in us: E x M x K, "up" where there is an up matrix.
+Plan plan_of(int64_t E, int64_t M, int64_t K, int64_t R, bool up, bool lora) {
+    Plan p = {};
+    const int64_t groups = E < R ? E : R;
+    const int64_t avg = groups ? (R + groups - 1) / groups : 0;  // rows a group, were all in use equally full
+    // Chunks of `most` rows that are likely: half a chunk a group is empty.
+    auto chunks = [&](int64_t most) {
+        const int64_t n = E == 1 ? (R + most - 1) / most : (2 * R + groups * most) / (2 * most);
+        return n > groups ? n : groups;
+    };
+    // The row kernel reads a group's codes for each row, but waits for less:
+    // row | chunk for 64 x 1408 x 2048 up, R = 8 9.1 | 16.7, 32 22.4 | 33.6,
+    // 64 34.8 | 44.1; 64 x 2048 x 1408, R = 16 9.3 | 12.2, 32 16.3 | 17.6, 48
+    // 22.0 | 17.5; 8 x 2048 x 4096, R = 4 9.4 | 14.8, 16 21.4 | 17.6;
+    // 1 x 4096 x 4096, R = 2 10.4 | 11.0, 8 20.6 | 11.4.
+    p.single = R <= 2 || R <= (up ? E : E / 2);
+    // Chunks of 16 rows | 32: with two matrices, 64 x 1408 x 2048 up, R = 256
+    // (4 a group) 56.2 | 58.8, 512 86.8 | 76.0, 1024 125 | 101.  With one, a
+    // compute unit holds two workgroups of 16 and one of 32, which pays where
+    // one group's codes would be read twice: 1 x 4096 x 4096, R = 32
+    // 17.2 | 13.4, 16 10.9 | 11.6; 64 x 2048 x 1408, R = 512 32 | 46, 2048 62 | 83.
+    p.cap = (up ? avg < 8 : E > 1 || R <= 16) ? 16 : 32;
+    // The chunk kernel's time goes with chunks x M, the tile kernel's (with 64
+    // or 128 rows for each of two waves, mt 2 or 4) with the times that its
+    // workgroups fill the 256 compute units, each a walk along K: in units of
+    // 1.8 ns for 64 weights of K.  Chunk | mt 2 | mt 4 for 1 x 11008 x 2048, R =
+    // 128 30 | 51 | 67, 256 52 | 53 | 71, 512 93 | 55 | 72, 1024 - | 101 | 78,
+    // 4096 - | 290 | 228; 1 x 2048 x 11008, R = 128 34 | 235 | 289, 512 113 |
+    // 226 | 299; 64 x 1408 x 2048 up, R = 1024 101 | - | -, 2048 146 | 149 |
+    // 205, 4096 285 | 191 | 217, 16384 809 | 340 | 355, 32768 - | 615 | 524.
+    const int64_t mats = up ? 2 : 1, rowtiles = (M * mats + 255) / 256;
+    const int64_t full2 = (chunks(128) * rowtiles + 255) / 256, full4 = (chunks(256) * rowtiles + 255) / 256;
+    p.mt = 3 * full4 <= 2 * full2 ? 4 : 2;
+    const int64_t tile_cost = 392000 * (2 * full2 < 3 * full4 ? 2 * full2 : 3 * full4);
+    const int64_t chunk_cost = chunks(p.cap) * M * mats * (p.cap == 16 ? 4 : 9);
+    p.tiles = !p.single && avg > 32 &&
+              (avg > 1024 || chunk_cost > tile_cost || (M + 255) / 256 * R >= INT64_C(1) << 24);
+    // A launch that converts the activations first, against a conversion in
+    // every workgroup: not | first for chunks of 32, 64 x 1408 x 2048 up, R =
+    // 512 79.0 | 76.0, 1024 105 | 101, 1 x 4096 x 4096, R = 32 14.3 | 13.4; of
+    // 16, 64 x 2048 x 1408, R = 48 17.5 | 19.6, 512 32.0 | 34.2.  Adapters
+    // have a launch before the product anyhow, and it does both.
+    p.pre = !p.single && !p.tiles && (lora || p.cap == 32);
+    p.ranges = p.single ? (int)((K + kRowRangeK - 1) / kRowRangeK)
+                       : (int)((slices_of(K) + kChunkWaves - 1) / kChunkWaves);
+    return p;
 }
 
 // The tile kernel's rows of X in fp16: one at least, which rows outside [0, T) read.
@@ -832,7 +865,7 @@ int compute_units() {
 }
 
 bool ragged_fits(int64_t E, int64_t M, int64_t K, int64_t T, int64_t R, bool up) {
-    const Plan p = plan_of(E, M, K, R, false);
+    const Plan p = plan_of(E, M, K, R, up, false);
     const int64_t most = INT64_C(1) << 32;  // threads of one launch
     if (p.tiles) {
         const int64_t rowtiles = (M + (up ? 127 : 255)) / (up ? 128 : 256);
@@ -842,7 +875,7 @@ bool ragged_fits(int64_t E, int64_t M, int64_t K, int64_t T, int64_t R, bool up)
 }
 
 size_t ragged_ws_bytes(int64_t E, int64_t M, int64_t K, int64_t T, int64_t R, bool up, bool lora) {
-    const Plan p = plan_of(E, M, K, R, lora);
+    const Plan p = plan_of(E, M, K, R, up, lora);
     const size_t mats = up ? 2 : 1;
     if (p.tiles)
         return tile_rows_bytes(T, K) + round16((size_t)T * 4) +
@@ -851,11 +884,12 @@ size_t ragged_ws_bytes(int64_t E, int64_t M, int64_t K, int64_t T, int64_t R, bo
 }
 
 bool ragged_takes_pieces(int64_t E, int64_t M, int64_t K, int64_t R, bool lora) {
-    const Plan p = plan_of(E, M, K, R, lora);
-    return !p.tiles && p.pre;
+    return plan_of(E, M, K, R, false, lora).pre;
 }
 
-bool ragged_shrinks(int64_t E, int64_t M, int64_t K, int64_t R) { return plan_of(E, M, K, R, true).single; }
+bool ragged_shrinks(int64_t E, int64_t M, int64_t K, int64_t R) {
+    return plan_of(E, M, K, R, false, true).single;
+}
 
 template <int MT>
 static const void *tile_fn(bool up, bool lora) {
@@ -875,18 +909,20 @@ static const void *row_fn(bool up, bool part, bool lora) {
 
 template <int NT, bool PRE>
 static const void *chunk_fn(bool up, bool part, bool lora) {
-    if (up)
-        return part ? reinterpret_cast<const void *>(&ragged_chunk_kernel<NT, 2, true, false, PRE>)
-                    : reinterpret_cast<const void *>(&ragged_chunk_kernel<NT, 2, false, false, PRE>);
+    // Chunks of 16 rows converted before are those beside adapters, and have one matrix.
+    if constexpr (NT == 2 || !PRE)
+        if (up)
+            return part ? reinterpret_cast<const void *>(&ragged_chunk_kernel<NT, 2, true, false, PRE>)
+                        : reinterpret_cast<const void *>(&ragged_chunk_kernel<NT, 2, false, false, PRE>);
     if (part) return reinterpret_cast<const void *>(&ragged_chunk_kernel<NT, 1, true, false, PRE>);
     if constexpr (PRE)
-        if (lora) return reinterpret_cast<const void *>(&ragged_chunk_kernel<NT, 1, false, true, true>);
-    return reinterpret_cast<const void *>(&ragged_chunk_kernel<NT, 1, false, false, PRE>);
+        if (NT == 1 || lora) return reinterpret_cast<const void *>(&ragged_chunk_kernel<NT, 1, false, true, true>);
+    if constexpr (NT == 2 || !PRE) return reinterpret_cast<const void *>(&ragged_chunk_kernel<NT, 1, false, false, PRE>);
 }
 
 hipError_t launch_ragged(const RaggedProduct &p, void *workspace, hipStream_t stream) {
     const bool up = p.up_codes != nullptr, lora = p.B != nullptr;
-    const Plan pl = plan_of(p.E, p.M, p.K, p.R, lora);
+    const Plan pl = plan_of(p.E, p.M, p.K, p.R, up, lora);
     Args a = {};
     a.codes[0] = p.codes;
     a.codes[1] = p.up_codes;
@@ -984,9 +1020,9 @@ hipError_t launch_ragged(const RaggedProduct &p, void *workspace, hipStream_t st
         const int64_t ntiles = (p.M + tile_rows - 1) / tile_rows * chunks;
         if (wgs > ntiles) wgs = ntiles;
         if (wgs < chunks) wgs = chunks;
-        const void *fn = pl.cap == 16
-                             ? pl.pre ? chunk_fn<1, true>(up, part, lora) : chunk_fn<1, false>(up, part, lora)
-                             : pl.pre ? chunk_fn<2, true>(up, part, lora) : chunk_fn<2, false>(up, part, lora);
+        const void *fn = pl.cap == 32 ? chunk_fn<2, true>(up, part, lora)
+                         : pl.pre     ? chunk_fn<1, true>(up, part, lora)
+                                      : chunk_fn<1, false>(up, part, lora);
         e = hipLaunchKernel(fn, dim3((unsigned)wgs, (unsigned)pl.ranges), dim3(kChunkWaves * 64), args, 0, stream);
     }
     if (e != hipSuccess || !part) return e;

@@ -98,10 +98,10 @@ def test_grouped_refusals(q4):
     # the tile kernel's workspace, and the partial planes of long rows
     assert q4.q4_gemm_grouped_ws_bytes(4, 32, 128, 5, 10, False) == 0
     assert q4.q4_gemm_grouped_ws_bytes(4, 32, 2112, 5, 10, True) == 2 * 2 * 10 * 32 * 4
-    assert q4.q4_gemm_grouped_ws_bytes(4, 32, 128, 5, 20, False) >= 20 * 128 * 2 + 20 * 4
-    need = q4.q4_gemm_grouped_ws_bytes(1, 32, 128, 500, 500, False)
+    assert q4.q4_gemm_grouped_ws_bytes(1, 32, 128, 5, 20, False) >= 20 * 128 * 2 + 20 * 4
+    need = q4.q4_gemm_grouped_ws_bytes(1, 32, 128, 500, 2000, False)
     assert need >= 500 * 128 * 2 + 500 * 4 + 32
-    kw = dict(E=1, T=500, R=500)
+    kw = dict(E=1, T=500, R=2000)
     assert _grouped(q4, **kw) == q4.Q4_ERR_WORKSPACE
     assert _grouped(q4, ws=P(9), nb=need - 1, **kw) == q4.Q4_ERR_WORKSPACE
     assert _grouped(q4, ws=P(9) + 8, nb=need, **kw) == q4.Q4_ERR_ALIGN
@@ -111,8 +111,8 @@ def test_grouped_refusals(q4):
 def test_grouped_workspace_without_rows(q4):
     """With no row of X every position reads as zeros; the tile kernel reads a
     row of its workspace for them all the same, so one row is held."""
-    with_one = q4.q4_gemm_grouped_ws_bytes(1, 32, 131072 // 2, 1, 500, False)
-    without = q4.q4_gemm_grouped_ws_bytes(1, 32, 131072 // 2, 0, 500, False)
+    with_one = q4.q4_gemm_grouped_ws_bytes(1, 32, 131072 // 2, 1, 2000, False)
+    without = q4.q4_gemm_grouped_ws_bytes(1, 32, 131072 // 2, 0, 2000, False)
     assert with_one - without == 16 and without >= 131072
 
 

@@ -158,11 +158,16 @@ GROUPED = [
     (2, 40, 2112, [5, 1], 4),             # two ranges of K
     (2, 31, 4160, [40, 3], 9),            # three ranges, two chunks
     (66, 17, 64, [1] * 66, 10),           # more experts than lanes
-    (2, 300, 256, [130, 129], 200),       # tile kernel, two pieces a group
+    (2, 300, 256, [130, 129], 200),       # many chunks a group
     (3, 129, 448, [200, 0, 70], 64),
-    (1, 520, 128, [257], 300),            # tile kernel of 256 rows
+    (1, 520, 128, [257], 300),
     (4, 257, 320, [513, 1, 0, 600], 333),
     (2, 128, 2112, [100, 90], 100),
+    (2, 5500, 128, [150, 200], 90),       # tile kernel, 128 rows a piece
+    (1, 129, 448, [1100], 300),
+    (3, 40, 2112, [1500, 0, 1300], 64),
+    (1, 1030, 64, [8300], 2000),          # 256 rows a piece
+    (2, 700, 192, [6100, 6300], 500),
 ]
 
 
@@ -174,7 +179,7 @@ def test_grouped(env, E, M, K, sizes, T, up):
             _grouped_case(env, E, M, K, sizes, T, up, gather, out_bf16, seed=E * 100 + M + K, tail=3)
 
 
-@pytest.mark.parametrize("sizes", [[3, 1], [150, 140]])
+@pytest.mark.parametrize("sizes", [[3, 1], [150, 140], [1100, 1200]])
 def test_grouped_scales_of_every_magnitude(env, sizes):
     _grouped_case(env, 2, 66, 512, sizes, 64, False, True, False, seed=11, small=True)
 
@@ -184,7 +189,7 @@ def test_grouped_rows_outside_and_values_that_are_not_finite(env):
     activation row leaves every other row's outputs as they were."""
     torch, q4, dev = env
     rng = np.random.default_rng(3)
-    for sizes in ([4, 5], [200, 190]):
+    for sizes in ([4, 5], [200, 190], [1100, 1050]):
         E, M, K, T = 2, 50, 256, 30
         R = sum(sizes)
         codes, scales = _packed(rng, E, M, K)
@@ -208,7 +213,7 @@ def test_grouped_rows_outside_and_values_that_are_not_finite(env):
         assert torch.isfinite(y2).all()
 
 
-@pytest.mark.parametrize("R", [3, 20, 300])
+@pytest.mark.parametrize("R", [2, 3, 20, 300, 2200])
 def test_grouped_without_rows(env, R):
     """No row of X at all: every index is outside, every output is zero."""
     torch, q4, dev = env
@@ -228,7 +233,7 @@ def test_grouped_on_another_stream_and_captured(env):
     own do not meet."""
     torch, q4, dev = env
     rng = np.random.default_rng(8)
-    for sizes, K in (([3, 5], 2112), ([120, 140], 256)):
+    for sizes, K in (([3, 5], 2112), ([120, 140], 256), ([1100, 1040], 256)):
         E, M, R = 2, 200, sum(sizes)
         codes, scales = (_dev(env, a) for a in _packed(rng, E, M, K))
         off = _dev(env, _groups(rng, E, sizes))

@@ -66,11 +66,15 @@ SHAPES = [
     (64, 2048, 32, 16, 9),
     (40, 2112, 3, 24, 2),      # two ranges of K
     (257, 192, 64, 32, 5),
-    (130, 320, 65, 40, 3),     # tile kernel, the shared first product
+    (130, 320, 65, 40, 3),
     (96, 448, 161, 64, 4),
     (300, 128, 300, 128, 2),
     (523, 192, 513, 16, 6),
     (2048, 128, 100, 8, 1),
+    (50, 2112, 2, 16, 2),
+    (64, 2048, 1000, 128, 2),  # a first product of 16 tokens a piece before chunks
+    (130, 320, 1300, 40, 3),   # tile kernel, the shared first product
+    (1030, 128, 8300, 72, 3),  # 256 rows a piece
 ]
 
 
@@ -105,7 +109,7 @@ def test_backward(env, M, K, N, r, L, ids):
     assert torch.equal(two[1], dA) and torch.equal(two[2], dB)
 
 
-@pytest.mark.parametrize("N", [5, 200])
+@pytest.mark.parametrize("N", [5, 200, 1100])
 def test_scales_of_every_magnitude(env, N):
     torch, q4, dev = env
     c = Case(env, 90, 256, N, 8, 2, seed=4, spread=True)
@@ -153,7 +157,7 @@ def test_no_adapters_and_no_tokens(env):
     assert dX.shape == (0, 128) and not dA.any() and not dB.any()
 
 
-@pytest.mark.parametrize("N", [4, 150])
+@pytest.mark.parametrize("N", [4, 150, 1100])
 def test_one_token_that_is_not_finite(env, N):
     torch, q4, dev = env
     c = Case(env, 64, 256, N, 16, 2, seed=9, ids="random")
@@ -170,7 +174,7 @@ def test_one_token_that_is_not_finite(env, N):
     assert not torch.isfinite(y1[2]).all() and not torch.isfinite(g1[2].float()).any()
 
 
-@pytest.mark.parametrize("M,K,N", [(200, 2112, 6), (300, 256, 150)])
+@pytest.mark.parametrize("M,K,N", [(200, 2112, 6), (300, 256, 150), (300, 256, 1100)])
 def test_captured_with_other_work_between(env, M, K, N):
     torch, q4, dev = env
     c = Case(env, M, K, N, 16, 3, seed=N)
