@@ -53,7 +53,7 @@ int q4_route_topk(const void *logits, int logits_type, int64_t T, int64_t E, int
 
 size_t q4_gemm_grouped_ws_bytes(int64_t E, int64_t M, int64_t K, int64_t T, int64_t R, int has_up) {
     if (!grouped_shape_ok(E, M, K, T, R, has_up != 0) || M == 0 || R == 0) return 0;
-    return q4::ragged_ws_bytes(E, M, K, T, R, has_up != 0, false);
+    return q4::ragged_ws_bytes(E, M, K, T, R, has_up != 0, 0);
 }
 
 int q4_gemm_grouped(const uint8_t *codes, const uint16_t *scales, const uint8_t *up_codes, const uint16_t *up_scales,
@@ -77,7 +77,7 @@ int q4_gemm_grouped(const uint8_t *codes, const uint16_t *scales, const uint8_t 
                          range_of(rows, (uint64_t)R * 4)};
     Range out[2] = {range_of(Y, (uint64_t)R * M * elt(out_type)), {0, 0}};
     if (clash(out, 1, in, 7)) return Q4_ERR_OVERLAP;
-    const size_t need = q4::ragged_ws_bytes(E, M, K, T, R, up, false);
+    const size_t need = q4::ragged_ws_bytes(E, M, K, T, R, up, 0);
     if (need > 0) {
         if (!workspace || workspace_bytes < need) return Q4_ERR_WORKSPACE;
         if (!aligned(workspace, 16)) return Q4_ERR_ALIGN;

@@ -30,8 +30,7 @@ struct ShrinkArgs {
     float *t;
 };
 
-constexpr int64_t kTokens = 1024;           // tokens on their own at most,
-constexpr int64_t kTokenBytes = 256 << 20;  // and the adapters' bytes that they may read
+constexpr int kTokens = 1024;  // tokens on their own at most; products that take pieces have no more
 
 // Few tokens: a workgroup takes one token and 4 ranks, a wave a rank.  The
 // workgroups behind those write the packed product's activations as pieces.
@@ -137,19 +136,17 @@ hipError_t launch_shrink(const ShrinkArgs &s, Pieces pieces, hipStream_t stream)
     const bool vec = a.K % 8 == 0;
     // A token of its own workgroups reads its adapter alone: many short waits
     // at once, but an adapter's bytes for every token; 16 tokens that share a
-    // workgroup read it once for all that use it.  With the product, K = 2048
-    // (tokens alone | 16 together): 512 tokens of rank 16 71.9 | 75.2 us, 4096
-    // 82.8 | 76.8, 512 of rank 64 85.9 | 96.1, 2048 108 | 103.
-    const bool alone = a.N <= 64 || (a.N <= kTokens && (int64_t)a.N * a.r * a.pitch * 2 <= kTokenBytes);
-    if (alone || pieces.x16) {
-        int shrinks = alone ? a.N * ((a.r + 3) / 4) : 0;
+    // workgroup read it once for all that use it.  With the product, in us
+    // (tokens alone | 16 together): K = 2048, 512 tokens of rank 16 71.9 |
+    // 75.2, 4096 82.8 | 76.8, 512 of rank 64 85.9 | 96.1, 2048 108 | 103; K =
+    // 11008, 256 of rank 64 76 | 150, 1024 303 | 316.
+    if (a.N <= kTokens) {
+        int shrinks = a.N * ((a.r + 3) / 4);
         void *targs[] = {&a, &pieces, &shrinks};
-        const hipError_t e =
-            hipLaunchKernel(vec ? reinterpret_cast<const void *>(&lora_shrink_token_kernel<true>)
-                                : reinterpret_cast<const void *>(&lora_shrink_token_kernel<false>),
-                            dim3((unsigned)(shrinks + (pieces.x16 ? pieces_blocks(a.K, a.N) : 0))), dim3(256), targs, 0,
-                            stream);
-        if (alone || e != hipSuccess) return e;
+        return hipLaunchKernel(vec ? reinterpret_cast<const void *>(&lora_shrink_token_kernel<true>)
+                                   : reinterpret_cast<const void *>(&lora_shrink_token_kernel<false>),
+                               dim3((unsigned)(shrinks + (pieces.x16 ? pieces_blocks(a.K, a.N) : 0))), dim3(256),
+                               targs, 0, stream);
     }
     const void *fn;
     if (a.r <= 16)
@@ -706,7 +703,7 @@ bool lora_backward_fits(int64_t M, int64_t K, int64_t N, int64_t L) {
 }
 
 size_t lora_ws_bytes(int64_t M, int64_t K, int64_t N, int64_t r, int64_t L) {
-    return (L > 0 ? round16((size_t)N * r * 4) : 0) + ragged_ws_bytes(1, M, K, N, N, false, L > 0);
+    return (L > 0 ? round16((size_t)N * r * 4) : 0) + ragged_ws_bytes(1, M, K, N, N, false, L > 0 ? r : 0);
 }
 
 hipError_t launch_lora(const LoraCall &c, bool bf16, void *Y, void *workspace, hipStream_t stream) {
@@ -721,7 +718,7 @@ hipError_t launch_lora(const LoraCall &c, bool bf16, void *Y, void *workspace, h
     p.bf16 = bf16;
     p.Y = Y;
     char *w = static_cast<char *>(workspace);
-    if (c.L > 0 && ragged_shrinks(1, c.M, c.K, c.N)) {
+    if (c.L > 0 && ragged_shrinks(1, c.M, c.K, c.N, c.r)) {
         p.A = c.A;
         p.scaling = c.scaling;
         p.t = reinterpret_cast<float *>(w);
@@ -729,7 +726,7 @@ hipError_t launch_lora(const LoraCall &c, bool bf16, void *Y, void *workspace, h
         ShrinkArgs s = {c.X,      c.A, c.scaling, c.ids, (int)c.N, (int)c.K, (int)c.K, (int)c.r, (int)c.L,
                         reinterpret_cast<float *>(w)};
         Pieces pieces = {};
-        if (ragged_takes_pieces(1, c.M, c.K, c.N, true))
+        if (ragged_takes_pieces(1, c.M, c.K, c.N, c.r))
             pieces = pieces_at(c.K, c.N, w + round16((size_t)c.N * c.r * 4));
         const hipError_t e = launch_shrink(s, pieces, stream);
         if (e != hipSuccess) return e;

@@ -32,7 +32,7 @@ struct RaggedProduct {
 
 // Whether the launches of this shape stay within what a grid can hold.
 bool ragged_fits(int64_t E, int64_t M, int64_t K, int64_t T, int64_t R, bool up);
-size_t ragged_ws_bytes(int64_t E, int64_t M, int64_t K, int64_t T, int64_t R, bool up, bool lora);
+size_t ragged_ws_bytes(int64_t E, int64_t M, int64_t K, int64_t T, int64_t R, bool up, int64_t r);
 hipError_t launch_ragged(const RaggedProduct &p, void *workspace, hipStream_t stream);
 
 inline size_t round16(size_t n) { return (n + 15) & ~(size_t)15; }
@@ -56,8 +56,8 @@ inline Pieces pieces_at(int64_t K, int64_t R, void *workspace) {
 // Workgroups that write them: a wave takes a slice of two positions.
 inline int64_t pieces_blocks(int64_t K, int64_t R) { return ((K + 255) / 256 * ((R + 1) / 2) + 3) / 4; }
 // Whether the product itself makes t (written to p.t) beside its first launch.
-bool ragged_shrinks(int64_t E, int64_t M, int64_t K, int64_t R);
-bool ragged_takes_pieces(int64_t E, int64_t M, int64_t K, int64_t R, bool lora);
+bool ragged_shrinks(int64_t E, int64_t M, int64_t K, int64_t R, int64_t r);
+bool ragged_takes_pieces(int64_t E, int64_t M, int64_t K, int64_t R, int64_t r);
 
 // The current device's number of compute units (256 where it cannot be read).
 int compute_units();

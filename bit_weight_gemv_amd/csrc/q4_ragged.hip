@@ -52,6 +52,7 @@ __device__ __forceinline__ float adapter_term(const Args &a, int id, int p, int 
     const uint16_t *b = a.B + ((int64_t)id * a.M + m) * a.r;
     const float *t = a.t + (int64_t)p * a.r;
     float s = 0.0f;
+#pragma unroll 4
     for (int j = j0; j < a.r; j += 8) {
         const uint4 v = *reinterpret_cast<const uint4 *>(b + j);
         const float4 t0 = *reinterpret_cast<const float4 *>(t + j), t1 = *reinterpret_cast<const float4 *>(t + j + 4);
@@ -803,8 +804,9 @@ int64_t chunk_bound(int64_t E, int64_t R, int64_t most) {
     return a < R ? a : R;
 }
 
-// The rules, with what both sides take in us: E x M x K, "up" where there is an up matrix.
-Plan plan_of(int64_t E, int64_t M, int64_t K, int64_t R, bool up, bool lora) {
+// The rules, with what both sides take in us: E x M x K, "up" where there is
+// an up matrix; r ranks of adapters, 0 without.
+Plan plan_of(int64_t E, int64_t M, int64_t K, int64_t R, bool up, int64_t r) {
     Plan p = {};
     const int64_t groups = E < R ? E : R;
     const int64_t avg = groups ? (R + groups - 1) / groups : 0;  // rows a group, were all in use equally full
@@ -837,7 +839,11 @@ Plan plan_of(int64_t E, int64_t M, int64_t K, int64_t R, bool up, bool lora) {
     const int64_t full2 = (chunks(128) * rowtiles + 255) / 256, full4 = (chunks(256) * rowtiles + 255) / 256;
     p.mt = 3 * full4 <= 2 * full2 ? 4 : 2;
     const int64_t tile_cost = 392000 * (2 * full2 < 3 * full4 ? 2 * full2 : 3 * full4);
-    const int64_t chunk_cost = chunks(p.cap) * M * mats * (p.cap == 16 ? 4 : 9);
+    // (Ranks past 16 are products on the vector units in the chunk kernel, and
+    // on the matrix units in the tile kernel: 1 x 11008 x 2048 of rank 64, R =
+    // 192 84 | 60.)
+    const int64_t chunk_cost =
+        chunks(p.cap) * M * mats * (p.cap == 16 ? 4 : 9) + (r > 16 ? R * M * (r - 16) * 15 / K : 0);
     p.tiles = !p.single && avg > 32 &&
               (avg > 1024 || chunk_cost > tile_cost || (M + 255) / 256 * R >= INT64_C(1) << 24);
     // A launch that converts the activations first, against a conversion in
@@ -845,7 +851,7 @@ Plan plan_of(int64_t E, int64_t M, int64_t K, int64_t R, bool up, bool lora) {
     // 512 79.0 | 76.0, 1024 105 | 101, 1 x 4096 x 4096, R = 32 14.3 | 13.4; of
     // 16, 64 x 2048 x 1408, R = 48 17.5 | 19.6, 512 32.0 | 34.2.  Adapters
     // have a launch before the product anyhow, and it does both.
-    p.pre = !p.single && !p.tiles && (lora || p.cap == 32);
+    p.pre = !p.single && !p.tiles && (r > 0 || p.cap == 32);
     p.ranges = p.single ? (int)((K + kRowRangeK - 1) / kRowRangeK)
                        : (int)((slices_of(K) + kChunkWaves - 1) / kChunkWaves);
     return p;
@@ -865,7 +871,7 @@ int compute_units() {
 }
 
 bool ragged_fits(int64_t E, int64_t M, int64_t K, int64_t T, int64_t R, bool up) {
-    const Plan p = plan_of(E, M, K, R, up, false);
+    const Plan p = plan_of(E, M, K, R, up, 0);
     const int64_t most = INT64_C(1) << 32;  // threads of one launch
     if (p.tiles) {
         const int64_t rowtiles = (M + (up ? 127 : 255)) / (up ? 128 : 256);
@@ -874,21 +880,21 @@ bool ragged_fits(int64_t E, int64_t M, int64_t K, int64_t T, int64_t R, bool up)
     return ((M + 255) / 256) * R * 256 < most && chunk_bound(E, R, p.single ? 1 : p.cap) < 65536;
 }
 
-size_t ragged_ws_bytes(int64_t E, int64_t M, int64_t K, int64_t T, int64_t R, bool up, bool lora) {
-    const Plan p = plan_of(E, M, K, R, up, lora);
+size_t ragged_ws_bytes(int64_t E, int64_t M, int64_t K, int64_t T, int64_t R, bool up, int64_t r) {
+    const Plan p = plan_of(E, M, K, R, up, r);
     const size_t mats = up ? 2 : 1;
     if (p.tiles)
         return tile_rows_bytes(T, K) + round16((size_t)T * 4) +
                mats * (round16((size_t)E * M) + round16((size_t)E * M * (K / 64) * 2));
-    return (p.pre ? pieces_bytes(K, R) : 0) + (p.ranges > 1 || (p.single && lora) ? mats * p.ranges * (size_t)R * M * 4 : 0);
+    return (p.pre ? pieces_bytes(K, R) : 0) + (p.ranges > 1 || (p.single && r > 0) ? mats * p.ranges * (size_t)R * M * 4 : 0);
 }
 
-bool ragged_takes_pieces(int64_t E, int64_t M, int64_t K, int64_t R, bool lora) {
-    return plan_of(E, M, K, R, false, lora).pre;
+bool ragged_takes_pieces(int64_t E, int64_t M, int64_t K, int64_t R, int64_t r) {
+    return plan_of(E, M, K, R, false, r).pre;
 }
 
-bool ragged_shrinks(int64_t E, int64_t M, int64_t K, int64_t R) {
-    return plan_of(E, M, K, R, false, true).single;
+bool ragged_shrinks(int64_t E, int64_t M, int64_t K, int64_t R, int64_t r) {
+    return plan_of(E, M, K, R, false, r).single;
 }
 
 template <int MT>
@@ -922,7 +928,7 @@ static const void *chunk_fn(bool up, bool part, bool lora) {
 
 hipError_t launch_ragged(const RaggedProduct &p, void *workspace, hipStream_t stream) {
     const bool up = p.up_codes != nullptr, lora = p.B != nullptr;
-    const Plan pl = plan_of(p.E, p.M, p.K, p.R, up, lora);
+    const Plan pl = plan_of(p.E, p.M, p.K, p.R, up, lora ? p.r : 0);
     Args a = {};
     a.codes[0] = p.codes;
     a.codes[1] = p.up_codes;

@@ -72,7 +72,7 @@ SHAPES = [
     (523, 192, 513, 16, 6),
     (2048, 128, 100, 8, 1),
     (50, 2112, 2, 16, 2),
-    (64, 2048, 1000, 128, 2),  # a first product of 16 tokens a piece before chunks
+    (64, 2048, 1000, 128, 2),  # many chunks, the largest rank
     (130, 320, 1300, 40, 3),   # tile kernel, the shared first product
     (1030, 128, 8300, 72, 3),  # 256 rows a piece
 ]
