@@ -78,7 +78,10 @@ int q4_gemm_lora_backward(const uint16_t *dY, const uint8_t *codes, const uint16
         !aligned(dA, 16) || !aligned(dB, 16))
         return Q4_ERR_ALIGN;
     if (L > 0 && (!aligned(A, 16) || !aligned(B, 16) || !aligned(scaling, 4) || !aligned(ids, 4))) return Q4_ERR_ALIGN;
-    if (L == 0) r = 0;
+    if (L == 0) {
+        r = 0;
+        if (!dX) return Q4_OK;  // (gradients of no adapter)
+    }
     const Range in[8] = {range_of(dY, (uint64_t)N * M * 2),
                          range_of(codes, (uint64_t)M * (K / 2)),
                          range_of(scales, (uint64_t)M * (K / 64) * 2),

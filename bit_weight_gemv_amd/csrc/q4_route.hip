@@ -11,6 +11,13 @@
 // own slots (a wave at a time, by ballots over the expert's bits).  A run
 // that holds every slot needs one launch.  No atomics on memory: the same
 // input gives the same plan.
+//
+// Measured (graph replay): 1 token, 64 experts, top 8 5.1 us in one launch (an
+// empty kernel takes 1.6; the k maxima and the ranks come one after the
+// other).  8192 tokens, 128 experts, top 8 14.2 us in two launches (6.8 + 7.4
+// by themselves) for 5.2 MB: bound by the k rounds of maxima, 6 DPP steps and
+// 8 compares a lane each, and by the ballots of the ranks, not by the bytes
+// (1 us).  With a wave a token it took 29 us.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -301,7 +308,9 @@ struct CombineArgs {
 };
 
 // A lane adds 8 neighbouring columns (VEC: rows of whole 16-byte pieces) or
-// one.
+// one: 4096 tokens x 8 rows of 2048, 151 MB, take 23.1 us (6.5 TB/s, most of it
+// from the Infinity Cache) with 8 columns and 66.5 with one.  Bound by the
+// bytes; one token's 8 rows by the launch (3.8 us).
 template <bool VEC>
 __global__ __launch_bounds__(256) void combine_kernel(const CombineArgs a) {
     constexpr int W = VEC ? 8 : 1;

@@ -195,6 +195,9 @@ def test_lora_backward_refusals(q4):
     assert need > 0
     assert _back(q4, ws=None) == q4.Q4_ERR_WORKSPACE and _back(q4, nb=need - 1) == q4.Q4_ERR_WORKSPACE
     assert _back(q4, ws=P(9)) == q4.Q4_ERR_OVERLAP
+    p = [P(j) for j in range(11)]
+    p[8] = None
+    assert _back(q4, p=p, L=0, ws=None) == q4.Q4_OK   # gradients of no adapter: nothing to launch
 
 
 def test_binding_refusals(q4):
