@@ -543,7 +543,9 @@ struct TileShared {
     int sid[LORA ? 64 * MT : 1];
 };
 
-template <int MT, int MATS, bool LORA>
+// PART: a workgroup takes one of a.ranges runs of 64-blocks (blockIdx.y) and
+// writes fp32 sums to that run's plane, the adapters' term with the first.
+template <int MT, int MATS, bool LORA, bool PART>
 __global__ __launch_bounds__(kTileWaves * 64) void ragged_tile_kernel(const Args a) {
     constexpr int TM = 64 * MT;
     constexpr int kRowsWg = MATS == 2 ? 128 : 256;
@@ -590,14 +592,19 @@ __global__ __launch_bounds__(kTileWaves * 64) void ragged_tile_kernel(const Args
     const u32x4_t *csrc[2];
     const uint16_t *ssrc[2];
     int e[2];
-    const int nb = a.K >> 6;
+    const int b0 = PART ? (a.K >> 6) * (int)blockIdx.y / a.ranges : 0;  // the first block
+    const int nb = (PART ? (a.K >> 6) * ((int)blockIdx.y + 1) / a.ranges : a.K >> 6) - b0;
+    if constexpr (PART) {
+#pragma unroll
+        for (int j = 0; j < kPieces; ++j) xsrc[j] += 8 * b0;
+    }
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
         const int mat = MATS == 2 ? q : 0;
         m[q] = rt0 * kRowsWg + (MATS == 2 ? wr * 32 : wr * 64 + q * 32) + col;
         const int64_t mrow = (int64_t)ck.e * a.M + min(m[q], a.M - 1);
-        csrc[q] = reinterpret_cast<const u32x4_t *>(a.codes[mat] + mrow * (a.K >> 1)) + g;
-        ssrc[q] = a.tscale[mat] + (int64_t)ck.e * nb * a.M + min(m[q], a.M - 1);
+        csrc[q] = reinterpret_cast<const u32x4_t *>(a.codes[mat] + mrow * (a.K >> 1)) + g + 2 * b0;
+        ssrc[q] = a.tscale[mat] + ((int64_t)ck.e * (a.K >> 6) + b0) * a.M + min(m[q], a.M - 1);
         e[q] = a.rowexp[mat][mrow];
     }
 
@@ -742,7 +749,7 @@ __global__ __launch_bounds__(kTileWaves * 64) void ragged_tile_kernel(const Args
         const int w0 = wt * 32 * MT;
         if (lane < 32 * MT) mine[0] = sid[w0 + lane];
         if (MT == 4) mine[1] = sid[w0 + 64 + lane];
-        while (true) {
+        while (!PART || blockIdx.y == 0) {
             const uint64_t p0 = __builtin_amdgcn_ballot_w64(mine[0] >= 0);
             const uint64_t p1 = __builtin_amdgcn_ballot_w64(mine[1] >= 0);
             if (!(p0 | p1)) break;
@@ -792,7 +799,13 @@ __global__ __launch_bounds__(kTileWaves * 64) void ragged_tile_kernel(const Args
             const int row = wt * 32 * MT + 32 * i + tile_row(j, lane);
             if (row >= ck.count) continue;
             const int64_t at = (int64_t)(ck.start + row) * a.M;
-            if constexpr (MATS == 2) {
+            if constexpr (PART) {
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const int64_t plane = (MATS == 2 ? q * a.ranges : 0) + (int)blockIdx.y;
+                    if (m[q] < a.M) a.part[plane * a.R * a.M + at + m[q]] = acc[i][q][j];
+                }
+            } else if constexpr (MATS == 2) {
                 if (m[0] < a.M) store_out(a.Y, a.bf16, at + m[0], swiglu(acc[i][0][j], acc[i][1][j]));
             } else {
                 if (m[0] < a.M) store_out(a.Y, a.bf16, at + m[0], acc[i][0][j]);
@@ -810,7 +823,7 @@ struct Plan {
     int mt;       // tile kernel: 32-row tiles a wave
     int cap;      // chunk kernel: rows a chunk
     bool pre;     // chunk kernel: the activations are converted by a launch before
-    int ranges;   // chunk kernel: ranges of K
+    int ranges;   // ranges of K, each with planes of partial sums (1: none but beside the row kernel's adapters)
 };
 
 // Chunks of `most` rows that R rows in E groups can make at most.
@@ -845,15 +858,30 @@ Plan plan_of(int64_t E, int64_t M, int64_t K, int64_t R, bool up, int64_t r) {
     // The chunk kernel's time goes with chunks x M, the tile kernel's (with 64
     // or 128 rows for each of two waves, mt 2 or 4) with the times that its
     // workgroups fill the 256 compute units, each a walk along K: in units of
-    // 1.8 ns for 64 weights of K.  Chunk | mt 2 | mt 4 for 1 x 11008 x 2048, R =
-    // 128 30 | 51 | 67, 256 52 | 53 | 71, 512 93 | 55 | 72, 1024 - | 101 | 78,
-    // 4096 - | 290 | 228; 1 x 2048 x 11008, R = 128 34 | 235 | 289, 512 113 |
-    // 226 | 299; 64 x 1408 x 2048 up, R = 1024 101 | - | -, 2048 146 | 149 |
+    // 1.8 ps for 64 weights of K (a us is 35.8e6 / K of them).  Chunk | mt 2 |
+    // mt 4 for 1 x 11008 x 2048, R = 128 30 | 51 | 67, 256 52 | 53 | 71, 512 93 | 55 | 72, 1024 - | 101 | 78,
+    // 4096 - | 290 | 228; 64 x 1408 x 2048 up, R = 1024 101 | - | -, 2048 146 | 149 |
     // 205, 4096 285 | 191 | 217, 16384 809 | 340 | 355, 32768 - | 615 | 524.
     const int64_t mats = up ? 2 : 1, rowtiles = (M * mats + 255) / 256;
     const int64_t full2 = (chunks(128) * rowtiles + 255) / 256, full4 = (chunks(256) * rowtiles + 255) / 256;
     p.mt = 3 * full4 <= 2 * full2 ? 4 : 2;
-    const int64_t tile_cost = 392000 * (2 * full2 < 3 * full4 ? 2 * full2 : 3 * full4);
+    int64_t tile_cost = 392000 * (2 * full2 < 3 * full4 ? 2 * full2 : 3 * full4) + 143000000 / K;
+    // Workgroups that leave half of the compute units empty share the walk
+    // along K, at the price of the planes' bytes and of the launch that adds
+    // them (8 us more).  Chunk | 1 run | 2 | 4 | 8 for 1 x 2048 x 11008, R = 256
+    // 54 | 207 | 120 | 77 | 56, 1024 219 | 220 | 142 | 111 | -; 1 x 4096 x 4096
+    // of rank 64, R = 128 34 | 96 | 67 | 51 | 44, 512 104 | 105 | 79 | 69 | -;
+    // 1 x 2048 x 2048, R = 512 25 | 50 | 41 | 36 | 36; 1 x 11008 x 2048, R = 256
+    // 52 | 53 | 44 | - | -.
+    const int64_t wgs = chunks(128) * rowtiles;
+    int splits = 1;
+    for (int64_t s = 2; s <= 16 && wgs * s <= 256 && K / 64 >= 4 * s; ++s) {
+        const int64_t cost = 700000 / s + (R * M * mats * s * 60 + 430000000) / K;
+        if (cost < tile_cost) {
+            tile_cost = cost;
+            splits = (int)s;
+        }
+    }
     // (Ranks past 16 are products on the vector units in the chunk kernel, and
     // on the matrix units in the tile kernel: 1 x 11008 x 2048 of rank 64, R =
     // 192 84 | 60.)
@@ -867,8 +895,10 @@ Plan plan_of(int64_t E, int64_t M, int64_t K, int64_t R, bool up, int64_t r) {
     // 16, 64 x 2048 x 1408, R = 48 17.5 | 19.6, 512 32.0 | 34.2.  Adapters
     // have a launch before the product anyhow, and it does both.
     p.pre = !p.single && !p.tiles && (r > 0 || p.cap == 32);
-    p.ranges = p.single ? (int)((K + kRowRangeK - 1) / kRowRangeK)
-                       : (int)((slices_of(K) + kChunkWaves - 1) / kChunkWaves);
+    p.ranges = p.tiles    ? splits
+               : p.single ? (int)((K + kRowRangeK - 1) / kRowRangeK)
+                          : (int)((slices_of(K) + kChunkWaves - 1) / kChunkWaves);
+    if (p.tiles && splits > 1) p.mt = 2;
     return p;
 }
 
@@ -900,7 +930,8 @@ size_t ragged_ws_bytes(int64_t E, int64_t M, int64_t K, int64_t T, int64_t R, bo
     const size_t mats = up ? 2 : 1;
     if (p.tiles)
         return tile_rows_bytes(T, K) + round16((size_t)T * 4) +
-               mats * (round16((size_t)E * M) + round16((size_t)E * M * (K / 64) * 2));
+               mats * (round16((size_t)E * M) + round16((size_t)E * M * (K / 64) * 2)) +
+               (p.ranges > 1 ? mats * p.ranges * (size_t)R * M * 4 : 0);
     return (p.pre ? pieces_bytes(K, R) : 0) + (p.ranges > 1 || (p.single && r > 0) ? mats * p.ranges * (size_t)R * M * 4 : 0);
 }
 
@@ -912,11 +943,11 @@ bool ragged_shrinks(int64_t E, int64_t M, int64_t K, int64_t R, int64_t r) {
     return plan_of(E, M, K, R, false, r).single;
 }
 
-template <int MT>
+template <int MT, bool PART>
 static const void *tile_fn(bool up, bool lora) {
-    if (up) return reinterpret_cast<const void *>(&ragged_tile_kernel<MT, 2, false>);
-    return lora ? reinterpret_cast<const void *>(&ragged_tile_kernel<MT, 1, true>)
-                : reinterpret_cast<const void *>(&ragged_tile_kernel<MT, 1, false>);
+    if (up) return reinterpret_cast<const void *>(&ragged_tile_kernel<MT, 2, false, PART>);
+    return lora ? reinterpret_cast<const void *>(&ragged_tile_kernel<MT, 1, true, PART>)
+                : reinterpret_cast<const void *>(&ragged_tile_kernel<MT, 1, false, PART>);
 }
 
 static const void *row_fn(bool up, bool part, bool lora) {
@@ -939,6 +970,15 @@ static const void *chunk_fn(bool up, bool part, bool lora) {
     if constexpr (PRE)
         if (NT == 1 || lora) return reinterpret_cast<const void *>(&ragged_chunk_kernel<NT, 1, false, true, true>);
     if constexpr (NT == 2 || !PRE) return reinterpret_cast<const void *>(&ragged_chunk_kernel<NT, 1, false, false, PRE>);
+}
+
+// Adds the planes (and, with lora, the adapters' terms).
+static hipError_t launch_finish(Args a, bool up, bool lora, hipStream_t stream) {
+    const void *fin = up     ? reinterpret_cast<const void *>(&ragged_finish_kernel<2, false>)
+                      : lora ? reinterpret_cast<const void *>(&ragged_finish_kernel<1, true>)
+                             : reinterpret_cast<const void *>(&ragged_finish_kernel<1, false>);
+    void *args[] = {&a};
+    return hipLaunchKernel(fin, dim3((unsigned)(((int64_t)a.M + 255) / 256 * a.R)), dim3(256), args, 0, stream);
 }
 
 hipError_t launch_ragged(const RaggedProduct &p, void *workspace, hipStream_t stream) {
@@ -995,9 +1035,15 @@ hipError_t launch_ragged(const RaggedProduct &p, void *workspace, hipStream_t st
         const int rows_wg = up ? 128 : 256;
         a.rowtiles = (int)((p.M + rows_wg - 1) / rows_wg);
         a.chunks = (int)chunk_bound(p.E, p.R, 64 * pl.mt);
-        const void *fn = pl.mt == 4 ? tile_fn<4>(up, lora) : tile_fn<2>(up, lora);
-        return hipLaunchKernel(fn, dim3((unsigned)(((int64_t)a.rowtiles * a.chunks + 7) / 8 * 8)), dim3(kTileWaves * 64),
-                               args, 0, stream);
+        const bool part = pl.ranges > 1;
+        a.ranges = pl.ranges;
+        a.part = part ? reinterpret_cast<float *>(w + sb * (up ? 2 : 1)) : nullptr;
+        const void *fn = part         ? tile_fn<2, true>(up, lora)
+                         : pl.mt == 4 ? tile_fn<4, false>(up, lora)
+                                      : tile_fn<2, false>(up, lora);
+        e = hipLaunchKernel(fn, dim3((unsigned)(((int64_t)a.rowtiles * a.chunks + 7) / 8 * 8), (unsigned)pl.ranges),
+                            dim3(kTileWaves * 64), args, 0, stream);
+        return e != hipSuccess || !part ? e : launch_finish(a, up, false, stream);
     }
     a.ranges = pl.ranges;
     a.slices_each = (int)(slices_of(p.K) / pl.ranges);
@@ -1046,11 +1092,7 @@ hipError_t launch_ragged(const RaggedProduct &p, void *workspace, hipStream_t st
                                       : chunk_fn<1, false>(up, part, lora);
         e = hipLaunchKernel(fn, dim3((unsigned)wgs, (unsigned)pl.ranges), dim3(kChunkWaves * 64), args, 0, stream);
     }
-    if (e != hipSuccess || !part) return e;
-    const void *fin = up     ? reinterpret_cast<const void *>(&ragged_finish_kernel<2, false>)
-                      : lora ? reinterpret_cast<const void *>(&ragged_finish_kernel<1, true>)
-                             : reinterpret_cast<const void *>(&ragged_finish_kernel<1, false>);
-    return hipLaunchKernel(fin, dim3((unsigned)((p.M + 255) / 256 * p.R)), dim3(256), args, 0, stream);
+    return e != hipSuccess || !part ? e : launch_finish(a, up, lora, stream);
 }
 
 }  // namespace q4

@@ -166,6 +166,8 @@ GROUPED = [
     (2, 5500, 128, [150, 200], 90),       # tile kernel, 128 rows a piece
     (1, 129, 448, [1100], 300),
     (3, 40, 2112, [1500, 0, 1300], 64),
+    (2, 40, 2112, [3000, 100], 64),       # tile kernel, eight runs of K
+    (1, 300, 512, [1200], 100),           # one run
     (1, 1030, 64, [8300], 2000),          # 256 rows a piece
     (2, 700, 192, [6100, 6300], 500),
 ]

@@ -75,6 +75,7 @@ SHAPES = [
     (64, 2048, 1000, 128, 2),  # many chunks, the largest rank
     (130, 320, 1300, 40, 3),   # tile kernel, the shared first product
     (1030, 128, 8300, 72, 3),  # 256 rows a piece
+    (300, 1088, 1100, 24, 2),  # runs of K
 ]
 
 
