@@ -425,7 +425,10 @@ __global__ __launch_bounds__(512) void lora_dx_kernel(const DxArgs a) {
         }
     const int k = kt * 256 + wk * 64 + 2 * col;  // this lane's two columns
 
-    if (!a.part) {
+    // With planes the first of them takes the adapters' term; with few tokens,
+    // each of which may have an adapter of its own, the launch that adds the
+    // planes makes it for all tokens at once.
+    if (!a.part || (MT > 1 && blockIdx.y == 0)) {
         int mine[2] = {-1, -1};
         const int w0 = wt * 32 * MT;
         mine[0] = sid[w0 + (lane & (32 * MT - 1))];
@@ -494,31 +497,32 @@ __global__ __launch_bounds__(512) void lora_dx_kernel(const DxArgs a) {
         }
 }
 
-// Adds the partial planes in order, and the adapter's term; two columns a lane.
+// Adds the partial planes in order, and the adapter's term where there are few
+// tokens (L is 0 elsewhere); four columns a lane.
 __global__ __launch_bounds__(256) void lora_dx_finish_kernel(const DxArgs a) {
-    const int per = (a.K + 511) >> 9;
-    const int n = blockIdx.x / per, k = ((blockIdx.x % per) * 256 + threadIdx.x) * 2;
+    const int per = (a.K + 1023) >> 10;
+    const int n = blockIdx.x / per, k = ((blockIdx.x % per) * 256 + threadIdx.x) * 4;
     if (k >= a.K) return;
     const int64_t at = (int64_t)n * a.K + k, plane = (int64_t)a.N * a.K;
-    float2 v = *reinterpret_cast<const float2 *>(a.part + at);
-    for (int z = 1; z < a.splits; ++z) {
-        const float2 o = *reinterpret_cast<const float2 *>(a.part + z * plane + at);
-        v.x += o.x;
-        v.y += o.y;
-    }
+    float4_t v = *reinterpret_cast<const float4_t *>(a.part + at);
+#pragma unroll 4
+    for (int z = 1; z < a.splits; ++z) v += *reinterpret_cast<const float4_t *>(a.part + z * plane + at);
     const int id = a.L > 0 ? a.ids[n] : -1;
     if (id >= 0 && id < a.L) {
-        float s0 = 0.0f, s1 = 0.0f;
+        float4_t s = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 8
         for (int j = 0; j < a.r; ++j) {
-            const uint32_t d = *reinterpret_cast<const uint32_t *>(a.A + ((int64_t)id * a.r + j) * a.K + k);
+            const uint2 d = *reinterpret_cast<const uint2 *>(a.A + ((int64_t)id * a.r + j) * a.K + k);
             const float t = a.u[(int64_t)n * a.r + j];
-            s0 = fmaf(t, bf16_lo(d), s0);
-            s1 = fmaf(t, bf16_hi(d), s1);
+            s[0] = fmaf(t, bf16_lo(d.x), s[0]);
+            s[1] = fmaf(t, bf16_hi(d.x), s[1]);
+            s[2] = fmaf(t, bf16_lo(d.y), s[2]);
+            s[3] = fmaf(t, bf16_hi(d.y), s[3]);
         }
-        v.x += s0;
-        v.y += s1;
+        v += s;
     }
-    *reinterpret_cast<uint32_t *>(a.dX + at) = (uint32_t)f32_bf16(v.x) | (uint32_t)f32_bf16(v.y) << 16;
+    *reinterpret_cast<uint2 *>(a.dX + at) = make_uint2((uint32_t)f32_bf16(v[0]) | (uint32_t)f32_bf16(v[1]) << 16,
+                                                       (uint32_t)f32_bf16(v[2]) | (uint32_t)f32_bf16(v[3]) << 16);
 }
 
 // ---------------------------------------------------------------------------
@@ -809,8 +813,9 @@ hipError_t launch_lora_backward(const LoraCall &c, const uint16_t *dY, uint16_t 
                                 stream);
             if (e != hipSuccess) return e;
             if (p.splits > 1) {
+                if (p.mt > 1) d.L = 0;
                 e = hipLaunchKernel(reinterpret_cast<const void *>(&lora_dx_finish_kernel),
-                                    dim3((unsigned)(c.N * ((c.K + 511) / 512))), dim3(256), dargs, 0, stream);
+                                    dim3((unsigned)(c.N * ((c.K + 1023) / 1024))), dim3(256), dargs, 0, stream);
                 if (e != hipSuccess) return e;
             }
         }
