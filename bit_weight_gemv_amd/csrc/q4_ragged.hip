@@ -298,7 +298,7 @@ __global__ __launch_bounds__(kChunkWaves * 64, NT * MATS == 1 && !LORA ? 4 : 2) 
                 for (int w = 1; w < kChunkWaves; ++w)
                     if (w < ns) v[q] += red[q][w][threadIdx.x];
             }
-            if (!PRE && a.rows && source_row(a, p) < 0) {
+            if (!PRE && source_row(a, p) < 0) {
 #pragma unroll
                 for (int q = 0; q < MATS; ++q) v[q] = 0.0f;
             }

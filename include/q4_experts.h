@@ -73,7 +73,8 @@ int q4_route_topk(const void *logits, int logits_type, int64_t T, int64_t E,
  *   offsets: int32 [E + 1], non-decreasing within 0 .. R.  Positions outside
  *     every group keep what Y held.  (Values outside that contract are held
  *     to 0 .. R: no access leaves the buffers, the results are unspecified.)
- *   rows: int32 [R] or NULL; a row outside [0, T) reads as zeros.
+ *   rows: int32 [R] or NULL; a row outside [0, T) reads as zeros (with rows
+ *     NULL, where R > T: every position from T on).
  *   Y: [R][M] of out_type (Q4_OUT_F32 or Q4_OUT_BF16), 16-byte aligned.
  * Accuracy: each sum is within (2^-10 + (K + 64) 2^-24) * sum_k |What x| +
  * 2^-27 * (max_k |x| * sum_k |What| + max_b |scale_b| * sum_k |x|) of its
