@@ -759,19 +759,20 @@ __global__ __launch_bounds__(kTileWaves * 64) void ragged_tile_kernel(const Args
             if (mine[1] == id) mine[1] = -1;
             for (int j0 = 0; j0 < a.r; j0 += 16) {
                 const bool live = j0 + 8 * g < a.r;
-                bf16x8_t bb[2];
+                u32x4_t bb[2];
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
-                    u32x4_t v = {0u, 0u, 0u, 0u};
+                    bb[q] = u32x4_t{0u, 0u, 0u, 0u};
                     if (live && m[q] < a.M)
-                        v = *reinterpret_cast<const u32x4_t *>(a.B + ((int64_t)id * a.M + m[q]) * a.r + j0 + 8 * g);
-                    bb[q] = __builtin_bit_cast(bf16x8_t, v);
+                        bb[q] = *reinterpret_cast<const u32x4_t *>(a.B + ((int64_t)id * a.M + m[q]) * a.r + j0 + 8 * g);
                 }
+                const bool wild = __builtin_amdgcn_ballot_w64(not_finite8(bb[0]) || not_finite8(bb[1])) != 0;
 #pragma unroll
                 for (int i = 0; i < MT; ++i) {
                     const int row = w0 + 32 * i + col;
                     const bool use = sid[row] == id;
-                    if (__builtin_amdgcn_ballot_w64(use) == 0) continue;
+                    const uint32_t users = (uint32_t)__builtin_amdgcn_ballot_w64(use);
+                    if (users == 0) continue;
                     float t[8];
 #pragma unroll
                     for (int x = 0; x < 8; ++x) t[x] = 0.0f;
@@ -783,10 +784,7 @@ __global__ __launch_bounds__(kTileWaves * 64) void ragged_tile_kernel(const Args
                     bf16x8_t hi, lo;
                     split2(t, hi, lo);
 #pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        acc[i][q] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(hi, bb[q], acc[i][q], 0, 0, 0);
-                        acc[i][q] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(lo, bb[q], acc[i][q], 0, 0, 0);
-                    }
+                    for (int q = 0; q < 2; ++q) add_adapter(acc[i][q], hi, lo, bb[q], wild, users);
                 }
             }
         }

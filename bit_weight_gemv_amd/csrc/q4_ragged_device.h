@@ -255,4 +255,42 @@ __device__ __forceinline__ void split2(const float (&v)[8], bf16x8_t &hi, bf16x8
     }
 }
 
+// Whether one of eight bf16 is an infinity or a NaN, and the eight with those
+// set to 0.
+__device__ __forceinline__ bool not_finite8(const u32x4_t &v) {
+    u16x2_t mx = {0, 0};
+#pragma unroll
+    for (int c = 0; c < 4; ++c) mx = __builtin_elementwise_max(mx, __builtin_bit_cast(u16x2_t, v[c] & 0x7FFF7FFFu));
+    return max((int)mx.x, (int)mx.y) >= 0x7F80;
+}
+__device__ __forceinline__ u32x4_t finite8(u32x4_t v) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        if ((v[c] & 0x7F80u) == 0x7F80u) v[c] &= 0xFFFF0000u;
+        if ((v[c] & 0x7F800000u) == 0x7F800000u) v[c] &= 0xFFFFu;
+    }
+    return v;
+}
+
+// acc (a 32 x 32 tile) += (hi + lo) b, an adapter's term: hi + lo is zero in
+// the rows of tokens that do not use it.  Where the adapter holds an infinity
+// or a NaN (wild, the same in every lane) those zeros would become NaN, and
+// the zeros of lo where hi is exact: then hi's products go to a tile of their
+// own, of which only the rows in `users` (a bit a row) are added, and lo meets
+// the finite values alone.
+__device__ __forceinline__ void add_adapter(float16_t &acc, const bf16x8_t &hi, const bf16x8_t &lo, const u32x4_t &b,
+                                            bool wild, uint32_t users) {
+    if (!wild) {
+        acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(hi, __builtin_bit_cast(bf16x8_t, b), acc, 0, 0, 0);
+        acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(lo, __builtin_bit_cast(bf16x8_t, b), acc, 0, 0, 0);
+        return;
+    }
+    const float16_t d =
+        __builtin_amdgcn_mfma_f32_32x32x16_bf16(hi, __builtin_bit_cast(bf16x8_t, b), float16_t{}, 0, 0, 0);
+    const uint32_t mine = users >> (4 * ((threadIdx.x >> 5) & 1));
+#pragma unroll
+    for (int j = 0; j < 16; ++j) acc[j] = mine >> tile_row(j, 0) & 1 ? acc[j] + d[j] : acc[j];
+    acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(lo, __builtin_bit_cast(bf16x8_t, finite8(b)), acc, 0, 0, 0);
+}
+
 }  // namespace q4

@@ -1,0 +1,49 @@
+"""Calls of the adapters' entry points at the borders of their contract
+(q4_lora.h), on the GPU, against plain 64-bit forms.  The bounds are those of
+tests/ragged_reference.py."""
+import numpy as np
+import pytest
+
+from test_gpu_lora import Case, env  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+# M, K, N, r: the row, chunk and tile kernels, tiles in runs of K, dX with and
+# without planes, ranks of one and of several matrix-core steps.
+MIXED = [(40, 192, 2, 8), (64, 256, 4, 16), (64, 256, 30, 8), (300, 256, 150, 24), (40, 256, 300, 16), (300, 256, 1100, 16),
+         (64, 192, 1100, 8), (300, 1088, 1100, 40), (2048, 128, 1030, 16), (1030, 128, 8300, 24)]
+
+
+def _spoiled(env, M, K, N, r, where):  # noqa: F811
+    """A case of four adapters, and the same call with an infinity or a NaN in
+    two of them: (case, arguments, (A, B, scaling), tokens of the others)."""
+    torch, q4, dev = env
+    c = Case(env, M, K, N, r, 4, seed=M + N + r, ids="random")
+    if N == 2:
+        c.ids = np.array([1, 2], np.int32)
+        c.args = c.args[:6] + (torch.from_numpy(c.ids).to(dev),)
+    A, B, s = (a.copy() for a in (c.A, c.B, c.scaling))
+    if where == "A":
+        A[1, 2, 5], A[2, r - 1, K - 1] = np.inf, -np.inf
+    elif where == "B":
+        B[1, 7, 3], B[2, M - 1, r - 1], B[2, 3, 0] = np.inf, -np.inf, np.nan
+    else:
+        s[1], s[2] = np.inf, np.nan
+    bf = lambda a: torch.from_numpy(a).to(dev).to(torch.bfloat16)  # noqa: E731
+    args = c.args[:3] + (bf(A), bf(B), torch.from_numpy(s).to(dev), c.args[6])
+    keep = torch.from_numpy((c.ids != 1) & (c.ids != 2)).to(dev)
+    return c, args, (A, B, s), keep
+
+
+@pytest.mark.parametrize("M,K,N,r", MIXED)
+@pytest.mark.parametrize("where", ["A", "B", "scaling"])
+def test_an_adapter_that_is_not_finite_leaves_other_tokens(env, M, K, N, r, where):  # noqa: F811
+    """An infinity or a NaN in one adapter: tokens of other adapters, and of
+    none, keep their bits."""
+    torch, q4, dev = env
+    c, args, _, keep = _spoiled(env, M, K, N, r, where)
+    y0 = q4.q4_gemm_lora(*c.args, out_dtype=torch.float32)
+    y1 = q4.q4_gemm_lora(*args, out_dtype=torch.float32)
+    assert torch.equal(y0[keep], y1[keep])
+    assert not torch.isfinite(y1[~keep]).all()
