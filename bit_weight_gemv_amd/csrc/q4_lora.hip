@@ -457,12 +457,13 @@ __global__ __launch_bounds__(512) void lora_dx_kernel(const DxArgs a) {
                     e[x] = __builtin_amdgcn_perm(d[2 * x + 1], d[2 * x], 0x05040100u);
                     o[x] = __builtin_amdgcn_perm(d[2 * x + 1], d[2 * x], 0x07060302u);
                 }
-                const bf16x8_t be = __builtin_bit_cast(bf16x8_t, e), bo = __builtin_bit_cast(bf16x8_t, o);
+                const bool wild = __builtin_amdgcn_ballot_w64(not_finite8(e) || not_finite8(o)) != 0;
 #pragma unroll
                 for (int i = 0; i < MT; ++i) {
                     const int row = w0 + 32 * i + col;
                     const bool use = sid[row] == id;
-                    if (__builtin_amdgcn_ballot_w64(use) == 0) continue;
+                    const uint32_t users = (uint32_t)__builtin_amdgcn_ballot_w64(use);
+                    if (users == 0) continue;
                     float t[8];
 #pragma unroll
                     for (int x = 0; x < 8; ++x) t[x] = 0.0f;
@@ -473,10 +474,8 @@ __global__ __launch_bounds__(512) void lora_dx_kernel(const DxArgs a) {
                     }
                     bf16x8_t hi, lo;
                     split2(t, hi, lo);
-                    acc[i][0] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(hi, be, acc[i][0], 0, 0, 0);
-                    acc[i][0] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(lo, be, acc[i][0], 0, 0, 0);
-                    acc[i][1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(hi, bo, acc[i][1], 0, 0, 0);
-                    acc[i][1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(lo, bo, acc[i][1], 0, 0, 0);
+                    add_adapter(acc[i][0], hi, lo, e, wild, users);
+                    add_adapter(acc[i][1], hi, lo, o, wild, users);
                 }
             }
         }

@@ -47,3 +47,15 @@ def test_an_adapter_that_is_not_finite_leaves_other_tokens(env, M, K, N, r, wher
     y1 = q4.q4_gemm_lora(*args, out_dtype=torch.float32)
     assert torch.equal(y0[keep], y1[keep])
     assert not torch.isfinite(y1[~keep]).all()
+
+
+@pytest.mark.parametrize("M,K,N,r", MIXED)
+@pytest.mark.parametrize("where", ["A", "B", "scaling"])
+def test_an_adapter_that_is_not_finite_leaves_other_gradients(env, M, K, N, r, where):  # noqa: F811
+    torch, q4, dev = env
+    c, args, _, keep = _spoiled(env, M, K, N, r, where)
+    g0 = q4.q4_gemm_lora_backward(c.dYd, *c.args)
+    g1 = q4.q4_gemm_lora_backward(c.dYd, *args)
+    assert torch.equal(g0[0][keep], g1[0][keep])
+    for a in (0, 3):
+        assert torch.equal(g0[1][a], g1[1][a]) and torch.equal(g0[2][a], g1[2][a])
