@@ -222,7 +222,9 @@ __global__ __launch_bounds__(256) void lora_dy_kernel(const uint16_t *__restrict
             // 2048 more than the exponent, and 0 for a zero (whatever stands
             // in the exponents behind the last packed row).
             const s16x2_t nz = __builtin_bit_cast(s16x2_t, __builtin_elementwise_min(mag, u16x2_t{1, 1}));
-            const s16x2_t key = __builtin_bit_cast(s16x2_t, ex) + __builtin_bit_cast(s16x2_t, e[c]) + s16x2_t{2048, 2048};
+            // (Copied first: a bit cast of a vector's element itself reads element 0.)
+            const uint32_t pair = e[c];
+            const s16x2_t key = __builtin_bit_cast(s16x2_t, ex) + __builtin_bit_cast(s16x2_t, pair) + s16x2_t{2048, 2048};
             best2 = __builtin_elementwise_max(best2, key & -nz);
         }
     };

@@ -4,7 +4,8 @@ tests/ragged_reference.py."""
 import numpy as np
 import pytest
 
-from test_gpu_lora import Case, env  # noqa: F401
+import ragged_reference as ref
+from test_gpu_lora import Case, _within, env  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -59,3 +60,17 @@ def test_an_adapter_that_is_not_finite_leaves_other_gradients(env, M, K, N, r, w
     assert torch.equal(g0[0][keep], g1[0][keep])
     for a in (0, 3):
         assert torch.equal(g0[1][a], g1[1][a]) and torch.equal(g0[2][a], g1[2][a])
+
+
+@pytest.mark.parametrize("M,K,N", [(66, 192, 5), (72, 192, 300), (300, 256, 1100), (1030, 64, 70), (14000, 64, 3)])
+@pytest.mark.parametrize("small", [(0, 1), (2, 3, 4, 5, 6, 7), (0, 2, 4, 6), (5,)])
+def test_gradients_of_rows_of_unlike_scales(env, M, K, N, small):  # noqa: F811
+    """Among eight neighbouring packed rows some have scales 2^-12 of the
+    others': each row counts with its own power of two."""
+    torch, q4, dev = env
+    c = Case(env, M, K, N, 8, 2, seed=N + M, ids="random")
+    c.scales[np.isin(np.arange(M) % 8, small)] *= np.float16(2.0 ** -12)
+    args = (c.args[0], torch.from_numpy(c.scales).to(dev)) + c.args[2:]
+    (x, ex), _, _ = ref.lora_backward(q4.codebook(), c.codes, c.scales, *c.host, c.dY.astype(np.float64))
+    dX, _, _ = q4.q4_gemm_lora_backward(c.dYd, *args, need_adapters=False)
+    _within(dX, x, ref.rounded(x, ex, True), f"dX of rows of unlike scales, {small}")
