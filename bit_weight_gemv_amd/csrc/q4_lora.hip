@@ -169,6 +169,10 @@ hipError_t launch_shrink(const ShrinkArgs &s, Pieces pieces, hipStream_t stream)
 // Backward: what is prepared.
 // ---------------------------------------------------------------------------
 
+// The exponent of a packed row of zeros: its dY then counts as nothing, in the
+// choice of a token's power of two too.
+constexpr int kZeroRow = -4096;
+
 // The packed rows' exponents and scales (16 rows a workgroup), and behind those
 // workgroups B transposed: bt[a][j][m], rows of `pitch` with zeros past M (a
 // workgroup takes 64 m of one adapter).
@@ -178,7 +182,7 @@ __global__ __launch_bounds__(256) void lora_rows_kernel(const uint16_t *__restri
                                                         int pitch, uint16_t *__restrict__ bt) {
     __shared__ uint16_t tile[64][130];
     if ((int)blockIdx.x < rowblocks) {
-        prepare_scales(scales, (int64_t)blockIdx.x * 16, M, M, nb, rowexp, tscale);
+        prepare_scales<kZeroRow>(scales, (int64_t)blockIdx.x * 16, M, M, nb, rowexp, tscale);
         return;
     }
     const int per = pitch / 64, w = blockIdx.x - rowblocks;
@@ -219,8 +223,8 @@ __global__ __launch_bounds__(256) void lora_dy_kernel(const uint16_t *__restrict
             const u16x2_t mag = __builtin_bit_cast(u16x2_t, v[c] & 0x7FFF7FFFu);
             u16x2_t ex = mag >> 7;
             ex = __builtin_elementwise_min(ex, u16x2_t{254, 254});
-            // 2048 more than the exponent, and 0 for a zero (whatever stands
-            // in the exponents behind the last packed row).
+            // 2048 more than the exponent, 0 for a zero (whatever stands in the
+            // exponents behind the last packed row), below 0 for kZeroRow.
             const s16x2_t nz = __builtin_bit_cast(s16x2_t, __builtin_elementwise_min(mag, u16x2_t{1, 1}));
             // (Copied first: a bit cast of a vector's element itself reads element 0.)
             const uint32_t pair = e[c];

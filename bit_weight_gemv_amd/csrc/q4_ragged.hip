@@ -510,7 +510,7 @@ __global__ __launch_bounds__(256) void ragged_prepare_kernel(const uint16_t *__r
     const int64_t row0 = ((int64_t)blockIdx.x - T) * 16;
 #pragma unroll
     for (int q = 0; q < 2; ++q)
-        if (q ? s1 : s0) prepare_scales(q ? s1 : s0, row0, nrows, M, K >> 6, q ? e1 : e0, q ? t1 : t0);
+        if (q ? s1 : s0) prepare_scales<0>(q ? s1 : s0, row0, nrows, M, K >> 6, q ? e1 : e0, q ? t1 : t0);
 }
 
 constexpr int kTileWaves = 8;

@@ -151,9 +151,9 @@ __device__ __forceinline__ void write_pieces(const uint16_t *__restrict__ X, con
 
 // A workgroup of 256 takes the 16 packed rows from row0 (below nrows; matrices
 // of M rows, nb blocks a row, one after the other): the exponent of each row's
-// largest scale (0 in a row of zeros), and scale 2^(14 - exponent) as fp16 at
+// largest scale (ZERO in a row of zeros), and scale 2^(14 - exponent) as fp16 at
 // [matrix][block][row].
-template <typename E>
+template <int ZERO, typename E>
 __device__ __forceinline__ void prepare_scales(const uint16_t *__restrict__ scales, int64_t row0, int64_t nrows, int M,
                                                int nb, E *__restrict__ rowexp, uint16_t *__restrict__ out) {
     __shared__ int16_t exps[16];
@@ -166,7 +166,7 @@ __device__ __forceinline__ void prepare_scales(const uint16_t *__restrict__ scal
 #pragma unroll
         for (int d = 8; d >= 1; d >>= 1) m = max(m, __shfl_xor(m, d));
         const float f = f16_bits_to_f32((uint32_t)m);
-        const int e = m == 0 ? 0 : min((int)(__builtin_bit_cast(uint32_t, f) >> 23) - 127, 16);
+        const int e = m == 0 ? ZERO : min((int)(__builtin_bit_cast(uint32_t, f) >> 23) - 127, 16);
         if ((threadIdx.x & 15) == 0) {
             exps[threadIdx.x >> 4] = (int16_t)e;
             if (row < nrows) rowexp[row] = (E)e;

@@ -62,6 +62,24 @@ def test_an_adapter_that_is_not_finite_leaves_other_gradients(env, M, K, N, r, w
         assert torch.equal(g0[1][a], g1[1][a]) and torch.equal(g0[2][a], g1[2][a])
 
 
+@pytest.mark.parametrize("M,K,N", [(66, 192, 5), (66, 192, 300), (300, 256, 1100), (1030, 64, 70)])
+@pytest.mark.parametrize("big", [2.0 ** 12, 2.0 ** 60, 3e38])
+def test_gradients_beside_a_packed_row_of_zeros(env, M, K, N, big):  # noqa: F811
+    """A packed row whose scales are all 0 adds nothing to dX, however large
+    its dY is."""
+    torch, q4, dev = env
+    c = Case(env, M, K, N, 8, 2, seed=N + M, ids="random")
+    c.scales[3] = 0
+    c.B[:, 3] = 0                       # (u has no part of it either)
+    c.dY[:, 3] = ref.bf16(np.float32(big))
+    bf = lambda a: torch.from_numpy(a).to(dev).to(torch.bfloat16)  # noqa: E731
+    args = (c.args[0], torch.from_numpy(c.scales).to(dev), c.args[2], c.args[3], bf(c.B), c.args[5], c.args[6])
+    host = (c.host[0], c.host[1], c.B.astype(np.float64), c.host[3], c.host[4])
+    (x, ex), _, _ = ref.lora_backward(q4.codebook(), c.codes, c.scales, *host, c.dY.astype(np.float64))
+    dX, _, _ = q4.q4_gemm_lora_backward(bf(c.dY), *args, need_adapters=False)
+    _within(dX, x, ref.rounded(x, ex, True), f"dX beside a row of zeros, {big}")
+
+
 @pytest.mark.parametrize("M,K,N", [(66, 192, 5), (72, 192, 300), (300, 256, 1100), (1030, 64, 70), (14000, 64, 3)])
 @pytest.mark.parametrize("small", [(0, 1), (2, 3, 4, 5, 6, 7), (0, 2, 4, 6), (5,)])
 def test_gradients_of_rows_of_unlike_scales(env, M, K, N, small):  # noqa: F811
