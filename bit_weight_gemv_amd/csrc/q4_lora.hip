@@ -431,6 +431,7 @@ __global__ __launch_bounds__(512) void lora_dx_kernel(const DxArgs a) {
             acc[i][1][j] = ldexpf(acc[i][1][j], x);
         }
     const int k = kt * 256 + wk * 64 + 2 * col;  // this lane's two columns
+    bool wild = false;  // an adapter of this wave's rows holds a value that is not finite
 
     // With planes the first of them takes the adapters' term; with few tokens,
     // each of which may have an adapter of its own, the launch that adds the
@@ -463,13 +464,17 @@ __global__ __launch_bounds__(512) void lora_dx_kernel(const DxArgs a) {
                     e[x] = __builtin_amdgcn_perm(d[2 * x + 1], d[2 * x], 0x05040100u);
                     o[x] = __builtin_amdgcn_perm(d[2 * x + 1], d[2 * x], 0x07060302u);
                 }
-                const bool wild = __builtin_amdgcn_ballot_w64(not_finite8(e) || not_finite8(o)) != 0;
+                if (__builtin_amdgcn_ballot_w64(not_finite8(e) || not_finite8(o))) {
+                    wild = true;
+                    e = finite8(e);
+                    o = finite8(o);
+                }
+                const bf16x8_t be = __builtin_bit_cast(bf16x8_t, e), bo = __builtin_bit_cast(bf16x8_t, o);
 #pragma unroll
                 for (int i = 0; i < MT; ++i) {
                     const int row = w0 + 32 * i + col;
                     const bool use = sid[row] == id;
-                    const uint32_t users = (uint32_t)__builtin_amdgcn_ballot_w64(use);
-                    if (users == 0) continue;
+                    if (__builtin_amdgcn_ballot_w64(use) == 0) continue;
                     float t[8];
 #pragma unroll
                     for (int x = 0; x < 8; ++x) t[x] = 0.0f;
@@ -480,8 +485,10 @@ __global__ __launch_bounds__(512) void lora_dx_kernel(const DxArgs a) {
                     }
                     bf16x8_t hi, lo;
                     split2(t, hi, lo);
-                    add_adapter(acc[i][0], hi, lo, e, wild, users);
-                    add_adapter(acc[i][1], hi, lo, o, wild, users);
+                    acc[i][0] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(hi, be, acc[i][0], 0, 0, 0);
+                    acc[i][0] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(lo, be, acc[i][0], 0, 0, 0);
+                    acc[i][1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(hi, bo, acc[i][1], 0, 0, 0);
+                    acc[i][1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(lo, bo, acc[i][1], 0, 0, 0);
                 }
             }
         }
@@ -502,6 +509,18 @@ __global__ __launch_bounds__(512) void lora_dx_kernel(const DxArgs a) {
                     (uint32_t)f32_bf16(acc[i][0][j]) | (uint32_t)f32_bf16(acc[i][1][j]) << 16;
             }
         }
+    if (!wild) return;
+    // (Every lane adds to the outputs that it has stored.)
+    for (int i = 0; i < 32 * MT; ++i) {
+        const int row = wt * 32 * MT + 32 * (i >> 5) + tile_row(i >> 1 & 15, lane);
+        if (row >= count || sid[row] < 0) continue;
+        const float y = wild_term(a.u + (int64_t)(n0 + row) * a.r, a.A + (int64_t)sid[row] * a.r * a.K + k + (i & 1), a.K,
+                                  a.r);
+        if (y == 0.0f) continue;
+        const int64_t at = (int64_t)(n0 + row) * a.K + k + (i & 1);
+        if (a.part) a.part[at] += y;  // (the first plane)
+        else a.dX[at] = f32_bf16(bf16_f32(a.dX[at]) + y);
+    }
 }
 
 // Adds the partial planes in order, and the adapter's term where there are few

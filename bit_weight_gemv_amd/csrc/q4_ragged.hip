@@ -742,6 +742,7 @@ __global__ __launch_bounds__(kTileWaves * 64) void ragged_tile_kernel(const Args
             acc[i][1][j] = x == kNoRow ? 0.0f : ldexpf(acc[i][1][j], x - 14 + e[1]);
         }
 
+    bool wild = false;  // an adapter of this wave's rows holds a value that is not finite
     if constexpr (LORA) {
         // The adapters among this wave's rows, one after the other; the rows
         // of others enter as zeros.
@@ -766,13 +767,16 @@ __global__ __launch_bounds__(kTileWaves * 64) void ragged_tile_kernel(const Args
                     if (live && m[q] < a.M)
                         bb[q] = *reinterpret_cast<const u32x4_t *>(a.B + ((int64_t)id * a.M + m[q]) * a.r + j0 + 8 * g);
                 }
-                const bool wild = __builtin_amdgcn_ballot_w64(not_finite8(bb[0]) || not_finite8(bb[1])) != 0;
+                if (__builtin_amdgcn_ballot_w64(not_finite8(bb[0]) || not_finite8(bb[1]))) {
+                    wild = true;
+                    bb[0] = finite8(bb[0]);
+                    bb[1] = finite8(bb[1]);
+                }
 #pragma unroll
                 for (int i = 0; i < MT; ++i) {
                     const int row = w0 + 32 * i + col;
                     const bool use = sid[row] == id;
-                    const uint32_t users = (uint32_t)__builtin_amdgcn_ballot_w64(use);
-                    if (users == 0) continue;
+                    if (__builtin_amdgcn_ballot_w64(use) == 0) continue;
                     float t[8];
 #pragma unroll
                     for (int x = 0; x < 8; ++x) t[x] = 0.0f;
@@ -784,7 +788,11 @@ __global__ __launch_bounds__(kTileWaves * 64) void ragged_tile_kernel(const Args
                     bf16x8_t hi, lo;
                     split2(t, hi, lo);
 #pragma unroll
-                    for (int q = 0; q < 2; ++q) add_adapter(acc[i][q], hi, lo, bb[q], wild, users);
+                    for (int q = 0; q < 2; ++q) {
+                        const bf16x8_t b = __builtin_bit_cast(bf16x8_t, bb[q]);
+                        acc[i][q] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(hi, b, acc[i][q], 0, 0, 0);
+                        acc[i][q] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(lo, b, acc[i][q], 0, 0, 0);
+                    }
                 }
             }
         }
@@ -810,6 +818,25 @@ __global__ __launch_bounds__(kTileWaves * 64) void ragged_tile_kernel(const Args
                 if (m[1] < a.M) store_out(a.Y, a.bf16, at + m[1], acc[i][1][j]);
             }
         }
+    if constexpr (LORA) {
+        if (!wild) return;
+        // (Every lane adds to the outputs that it has stored.)
+        const int w0 = wt * 32 * MT;
+        for (int i = 0; i < 16 * MT; ++i) {
+            const int row = w0 + 32 * (i >> 4) + tile_row(i & 15, lane);
+            if (row >= ck.count || sid[row] < 0) continue;
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                if (m[q] >= a.M) continue;
+                const float y = wild_term(a.t + (int64_t)(ck.start + row) * a.r,
+                                          a.B + ((int64_t)sid[row] * a.M + m[q]) * a.r, 1, a.r);
+                if (y == 0.0f) continue;
+                const int64_t at = (int64_t)(ck.start + row) * a.M + m[q];
+                if constexpr (PART) a.part[at] += y;  // (the first plane)
+                else store_out(a.Y, a.bf16, at, load_out(a.Y, a.bf16, at) + y);
+            }
+        }
+    }
 }
 
 int64_t slices_of(int64_t K) { return (K + kSliceK - 1) / kSliceK; }
