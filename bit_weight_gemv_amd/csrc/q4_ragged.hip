@@ -22,7 +22,7 @@ struct Args {
     const int8_t *rowexp[2];   // tile kernel: exponent of each row's largest scale,
     const uint16_t *tscale[2]; // and the scales over 2^(exponent - 14) as fp16, [E][K/64][M]
     int M, K, E, R;
-    const uint16_t *X;         // bf16 [T][K]; fp16 [T][K] (tile kernel) or [K/8][R][8] (chunk kernel, PRE) times 2^-xexp
+    const uint16_t *X;         // bf16 [T][K]; fp16 [T][tile_pitch(K)] (tile kernel) or [K/8][R][8] (chunk kernel, PRE) times 2^-xexp
     const int32_t *xexp;       // the power of two of each row of X (tile kernel) or slice and position (chunk kernel)
     int T;
     const int32_t *offsets, *rows;
@@ -469,6 +469,11 @@ __global__ __launch_bounds__(256) void ragged_finish_kernel(const Args a) {
 // Many rows a group.
 // ---------------------------------------------------------------------------
 
+// The tile kernel takes two 64-blocks at a time: its rows of X are padded to
+// that with zeros, so that the step past an odd row adds zeros (what it met in
+// place of them, times a scale of 0, would make NaN of an infinity).
+__host__ __device__ constexpr int64_t tile_pitch(int64_t K) { return (K + 127) & ~(int64_t)127; }
+
 // One workgroup a row of X: fp16 under a power of two (the row's largest
 // magnitude goes to [2^14, 2^15)), and that power of two.  The workgroups
 // behind them take 16 packed rows each: the exponent of a row's largest scale,
@@ -484,7 +489,7 @@ __global__ __launch_bounds__(256) void ragged_prepare_kernel(const uint16_t *__r
     __shared__ uint32_t wmax[4];
     if ((int)blockIdx.x < T) {
         const u32x4_t *src = reinterpret_cast<const u32x4_t *>(X + (int64_t)blockIdx.x * K);
-        u32x4_t *dst = reinterpret_cast<u32x4_t *>(x16 + (int64_t)blockIdx.x * K);
+        u32x4_t *dst = reinterpret_cast<u32x4_t *>(x16 + (int64_t)blockIdx.x * tile_pitch(K));
         const int n = K / 8;
         u16x2_t mx = {0, 0};
         for (int i = threadIdx.x; i < n; i += 256) {
@@ -504,6 +509,7 @@ __global__ __launch_bounds__(256) void ragged_prepare_kernel(const uint16_t *__r
             for (int c = 0; c < 4; ++c) v[c] = bf16x2_to_f16x2(v[c], f);
             dst[i] = v;
         }
+        if (threadIdx.x < (uint32_t)(tile_pitch(K) - K) / 8) dst[n + threadIdx.x] = u32x4_t{0u, 0u, 0u, 0u};
         if (threadIdx.x == 0) xexp[blockIdx.x] = -shift;
         return;
     }
@@ -585,15 +591,18 @@ __global__ __launch_bounds__(kTileWaves * 64) void ragged_tile_kernel(const Args
         const int i = (threadIdx.x >> 3) + 64 * j;
         const int row = max(source_row(a, ck.start + min(i, ck.count - 1)), 0);
         const int piece = (threadIdx.x & 7) ^ ((i >> 1) & 7);
-        xsrc[j] = reinterpret_cast<const u32x4_t *>(a.X + (int64_t)row * a.K) + piece;
+        xsrc[j] = reinterpret_cast<const u32x4_t *>(a.X + row * tile_pitch(a.K)) + piece;
     }
 
     int m[2];
     const u32x4_t *csrc[2];
     const uint16_t *ssrc[2];
     int e[2];
-    const int b0 = PART ? (a.K >> 6) * (int)blockIdx.y / a.ranges : 0;  // the first block
-    const int nb = (PART ? (a.K >> 6) * ((int)blockIdx.y + 1) / a.ranges : a.K >> 6) - b0;
+    // Runs of pairs of blocks: only the last may end in an odd one.
+    const int pairs = (a.K + 127) >> 7;
+    const int b0 = PART ? 2 * (pairs * (int)blockIdx.y / a.ranges) : 0;  // the first block
+    const int nb = (PART ? min(2 * (pairs * ((int)blockIdx.y + 1) / a.ranges), a.K >> 6) : a.K >> 6) - b0;
+    const int nbx = (nb + 1) & ~1;                                       // with the padding of X
     if constexpr (PART) {
 #pragma unroll
         for (int j = 0; j < kPieces; ++j) xsrc[j] += 8 * b0;
@@ -634,7 +643,7 @@ __global__ __launch_bounds__(kTileWaves * 64) void ragged_tile_kernel(const Args
     load_codes(min(1, nb - 1), c1, v1);
     fill_lut(sm.lut);
     stage(0);
-    load_x(min(1, nb - 1));
+    load_x(1);
 
     float16_t acc[MT][2];
 #pragma unroll
@@ -678,7 +687,7 @@ __global__ __launch_bounds__(kTileWaves * 64) void ragged_tile_kernel(const Args
                     const uint32_t (&snext)[2]) {
         // (The last steps stage and load what is there already.)
         stage(b + 1);
-        load_x(min(b + 2, nb - 1));
+        load_x(min(b + 2, nbx - 1));
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
             const half8_t wn[2] = {w[0], w[1]};
@@ -726,7 +735,7 @@ __global__ __launch_bounds__(kTileWaves * 64) void ragged_tile_kernel(const Args
     look(c0, 0);
     rows(0, 0);
     weigh();
-    // (An odd last step runs with scales of 0.)
+    // (The step past an odd last one has scales of 0, and zeros for X.)
     for (int b = 0; b < nb; b += 2) {
         step(b, c0, v0, c1, v1);
         step(b + 1, c1, v1, c0, v0);
@@ -928,7 +937,7 @@ Plan plan_of(int64_t E, int64_t M, int64_t K, int64_t R, bool up, int64_t r) {
 }
 
 // The tile kernel's rows of X in fp16: one at least, which rows outside [0, T) read.
-size_t tile_rows_bytes(int64_t T, int64_t K) { return (size_t)(T > 0 ? T : 1) * K * 2; }
+size_t tile_rows_bytes(int64_t T, int64_t K) { return (size_t)(T > 0 ? T : 1) * tile_pitch(K) * 2; }
 
 }  // namespace
 

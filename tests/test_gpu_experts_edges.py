@@ -68,3 +68,47 @@ def test_grouped_rows_beyond_x_without_an_index(env, E, M, K, sizes, T, up):  # 
             y, b = ref.swiglu(y, b, u, bu)
         want[lo:hi], bound[lo:hi] = y, ref.rounded(y, b, False)
     _within(Y, want, bound, f"beyond X: E={E} R={R} T={T}")
+
+
+def _same_kind(got, want, what):
+    """NaN, +infinity and -infinity where the formula has them, finite elsewhere."""
+    got = got.float().cpu().numpy()
+    for name, f in (("nan", np.isnan), ("inf", np.isposinf), ("-inf", np.isneginf)):
+        bad = f(got) != f(want)
+        assert not bad.any(), f"{what}: {name} differs at {np.argwhere(bad)[:4].tolist()}"
+
+
+@pytest.mark.parametrize("E,M,K,sizes", [
+    (8, 33, 192, [1, 0, 1, 0, 0, 1, 0, 1]),
+    (2, 130, 192, [1200, 1190]),
+    (1, 300, 64, [1100]),
+    (2, 40, 2112, [3000, 100]),
+    (1, 1030, 192, [8300]),
+])
+def test_grouped_infinite_activation(env, E, M, K, sizes):  # noqa: F811
+    """An infinity in a row, also in its last weights, where a kernel's steps
+    reach past the row, gives what the formula gives: infinities, and NaN where
+    the weight is 0."""
+    torch, q4, dev = env
+    rng = np.random.default_rng(M + K)
+    R = sum(sizes)
+    codes, scales = _packed(rng, E, M, K)
+    X = _x(rng, R, K)
+    off = _groups(rng, E, sizes)
+    at = {0: K - 1, R // 2: K - 33, R - 1: 5}
+    for i, k in at.items():
+        X[i, k] = np.inf if i else -np.inf
+    y = q4.q4_gemm_grouped(_dev(env, codes), _dev(env, scales), _dev(env, X).to(torch.bfloat16), _dev(env, off),
+                           out_dtype=torch.float32)
+    levels = q4.codebook()
+    rows = sorted(at)
+    want = np.zeros((len(rows), M))
+    for j, i in enumerate(rows):
+        e = int(np.searchsorted(off[1:], i, side="right"))
+        with np.errstate(invalid="ignore"):
+            want[j] = (ref.dequantise(levels, codes[e], scales[e]) * X[i].astype(np.float64)[None, :]).sum(1)
+    assert np.isinf(want).any()
+    _same_kind(y[torch.tensor(rows, device=dev)], want, f"E={E} M={M} K={K}")
+    keep = torch.ones(R, dtype=torch.bool, device=dev)
+    keep[torch.tensor(rows, device=dev)] = False
+    assert torch.isfinite(y[keep]).all()
