@@ -117,6 +117,7 @@ __global__ __launch_bounds__(kChunkWaves * 64, NT * MATS == 1 && !LORA ? 4 : 2) 
     // This lane's two pieces of 32 k, and whether they lie within the row.
     const int pc[2] = {8 * (s0 + wave) + g, 8 * (s0 + wave) + 4 + g};
     const bool live[2] = {pc[0] < 2 * nb, pc[1] < 2 * nb};
+    const bool whole = 8 * (s0 + wave) + 8 <= 2 * nb;
     const int at[2] = {min(pc[0], 2 * nb - 1), min(pc[1], 2 * nb - 1)};
     const int ntiles = (a.M + ROWS - 1) / ROWS;
     const int t0 = (int)((uint32_t)ntiles * share.part / share.nparts);
@@ -159,6 +160,16 @@ __global__ __launch_bounds__(kChunkWaves * 64, NT * MATS == 1 && !LORA ? 4 : 2) 
     };
     u32x4_t x[NT][8];
     int back[NT][4];                    // the inverse power of two of each register's row, less 14
+    // Pieces past the row have scales of 0, and zeros for x: the values that
+    // their clamped addresses read could be infinite.
+    auto cut = [&]() {
+        if (whole) return;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int s = 0; s < 8; ++s)
+                if (!live[s >> 2]) x[n][s] = u32x4_t{0u, 0u, 0u, 0u};
+    };
     if constexpr (PRE) {
         // [piece of 8 k][position]: 16 lanes read 256 neighbouring bytes.
         const u32x4_t *src = reinterpret_cast<const u32x4_t *>(a.X) + ck.start;
@@ -174,6 +185,7 @@ __global__ __launch_bounds__(kChunkWaves * 64, NT * MATS == 1 && !LORA ? 4 : 2) 
 #pragma unroll
         for (int u = 0; u < D; ++u) load_tile(u, min(t0 + u, t1 - 1));
         fill_lut(lut);
+        cut();
     } else {
         int row[NT];
 #pragma unroll
@@ -194,6 +206,7 @@ __global__ __launch_bounds__(kChunkWaves * 64, NT * MATS == 1 && !LORA ? 4 : 2) 
 #pragma unroll
         for (int u = 1; u < D; ++u) load_tile(u, min(t0 + u, t1 - 1));
         fill_lut(lut);
+        cut();
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             u16x2_t mx = {0, 0};

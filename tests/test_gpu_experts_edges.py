@@ -80,6 +80,10 @@ def _same_kind(got, want, what):
 
 @pytest.mark.parametrize("E,M,K,sizes", [
     (8, 33, 192, [1, 0, 1, 0, 0, 1, 0, 1]),
+    (16, 70, 192, [2, 3] * 8),
+    (4, 40, 2112, [9, 0, 11, 7]),
+    (1, 70, 320, [21]),
+    (1, 70, 64, [40]),
     (2, 130, 192, [1200, 1190]),
     (1, 300, 64, [1100]),
     (2, 40, 2112, [3000, 100]),
