@@ -294,9 +294,13 @@ __global__ __launch_bounds__(kChunkWaves * 64, NT * MATS == 1 && !LORA ? 4 : 2) 
         float term = 0.0f;
         if constexpr (LORA) {
 #pragma unroll
-            for (int c = 0; c < 8; ++c) {
-                term = fmaf(bf16_lo(bw[u][c >> 2][c & 3]), tv[2 * c], term);
-                term = fmaf(bf16_hi(bw[u][c >> 2][c & 3]), tv[2 * c + 1], term);
+            for (int h = 0; h < 2; ++h) {
+                if (h == 1 && a.r == 8) break;  // (8 ranks: the second half is the first again)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    term = fmaf(bf16_lo(bw[u][h][c]), tv[8 * h + 2 * c], term);
+                    term = fmaf(bf16_hi(bw[u][h][c]), tv[8 * h + 2 * c + 1], term);
+                }
             }
         }
         if (t + D < t1) load_tile(u, t + D);

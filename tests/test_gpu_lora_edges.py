@@ -5,9 +5,29 @@ import numpy as np
 import pytest
 
 import ragged_reference as ref
+from test_gpu_experts_edges import _same_kind
 from test_gpu_lora import Case, _within, env  # noqa: F401
 
 pytestmark = pytest.mark.gpu
+
+
+def _plain(levels, c, X, A, B, s, dY=None):
+    """The formulas in 64 bits, product by product, so that an infinity times a
+    zero is NaN only where the formula has that product."""
+    W = ref.dequantise(levels, c.codes, c.scales)
+    with np.errstate(invalid="ignore", over="ignore"):
+        Y = X @ W.T
+        dA, dB = np.zeros(A.shape), np.zeros(B.shape)
+        dX = dY @ W
+        for n, a in enumerate(c.ids):
+            if not 0 <= a < len(A):
+                continue
+            t, u = s[a] * (A[a] @ X[n]), s[a] * (B[a].T @ dY[n])
+            Y[n] += B[a] @ t
+            dX[n] += u @ A[a]
+            dA[a] += np.outer(u, X[n])
+            dB[a] += np.outer(dY[n], t)
+    return Y, dX, dA, dB
 
 
 # M, K, N, r: the row, chunk and tile kernels, tiles in runs of K, dX with and
@@ -60,6 +80,20 @@ def test_an_adapter_that_is_not_finite_leaves_other_gradients(env, M, K, N, r, w
     assert torch.equal(g0[0][keep], g1[0][keep])
     for a in (0, 3):
         assert torch.equal(g0[1][a], g1[1][a]) and torch.equal(g0[2][a], g1[2][a])
+
+
+@pytest.mark.parametrize("M,K,N,r", MIXED)
+@pytest.mark.parametrize("where", ["A", "B", "scaling"])
+def test_an_adapter_that_is_not_finite_gives_what_the_formula_gives(env, M, K, N, r, where):  # noqa: F811
+    """Infinities of the right sign, and NaN only where the formula has one."""
+    torch, q4, dev = env
+    c, args, (A, B, s), _ = _spoiled(env, M, K, N, r, where)
+    y = q4.q4_gemm_lora(*args, out_dtype=torch.float32)
+    g = q4.q4_gemm_lora_backward(c.dYd, *args)
+    f = np.float64
+    want = _plain(q4.codebook(), c, c.X.astype(f), A.astype(f), B.astype(f), s.astype(f), c.dY.astype(f))
+    for got, w, what in zip((y,) + tuple(g), want, ("Y", "dX", "dA", "dB")):
+        _same_kind(got, w, what)
 
 
 @pytest.mark.parametrize("M,K,N", [(66, 192, 5), (66, 192, 300), (300, 256, 1100), (1030, 64, 70)])
