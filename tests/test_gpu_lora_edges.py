@@ -96,6 +96,26 @@ def test_an_adapter_that_is_not_finite_gives_what_the_formula_gives(env, M, K, N
         _same_kind(got, w, what)
 
 
+@pytest.mark.parametrize("M,K,N,r", MIXED)
+def test_scaling_of_zero_and_below(env, M, K, N, r):  # noqa: F811
+    """s B x = |s| (sign(s) B) x, so that the reference's bounds keep their sign."""
+    torch, q4, dev = env
+    c = Case(env, M, K, N, r, 3, seed=M + N, ids="random")
+    s = np.array([-0.75, 0.0, 1.5], np.float32)
+    args = c.args[:5] + (torch.from_numpy(s).to(dev), c.args[6])
+    X, A, B, _, ids = c.host
+    sign = np.sign(s.astype(np.float64))[:, None, None]
+    host = (X, A, B * np.where(sign == 0, 1, sign), np.abs(s.astype(np.float64)), ids)
+    want, e = ref.lora(q4.codebook(), c.codes, c.scales, *host)
+    _within(q4.q4_gemm_lora(*args, out_dtype=torch.float32), want, ref.rounded(want, e, False), "forward")
+    (x, ex), (a, ea), (b, eb) = ref.lora_backward(q4.codebook(), c.codes, c.scales, *host, c.dY.astype(np.float64))
+    dX, dA, dB = q4.q4_gemm_lora_backward(c.dYd, *args)
+    _within(dX, x, ref.rounded(x, ex, True), "dX")
+    _within(dA, a, ea + 2.0 ** -24 * np.abs(a) + 1e-37, "dA")
+    b, eb = b * np.where(sign == 0, 1, sign), eb
+    _within(dB, b, eb + 2.0 ** -24 * np.abs(b) + 1e-37, "dB")
+
+
 @pytest.mark.parametrize("M,K,N", [(66, 192, 5), (66, 192, 300), (300, 256, 1100), (1030, 64, 70)])
 @pytest.mark.parametrize("big", [2.0 ** 12, 2.0 ** 60, 3e38])
 def test_gradients_beside_a_packed_row_of_zeros(env, M, K, N, big):  # noqa: F811
@@ -112,6 +132,24 @@ def test_gradients_beside_a_packed_row_of_zeros(env, M, K, N, big):  # noqa: F81
     (x, ex), _, _ = ref.lora_backward(q4.codebook(), c.codes, c.scales, *host, c.dY.astype(np.float64))
     dX, _, _ = q4.q4_gemm_lora_backward(bf(c.dY), *args, need_adapters=False)
     _within(dX, x, ref.rounded(x, ex, True), f"dX beside a row of zeros, {big}")
+
+
+@pytest.mark.parametrize("M,K,N,r", MIXED)
+def test_one_infinite_token(env, M, K, N, r):  # noqa: F811
+    """An infinity in a token's row, also in its last values, where a kernel's
+    steps reach past the row."""
+    torch, q4, dev = env
+    c = Case(env, M, K, N, r, 3, seed=M + r, ids="random")
+    X, dY = c.X.copy(), c.dY.copy()
+    X[0, K - 1], X[N - 1, K - 33] = np.inf, -np.inf
+    dY[0, M - 1], dY[N - 1, 3] = np.inf, -np.inf
+    bf = lambda a: torch.from_numpy(a).to(dev).to(torch.bfloat16)  # noqa: E731
+    y = q4.q4_gemm_lora(*c.args[:2], bf(X), *c.args[3:], out_dtype=torch.float32)
+    g = q4.q4_gemm_lora_backward(bf(dY), *c.args[:2], bf(X), *c.args[3:])
+    f = np.float64
+    want = _plain(q4.codebook(), c, X.astype(f), c.A.astype(f), c.B.astype(f), c.scaling.astype(f), dY.astype(f))
+    for got, w, what in zip((y,) + tuple(g), want, ("Y", "dX", "dA", "dB")):
+        _same_kind(got, w, what)
 
 
 @pytest.mark.parametrize("M,K,N", [(66, 192, 5), (72, 192, 300), (300, 256, 1100), (1030, 64, 70), (14000, 64, 3)])
