@@ -105,7 +105,7 @@ int q4_gemm_grouped(const uint8_t *codes, const uint16_t *scales, const uint8_t 
 int q4_moe_combine(const void *Y, int y_type, int64_t R, int64_t M, const float *weights, const int32_t *pos,
                    int64_t T, int64_t k, int out_type, void *out, void *stream) {
     if (!type_ok(y_type) || !type_ok(out_type) || R < 0 || R > Q4_MAX_SLOTS || M < 0 || M > Q4_MAX_ROWS || T < 0 ||
-        T > Q4_MAX_SLOTS || k < 1 || k > Q4_MAX_TOPK || T * ((M + 255) / 256) >= INT64_C(1) << 24)
+        T > Q4_MAX_SLOTS || k < 1 || k > Q4_MAX_TOPK || !q4::combine_fits(M, T))
         return Q4_ERR_SHAPE;
     if (T == 0 || M == 0) return Q4_OK;
     if ((R > 0 && !Y) || !weights || !pos || !out) return Q4_ERR_NULL;

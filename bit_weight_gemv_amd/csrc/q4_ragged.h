@@ -74,6 +74,7 @@ size_t route_ws_bytes(int64_t T, int64_t E, int64_t k);
 hipError_t launch_route(const void *logits, bool bf16, int64_t T, int64_t E, int64_t k, bool all, int32_t *experts,
                         float *weights, int32_t *offsets, int32_t *rows, int32_t *pos, void *workspace,
                         hipStream_t stream);
+bool combine_fits(int64_t M, int64_t T);  // (within what a grid can hold)
 hipError_t launch_combine(const void *Y, bool y_bf16, int64_t R, int64_t M, const float *weights, const int32_t *pos,
                           int64_t T, int64_t k, bool out_bf16, void *out, hipStream_t stream);
 

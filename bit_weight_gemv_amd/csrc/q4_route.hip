@@ -371,6 +371,13 @@ int64_t run_of(int64_t n, int64_t least) {
     return per <= least ? least : (per + least - 1) / least * least;
 }
 
+// Workgroups of the weighted sum for each token: eight columns a lane where
+// every row starts on 16 bytes.
+int64_t combine_per(int64_t M) {
+    const int64_t columns = M % 8 == 0 ? 2048 : 256;
+    return (M + columns - 1) / columns;
+}
+
 const void *route_fn(int64_t E) {
     if (E <= 16) return reinterpret_cast<const void *>(&route_kernel<1, 16>);
     if (E <= 64) return reinterpret_cast<const void *>(&route_kernel<4, 16>);
@@ -456,6 +463,10 @@ hipError_t launch_route(const void *logits, bool bf16, int64_t T, int64_t E, int
                            sargs, 0, stream);
 }
 
+bool combine_fits(int64_t M, int64_t T) {
+    return T * combine_per(M) * 256 < INT64_C(1) << 32;  // threads of one launch
+}
+
 hipError_t launch_combine(const void *Y, bool y_bf16, int64_t R, int64_t M, const float *weights, const int32_t *pos,
                           int64_t T, int64_t k, bool out_bf16, void *out, hipStream_t stream) {
     CombineArgs a = {};
@@ -469,8 +480,8 @@ hipError_t launch_combine(const void *Y, bool y_bf16, int64_t R, int64_t M, cons
     a.k = (int)k;
     a.out_bf16 = out_bf16;
     a.out = out;
-    const bool vec = M % 8 == 0;  // every row starts on 16 bytes
-    a.per = (int)((M + (vec ? 2047 : 255)) / (vec ? 2048 : 256));
+    const bool vec = M % 8 == 0;
+    a.per = (int)combine_per(M);
     void *args[] = {&a};
     return hipLaunchKernel(vec ? reinterpret_cast<const void *>(&combine_kernel<true>)
                                : reinterpret_cast<const void *>(&combine_kernel<false>),

@@ -116,3 +116,18 @@ def test_grouped_infinite_activation(env, E, M, K, sizes):  # noqa: F811
     keep = torch.ones(R, dtype=torch.bool, device=dev)
     keep[torch.tensor(rows, device=dev)] = False
     assert torch.isfinite(y[keep]).all()
+
+
+def test_combine_of_many_columns(env):  # noqa: F811
+    """Tokens times columns past what a column a lane could launch."""
+    torch, q4, dev = env
+    T, M = 1 << 17, 1 << 15
+    g = torch.Generator(device=dev)
+    g.manual_seed(3)
+    Y = torch.randn((3, M), generator=g, device=dev).to(torch.bfloat16)
+    w = torch.rand((T, 1), generator=g, device=dev)
+    pos = torch.randint(0, 3, (T, 1), generator=g, device=dev).to(torch.int32)
+    out = q4.q4_moe_combine(Y, w, pos)
+    for t in (0, 1, 4097, T // 2, T - 2):
+        want = (w[t, 0] * Y[pos[t, 0]].float()).to(torch.bfloat16)   # one product: exact in fp32, one rounding
+        assert torch.equal(out[t], want), t
