@@ -973,7 +973,8 @@ bool ragged_fits(int64_t E, int64_t M, int64_t K, int64_t T, int64_t R, bool up)
         const int64_t rowtiles = (M + (up ? 127 : 255)) / (up ? 128 : 256);
         return (T + (E * M + 15) / 16) * 256 < most && rowtiles * chunk_bound(E, R, 64 * p.mt) * 512 < most;
     }
-    return ((M + 255) / 256) * R * 256 < most && chunk_bound(E, R, p.single ? 1 : p.cap) < 65536;
+    return ((M + 255) / 256) * R * 256 < most && chunk_bound(E, R, p.single ? 1 : p.cap) < 65536 &&
+           (!p.pre || pieces_blocks(K, R) * 256 < most);
 }
 
 size_t ragged_ws_bytes(int64_t E, int64_t M, int64_t K, int64_t T, int64_t R, bool up, int64_t r) {
