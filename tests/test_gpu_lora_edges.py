@@ -164,3 +164,21 @@ def test_gradients_of_rows_of_unlike_scales(env, M, K, N, small):  # noqa: F811
     (x, ex), _, _ = ref.lora_backward(q4.codebook(), c.codes, c.scales, *c.host, c.dY.astype(np.float64))
     dX, _, _ = q4.q4_gemm_lora_backward(c.dYd, *args, need_adapters=False)
     _within(dX, x, ref.rounded(x, ex, True), f"dX of rows of unlike scales, {small}")
+
+
+# M, K, N, r, L: the longest rows, many packed rows, many adapters, the largest rank.
+LARGEST = [(5, 131072, 1, 8, 2), (5, 131072, 20, 16, 2), (3, 131008, 300, 8, 1), (70000, 64, 3, 8, 2), (30, 64, 3000, 8, 1024),
+           (40, 192, 700, 16, 700), (70, 192, 1500, 128, 2), (130, 64, 70, 128, 40)]
+
+
+@pytest.mark.parametrize("M,K,N,r,L", LARGEST)
+def test_largest(env, M, K, N, r, L):  # noqa: F811
+    torch, q4, dev = env
+    c = Case(env, M, K, N, r, L, seed=M + K + N + r, ids="random")
+    want, e = ref.lora(q4.codebook(), c.codes, c.scales, *c.host)
+    _within(q4.q4_gemm_lora(*c.args, out_dtype=torch.float32), want, ref.rounded(want, e, False), "forward")
+    (x, ex), (a, ea), (b, eb) = ref.lora_backward(q4.codebook(), c.codes, c.scales, *c.host, c.dY.astype(np.float64))
+    dX, dA, dB = q4.q4_gemm_lora_backward(c.dYd, *c.args)
+    _within(dX, x, ref.rounded(x, ex, True), "dX")
+    _within(dA, a, ea + 2.0 ** -24 * np.abs(a) + 1e-37, "dA")
+    _within(dB, b, eb + 2.0 ** -24 * np.abs(b) + 1e-37, "dB")
