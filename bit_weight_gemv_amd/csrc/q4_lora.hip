@@ -293,10 +293,13 @@ struct DxArgs {
 // lanes' columns; a lane's two weights of a byte are the columns 2c and 2c+1
 // of two tiles).  The contraction runs over 64 packed rows a step: their code
 // bytes are transposed into LDS so that a lane reads its column's bytes of 32
-// rows as two 16-byte pieces.  Bound as the forward tile kernel, by the lookups
-// beside the matrix cores: 4096 tokens, 11008 x 2048 235 us (780 TFLOP/s) in
-// two parts of the packed rows, and 13 to add them; few tokens by the walk
-// along the packed rows, which is split over workgroups.
+// rows as two 16-byte pieces.  The scaled weights are rounded to fp16 as in the
+// forward kernels.  4096 tokens, 11008 x 2048 take 245 us (750 TFLOP/s) in two
+// parts of the packed rows, and 13 to add them: bound by the lookups beside the
+// matrix cores, which are busy 0.40 of the time, and by dY, which is read eight
+// times (736 MB: workgroups go round the XCDs by column tile, so each XCD's L2
+// takes in all of it).  Few tokens are bound by the walk along the packed rows,
+// which is split over workgroups.
 template <int MT>
 __global__ __launch_bounds__(512) void lora_dx_kernel(const DxArgs a) {
     constexpr int TM = 64 * MT;
@@ -691,6 +694,7 @@ DxPlan dx_plan(int64_t M, int64_t K, int64_t N) {
     // Packed rows are split while there are fewer workgroups than compute
     // units, into parts of 256 rows at least: 2048 x 2048, N = 64 in 1, 4, 8,
     // 16 parts 71.5, 42.2, 38.5, 40.4 us; N = 128 in 4, 8, 16 48.3, 47.1, 52.9.
+    // (256: an MI355X's; the workspace's size follows from the shape alone.)
     const int64_t steps = (M + 63) / 64, have = p.tiles * p.ktiles, cus = 256;
     int64_t s = have >= cus || have == 0 ? 1 : (cus + have - 1) / have;
     if (s > (steps + 3) / 4) s = (steps + 3) / 4;

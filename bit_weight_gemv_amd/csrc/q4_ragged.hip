@@ -79,8 +79,12 @@ __device__ __forceinline__ float adapter_term(const Args &a, int id, int p, int 
 // (r, g) holds the pieces g and 4 + g of 32 weights of row r, so that a load
 // takes 64 neighbouring bytes of a row and a piece has one scale.  The weights
 // are multiplied by the scale in fp16, under a power of two that brings the
-// largest of the row's four scales to [2^14, 2^15).  The waves' tiles are
-// added through LDS.
+// largest of the row's four scales to [2^14, 2^15): one more rounding of 2^-11
+// than a scale applied to fp32 sums would cost, which the four blocks of a
+// product do not allow.  Held exactly, in two fp16 and two products, they took
+// 13.1 -> 13.9 us (32 tokens, 11008 x 2048), 34 -> 40 (512 rows in 64 groups of
+// 2048 x 1408), for 2.2e-4 -> 1.6e-4 of the outputs' magnitude; a bf16 output's
+// own rounding is 1.7e-3.  The waves' tiles are added through LDS.
 //
 // Such calls are bound by their waits and by the instructions of a wave (four
 // cycles each) more than by their bytes: nothing is cleared that a clamped
@@ -90,8 +94,9 @@ __device__ __forceinline__ float adapter_term(const Args &a, int id, int p, int 
 // an earlier launch, and lie in the order of the loads.
 //
 // Measured (graph replay, whole calls): 74 rows in 16 groups of 2048 x 1408,
-// 25 MB, 12.7 us; 32 tokens beside adapters of rank 16 on 11008 x 2048, 23 MB,
-// 13.0 us (4.8 and 4.4 us at the rate of a large copy).
+// 25 MB, 13.6 us; 32 tokens beside adapters of rank 16 on 11008 x 2048, 23 MB,
+// 13.1 us (4.8 and 4.4 us at the rate of a large copy).  K = 1408 makes six
+// slices: two of the eight waves have none.
 // ---------------------------------------------------------------------------
 constexpr int kChunkWaves = 8;
 constexpr int kSliceK = 256;
@@ -550,12 +555,16 @@ constexpr int kTileWaves = 8;
 // a quarter step (16 k a lane group) are under way during the products of the
 // quarter before, the last quarter's across the barrier.
 //
-// Measured: 4093 tokens beside adapters of rank 64 on 11008 x 2048 260 us, of
-// which 242 here (191 GFLOP: 790 TFLOP/s; a library fp16 product of 8192^3
-// reaches 1450); 32768 rows in 64 groups of 1408 x 2048, gate and up, 512 us
-// (738 TFLOP/s, ragged last pieces among them).  What is left is the lookups'
+// Measured (cards differ): 4093 tokens beside adapters of rank 64 on 11008 x
+// 2048 264-277 us, of which 251 here (191 GFLOP: 760 TFLOP/s; a library fp16
+// product of 8192^3 reaches 1450); 32768 rows in 64 groups of 1408 x 2048, gate
+// and up, 526-550 us (690-720 TFLOP/s, ragged last pieces among them).  What is
+// left is the lookups'
 // and scalings' instructions beside the products, and the clock that the
-// power of both allows.  Not faster: 16 waves a workgroup (310 us where 8 took
+// power of both allows, and in ragged last pieces the rows that are not there:
+// all 32-row tiles are multiplied.  The scaled weights are rounded to fp16 as in
+// the chunk kernel; held exactly, in two products, the same calls took 381 and
+// 807 us.  Not faster: 16 waves a workgroup (310 us where 8 took
 // 278), waves of other corners of the tile (618 against 555), codes through
 // LDS (spills), 16-bit results of two rows stored together (+35 us).
 template <int MT, bool LORA>
@@ -884,7 +893,9 @@ int64_t chunk_bound(int64_t E, int64_t R, int64_t most) {
 }
 
 // The rules, with what both sides take in us: E x M x K, "up" where there is
-// an up matrix; r ranks of adapters, 0 without.
+// an up matrix; r ranks of adapters, 0 without.  Their costs were measured on
+// the 256 compute units of an MI355X and count those; a size of a workspace
+// has to follow from the shape alone.
 Plan plan_of(int64_t E, int64_t M, int64_t K, int64_t R, bool up, int64_t r) {
     Plan p = {};
     const int64_t groups = E < R ? E : R;
@@ -895,10 +906,14 @@ Plan plan_of(int64_t E, int64_t M, int64_t K, int64_t R, bool up, int64_t r) {
         return n > groups ? n : groups;
     };
     // The row kernel reads a group's codes for each row, but waits for less:
-    // row | chunk for 64 x 1408 x 2048 up, R = 8 9.1 | 16.7, 32 22.4 | 33.6,
-    // 64 34.8 | 44.1; 64 x 2048 x 1408, R = 16 9.3 | 12.2, 32 16.3 | 17.6, 48
-    // 22.0 | 17.5; 8 x 2048 x 4096, R = 4 9.4 | 14.8, 16 21.4 | 17.6;
-    // 1 x 4096 x 4096, R = 2 10.4 | 11.0, 8 20.6 | 11.4.
+    // row | chunk for 64 x 1408 x 2048 up, R = 8 9.1 | 16.7, 32 23.1 | 34.5,
+    // 64 36.1 | 45.1, 80 44.6 | 45.1, 96 51.9 | 44.6, 192 108 | 56; 16 x 2048 x
+    // 4096 up, R = 16 32.7 | 36.2, 24 45.7 | 47.0, 32 53.8 | 51.8; 8 x 1408 x 2048
+    // up, R = 8 8.9 | 16.8, 16 14.7 | 16.9; 64 x 2048 x 1408, R = 16 9.3 | 12.9, 32
+    // 16.2 | 18.6, 40 20.4 | 18.4, 48 21.8 | 18.4; 16 x 2048 x 4096, R = 8 13.2 |
+    // 17.3, 12 19.7 | 18.3; 8 x 2048 x 4096, R = 4 9.4 | 14.8, 16 21.4 | 17.6;
+    // 1 x 4096 x 4096, R = 2 10.4 | 11.0, 8 20.6 | 11.4.  (The sides meet between
+    // E and 2 E with an up matrix, between E / 2 and E without.)
     p.single = R <= 2 || R <= (up ? E : E / 2);
     // Chunks of 16 rows | 32: with two matrices, 64 x 1408 x 2048 up, R = 256
     // (4 a group) 56.2 | 58.8, 512 86.8 | 76.0, 1024 125 | 101.  With one, a

@@ -15,9 +15,11 @@
 // Measured (graph replay): 1 token, 64 experts, top 8 5.1 us in one launch (an
 // empty kernel takes 1.6; the k maxima and the ranks come one after the
 // other).  8192 tokens, 128 experts, top 8 14.2 us in two launches (6.8 + 7.4
-// by themselves) for 5.2 MB: bound by the k rounds of maxima, 6 DPP steps and
-// 8 compares a lane each, and by the ballots of the ranks, not by the bytes
-// (1 us).  With a wave a token it took 29 us.
+// by themselves) for 5.2 MB: bound by the k rounds of two maxima (the value,
+// then the index: 4 DPP steps and 8 compares a lane each), by the ranks (a
+// ballot a bit, the waves one after the other), and by every workgroup of the
+// second launch reading all runs' counts, not by the bytes (1 us).  With a
+// wave a token it took 29 us.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

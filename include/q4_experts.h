@@ -78,11 +78,17 @@ int q4_route_topk(const void *logits, int logits_type, int64_t T, int64_t E,
  *   Y: [R][M] of out_type (Q4_OUT_F32 or Q4_OUT_BF16), 16-byte aligned.
  * Accuracy: each sum is within (2^-10 + (K + 64) 2^-24) * sum_k |What x| +
  * 2^-27 * (max_k |x| * sum_k |What| + max_b |scale_b| * sum_k |x|) of its
- * exact value (fp16 table entries times the block's scale, in fp16 under a
- * power of two per row where groups are large, activations in fp16 under a
- * power of two per token, fp32 sums), then
- * silu and the product in fp32 and one rounding to out_type.  A non-finite
- * activation reaches only the outputs of its own row.
+ * exact value: fp16 table entries, times the block's scale rounded to fp16
+ * (under a power of two per row; calls of single rows take the scale in
+ * fp32), activations in fp16 under a power of two per row, exact where they
+ * are above 2^-28 of the row's largest, fp32 sums.  Unlike the products of
+ * q4.h, smaller activations lose bits, and the scaled weight is rounded: with
+ * bf16 outputs their own rounding covers both, with fp32 outputs the error
+ * (2.2e-4 of the outputs' magnitude, 1.6e-4 from the table entries alone) is
+ * this one.  silu is within 2^-16 of its value and -0 for sums below -88; it
+ * and the product are in fp32, with one rounding to out_type.  A non-finite
+ * activation reaches only the outputs of its own row, as in the formula
+ * (a weight of 0 times an infinity is NaN).
  *   workspace: q4_gemm_grouped_ws_bytes(...) bytes, 16-byte aligned; calls
  *     that may run at the same time need different ones.
  * R == 0 or M == 0 is a no-op; T == 0 makes every row zeros.

@@ -34,6 +34,7 @@ extern "C" {
  *   With L == 0 the adapter arrays may be NULL and Y = What X.
  * Accuracy: the packed product as q4_gemm_grouped; A_a X[n] in fp32, carried
  * to the second product to 2^-16 of each value; one rounding to out_type.
+ * Values of one adapter that are not finite reach only its own tokens.
  * N == 0 or M == 0 is a no-op.
  */
 size_t q4_gemm_lora_ws_bytes(int64_t M, int64_t K, int64_t N, int64_t r,
@@ -54,7 +55,11 @@ int q4_gemm_lora(const uint8_t *codes, const uint16_t *scales, int64_t M,
  *                 (fp32, 16-byte aligned; adapters without a token get 0)
  * dX may be NULL (the first layer), as may dA and dB together (frozen
  * adapters).  Sums are added in a fixed order: every call gives the same bits.
- * Accuracy: dX as q4_gemm_lora; dA and dB in fp32.
+ * Accuracy: the packed product of dX is within (2^-10 + (M + 64) 2^-24) *
+ * sum_m |What dY| + 2^-25 * sum_m s_m |dY_m| + 2^-26 * M * max_m s_m |dY_m| of
+ * its exact value, s_m the largest |scale| of packed row m; u is carried to
+ * 2^-16 of each value, one rounding to bf16; dA and dB in fp32.
+ * M >= 1 (a matrix of no rows has no gradients and is refused as a shape);
  * N == 0 clears dA and dB.
  */
 size_t q4_gemm_lora_backward_ws_bytes(int64_t M, int64_t K, int64_t N,
