@@ -182,3 +182,22 @@ def test_largest(env, M, K, N, r, L):  # noqa: F811
     _within(dX, x, ref.rounded(x, ex, True), "dX")
     _within(dA, a, ea + 2.0 ** -24 * np.abs(a) + 1e-37, "dA")
     _within(dB, b, eb + 2.0 ** -24 * np.abs(b) + 1e-37, "dB")
+
+
+@pytest.mark.parametrize("M,K,N,r", [(64, 256, 4, 16), (200, 2112, 30, 24), (300, 1088, 1100, 40)])
+def test_two_calls_at_once(env, M, K, N, r):  # noqa: F811
+    """Calls on two streams without a wait between them, each with scratch of
+    its own: the bits of calls by themselves."""
+    torch, q4, dev = env
+    cases = [Case(env, M, K, N, r, 3, seed=s, ids="random") for s in (1, 2)]
+    alone = [(q4.q4_gemm_lora(*c.args),) + q4.q4_gemm_lora_backward(c.dYd, *c.args) for c in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    got = [[], []]
+    for _ in range(5):
+        for c, s, g in zip(cases, streams, got):
+            g.append((q4.q4_gemm_lora(*c.args, stream=s),) + q4.q4_gemm_lora_backward(c.dYd, *c.args, stream=s))
+    torch.cuda.synchronize()
+    for g, want in zip(got, alone):
+        for out in g:
+            assert all(torch.equal(a, b) for a, b in zip(out, want))
