@@ -691,3 +691,5 @@ from .experts import (q4_gemm_grouped, q4_gemm_grouped_ws_bytes, q4_moe_combine,
                       q4_route_topk_ws_bytes)
 from .lora import (q4_gemm_lora, q4_gemm_lora_backward, q4_gemm_lora_backward_ws_bytes,  # noqa: E402
                    q4_gemm_lora_ws_bytes)
+from .cache import (KVCache, q4_cache_append, q4_cache_attend, q4_cache_attend_ws_bytes,  # noqa: E402
+                    q4_cache_new, q4_cache_read)
