@@ -12,6 +12,7 @@ using namespace q4::checks;
 namespace {
 
 constexpr int64_t kMost = Q4_CACHE_MAX_TOKENS;
+constexpr int64_t kMostKeys = Q4_CACHE_MAX_KEYS;
 
 bool d_ok(int64_t D) { return D > 0 && D % 64 == 0 && D <= Q4_CACHE_MAX_D; }
 
@@ -50,7 +51,7 @@ Range strided(const void *p, int64_t T, int64_t stride, int64_t width, uint64_t 
 
 bool attend_shape_ok(int64_t T, int64_t q_heads, int64_t heads, int64_t D, int64_t B, int64_t max_q) {
     return T >= 0 && T <= kMost && heads >= 1 && heads <= Q4_CACHE_MAX_HEADS && q_heads >= 1 &&
-           q_heads <= Q4_CACHE_MAX_HEADS && q_heads % heads == 0 && d_ok(D) && B >= 0 && B <= kMost && max_q >= 1 &&
+           q_heads <= Q4_CACHE_MAX_HEADS && q_heads % heads == 0 && d_ok(D) && B >= 0 && B <= kMost && B * heads <= kMost && max_q >= 1 &&
            max_q <= kMost;
 }
 
@@ -140,7 +141,7 @@ int q4_cache_attend(const uint16_t *q, int64_t T, int64_t q_heads, int64_t q_str
     if (!cache) return Q4_ERR_NULL;
     const q4_cache &c = *cache;
     if (!cache_shape_ok(c) || !attend_shape_ok(T, q_heads, c.heads, c.D, B, max_q) || !type_ok(out_type) ||
-        table_pages < 0 || table_pages > INT32_MAX / c.page || window < 0 || window > INT32_MAX ||
+        table_pages < 0 || table_pages > kMostKeys / c.page || window < 0 || window > INT32_MAX ||
         (!causal && window != 0) || !isfinite(scale) || !(scale > 0))
         return Q4_ERR_SHAPE;
     if (!q_offsets && (T != B || max_q != 1)) return Q4_ERR_SHAPE;

@@ -10,6 +10,14 @@ at most D + 16 steps.  With d the largest error of a row's scores, every
 softmax weight is within a factor e^(2 d) of its value.  Weights and values
 enter the second product as fp16: 2^-11 each, 2^-24 a sum; weights below 2^-24
 of the largest may be lost: 2^-24 of the values' magnitudes for each key.
+
+Where codes and zero points are summed apart, out = sum w scale c - sum w scale
+zero, each sum has up to 15 scale a weight, rounded by 2^-24 at every one of
+(keys + 16) additions: 2^-24 (keys + 16) 30 sum w scale.  A matrix core drops
+what lies 2^-24 below the largest product of its 32, aligned as if codes (in
+bits 4 to 7 of an fp16) had the smallest normal exponent 2^-14, that is 2^-18
+of the largest weight (or q) times one code for every product: 32 2^-18 sum w
+scale at most over all keys, and for a score D 2^-18 scale_b max |q|.
 """
 import numpy as np
 
@@ -74,7 +82,7 @@ def attend(q, cache, table, lens, offsets, causal=True, window=0, scale=None, ou
     scale = D ** -0.5 if scale is None else scale
     K = values(cache["k_codes"], cache["k_scales"], cache["k_zeros"])
     V = values(cache["v_codes"], cache["v_scales"], cache["v_zeros"])
-    ks = cache["k_scales"].astype(np.float64)
+    ks, vs = cache["k_scales"].astype(np.float64), cache["v_scales"].astype(np.float64)
     out, bound = np.zeros((T, Hq, D)), np.full((T, Hq, D), 1e-37)
     lse, lse_bound = np.full((T, Hq), -np.inf), np.full((T, Hq), 1e-37)
     touched = np.zeros(T, bool)
@@ -94,13 +102,14 @@ def attend(q, cache, table, lens, offsets, causal=True, window=0, scale=None, ou
             if not len(at):
                 continue
             k, v, s16 = K[ids, :, at % page], V[ids, :, at % page], ks[ids, :, at % page]  # [m, Hkv, .]
+            vs16 = vs[ids, :, at % page]
             for h in range(Hq):
                 kh, vh, sh = k[:, h // G], v[:, h // G], s16[:, h // G]
                 x = q[t, h]
                 s = scale * (kh @ x)
                 ax = np.abs(x)
                 d = scale * (2.0 ** -11 * (np.abs(kh) @ ax) + (D + 16) * 2.0 ** -24 * 30 * (sh @ ax.reshape(-1, 64).sum(1))
-                             + 2.0 ** -24 * ax.max() * np.abs(kh).sum(1)).max() + 2.0 ** -20 * (1 + np.abs(s).max())
+                             + 2.0 ** -24 * ax.max() * np.abs(kh).sum(1) + 64 * 2.0 ** -18 * ax.max() * sh.sum(1)).max() + 2.0 ** -20 * (1 + np.abs(s).max())
                 top = s.max()
                 e = np.exp(s - top)
                 w = e / e.sum()
@@ -108,6 +117,7 @@ def attend(q, cache, table, lens, offsets, causal=True, window=0, scale=None, ou
                 lse_bound[t, h] = d + 2.0 ** -22 * abs(lse[t, h]) + 2.0 ** -20
                 out[t, h] = w @ vh
                 S = w @ np.abs(vh)
-                err = (np.expm1(2 * d) + 2.0 ** -10 + (len(at) + 16) * 2.0 ** -24) * S + 2.0 ** -24 * w.max() * np.abs(vh).sum(0)
+                err = (np.expm1(2 * d) + 2.0 ** -10 + (len(at) + 16) * 2.0 ** -24) * S + np.repeat(
+                    w @ vs16[:, h // G], 64) * (2.0 ** -24 * (len(at) + 16) * 30 + 2.0 ** -13) + 2.0 ** -24 * w.max() * np.abs(vh).sum(0)
                 bound[t, h] += err + (2.0 ** -8 if out_bf16 else 2.0 ** -24) * (np.abs(out[t, h]) + err)
     return out, bound, lse, lse_bound, touched
