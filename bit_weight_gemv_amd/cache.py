@@ -17,6 +17,7 @@ EXPORTED = ("q4_cache_append", "q4_cache_read", "q4_cache_attend_ws_bytes", "q4_
 Q4_CACHE_MAX_HEADS = 1024
 Q4_CACHE_MAX_TOKENS = 4194304
 Q4_CACHE_MAX_KEYS = 1073741824
+Q4_CACHE_MAX_ROWS = 536870912
 Q4_CACHE_MAX_D = 256
 Q4_CACHE_MIN_PAGE = 16
 Q4_CACHE_MAX_PAGE = 4096

@@ -23,6 +23,8 @@ struct AttendArgs {
     int max_rows;     // rows a partial result is kept for
     float *part;      // partial results: [slot][max_rows][D], then (ref, sum) pairs
     float *part_sums;
+    int64_t row_tiles;  // tile kernel: tiles of rows at most
+    int parts;          // workgroups the keys of one are dealt to at most
 };
 
 // A sequence as a kernel sees it, every value within its bounds.
@@ -178,6 +180,17 @@ __device__ __forceinline__ half8_t subnormals(uint32_t w) {
 __device__ __forceinline__ float half_at(const uint32_t *w, int i) {
     const uint32_t u = w[i >> 1];
     return (float)__builtin_bit_cast(_Float16, (unsigned short)(i & 1 ? u >> 16 : u));
+}
+
+// Stores 4 outputs.
+__device__ __forceinline__ void store4(const CacheAttend &a, int64_t at, float4_t v) {
+    if (a.bf16) {
+        typedef __bf16 bf4 __attribute__((ext_vector_type(4)));
+        const bf4 b = {(__bf16)v.x, (__bf16)v.y, (__bf16)v.z, (__bf16)v.w};
+        *reinterpret_cast<bf4 *>(static_cast<uint16_t *>(a.out) + at) = b;
+    } else {
+        *reinterpret_cast<float4_t *>(static_cast<float *>(a.out) + at) = v;
+    }
 }
 
 // What a wave has asked for of a tile of 32 keys.
@@ -673,94 +686,565 @@ __global__ __launch_bounds__(64 * ND) void attend_join_kernel(AttendArgs g) {
         a.lse[t * a.q_heads + hq] = lt == 0 ? -INFINITY : (top + __builtin_amdgcn_logf(lt)) * 0.693147180559945f;
 }
 
-// The sequence that token t belongs to: the last b with q_offsets[b] <= t.
-__device__ __forceinline__ int64_t sequence_of(const int32_t *offsets, int64_t B, int64_t t) {
-    int64_t lo = 0, hi = B + 1;  // offsets before lo are <= t, from hi on > t
-    while (lo < hi) {
-        const int64_t mid = (lo + hi) >> 1;
-        if (offsets[mid] <= t) lo = mid + 1;
-        else hi = mid;
-    }
-    return lo - 1;
+// ---------------------------------------------------------------------------
+// Many rows a sequence (prompts and chunks of them): the tile kernel.
+//
+// Bound by the matrix cores and the exponentials.  A workgroup of 8 waves takes
+// 256 rows of one key head (32 a wave) and walks the keys 64 at a time: they
+// are decoded once, by all waves, into LDS as fp16 (c - zero) scale 2^-E, one
+// buffer ahead of the one in use, so that a tile costs one barrier.  32 x 32 x
+// 16 products: S^T = K Q^T, whose result is the operand of O^T = V^T P^T as it
+// stands; V is turned by the transposing 16-bit LDS read.
+// 2^E is above every scale of the keys so far (of the values': the sums are
+// rescaled when it grows), so that a decoded value is rounded by 2^-11 of
+// itself and none passes fp16.  The sum of a row's weights is that of the
+// rounded weights.
+//
+// Where the rows are few for the card, the keys of a tile of rows are dealt to
+// several workgroups, whose results a second launch joins.
+// ---------------------------------------------------------------------------
+
+constexpr int kRowTile = 256;
+constexpr int kTileWaves = 8;
+constexpr int kTileThreads = 64 * kTileWaves;
+constexpr int kKeys = 64;
+constexpr int kMinKeyTiles = 8;  // tiles of keys a part should have
+constexpr float kTop = 9;        // a weight of 1 is 2^9
+
+struct RowTile {
+    int64_t b;
+    Sequence s;
+    int row0, rows;   // first row, rows of the sequence
+    int lo, hi;       // keys that some row of the tile sees: lo (a multiple of 64) .. hi - 1
+    int parts;        // workgroups its keys are dealt to
+};
+
+__device__ __forceinline__ int row_tiles_of(const AttendArgs &g, const Sequence &s, int64_t *rows) {
+    const int n = s.n < g.a.max_q ? s.n : (int)g.a.max_q;
+    *rows = (int64_t)n * g.G;
+    return n <= 0 || *rows <= g.limit ? 0 : (int)((*rows + kRowTile - 1) / kRowTile);
 }
+
+// The index-th tile of rows; false past the last.
+template <int THREADS>
+__device__ __forceinline__ bool find_row_tile(const AttendArgs &g, int64_t index, int64_t *sums, int64_t *found,
+                                              RowTile &r) {
+    const CacheAttend &a = g.a;
+    const int tid = (int)threadIdx.x, wave = tid >> 6;
+    if (tid == 0) found[0] = -1;
+    int64_t before = 0;
+    for (int64_t b0 = 0; b0 < a.B; b0 += THREADS) {
+        const int64_t b = b0 + tid;
+        int64_t rows;
+        const int t = b < a.B ? row_tiles_of(g, sequence_at(a, b), &rows) : 0;
+        int64_t x = t;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int64_t y = __shfl_up(x, d);
+            if ((tid & 63) >= d) x += y;
+        }
+        if ((tid & 63) == 63) sums[wave] = x;
+        __syncthreads();
+        int64_t off = before, all = 0;
+#pragma unroll
+        for (int w = 0; w < THREADS / 64; ++w) {
+            if (w < wave) off += sums[w];
+            all += sums[w];
+        }
+        if (index >= off + x - t && index < off + x) {
+            found[0] = b;
+            found[1] = index - (off + x - t);
+        }
+        before += all;
+        __syncthreads();
+        if (before > index) break;
+    }
+    if (a.B <= 0) return false;
+    r.b = uniform64(found[0]);
+    if (r.b < 0) return false;
+    r.s = sequence_at(a, r.b);
+    int64_t rows;
+    row_tiles_of(g, r.s, &rows);
+    r.rows = (int)rows;
+    r.row0 = (int)uniform64(found[1]) * kRowTile;
+    const int last = r.row0 + kRowTile < r.rows ? r.row0 + kRowTile : r.rows;
+    const int first_pos = r.s.len - r.s.n + r.row0 / g.G, last_pos = r.s.len - r.s.n + (last - 1) / g.G;
+    r.hi = a.causal ? last_pos + 1 : r.s.len;
+    if (r.hi < 0) r.hi = 0;
+    const int64_t lo = a.window > 0 ? (int64_t)first_pos - a.window + 1 : 0;
+    r.lo = lo > 0 ? (int)(lo < r.hi ? lo : r.hi) & ~(kKeys - 1) : 0;
+    const int nt = (r.hi - r.lo + kKeys - 1) / kKeys;
+    const int most = (nt + kMinKeyTiles - 1) / kMinKeyTiles;
+    r.parts = most < g.parts ? (most < 1 ? 1 : most) : g.parts;
+    return true;
+}
+
+// The pieces of 16 bytes of a row of LDS are dealt so that neither 8 keys at
+// one piece (reads of keys) nor 4 keys at two pieces (transposing reads of
+// values) meet in a bank.
+__device__ __forceinline__ int key_turn(int key) { return key & 7; }
+__device__ __forceinline__ int value_turn(int key) { return ((key & 3) << 1) | ((key >> 2) & 1); }
+
+typedef short short4_t __attribute__((ext_vector_type(4)));
+
+// (code - zero) scale of 8 codes in fp16, in natural order if NATURAL, else 0 4 1 5 2 6 3 7.
+template <bool NATURAL>
+__device__ __forceinline__ u32x4_t decode8(uint32_t w, half2_t off, half2_t s) {
+    uint32_t r[4] = {(w & 0x000F000Fu) | 0x64006400u,  // 1024 + code
+                     ((w >> 4) & 0x000F000Fu) | 0x64006400u, ((w >> 8) & 0x000F000Fu) | 0x64006400u,
+                     ((w >> 12) & 0x000F000Fu) | 0x64006400u};
+    u32x4_t o;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const half2_t h = (__builtin_bit_cast(half2_t, r[i]) + off) * s;
+        r[i] = __builtin_bit_cast(uint32_t, h);
+    }
+    if constexpr (NATURAL) {
+        o[0] = __builtin_amdgcn_perm(r[1], r[0], 0x05040100u);
+        o[1] = __builtin_amdgcn_perm(r[3], r[2], 0x05040100u);
+        o[2] = __builtin_amdgcn_perm(r[1], r[0], 0x07060302u);
+        o[3] = __builtin_amdgcn_perm(r[3], r[2], 0x07060302u);
+    } else {
+        o[0] = r[0];
+        o[1] = r[1];
+        o[2] = r[2];
+        o[3] = r[3];
+    }
+    return o;
+}
+
+// The exponent e with a finite fp16 of these bits below 2^e.
+__device__ __forceinline__ int exponent_above(uint32_t bits) {
+    return bits == 0 ? -24 : bits < 0x400u ? -14 : (int)(bits >> 10) - 14;
+}
+
+struct TileNews {
+    uint32_t key_scale, value_scale;  // the largest finite scales (bits) of a tile
+    uint32_t wild;                    // kWild, kHidden
+};
+enum { kWild = 1, kHidden = 2 };  // some scale of a value is not finite; some page of the table is not one
 
 template <int ND>
-__global__ __launch_bounds__(64) void attend_row_kernel(AttendArgs g) {
+__global__ __launch_bounds__(kTileThreads, 1) void attend_tile_kernel(AttendArgs g) {
+    constexpr int D = ND * 64;
+    constexpr int kUnits = 128 * ND;                 // pieces of 16 bytes of codes of a tile of keys
+    constexpr int kLoads = (2 * kUnits + kTileThreads - 1) / kTileThreads;
+    __shared__ __attribute__((aligned(16))) uint16_t sk[2][kKeys * D];
+    __shared__ __attribute__((aligned(16))) uint16_t sv[2][kKeys * D];
+    __shared__ int64_t sums[kTileWaves], found[2];
+    __shared__ TileNews news[3];
     const CacheAttend &a = g.a;
-    const int lane = (int)threadIdx.x, D = ND * 64;
-    const int64_t t = blockIdx.x / a.q_heads, hq = blockIdx.x % a.q_heads;
-    int64_t b = t, n = 1, j = 0;
-    if (a.q_offsets) {
-        b = sequence_of(a.q_offsets, a.B, t);
-        if (b < 0 || b >= a.B) return;
-        const int64_t first = a.q_offsets[b] < 0 ? 0 : a.q_offsets[b];
-        n = a.q_offsets[b + 1];
-        n = (n > a.T ? a.T : n) - first;
-        j = t - first;
-        if (j >= a.max_q) return;
-        if ((n < a.max_q ? n : a.max_q) * g.G <= g.limit) return;
-    }
-    const int64_t heads = a.cache.heads, page = a.cache.page, h = hq / (a.q_heads / heads);
-    int64_t len = a.lens[b];
-    const int64_t most = a.table_pages * page;
-    len = len < 0 ? 0 : len > most ? most : len;
-    const int64_t pos = len - n + j;
-    const int64_t hi = a.causal ? pos + 1 : len;
-    const int64_t lo = a.window > 0 && pos - a.window + 1 > 0 ? pos - a.window + 1 : 0;
-    float q[ND], o[ND];
+    const int tid = (int)threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int col = lane & 31, half = lane >> 5;
+    const int heads = (int)a.cache.heads, page = (int)a.cache.page, pages = (int)a.cache.pages;
+    // The last tiles of rows see the most keys: they begin first.
+    const int64_t per = (int64_t)heads * g.parts;
+    const int64_t index = g.row_tiles - 1 - blockIdx.x / per;
+    const int part = (int)(blockIdx.x % per) / heads, h = (int)(blockIdx.x % heads);
+    RowTile rt;
+    if (!find_row_tile<kTileThreads>(g, index, sums, found, rt)) return;
+    if (part >= rt.parts) return;
+    const Sequence s = rt.s;
+    const int nt_all = (rt.hi - rt.lo + kKeys - 1) / kKeys;
+    const int t0 = (int)((int64_t)nt_all * part / rt.parts), t1 = (int)((int64_t)nt_all * (part + 1) / rt.parts);
+
+    // Queries: the lane's row, 8 dimensions of every 16.
+    const int r = rt.row0 + 32 * wave + col;
+    const bool live = r < rt.rows;
+    const int j = live ? r / g.G : 0, hq = h * g.G + (live ? r % g.G : 0);
+    half8_t qf[ND * 4];
+    float kappa;
+    {
+        const uint16_t *q = a.q + (int64_t)(s.first + j) * a.q_stride + (int64_t)hq * D + 8 * half;
+        float v[ND * 4][8], top = 0;
 #pragma unroll
-    for (int i = 0; i < ND; ++i) {
-        q[i] = __builtin_bit_cast(float, (uint32_t)a.q[t * a.q_stride + hq * D + 64 * i + lane] << 16);
-        o[i] = 0;
-    }
-    float m = -INFINITY, l = 0;
-    for (int64_t i = lo; i < hi; ++i) {
-        const int32_t id = a.table[b * a.table_pages + (i >> g.page_shift)];
-        if (id < 0 || id >= a.cache.pages) continue;
-        const int64_t r = ((int64_t)id * heads + h) * page + (i & (page - 1));
-        float s = 0;
+        for (int d = 0; d < ND * 4; ++d) {
+            const u32x4_t raw = *reinterpret_cast<const u32x4_t *>(q + 16 * d);
 #pragma unroll
-        for (int d = 0; d < ND; ++d) {
-            const int c = (a.cache.k_codes[r * (D / 2) + 32 * d + lane / 2] >> (4 * (lane & 1))) & 15;
-            s += q[d] * ((float)c - f16_bits_to_f32(a.cache.k_zeros[r * ND + d])) * f16_bits_to_f32(a.cache.k_scales[r * ND + d]);
+            for (int y = 0; y < 4; ++y) {
+                const uint32_t p = raw[y];
+                v[d][2 * y] = __builtin_bit_cast(float, p << 16);
+                v[d][2 * y + 1] = __builtin_bit_cast(float, p & 0xFFFF0000u);
+            }
+#pragma unroll
+            for (int y = 0; y < 8; ++y) {
+                const float m = fabsf(v[d][y]);
+                if (m < INFINITY) top = fmaxf(top, m);
+            }
         }
-        s = wave_sum(s) * a.scale;
-        const float top = fmaxf(m, s);
-        const float base = top == -INFINITY ? 0.0f : top;
-        const float fade = expf(m - base), p = expf(s - base);
-        m = top;
-        l = l * fade + p;
+        top = fmaxf(top, __shfl_xor(top, 32));
+        const int ex = top > 0 ? 10 - (int)__builtin_amdgcn_frexp_expf(top) : 0;  // the largest to 2^9 .. 2^10
+        kappa = ldexpf(a.scale * 1.44269504088896f, -ex);
 #pragma unroll
-        for (int d = 0; d < ND; ++d) {
-            const int c = (a.cache.v_codes[r * (D / 2) + 32 * d + lane / 2] >> (4 * (lane & 1))) & 15;
-            const float v = ((float)c - f16_bits_to_f32(a.cache.v_zeros[r * ND + d])) * f16_bits_to_f32(a.cache.v_scales[r * ND + d]);
-            o[d] = o[d] * fade + p * v;
+        for (int d = 0; d < ND * 4; ++d)
+#pragma unroll
+            for (int y = 0; y < 8; ++y) qf[d][y] = (_Float16)(live ? ldexpf(v[d][(y & 1) * 4 + (y >> 1)], ex) : 0.0f);
+    }
+    const int pos = s.len - s.n + j;
+    const int seen_to = live ? (a.causal ? pos : s.len - 1) : -1;
+    const int seen_from = a.window > 0 ? pos - (int)a.window + 1 : 0;
+    // For the wave: keys that all its rows see, and that some row sees.
+    const int wr0 = rt.row0 + 32 * wave, wr1 = wr0 + 31 < rt.rows ? wr0 + 31 : rt.rows - 1;
+    const bool wave_live = wr0 < rt.rows;
+    const int p0 = s.len - s.n + wr0 / g.G, p1 = s.len - s.n + (wave_live ? wr1 / g.G : 0);
+    const int all_to = a.causal ? p0 : s.len - 1, some_to = wave_live ? (a.causal ? p1 : s.len - 1) : -1;
+    const int64_t all_from = a.window > 0 ? (int64_t)p1 - a.window + 1 : 0;
+    const int64_t some_from = a.window > 0 ? (int64_t)p0 - a.window + 1 : 0;
+
+    const int32_t *table = a.table + rt.b * a.table_pages;
+    auto page_at = [&](int key) -> int {
+        if (key >= s.len) return -1;
+        const int id = table[key >> g.page_shift];
+        return id >= 0 && id < pages ? id : -1;
+    };
+
+    // What the thread decodes: pieces of 32 codes, keys' before values'.
+    u32x4_t raw[kLoads];
+    uint32_t raw_s[kLoads], raw_z[kLoads];
+    int raw_id[kLoads];
+    bool hidden = false;
+    auto ids = [&](int tile) {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const int u = tid + kTileThreads * i, in = u % kUnits;
+            raw_id[i] = u < 2 * kUnits ? page_at(rt.lo + tile * kKeys + in / (2 * ND)) : -1;
+        }
+    };
+    auto load = [&](int tile) {
+        hidden = false;
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const int u = tid + kTileThreads * i, in = u % kUnits, piece = in % (2 * ND);
+            const bool value = u >= kUnits;  // the same for a wave
+            const int key = rt.lo + tile * kKeys + in / (2 * ND);
+            raw_s[i] = raw_z[i] = 0;
+            raw[i] = u32x4_t{0, 0, 0, 0};
+            hidden = hidden || (raw_id[i] < 0 && u < 2 * kUnits && key < s.len);
+            if (raw_id[i] >= 0) {
+                const int64_t row = ((int64_t)raw_id[i] * heads + h) * page + (key & (page - 1));
+                raw[i] = *reinterpret_cast<const u32x4_t *>((value ? a.cache.v_codes : a.cache.k_codes) + row * (D / 2) + piece * 16);
+                raw_s[i] = (value ? a.cache.v_scales : a.cache.k_scales)[row * ND + piece / 2];
+                raw_z[i] = (value ? a.cache.v_zeros : a.cache.k_zeros)[row * ND + piece / 2];
+            }
+        }
+    };
+    auto publish = [&](int tile) {
+        TileNews &n = news[tile % 3];
+        if (__any(hidden) && lane == 0) atomicOr(&n.wild, (uint32_t)kHidden);
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const int u = tid + kTileThreads * i;
+            const bool value = u >= kUnits;
+            const bool fin = raw_s[i] < 0x7C00u;
+            const uint32_t top = wave_max_u32(fin ? raw_s[i] : 0);
+            const bool wild = value && __any(!fin);
+            if (lane == 0 && u < 2 * kUnits) {
+                atomicMax(value ? &n.value_scale : &n.key_scale, top);
+                if (wild) atomicOr(&n.wild, (uint32_t)kWild);
+            }
+        }
+    };
+    auto decode = [&](int buf, int ek, int ev) {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const int u = tid + kTileThreads * i, in = u % kUnits, piece = in % (2 * ND), key = in / (2 * ND);
+            const bool value = u >= kUnits;
+            if (u >= 2 * kUnits) break;
+            uint32_t sb = raw_s[i];
+            if (value && sb >= 0x7C00u) sb = 0;  // (rows that see it are made NaN below)
+            const _Float16 sc = (_Float16)ldexpf(f16_bits_to_f32(sb), -(value ? ev : ek));
+            const _Float16 of = (_Float16)(-1024.0f - f16_bits_to_f32(raw_z[i]));
+            const half2_t s2 = {sc, sc}, o2 = {of, of};
+            // The 4 pieces of 16 bytes are written in an order that depends on
+            // the lane, so that neighbours' do not meet in a bank.
+            const int turn = piece & 3;
+            uint32_t w0 = raw[i].x, w1 = raw[i].y, w2 = raw[i].z, w3 = raw[i].w, x;
+            if (turn & 1) { x = w0; w0 = w1; w1 = w2; w2 = w3; w3 = x; }
+            if (turn & 2) { x = w0; w0 = w2; w2 = x; x = w1; w1 = w3; w3 = x; }
+            const uint32_t w[4] = {w0, w1, w2, w3};
+            uint16_t *row = (value ? sv[buf] : sk[buf]) + key * D;
+            const int swap = value ? value_turn(key) : key_turn(key);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const int at = (4 * piece + ((c + turn) & 3)) ^ swap;
+                const u32x4_t v = value ? decode8<true>(w[c], o2, s2) : decode8<false>(w[c], o2, s2);
+                *reinterpret_cast<u32x4_t *>(row + at * 8) = v;
+            }
+        }
+    };
+
+    float16_t o[2 * ND];
+#pragma unroll
+    for (int y = 0; y < 2 * ND; ++y)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[y][i] = 0;
+    float top = -INFINITY, nk = kTop, ck = INFINITY, l = 0;
+    int ek = -24, ev = -24;      // of the tile in use
+    int ek_next = -24, ev_next = -24;
+    uint32_t wild = 0, wild_next = 0;
+
+    if (t0 < t1) {
+        if (tid < 3) news[tid] = TileNews{0, 0, 0};
+        ids(t0);
+        load(t0);
+        __syncthreads();
+        publish(t0);
+        __syncthreads();
+        {
+            const TileNews n = news[t0 % 3];
+            ek_next = __builtin_amdgcn_readfirstlane(exponent_above(n.key_scale));
+            ev_next = __builtin_amdgcn_readfirstlane(exponent_above(n.value_scale));
+            wild_next = __builtin_amdgcn_readfirstlane(n.wild);
+        }
+        decode(t0 & 1, ek_next, ev_next);
+        if (t0 + 1 < t1) {
+            ids(t0 + 1);
+            load(t0 + 1);
+            publish(t0 + 1);
+        }
+        if (t0 + 2 < t1) ids(t0 + 2);
+    }
+    for (int tile = t0; tile < t1; ++tile) {
+        __syncthreads();
+        // This tile is in LDS, the next one in registers.
+        ek = ek_next;
+        wild = wild_next;
+        if (ev_next != ev) {
+            const float f = exp2i(ev - ev_next);
+            ev = ev_next;
+#pragma unroll
+            for (int y = 0; y < 2 * ND; ++y) o[y] *= f;
+        }
+        if (tile + 1 < t1) {
+            const TileNews n = news[(tile + 1) % 3];
+            const int e1 = __builtin_amdgcn_readfirstlane(exponent_above(n.key_scale));
+            const int e2 = __builtin_amdgcn_readfirstlane(exponent_above(n.value_scale));
+            wild_next = __builtin_amdgcn_readfirstlane(n.wild);
+            ek_next = e1 > ek ? e1 : ek;
+            ev_next = e2 > ev ? e2 : ev;
+            decode((tile + 1) & 1, ek_next, ev_next);
+            if (tid == 0) news[tile % 3] = TileNews{0, 0, 0};  // (read before this barrier, written after the next)
+            if (tile + 2 < t1) load(tile + 2);
+            if (tile + 3 < t1) ids(tile + 3);
+        }
+        const int key0 = rt.lo + tile * kKeys;
+        if (key0 <= some_to && key0 + kKeys - 1 >= some_from) {
+            const uint16_t *kb = sk[tile & 1], *vb = sv[tile & 1];
+            float16_t S[2];
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) S[x][i] = 0;
+#pragma unroll
+                for (int d = 0; d < ND * 4; ++d) {
+                    const u32x4_t k = *reinterpret_cast<const u32x4_t *>(kb + (32 * x + col) * D + ((2 * d + half) ^ key_turn(col)) * 8);
+                    S[x] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(half8_t, k), qf[d], S[x], 0, 0, 0);
+                }
+            }
+            const float kap = ldexpf(kappa, ek);
+            if (key0 + kKeys - 1 > all_to || key0 < all_from || (wild & kHidden)) {
+                uint64_t shown = ~0ull;
+                if (wild & kHidden) shown = __ballot(page_at(key0 + lane) >= 0);
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const int key = key0 + 32 * x + 8 * (i / 4) + 4 * half + (i & 3);
+                        if (key > seen_to || key < seen_from || !(shown >> (key - key0) & 1)) S[x][i] = -INFINITY;
+                    }
+            }
+            float tm = S[0][0];
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) tm = fmaxf(tm, S[x][i]);
+            if (__any(fmaf(tm, kap, ck) > kTop + kHeadroom)) {
+                const float m = fmaxf(top, fmaxf(tm, __shfl_xor(tm, 32)) * kap);
+                const float kn = m == -INFINITY ? kTop : kTop - m;
+                const float fade = top == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(kn - nk);
+                top = m;
+                nk = kn;
+                ck = m == -INFINITY ? INFINITY : kn;
+                l *= fade;
+#pragma unroll
+                for (int y = 0; y < 2 * ND; ++y) o[y] *= fade;
+            }
+            half8_t pf[2][2];
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    u32x4_t w;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float pa = __builtin_amdgcn_exp2f(fmaf(S[x][8 * y + 2 * i], kap, nk));
+                        const float pb = __builtin_amdgcn_exp2f(fmaf(S[x][8 * y + 2 * i + 1], kap, nk));
+                        const half2_t p2 = __builtin_bit_cast(half2_t, __builtin_amdgcn_cvt_pkrtz(pa, pb));
+                        l = __builtin_amdgcn_fdot2(p2, half2_t{1, 1}, l, false);
+                        w[i] = __builtin_bit_cast(uint32_t, p2);
+                    }
+                    pf[x][y] = __builtin_bit_cast(half8_t, w);
+                }
+            const int gk = 4 * half + ((lane & 15) >> 2);               // the key of 8 that the lane's address names
+            const int gd = ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1);   // its piece of a block of 32 dimensions
+#pragma unroll
+            for (int y = 0; y < 2 * ND; ++y) {
+                const uint16_t *va = vb + gk * D + ((4 * y + gd) ^ value_turn(gk)) * 8 + (lane & 1) * 4;
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+#pragma unroll
+                    for (int z = 0; z < 2; ++z) {
+                        typedef __attribute__((address_space(3))) short4_t lds_short4;
+                        const short4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_short4 *)(va + (32 * x + 16 * z) * D));
+                        const short4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_short4 *)(va + (32 * x + 16 * z + 8) * D));
+                        typedef short short8_t __attribute__((ext_vector_type(8)));
+                        const short8_t v8 = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+                        o[y] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(half8_t, v8), pf[x][z], o[y], 0, 0, 0);
+                    }
+            }
+            if (wild & kWild) {
+                // Rows that see a value whose scale is not finite.
+                for (int k = 0; k < kKeys; ++k) {
+                    const int key = key0 + k, id = page_at(key);
+                    if (id < 0) continue;
+                    const int64_t row = ((int64_t)id * heads + h) * page + (key & (page - 1));
+#pragma unroll
+                    for (int d = 0; d < ND; ++d) {
+                        const float bad = a.cache.v_scales[row * ND + d] >= 0x7C00u && key <= seen_to && key >= seen_from ? NAN : 0.0f;
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            o[2 * d][i] += bad;
+                            o[2 * d + 1][i] += bad;
+                        }
+                    }
+                }
+            }
+        }
+        if (tile + 2 < t1) publish(tile + 2);
+    }
+
+    // Results.
+    const float sum = l + __shfl_xor(l, 32), ref = -nk;
+    if (!live) return;
+    const int64_t t = s.first + j;
+    if (rt.parts == 1) {
+        const float f = sum == 0 ? 0.0f : exp2i(ev) / sum;
+        const int64_t at = (t * a.q_heads + hq) * D + 4 * half;
+#pragma unroll
+        for (int y = 0; y < 2 * ND; ++y)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float4_t v;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] = sum == 0 ? 0.0f : o[y][4 * i + e] * f;
+                store4(a, at + 32 * y + 8 * i, v);
+            }
+        if (a.lse && half == 0)
+            a.lse[t * a.q_heads + hq] = sum == 0 ? -INFINITY : (ref + __builtin_amdgcn_logf(sum)) * 0.693147180559945f;
+    } else {
+        const float f = exp2i(ev);
+        const int64_t slot = ((index * heads + h) * g.parts + part) * kRowTile + 32 * wave + col;
+        float *p = g.part + slot * D + 4 * half;
+#pragma unroll
+        for (int y = 0; y < 2 * ND; ++y)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float4_t v;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] = o[y][4 * i + e] * f;
+                *reinterpret_cast<float4_t *>(p + 32 * y + 8 * i) = v;
+            }
+        if (half == 0) {
+            g.part_sums[slot * 2] = ref;
+            g.part_sums[slot * 2 + 1] = sum;
         }
     }
-    const float inv = l == 0 ? 0.0f : 1.0f / l;
-#pragma unroll
-    for (int d = 0; d < ND; ++d) {
-        const int64_t at = (t * a.q_heads + hq) * D + 64 * d + lane;
-        const float y = l == 0 ? 0.0f : o[d] * inv;
-        if (a.bf16)
-            static_cast<__bf16 *>(a.out)[at] = (__bf16)y;
-        else
-            static_cast<float *>(a.out)[at] = y;
-    }
-    if (a.lse && lane == 0) a.lse[t * a.q_heads + hq] = l == 0 ? -INFINITY : m + logf(l);
 }
 
+// Joins the parts of a tile of rows, 16 rows a workgroup.
+template <int ND>
+__global__ __launch_bounds__(256) void attend_tile_join_kernel(AttendArgs g) {
+    constexpr int D = ND * 64;
+    __shared__ int64_t sums[4], found[2];
+    const CacheAttend &a = g.a;
+    const int heads = (int)a.cache.heads, h = (int)(blockIdx.x % heads);
+    const int64_t index = blockIdx.x / heads;
+    RowTile rt;
+    if (!find_row_tile<256>(g, index, sums, found, rt) || rt.parts == 1) return;
+    for (int e = (int)threadIdx.x; e < 16 * D / 4; e += 256) {
+        const int c = (int)blockIdx.y * 16 + e / (D / 4), d = e % (D / 4) * 4, r = rt.row0 + c;
+        if (r >= rt.rows) break;
+        const int64_t slot0 = (index * heads + h) * g.parts * kRowTile + c;
+        float top = -INFINITY;
+        for (int p = 0; p < rt.parts; ++p) {
+            const float *q = g.part_sums + (slot0 + (int64_t)p * kRowTile) * 2;
+            if (q[1] != 0) top = fmaxf(top, q[0]);
+        }
+        float lt = 0;
+        float4_t ot = {0, 0, 0, 0};
+        for (int p = 0; p < rt.parts; ++p) {
+            const int64_t slot = slot0 + (int64_t)p * kRowTile;
+            const float *q = g.part_sums + slot * 2;
+            if (q[1] != 0) {
+                const float f = __builtin_amdgcn_exp2f(q[0] - top);
+                lt = fmaf(f, q[1], lt);
+                const float4_t v = *reinterpret_cast<const float4_t *>(g.part + slot * D + d);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) ot[i] = fmaf(f, v[i], ot[i]);
+            }
+        }
+        const int64_t t = rt.s.first + r / g.G, hq = (int64_t)h * g.G + r % g.G;
+        float4_t v;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = lt == 0 ? 0.0f : ot[i] / lt;
+        store4(a, (t * a.q_heads + hq) * D + d, v);
+        if (a.lse && d == 0) a.lse[t * a.q_heads + hq] = lt == 0 ? -INFINITY : (top + __builtin_amdgcn_logf(lt)) * 0.693147180559945f;
+    }
+}
 
 // Rows of a sequence that the split kernel takes: its accumulators have to
 // stay in registers (16 rows of 64 dimensions are 16 of them).
 static int split_limit(int64_t D) { return D <= 128 ? 64 : 32; }
 
+struct AttendPlan {
+    int64_t split_rows;  // the most rows of a sequence in the split kernel
+    bool tiles;          // whether the tile kernel runs
+    int64_t row_tiles;   // its tiles of rows at most
+    int parts;           // workgroups the keys of one are dealt to
+    size_t split_floats, floats;
+};
+
+static AttendPlan attend_plan(int64_t T, int64_t q_heads, int64_t heads, int64_t D, int64_t B, int64_t max_q) {
+    AttendPlan p = {};
+    const int64_t G = q_heads / heads, limit = split_limit(D);
+    const int64_t q = max_q < T ? max_q : T;
+    p.tiles = q * G > limit;
+    p.split_rows = p.tiles ? limit : q * G;
+    p.split_floats = (size_t)(2 * kSplitGroups) * p.split_rows * (D + 2);
+    p.floats = p.split_floats;
+    if (p.tiles) {
+        // Sequences that have more rows than the limit, and their tiles.
+        const int64_t most = T * G / (limit + 1);
+        p.row_tiles = T * G / kRowTile + (B < most ? B : most);
+        // Parts: as few rounds of the card's 256 compute units for a tile of
+        // rows as possible, a part costing 4 in 100 for the joining.
+        const int64_t n = p.row_tiles * heads;
+        double best = 0;
+        for (int parts = 1; parts <= 8 && (parts == 1 || n * parts <= 1024); ++parts) {
+            const double cost = (double)((n * parts + 255) / 256) / parts * (1 + 0.04 * (parts - 1));
+            if (parts == 1 || cost < best) {
+                best = cost;
+                p.parts = parts;
+            }
+        }
+        const size_t f = p.parts == 1 ? 0 : (size_t)n * p.parts * kRowTile * (D + 2);
+        if (f > p.floats) p.floats = f;
+    }
+    return p;
+}
+
 size_t attend_ws_bytes(int64_t T, int64_t q_heads, int64_t heads, int64_t D, int64_t B, int64_t max_q) {
-    (void)B;
-    const int64_t q = max_q < T ? max_q : T, limit = split_limit(D);
-    int64_t rows = q * (q_heads / heads);
-    if (rows > limit) rows = limit;
-    return (size_t)(2 * kSplitGroups) * rows * (D + 2) * sizeof(float);
+    return attend_plan(T, q_heads, heads, D, B, max_q).floats * sizeof(float);
 }
 
 template <int ND>
@@ -772,6 +1256,29 @@ static const void *split_kernel(int64_t rows) {
     return reinterpret_cast<const void *>(&attend_split_kernel<ND, 2>);
 }
 
+template <int ND>
+static hipError_t launch_attend(AttendArgs &g, const AttendPlan &p, float *workspace, hipStream_t stream) {
+    const CacheAttend &a = g.a;
+    void *args[] = {&g};
+    g.max_rows = (int)p.split_rows;
+    g.part = workspace;
+    g.part_sums = g.part + (size_t)(2 * kSplitGroups) * p.split_rows * a.cache.D;
+    hipError_t e = hipLaunchKernel(split_kernel<ND>(p.split_rows), dim3(kSplitGroups), dim3(kSplitThreads), args, 0, stream);
+    if (e != hipSuccess) return e;
+    e = hipLaunchKernel(reinterpret_cast<const void *>(&attend_join_kernel<ND>),
+                        dim3((unsigned)(a.B * a.cache.heads), (unsigned)p.split_rows), dim3(64 * ND), args, 0, stream);
+    if (e != hipSuccess || !p.tiles) return e;
+    g.row_tiles = p.row_tiles;
+    g.parts = p.parts;
+    const int64_t n = p.row_tiles * a.cache.heads;
+    g.part_sums = g.part + (size_t)n * p.parts * kRowTile * a.cache.D;
+    e = hipLaunchKernel(reinterpret_cast<const void *>(&attend_tile_kernel<ND>), dim3((unsigned)(n * p.parts)),
+                        dim3(kTileThreads), args, 0, stream);
+    if (e != hipSuccess || p.parts == 1) return e;
+    return hipLaunchKernel(reinterpret_cast<const void *>(&attend_tile_join_kernel<ND>), dim3((unsigned)n, kRowTile / 16), dim3(256),
+                           args, 0, stream);
+}
+
 hipError_t launch_cache_attend(const CacheAttend &a, void *workspace, hipStream_t stream) {
     AttendArgs g = {};
     g.a = a;
@@ -779,24 +1286,14 @@ hipError_t launch_cache_attend(const CacheAttend &a, void *workspace, hipStream_
     g.page_shift = __builtin_ctzll((unsigned long long)a.cache.page);
     g.G = (int)(a.q_heads / a.cache.heads);
     g.limit = split_limit(a.cache.D);
-    int64_t rows = a.max_q * g.G;
-    const bool longer = rows > g.limit;
-    if (longer) rows = g.limit;
-    g.max_rows = (int)rows;
-    g.part = static_cast<float *>(workspace);
-    g.part_sums = g.part + (size_t)(2 * kSplitGroups) * rows * a.cache.D;
-    const int nd = (int)(a.cache.D / 64);
-    void *args[] = {&g};
-    const void *split = nd == 1 ? split_kernel<1>(rows) : nd == 2 ? split_kernel<2>(rows) : nd == 3 ? split_kernel<3>(rows) : split_kernel<4>(rows);
-    hipError_t e = hipLaunchKernel(split, dim3(kSplitGroups), dim3(kSplitThreads), args, 0, stream);
-    if (e != hipSuccess) return e;
-    const void *join[4] = {reinterpret_cast<const void *>(&attend_join_kernel<1>), reinterpret_cast<const void *>(&attend_join_kernel<2>),
-                           reinterpret_cast<const void *>(&attend_join_kernel<3>), reinterpret_cast<const void *>(&attend_join_kernel<4>)};
-    e = hipLaunchKernel(join[nd - 1], dim3((unsigned)(a.B * a.cache.heads), (unsigned)rows), dim3(64 * nd), args, 0, stream);
-    if (e != hipSuccess || !longer) return e;
-    const void *row[4] = {reinterpret_cast<const void *>(&attend_row_kernel<1>), reinterpret_cast<const void *>(&attend_row_kernel<2>),
-                          reinterpret_cast<const void *>(&attend_row_kernel<3>), reinterpret_cast<const void *>(&attend_row_kernel<4>)};
-    return hipLaunchKernel(row[nd - 1], dim3((unsigned)(a.T * a.q_heads)), dim3(64), args, 0, stream);
+    const AttendPlan p = attend_plan(a.T, a.q_heads, a.cache.heads, a.cache.D, a.B, a.max_q);
+    float *ws = static_cast<float *>(workspace);
+    switch (a.cache.D / 64) {
+        case 1: return launch_attend<1>(g, p, ws, stream);
+        case 2: return launch_attend<2>(g, p, ws, stream);
+        case 3: return launch_attend<3>(g, p, ws, stream);
+        default: return launch_attend<4>(g, p, ws, stream);
+    }
 }
 
 }  // namespace q4

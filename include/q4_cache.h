@@ -28,7 +28,8 @@ extern "C" {
 
 #define Q4_CACHE_MAX_HEADS 1024     /* heads of the cache, heads of q           */
 #define Q4_CACHE_MAX_TOKENS 4194304 /* T, n, B * heads of one call              */
-#define Q4_CACHE_MAX_KEYS 1073741824 /* table_pages * page                      */
+#define Q4_CACHE_MAX_KEYS 1073741824 /* table_pages * page of q4_cache_attend   */
+#define Q4_CACHE_MAX_ROWS 536870912 /* T * q_heads of q4_cache_attend           */
 #define Q4_CACHE_MAX_D 256          /* D: a multiple of 64 up to this           */
 #define Q4_CACHE_MIN_PAGE 16        /* page: a power of two between these       */
 #define Q4_CACHE_MAX_PAGE 4096

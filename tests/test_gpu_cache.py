@@ -199,6 +199,9 @@ ATTEND = [  # lens, new tokens, heads, G, D, page
     ([300, 70], [200, 1], 2, 2, 64, 16),
     ([190, 250], [33, 140], 1, 4, 256, 64),
     ([140], [77], 1, 3, 192, 16),
+    ([1100], [520], 1, 2, 128, 32),
+    ([700, 20, 2000], [130, 20, 1], 2, 3, 64, 16),
+    ([777], [300], 1, 1, 256, 128),
 ]
 
 
