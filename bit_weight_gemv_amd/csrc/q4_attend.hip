@@ -15,6 +15,16 @@ namespace q4 {
 typedef _Float16 half8_t __attribute__((ext_vector_type(8)));
 typedef int int2_t __attribute__((ext_vector_type(2)));
 
+typedef __attribute__((address_space(4))) int32_t scalar_int;  // read-only: uniform loads are scalar
+
+// What a workgroup of the split kernel leaves for the joining: the rows whose
+// last piece it holds.
+struct End {
+    int first;   // the workgroup of the first piece; -1: nothing to join
+    int second;  // whether that is its second slot
+    int token, rows, h;
+};
+
 struct AttendArgs {
     CacheAttend a;
     int page_shift;
@@ -23,6 +33,7 @@ struct AttendArgs {
     int max_rows;     // rows a partial result is kept for
     float *part;      // partial results: [slot][max_rows][D], then (ref, sum) pairs
     float *part_sums;
+    End *ends;          // split kernel: [workgroup]
     int64_t row_tiles;  // tile kernel: tiles of rows at most
     int parts;          // workgroups the keys of one are dealt to at most
 };
@@ -87,12 +98,8 @@ constexpr int kTile = 32;        // keys a wave takes at a time
 constexpr int kSplitWaves = 4;
 constexpr int kSplitThreads = 64 * kSplitWaves;
 constexpr int kSplitGroups = 512;  // workgroups: two a compute unit
-constexpr int kMinTiles = 8;       // tiles a workgroup should have at least
+constexpr int kMinTiles = 4;       // tiles a workgroup should have at least: one a wave
 constexpr int kHeadroom = 6;       // powers of two that weights may pass 1 by
-
-struct Share {
-    int64_t total, workers;
-};
 
 // Tiles of one key head of a sequence (one at least where it has rows, so
 // that rows without keys are written).
@@ -110,29 +117,40 @@ __device__ __forceinline__ int tiles_of(const AttendArgs &g, const Sequence &s, 
     return t < 1 ? 1 : t;
 }
 
-__device__ __forceinline__ int64_t workers_of(int64_t total) {
-    const int64_t w = (total + kMinTiles - 1) / kMinTiles;
-    return w < 1 ? 1 : w > kSplitGroups ? kSplitGroups : w;
-}
-__device__ __forceinline__ int64_t share_start(int64_t total, int64_t workers, int64_t w) { return total * w / workers; }
-// The worker that holds tile i.
-__device__ __forceinline__ int64_t worker_at(int64_t total, int64_t workers, int64_t i) {
-    int64_t w = (i * workers) / total;
-    while (share_start(total, workers, w + 1) <= i) ++w;
-    while (share_start(total, workers, w) > i) --w;
-    return w;
-}
+// `total` tiles dealt to workgroups: the first `more` get each + 1, the others
+// each.  (32-bit arithmetic where it holds: a 64-bit division is 100 scalar
+// instructions.)
+struct Shares {
+    int64_t each, more, workers;
+    __device__ __forceinline__ explicit Shares(int64_t total) {
+        if (total <= (int64_t)kSplitGroups * kMinTiles) {
+            workers = ((uint32_t)total + kMinTiles - 1) / kMinTiles;
+            each = (uint32_t)total / (uint32_t)workers;
+        } else {
+            workers = kSplitGroups;
+            each = total / kSplitGroups;
+        }
+        more = total - each * workers;
+    }
+    __device__ __forceinline__ int64_t start(int64_t w) const { return each * w + (w < more ? w : more); }
+    // The workgroup that holds tile i.
+    __device__ __forceinline__ int64_t at(int64_t i) const {
+        const int64_t large = more * (each + 1);
+        const int64_t x = i < large ? i : i - large, by = i < large ? each + 1 : each;
+        const int64_t n = ((uint64_t)x | (uint64_t)by) >> 32 ? x / by : (int64_t)((uint32_t)x / (uint32_t)by);
+        return i < large ? n : more + n;
+    }
+};
 
-// Prefix sums of the sequences' tiles by a workgroup of THREADS: the total,
-// and for `find` (a sequence's index, or a position in the sum) where it lies.
-template <int THREADS, class Found>
-__device__ __forceinline__ int64_t scan_tiles(const AttendArgs &g, int64_t *sums, Found found) {
+// Exclusive prefix sums of the sequences' counts by a workgroup of THREADS:
+// found(b, before, count) for every sequence; the total.
+template <int THREADS, class Count, class Found>
+__device__ __forceinline__ int64_t scan_sequences(int64_t B, int64_t *sums, Count count, Found found) {
     const int tid = (int)threadIdx.x, wave = tid >> 6;
     int64_t before = 0;
-    for (int64_t b0 = 0; b0 < g.a.B; b0 += THREADS) {
+    for (int64_t b0 = 0; b0 < B; b0 += THREADS) {
         const int64_t b = b0 + tid;
-        int lo, t = 0;
-        if (b < g.a.B) t = tiles_of(g, sequence_at(g.a, b), &lo);
+        const int64_t t = b < B ? count(b) : 0;
         int64_t x = t;
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) {
@@ -147,7 +165,7 @@ __device__ __forceinline__ int64_t scan_tiles(const AttendArgs &g, int64_t *sums
             if (w < wave) off += sums[w];
             all += sums[w];
         }
-        if (b < g.a.B) found(b, off + x - t, t);
+        if (b < B) found(b, off + x - t, t);
         before += all;
         __syncthreads();
     }
@@ -164,6 +182,17 @@ __device__ __forceinline__ float sum4(float v) {  // over lanes l, l ^ 16, l ^ 3
 __device__ __forceinline__ float max4(float v) {
     v = fmaxf(v, xor16(v));
     return fmaxf(v, __shfl_xor(v, 32));
+}
+
+// The larger of two pairs of 16-bit integers.
+__device__ __forceinline__ uint32_t pk_max(uint32_t a, uint32_t b) {
+    return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2_t, a), __builtin_bit_cast(u16x2_t, b)));
+}
+__device__ __forceinline__ uint32_t half_max(uint32_t v) { return (v >> 16) > (v & 0xFFFF) ? v >> 16 : v & 0xFFFF; }
+// The largest 16-bit integer over lanes l, l ^ 16, l ^ 32, l ^ 48.
+__device__ __forceinline__ uint32_t half_max4(uint32_t v) {
+    v = pk_max(v, (uint32_t)__builtin_amdgcn_ds_swizzle((int)v, 0x401F));
+    return half_max(pk_max(v, (uint32_t)__shfl_xor((int)v, 32)));
 }
 
 // 8 codes as 8 fp16 subnormals c 2^-20, in the order 0 4 1 5 2 6 3 7.
@@ -236,7 +265,7 @@ struct SplitShared {
     int64_t start_b, start_at;
 };
 
-template <int ND, int NT>
+template <int ND, int NT, bool DIRECT>
 __global__ __launch_bounds__(kSplitThreads, NT * ND > 4 ? 1 : 2) void attend_split_kernel(AttendArgs g) {
     constexpr int D = ND * 64;
     __shared__ __attribute__((aligned(16))) SplitShared<ND, NT> sh;
@@ -245,33 +274,73 @@ __global__ __launch_bounds__(kSplitThreads, NT * ND > 4 ? 1 : 2) void attend_spl
     const int col = lane & 15, grp = lane >> 4;
     const int heads = (int)a.cache.heads, page = (int)a.cache.page, pages = (int)a.cache.pages;
 
-    const int64_t tiles = scan_tiles<kSplitThreads>(g, sh.sums, [](int64_t, int64_t, int) {});
-    const int64_t total = tiles * heads, workers = workers_of(total);
     const int64_t w = blockIdx.x;
-    if (total == 0 || w >= workers) return;
-    const int64_t begin = share_start(total, workers, w), end = share_start(total, workers, w + 1);
-    scan_tiles<kSplitThreads>(g, sh.sums, [&](int64_t b, int64_t before, int t) {
-        if (begin >= before * heads && begin < (before + t) * heads) {
-            sh.start_b = b;
-            sh.start_at = before * heads;
+    int64_t begin = 0, end = 1, b, at = 0;  // the share; tiles before sequence b
+    int64_t one_b = 0, one_at = 0, one_t = 0, total = 0;
+    Shares shares(1);
+    if (DIRECT) {
+        // A workgroup per sequence and key head.
+        b = w / heads;
+    } else {
+        total = heads * scan_sequences<kSplitThreads>(
+                            a.B, sh.sums,
+                            [&](int64_t x) {
+                                int lo;
+                                return (int64_t)tiles_of(g, sequence_at(a, x), &lo);
+                            },
+                            [&](int64_t x, int64_t before, int64_t t) { one_b = x; one_at = before; one_t = t; });
+        if (total == 0) {
+            if (tid == 0) g.ends[w].first = -1;
+            return;
         }
-    });
-    int64_t b = uniform64(sh.start_b), at = uniform64(sh.start_at);  // tiles before sequence b
+        shares = Shares(total);
+        if (tid == 0) g.ends[w].first = -1;
+        if (w >= shares.workers) return;
+        begin = shares.start(w);
+        end = shares.start(w + 1);
+        if (a.B <= kSplitThreads) {  // what the scan left with each thread
+            if (tid < a.B && begin >= one_at * heads && begin < (one_at + one_t) * heads) {
+                sh.start_b = one_b;
+                sh.start_at = one_at * heads;
+            }
+            __syncthreads();
+        } else {
+            scan_sequences<kSplitThreads>(
+                a.B, sh.sums,
+                [&](int64_t x) {
+                    int lo;
+                    return (int64_t)tiles_of(g, sequence_at(a, x), &lo);
+                },
+                [&](int64_t x, int64_t before, int64_t t) {
+                    if (begin >= before * heads && begin < (before + t) * heads) {
+                        sh.start_b = x;
+                        sh.start_at = before * heads;
+                    }
+                });
+        }
+        b = uniform64(sh.start_b);
+        at = uniform64(sh.start_at);
+    }
 
     int64_t i = begin;
     while (i < end) {
         const Sequence s = sequence_at(a, b);
         int lo_key;
         const int nt = tiles_of(g, s, &lo_key);
-        if (i >= at + (int64_t)nt * heads) {
+        if (DIRECT) {
+            if (nt == 0) return;
+        } else if (i >= at + (int64_t)nt * heads) {
             at += (int64_t)nt * heads;
             ++b;
             continue;
         }
-        const int h = (int)((i - at) / nt);
-        const int64_t row_start = at + (int64_t)h * nt;
-        const int t0 = (int)(i - row_start);
-        const int t1 = (int)(end - row_start < nt ? end - row_start : nt);
+        // (i - at < nt heads, at most 2^25 2^10.)
+        const int64_t ahead = i - at;
+        const int h = DIRECT ? (int)(w % heads)
+                             : (int)((uint64_t)ahead >> 32 ? ahead / nt : (int64_t)((uint32_t)ahead / (uint32_t)nt));
+        const int64_t row_start = DIRECT ? 0 : at + (int64_t)h * nt;
+        const int t0 = DIRECT ? 0 : (int)(i - row_start);
+        const int t1 = DIRECT ? nt : (int)(end - row_start < nt ? end - row_start : nt);
         const int n = s.n < a.max_q ? s.n : (int)a.max_q;
         const int rows = n * g.G;
 
@@ -284,48 +353,43 @@ __global__ __launch_bounds__(kSplitThreads, NT * ND > 4 ? 1 : 2) void attend_spl
             const int r = 16 * x + col;
             const int j = r < rows ? r / g.G : 0, hq = h * g.G + (r < rows ? r % g.G : 0);
             const uint16_t *q = a.q + (int64_t)(s.first + j) * a.q_stride + (int64_t)hq * D + 16 * grp;
-            float v[ND][16], top = 0;
+            u32x4_t raw[ND][2];
+            uint32_t most = 0;  // of the magnitudes' bits
 #pragma unroll
             for (int d = 0; d < ND; ++d)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const u32x4_t u = *reinterpret_cast<const u32x4_t *>(q + 64 * d + 8 * e);
+                    raw[d][e] = *reinterpret_cast<const u32x4_t *>(q + 64 * d + 8 * e);
 #pragma unroll
                     for (int y = 0; y < 4; ++y) {
-                        const uint32_t p = u[y];
-                        v[d][8 * e + 2 * y] = __builtin_bit_cast(float, p << 16);
-                        v[d][8 * e + 2 * y + 1] = __builtin_bit_cast(float, p & 0xFFFF0000u);
+                        const uint32_t p = raw[d][e][y];
+                        most = pk_max(most, p & 0x7FFF7FFFu);
                     }
                 }
-#pragma unroll
-            for (int d = 0; d < ND; ++d)
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const float m = fabsf(v[d][e]);
-                    if (m < INFINITY) top = fmaxf(top, m);
-                }
-            top = max4(top);
-            // The largest to 2^14 .. 2^15.
-            int ex = 0;
-            if (top > 0) ex = 15 - (int)__builtin_amdgcn_frexp_expf(top);
+            // The row's largest to 2^14 .. 2^15 (a row with an infinity has no
+            // finite result, whatever its other values become).
+            const int ex = r < rows ? 141 - (int)(half_max4(most) >> 7) : -300;
             kappa[x] = ldexpf(a.scale * 1.44269504088896f, 20 - ex);
+            const uint32_t one = 0x00100010u;  // the code 1, twice
+            const half8_t ones = __builtin_bit_cast(half8_t, u32x4_t{one, one, one, one});
 #pragma unroll
             for (int d = 0; d < ND; ++d) {
-                float sum = 0;
+                float4_t sum = {0, 0, 0, 0};
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     half8_t f;
 #pragma unroll
-                    for (int y = 0; y < 8; ++y) {
+                    for (int y = 0; y < 4; ++y) {
                         // Codes come in the order 0 4 1 5 2 6 3 7.
-                        const int src = 8 * e + (y & 1) * 4 + (y >> 1);
-                        const float z = r < rows ? ldexpf(v[d][src], ex) : 0.0f;
-                        f[y] = (_Float16)z;
-                        sum += z;
+                        const uint32_t p = raw[d][e][y];
+                        const int to0 = 2 * y < 4 ? 4 * y : 4 * y - 7, to1 = to0 + 2;
+                        f[to0] = (_Float16)ldexpf(__builtin_bit_cast(float, p << 16), ex);
+                        f[to1] = (_Float16)ldexpf(__builtin_bit_cast(float, p & 0xFFFF0000u), ex);
                     }
                     qf[x][d][e] = f;
+                    sum = __builtin_amdgcn_mfma_f32_16x16x32_f16(ones, f, sum, 0, 0, 0);
                 }
-                qsum[x][d] = sum4(sum) * 0x1p-20f;
+                qsum[x][d] = sum[0];
             }
             const int pos = s.len - s.n + j;
             seen_to[x] = r < rows ? (a.causal ? pos : s.len - 1) : -1;
@@ -353,11 +417,12 @@ __global__ __launch_bounds__(kSplitThreads, NT * ND > 4 ? 1 : 2) void attend_spl
             }
         }
 
-        const int32_t *table = a.table + b * a.table_pages;
-        auto page_of = [&](int key) -> int {
-            if (key >= s.len) return -1;
-            const int id = table[key >> g.page_shift];
-            return id >= 0 && id < pages ? id : -1;
+        // Scalar loads: a vector load here would wait for the codes on the way.
+        const scalar_int *table = (const scalar_int *)(a.table + b * a.table_pages);
+        const int last_page = (s.len - 1) >> g.page_shift;
+        auto entry = [&](int key) -> int {
+            const int p = key >> g.page_shift;
+            return table[p < last_page ? p : last_page];
         };
         // Where the lane's dwords of the scales and zeros lie.
         const uint32_t *par_base[ND];
@@ -374,7 +439,7 @@ __global__ __launch_bounds__(kSplitThreads, NT * ND > 4 ? 1 : 2) void attend_spl
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
                 const int id = t ? id1 : id0;
-                row[t] = ((int64_t)(id < 0 ? 0 : id) * heads + h) * page + ((key + 16 * t) & (page - 1));
+                row[t] = ((int64_t)((uint32_t)id < (uint32_t)pages ? id : 0) * heads + h) * page + ((key + 16 * t) & (page - 1));
             }
         };
         auto load_keys = [&](const int64_t (&row)[2], Tile<ND> &T) {
@@ -396,25 +461,27 @@ __global__ __launch_bounds__(kSplitThreads, NT * ND > 4 ? 1 : 2) void attend_spl
             }
         };
 
+        // The loads of the next tile are made in the last round too (of the
+        // same tile), so that no wait has to hold for both cases.
+        const int tend = s.len > 0 ? t1 : t0;
         int tile = t0 + wave;
         Tile<ND> T;
-        int id0 = -1, id1 = -1;
+        int id0 = -1, id1 = -1, next0 = -1, next1 = -1;  // table entries of this tile and the next
         int64_t row[2];
         uint32_t *const par = sh.in.par[wave];
-        if (tile < t1) {
-            id0 = page_of(lo_key + tile * kTile);
-            id1 = page_of(lo_key + tile * kTile + 16);
+        auto later = [&](int by) { return tile + by * kSplitWaves < tend ? tile + by * kSplitWaves : tile; };
+        if (tile < tend) {
+            id0 = entry(lo_key + tile * kTile);
+            id1 = entry(lo_key + tile * kTile + 16);
+            next0 = entry(lo_key + later(1) * kTile);
+            next1 = entry(lo_key + later(1) * kTile + 16);
             rows_of(tile, id0, id1, row);
             load_values(row, T);
             load_keys(row, T);
         }
-        for (; tile < t1; tile += kSplitWaves) {
-            const bool ok[2] = {id0 >= 0, id1 >= 0};
-            const bool more = tile + kSplitWaves < t1;
-            if (more) {
-                id0 = page_of(lo_key + (tile + kSplitWaves) * kTile);
-                id1 = page_of(lo_key + (tile + kSplitWaves) * kTile + 16);
-            }
+        for (; tile < tend; tile += kSplitWaves) {
+            const bool ok[2] = {(uint32_t)id0 < (uint32_t)pages && lo_key + tile * kTile < s.len,
+                                (uint32_t)id1 < (uint32_t)pages && lo_key + tile * kTile + 16 < s.len};
             const int key = lo_key + tile * kTile;
             uint8_t *vl = sh.in.v[wave];
 #pragma unroll
@@ -423,10 +490,12 @@ __global__ __launch_bounds__(kSplitThreads, NT * ND > 4 ? 1 : 2) void attend_spl
                 par[lane + 64 * d] = T.par[d];
             }
             wave_fence();
-            if (more) {
-                rows_of(tile + kSplitWaves, id0, id1, row);
-                load_values(row, T);
-            }
+            id0 = next0;
+            id1 = next1;
+            rows_of(later(1), id0, id1, row);
+            load_values(row, T);
+            next0 = entry(lo_key + later(2) * kTile);
+            next1 = entry(lo_key + later(2) * kTile + 16);
 
             // Scores.
             float S[NT][2][4];
@@ -452,7 +521,7 @@ __global__ __launch_bounds__(kSplitThreads, NT * ND > 4 ? 1 : 2) void attend_spl
                     }
                 }
             }
-            if (more) load_keys(row, T);
+            load_keys(row, T);
             uint32_t vs[2][2 * ND], vz[2][2 * ND];
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
@@ -460,7 +529,8 @@ __global__ __launch_bounds__(kSplitThreads, NT * ND > 4 ? 1 : 2) void attend_spl
                 read_par<ND>(par, kValueZeros, t, grp, vz[t]);
             }
             const bool masked = key + kTile - 1 > all_to || key < all_from || !ok[0] || !ok[1];
-            if (masked) {
+            if (__builtin_expect(masked, 0)) {
+                asm volatile("");  // (a branch, not selects)
 #pragma unroll
                 for (int t = 0; t < 2; ++t)
 #pragma unroll
@@ -486,12 +556,8 @@ __global__ __launch_bounds__(kSplitThreads, NT * ND > 4 ? 1 : 2) void attend_spl
 #pragma unroll
             for (int t = 0; t < 2; ++t)
 #pragma unroll
-                for (int y = 0; y < 2 * ND; ++y) {
-                    const u16x2_t p = __builtin_bit_cast(u16x2_t, top_bits), c = __builtin_bit_cast(u16x2_t, vs[t][y]);
-                    top_bits = __builtin_bit_cast(uint32_t, __builtin_elementwise_max(p, c));
-                }
-            top_bits = (top_bits >> 16) > (top_bits & 0xFFFF) ? top_bits >> 16 : top_bits & 0xFFFF;
-            bool grown = top_bits > limit_bits;
+                for (int y = 0; y < 2 * ND; ++y) top_bits = pk_max(top_bits, vs[t][y]);
+            bool grown = half_max(top_bits) > limit_bits;
             float tmax[NT];
 #pragma unroll
             for (int x = 0; x < NT; ++x) {
@@ -507,6 +573,15 @@ __global__ __launch_bounds__(kSplitThreads, NT * ND > 4 ? 1 : 2) void attend_spl
                     for (int y = 0; y < 4 * ND; ++y) {
                         const uint32_t v = (vs[t][y >> 1] >> (16 * (y & 1))) & 0xFFFF;
                         fin = v < 0x7C00u && v > fin ? v : fin;
+                        // A scale that is not finite makes the block NaN in the
+                        // rows that see the key, and does not reach the others.
+                        if (v >= 0x7C00u) {
+                            vs[t][y >> 1] &= y & 1 ? 0x0000FFFFu : 0xFFFF0000u;
+                            vz[t][y >> 1] &= y & 1 ? 0x0000FFFFu : 0xFFFF0000u;
+#pragma unroll
+                            for (int x = 0; x < NT; ++x)
+                                if (S[x][t][y / ND] != -INFINITY) zs[x][y % ND] = NAN;
+                        }
                     }
                 fin = wave_max_u32(fin);
                 // Below 2^e: the exponent of the next power of two.
@@ -552,8 +627,7 @@ __global__ __launch_bounds__(kSplitThreads, NT * ND > 4 ? 1 : 2) void attend_spl
                     for (int t = 0; t < 2; ++t)
 #pragma unroll
                         for (int r = 0; r < 4; ++r) {
-                            _Float16 w16 = (_Float16)(p[t][r] * half_at(vs[t], r * ND + d));
-                            if (masked && S[x][t][r] == -INFINITY) w16 = (_Float16)0.0f;
+                            const _Float16 w16 = (_Float16)(p[t][r] * half_at(vs[t], r * ND + d));
                             pf[x][d][2 * r + t] = w16;
                             zs[x][d] = fmaf((float)w16, half_at(vz[t], r * ND + d), zs[x][d]);
                         }
@@ -580,6 +654,11 @@ __global__ __launch_bounds__(kSplitThreads, NT * ND > 4 ? 1 : 2) void attend_spl
         // relative to 2^ref.
         const bool whole = t0 == 0 && t1 == nt;
         const int64_t slot = 2 * w + (i == begin ? 0 : 1);
+        if (!whole && t1 == nt && tid == 0) {
+            // The last piece: it names the others for the joining.
+            const int64_t first = shares.at(row_start);
+            g.ends[w] = End{(int)first, shares.start(first) == row_start ? 0 : 1, s.first, rows, h};
+        }
 #pragma unroll
         for (int x = 0; x < NT; ++x) {
             if (16 * x >= rows) break;
@@ -639,51 +718,58 @@ __global__ __launch_bounds__(kSplitThreads, NT * ND > 4 ? 1 : 2) void attend_spl
     }
 }
 
-// Joins the pieces of one (sequence, key head), a workgroup per row.
+// Joins the pieces of the rows that end with workgroup blockIdx.x, a workgroup
+// per row: 16 ND lanes a piece, the pieces dealt to groups of lanes.
 template <int ND>
-__global__ __launch_bounds__(64 * ND) void attend_join_kernel(AttendArgs g) {
-    constexpr int D = ND * 64;
-    __shared__ int64_t sums[ND];
-    __shared__ int64_t found_at;
+__global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs g) {
+    constexpr int D = ND * 64, kLanes = 16 * ND, kGroups = 256 / kLanes;
+    __shared__ float4_t so[kGroups][kLanes];
+    __shared__ float ss[kGroups];
     const CacheAttend &a = g.a;
-    const int64_t b = blockIdx.x / a.cache.heads;
-    const int h = (int)(blockIdx.x % a.cache.heads), r = (int)blockIdx.y, heads = (int)a.cache.heads;
-    const Sequence s = sequence_at(a, b);
-    int lo_key;
-    const int nt = tiles_of(g, s, &lo_key);
-    const int n = s.n < a.max_q ? s.n : (int)a.max_q;
-    if (nt < 2 || r >= n * g.G) return;
-    const int64_t tiles = scan_tiles<64 * ND>(g, sums, [&](int64_t x, int64_t before, int) {
-        if (x == b) found_at = before;
-    });
-    const int64_t total = tiles * heads, workers = workers_of(total);
-    const int64_t start = found_at * heads + (int64_t)h * nt;
-    const int64_t w0 = worker_at(total, workers, start), w1 = worker_at(total, workers, start + nt - 1);
-    if (w0 == w1) return;
+    const int w1 = (int)blockIdx.x, r = (int)blockIdx.y, tid = (int)threadIdx.x;
+    const End e = g.ends[w1];
+    if (e.first < 0 || r >= e.rows) return;
+    const int pieces = w1 - e.first + 1;
+    const float *sums = g.part_sums + 2 * r;
+    auto slot = [&](int p) { return (int64_t)(2 * (e.first + p) + (p == 0 ? e.second : 0)) * g.max_rows; };
     float top = -INFINITY;
-    for (int64_t w = w0; w <= w1; ++w) {
-        const int64_t slot = 2 * w + (w == w0 && share_start(total, workers, w) != start ? 1 : 0);
-        const float *p = g.part_sums + (slot * g.max_rows + r) * 2;
-        if (p[1] != 0) top = fmaxf(top, p[0]);
+    for (int p = tid & 63; p < pieces; p += 64) {
+        const float *q = sums + 2 * slot(p);
+        if (q[1] != 0) top = fmaxf(top, q[0]);
     }
-    float lt = 0, ot = 0;
-    const int d = (int)threadIdx.x;
-    for (int64_t w = w0; w <= w1; ++w) {
-        const int64_t slot = 2 * w + (w == w0 && share_start(total, workers, w) != start ? 1 : 0);
-        const float *p = g.part_sums + (slot * g.max_rows + r) * 2;
-        if (p[1] != 0) {
-            const float f = __builtin_amdgcn_exp2f(p[0] - top);
-            lt = fmaf(f, p[1], lt);
-            ot = fmaf(f, g.part[(slot * g.max_rows + r) * D + d], ot);
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
+    const int c = tid % kLanes, gr = tid / kLanes;
+    float4_t ot = {0, 0, 0, 0};
+    float lt = 0;
+    if (gr < kGroups)
+        for (int p = gr; p < pieces; p += kGroups) {
+            const int64_t x = slot(p) + r;
+            const float2 q = *reinterpret_cast<const float2 *>(g.part_sums + 2 * x);
+            const float4_t v = *reinterpret_cast<const float4_t *>(g.part + x * D + 4 * c);
+            const float f = q.y != 0 ? __builtin_amdgcn_exp2f(q.x - top) : 0.0f;
+            if (q.y != 0) lt = fmaf(f, q.y, lt);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (q.y != 0) ot[i] = fmaf(f, v[i], ot[i]);
         }
+    if (gr < kGroups) {
+        so[gr][c] = ot;
+        if (c == 0) ss[gr] = lt;
     }
-    const int64_t t = s.first + r / g.G, hq = (int64_t)h * g.G + r % g.G;
-    const float out = lt == 0 ? 0.0f : ot / lt;
-    const int64_t at = (t * a.q_heads + hq) * D + d;
-    if (a.bf16) static_cast<__bf16 *>(a.out)[at] = (__bf16)out;
-    else static_cast<float *>(a.out)[at] = out;
-    if (a.lse && d == 0)
-        a.lse[t * a.q_heads + hq] = lt == 0 ? -INFINITY : (top + __builtin_amdgcn_logf(lt)) * 0.693147180559945f;
+    __syncthreads();
+    if (tid >= kLanes) return;
+    for (int p = 1; p < kGroups; ++p) {
+        lt += ss[p];
+        const float4_t v = so[p][c];
+        ot += v;
+    }
+    const int64_t t = e.token + r / g.G, hq = (int64_t)e.h * g.G + r % g.G;
+    float4_t v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = lt == 0 ? 0.0f : ot[i] / lt;
+    store4(a, (t * a.q_heads + hq) * D + 4 * c, v);
+    if (a.lse && c == 0) a.lse[t * a.q_heads + hq] = lt == 0 ? -INFINITY : (top + __builtin_amdgcn_logf(lt)) * 0.693147180559945f;
 }
 
 // ---------------------------------------------------------------------------
@@ -730,36 +816,19 @@ template <int THREADS>
 __device__ __forceinline__ bool find_row_tile(const AttendArgs &g, int64_t index, int64_t *sums, int64_t *found,
                                               RowTile &r) {
     const CacheAttend &a = g.a;
-    const int tid = (int)threadIdx.x, wave = tid >> 6;
-    if (tid == 0) found[0] = -1;
-    int64_t before = 0;
-    for (int64_t b0 = 0; b0 < a.B; b0 += THREADS) {
-        const int64_t b = b0 + tid;
-        int64_t rows;
-        const int t = b < a.B ? row_tiles_of(g, sequence_at(a, b), &rows) : 0;
-        int64_t x = t;
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const int64_t y = __shfl_up(x, d);
-            if ((tid & 63) >= d) x += y;
-        }
-        if ((tid & 63) == 63) sums[wave] = x;
-        __syncthreads();
-        int64_t off = before, all = 0;
-#pragma unroll
-        for (int w = 0; w < THREADS / 64; ++w) {
-            if (w < wave) off += sums[w];
-            all += sums[w];
-        }
-        if (index >= off + x - t && index < off + x) {
-            found[0] = b;
-            found[1] = index - (off + x - t);
-        }
-        before += all;
-        __syncthreads();
-        if (before > index) break;
-    }
-    if (a.B <= 0) return false;
+    if (threadIdx.x == 0) found[0] = -1;
+    scan_sequences<THREADS>(
+        a.B, sums,
+        [&](int64_t b) {
+            int64_t rows;
+            return (int64_t)row_tiles_of(g, sequence_at(a, b), &rows);
+        },
+        [&](int64_t b, int64_t before, int64_t t) {
+            if (index >= before && index < before + t) {
+                found[0] = b;
+                found[1] = index - before;
+            }
+        });
     r.b = uniform64(found[0]);
     if (r.b < 0) return false;
     r.s = sequence_at(a, r.b);
@@ -1211,7 +1280,7 @@ struct AttendPlan {
     bool tiles;          // whether the tile kernel runs
     int64_t row_tiles;   // its tiles of rows at most
     int parts;           // workgroups the keys of one are dealt to
-    size_t split_floats, floats;
+    size_t floats;         // workspace
 };
 
 static AttendPlan attend_plan(int64_t T, int64_t q_heads, int64_t heads, int64_t D, int64_t B, int64_t max_q) {
@@ -1220,8 +1289,7 @@ static AttendPlan attend_plan(int64_t T, int64_t q_heads, int64_t heads, int64_t
     const int64_t q = max_q < T ? max_q : T;
     p.tiles = q * G > limit;
     p.split_rows = p.tiles ? limit : q * G;
-    p.split_floats = (size_t)(2 * kSplitGroups) * p.split_rows * (D + 2);
-    p.floats = p.split_floats;
+    p.floats = (size_t)(2 * kSplitGroups) * p.split_rows * (D + 2) + kSplitGroups * sizeof(End) / sizeof(float);
     if (p.tiles) {
         // Sequences that have more rows than the limit, and their tiles.
         const int64_t most = T * G / (limit + 1);
@@ -1247,14 +1315,18 @@ size_t attend_ws_bytes(int64_t T, int64_t q_heads, int64_t heads, int64_t D, int
     return attend_plan(T, q_heads, heads, D, B, max_q).floats * sizeof(float);
 }
 
-template <int ND>
+template <int ND, bool DIRECT>
 static const void *split_kernel(int64_t rows) {
-    if (rows <= 16) return reinterpret_cast<const void *>(&attend_split_kernel<ND, 1>);
+    if (rows <= 16) return reinterpret_cast<const void *>(&attend_split_kernel<ND, 1, DIRECT>);
     if constexpr (ND <= 2) {
-        if (rows > 32) return reinterpret_cast<const void *>(&attend_split_kernel<ND, 4>);
+        if (rows > 32) return reinterpret_cast<const void *>(&attend_split_kernel<ND, 4, DIRECT>);
     }
-    return reinterpret_cast<const void *>(&attend_split_kernel<ND, 2>);
+    return reinterpret_cast<const void *>(&attend_split_kernel<ND, 2, DIRECT>);
 }
+
+// Tables that hold at most this many keys a sequence: a workgroup for each
+// (sequence, key head), which needs no plan and no joining.
+constexpr int64_t kDirectKeys = 512;
 
 template <int ND>
 static hipError_t launch_attend(AttendArgs &g, const AttendPlan &p, float *workspace, hipStream_t stream) {
@@ -1263,10 +1335,17 @@ static hipError_t launch_attend(AttendArgs &g, const AttendPlan &p, float *works
     g.max_rows = (int)p.split_rows;
     g.part = workspace;
     g.part_sums = g.part + (size_t)(2 * kSplitGroups) * p.split_rows * a.cache.D;
-    hipError_t e = hipLaunchKernel(split_kernel<ND>(p.split_rows), dim3(kSplitGroups), dim3(kSplitThreads), args, 0, stream);
-    if (e != hipSuccess) return e;
-    e = hipLaunchKernel(reinterpret_cast<const void *>(&attend_join_kernel<ND>),
-                        dim3((unsigned)(a.B * a.cache.heads), (unsigned)p.split_rows), dim3(64 * ND), args, 0, stream);
+    g.ends = reinterpret_cast<End *>(g.part_sums + (size_t)(2 * kSplitGroups) * p.split_rows * 2);
+    hipError_t e;
+    if (a.table_pages * a.cache.page <= kDirectKeys) {
+        e = hipLaunchKernel(split_kernel<ND, true>(p.split_rows), dim3((unsigned)(a.B * a.cache.heads)), dim3(kSplitThreads), args, 0,
+                            stream);
+    } else {
+        e = hipLaunchKernel(split_kernel<ND, false>(p.split_rows), dim3(kSplitGroups), dim3(kSplitThreads), args, 0, stream);
+        if (e != hipSuccess) return e;
+        e = hipLaunchKernel(reinterpret_cast<const void *>(&attend_join_kernel<ND>), dim3(kSplitGroups, (unsigned)p.split_rows),
+                            dim3(256), args, 0, stream);
+    }
     if (e != hipSuccess || !p.tiles) return e;
     g.row_tiles = p.row_tiles;
     g.parts = p.parts;
