@@ -7,6 +7,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "q4_cache_internal.h"
 #include "q4_device.h"
 
@@ -14,6 +16,15 @@ namespace q4 {
 
 typedef _Float16 half8_t __attribute__((ext_vector_type(8)));
 typedef int int2_t __attribute__((ext_vector_type(2)));
+
+typedef __attribute__((address_space(4))) int32_t scalar_int;  // read-only: uniform loads are scalar
+
+// Where the pieces of a (sequence, key head) lie that the split kernel dealt to
+// several waves; first == last: it was not.
+struct Pieces {
+    int first, last;  // the waves of the first and the last piece
+    int second;       // whether the first is its wave's second slot
+};
 
 typedef __attribute__((address_space(4))) int32_t scalar_int;  // read-only: uniform loads are scalar
 
@@ -29,11 +40,13 @@ struct AttendArgs {
     CacheAttend a;
     int page_shift;
     int G;            // query heads a key head
+    uint32_t inv_G;   // 2^16 / G, rounded up: r inv_G / 2^16 is r / G for r < 64, G <= 64
     int limit;        // the split kernel takes sequences of at most this many rows
     int max_rows;     // rows a partial result is kept for
     float *part;      // partial results: [slot][max_rows][D], then (ref, sum) pairs
     float *part_sums;
-    End *ends;          // split kernel: [workgroup]
+    Pieces *pieces;     // split kernel: [sequence][key head]
+    int waves;          // its waves at most
     int64_t row_tiles;  // tile kernel: tiles of rows at most
     int parts;          // workgroups the keys of one are dealt to at most
 };
@@ -57,6 +70,24 @@ __device__ __forceinline__ Sequence sequence_at(const CacheAttend &a, int64_t b)
     }
     const int64_t most = a.table_pages * a.cache.page;
     const int len = a.lens[b];
+    s.len = len < 0 ? 0 : len > most ? (int)most : len;
+    return s;
+}
+
+// The same for a uniform b, by scalar loads.
+__device__ __forceinline__ Sequence sequence_uniform(const CacheAttend &a, int64_t b) {
+    Sequence s;
+    s.first = (int)b;
+    s.n = 1;
+    const int T = (int)a.T;
+    if (a.q_offsets) {
+        const scalar_int *o = (const scalar_int *)a.q_offsets;
+        const int lo = o[b], hi = o[b + 1];
+        s.first = lo < 0 ? 0 : lo > T ? T : lo;
+        s.n = (hi < s.first ? s.first : hi > T ? T : hi) - s.first;
+    }
+    const int64_t most = a.table_pages * a.cache.page;
+    const int len = ((const scalar_int *)a.lens)[b];
     s.len = len < 0 ? 0 : len > most ? (int)most : len;
     return s;
 }
@@ -88,17 +119,16 @@ __device__ __forceinline__ Sequence sequence_at(const CacheAttend &a, int64_t b)
 // grows by less than 2^6 nothing is rescaled.
 //
 // The work is the list of all tiles of 32 keys of all (sequence, key head),
-// dealt evenly to a fixed number of workgroups, whatever the lengths: each
-// finds its share from the lengths.  What a workgroup begins and does not end,
-// or ends and did not begin, goes to the workspace, and a second launch joins
-// the pieces in order (the same bits on every call).
+// dealt evenly to a fixed number of waves, whatever the lengths: each finds its
+// share from the lengths.  What a wave begins and does not end, or ends and did
+// not begin, goes to the workspace, and a second launch joins the pieces in
+// order (the same bits on every call).
 // ---------------------------------------------------------------------------
 
 constexpr int kTile = 32;        // keys a wave takes at a time
 constexpr int kSplitWaves = 4;
 constexpr int kSplitThreads = 64 * kSplitWaves;
-constexpr int kSplitGroups = 512;  // workgroups: two a compute unit
-constexpr int kMinTiles = 4;       // tiles a workgroup should have at least: one a wave
+constexpr int kMinTiles = 3;       // tiles a wave should have at least
 constexpr int kHeadroom = 6;       // powers of two that weights may pass 1 by
 
 // Tiles of one key head of a sequence (one at least where it has rows, so
@@ -117,23 +147,19 @@ __device__ __forceinline__ int tiles_of(const AttendArgs &g, const Sequence &s, 
     return t < 1 ? 1 : t;
 }
 
-// `total` tiles dealt to workgroups: the first `more` get each + 1, the others
-// each.  (32-bit arithmetic where it holds: a 64-bit division is 100 scalar
-// instructions.)
+// `total` tiles dealt to at most `waves` waves: the first `more` get each + 1,
+// the others each.  (32-bit arithmetic where it holds: a 64-bit division is
+// 100 scalar instructions.)
 struct Shares {
     int64_t each, more, workers;
-    __device__ __forceinline__ explicit Shares(int64_t total) {
-        if (total <= (int64_t)kSplitGroups * kMinTiles) {
-            workers = ((uint32_t)total + kMinTiles - 1) / kMinTiles;
-            each = (uint32_t)total / (uint32_t)workers;
-        } else {
-            workers = kSplitGroups;
-            each = total / kSplitGroups;
-        }
+    __device__ __forceinline__ Shares(int64_t total, int waves) {
+        workers = waves;
+        if (total <= (int64_t)waves * kMinTiles) workers = ((uint32_t)total + kMinTiles - 1) / kMinTiles;
+        each = (uint64_t)total >> 32 ? total / workers : (int64_t)((uint32_t)total / (uint32_t)workers);
         more = total - each * workers;
     }
     __device__ __forceinline__ int64_t start(int64_t w) const { return each * w + (w < more ? w : more); }
-    // The workgroup that holds tile i.
+    // The wave that holds tile i.
     __device__ __forceinline__ int64_t at(int64_t i) const {
         const int64_t large = more * (each + 1);
         const int64_t x = i < large ? i : i - large, by = i < large ? each + 1 : each;
@@ -250,81 +276,80 @@ __device__ __forceinline__ void read_par(const uint32_t *lds, int plane, int t, 
     }
 }
 
-template <int ND, int NT>
+// Workgroups a compute unit: what the registers allow.
+constexpr int split_occupancy(int ND, int NT) { return NT * ND <= 2 ? 3 : NT * ND <= 4 ? 2 : 1; }
+
+template <int ND, bool DIRECT>
 struct SplitShared {
-    static constexpr int kPad = 4;
-    union {
-        struct {
-            uint8_t v[kSplitWaves][kTile * ND * 32];
-            uint32_t par[kSplitWaves][64 * ND];
-        } in;
-        float o[kSplitWaves][16][ND * 64 + kPad];
+    struct In {
+        uint8_t v[kSplitWaves][kTile * ND * 32];
+        uint32_t par[kSplitWaves][64 * ND];
     };
-    float ref[kSplitWaves][16 * NT], sum[kSplitWaves][16 * NT];
+    struct Out {  // of the waves that share a (sequence, key head)
+        float o[kSplitWaves][16][ND * 64 + 4];
+        float ref[kSplitWaves][16], sum[kSplitWaves][16];
+    };
+    struct None {};
+    union {
+        In in;
+        std::conditional_t<DIRECT, Out, None> out;
+    };
     int64_t sums[kSplitWaves];
-    int64_t start_b, start_at;
+    int64_t start_b[kSplitWaves], start_at[kSplitWaves];
 };
 
 template <int ND, int NT, bool DIRECT>
-__global__ __launch_bounds__(kSplitThreads, NT * ND > 4 ? 1 : 2) void attend_split_kernel(AttendArgs g) {
+__global__ __launch_bounds__(kSplitThreads, split_occupancy(ND, NT)) void attend_split_kernel(AttendArgs g) {
     constexpr int D = ND * 64;
-    __shared__ __attribute__((aligned(16))) SplitShared<ND, NT> sh;
+    __shared__ __attribute__((aligned(16))) SplitShared<ND, DIRECT> sh;
     const CacheAttend &a = g.a;
     const int tid = (int)threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int col = lane & 15, grp = lane >> 4;
     const int heads = (int)a.cache.heads, page = (int)a.cache.page, pages = (int)a.cache.pages;
 
-    const int64_t w = blockIdx.x;
-    int64_t begin = 0, end = 1, b, at = 0;  // the share; tiles before sequence b
+    int64_t w = DIRECT ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * kSplitWaves + wave;
+    int64_t begin = 0, end = 1, b, at = 0;  // the wave's share; tiles before sequence b
     int64_t one_b = 0, one_at = 0, one_t = 0, total = 0;
-    Shares shares(1);
+    Shares shares(1, 1);
     if (DIRECT) {
-        // A workgroup per sequence and key head.
+        // A workgroup per sequence and key head: its waves take tiles in turn.
         b = w / heads;
     } else {
+        auto count = [&](int64_t x) {
+            int lo;
+            return (int64_t)tiles_of(g, sequence_at(a, x), &lo);
+        };
         total = heads * scan_sequences<kSplitThreads>(
-                            a.B, sh.sums,
-                            [&](int64_t x) {
-                                int lo;
-                                return (int64_t)tiles_of(g, sequence_at(a, x), &lo);
-                            },
-                            [&](int64_t x, int64_t before, int64_t t) { one_b = x; one_at = before; one_t = t; });
-        if (total == 0) {
-            if (tid == 0) g.ends[w].first = -1;
-            return;
+                            a.B, sh.sums, count, [&](int64_t x, int64_t before, int64_t t) { one_b = x; one_at = before; one_t = t; });
+        if (total == 0) return;
+        shares = Shares(total, g.waves);
+        auto place = [&](int64_t x, int64_t before, int64_t t) {
+#pragma unroll
+            for (int y = 0; y < kSplitWaves; ++y) {
+                const int64_t i = shares.start((int64_t)blockIdx.x * kSplitWaves + y);
+                if (i >= before * heads && i < (before + t) * heads) {
+                    sh.start_b[y] = x;
+                    sh.start_at[y] = before * heads;
+                }
+            }
+        };
+        if (a.B <= kSplitThreads) {  // what the scan left with each thread
+            place(one_b, one_at, one_t);
+            __syncthreads();
+        } else {
+            scan_sequences<kSplitThreads>(a.B, sh.sums, count, place);
         }
-        shares = Shares(total);
-        if (tid == 0) g.ends[w].first = -1;
+        // From here on the waves go their own ways.
         if (w >= shares.workers) return;
         begin = shares.start(w);
         end = shares.start(w + 1);
-        if (a.B <= kSplitThreads) {  // what the scan left with each thread
-            if (tid < a.B && begin >= one_at * heads && begin < (one_at + one_t) * heads) {
-                sh.start_b = one_b;
-                sh.start_at = one_at * heads;
-            }
-            __syncthreads();
-        } else {
-            scan_sequences<kSplitThreads>(
-                a.B, sh.sums,
-                [&](int64_t x) {
-                    int lo;
-                    return (int64_t)tiles_of(g, sequence_at(a, x), &lo);
-                },
-                [&](int64_t x, int64_t before, int64_t t) {
-                    if (begin >= before * heads && begin < (before + t) * heads) {
-                        sh.start_b = x;
-                        sh.start_at = before * heads;
-                    }
-                });
-        }
-        b = uniform64(sh.start_b);
-        at = uniform64(sh.start_at);
+        b = uniform64(sh.start_b[wave]);
+        at = uniform64(sh.start_at[wave]);
     }
 
     int64_t i = begin;
     while (i < end) {
-        const Sequence s = sequence_at(a, b);
+        const Sequence s = sequence_uniform(a, b);
         int lo_key;
         const int nt = tiles_of(g, s, &lo_key);
         if (DIRECT) {
@@ -344,6 +369,69 @@ __global__ __launch_bounds__(kSplitThreads, NT * ND > 4 ? 1 : 2) void attend_spl
         const int n = s.n < a.max_q ? s.n : (int)a.max_q;
         const int rows = n * g.G;
 
+        // Scalar loads: a vector load here would wait for the codes on the way.
+        const scalar_int *table = (const scalar_int *)(a.table + b * a.table_pages);
+        const int last_page = (s.len - 1) >> g.page_shift;
+        auto entry = [&](int key) -> int {
+            const int p = key >> g.page_shift;
+            return table[p < last_page ? p : last_page];
+        };
+        // Where the lane's dwords of the scales and zeros lie.
+        const uint32_t *par_base[ND];
+        bool par_second[ND];
+#pragma unroll
+        for (int d = 0; d < ND; ++d) {
+            const int c = lane + 64 * d, plane = c / (16 * ND), in = c - plane * 16 * ND;
+            const uint16_t *pp = plane == 0 ? a.cache.k_scales : plane == 1 ? a.cache.k_zeros : plane == 2 ? a.cache.v_scales : a.cache.v_zeros;
+            par_second[d] = in >= 8 * ND;
+            par_base[d] = reinterpret_cast<const uint32_t *>(pp) + (in >= 8 * ND ? in - 8 * ND : in);
+        }
+        auto rows_of = [&](int tile, int id0, int id1, int64_t (&row)[2]) {
+            const int key = lo_key + tile * kTile;
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                const int id = t ? id1 : id0;
+                row[t] = ((int64_t)((uint32_t)id < (uint32_t)pages ? id : 0) * heads + h) * page + ((key + 16 * t) & (page - 1));
+            }
+        };
+        auto load_keys = [&](const int64_t (&row)[2], Tile<ND> &T) {
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                const uint8_t *kc = a.cache.k_codes + row[t] * (D / 2) + (col * (D / 2) + 8 * grp);
+#pragma unroll
+                for (int d = 0; d < ND; ++d) T.k[t][d] = *reinterpret_cast<const u32x2_t *>(kc + 32 * d);
+            }
+        };
+        auto load_values = [&](const int64_t (&row)[2], Tile<ND> &T) {
+#pragma unroll
+            for (int d = 0; d < ND; ++d) {
+                const int c = lane + 64 * d;
+                const bool t = c >= 32 * ND;
+                T.v[d] = *reinterpret_cast<const u32x4_t *>(a.cache.v_codes + (t ? row[1] : row[0]) * (D / 2) +
+                                                            (t ? c - 32 * ND : c) * 16);
+                T.par[d] = par_base[d][(par_second[d] ? row[1] : row[0]) * ND / 2];
+            }
+        };
+
+        // The loads of the next tile are made in the last round too (of the
+        // same tile), so that no wait has to hold for both cases.
+        const int tend = s.len > 0 ? t1 : t0;
+        constexpr int kStep = DIRECT ? kSplitWaves : 1;
+        int tile = t0 + (DIRECT ? wave : 0);
+        Tile<ND> T;
+        int id0 = -1, id1 = -1, next0 = -1, next1 = -1;  // table entries of this tile and the next
+        int64_t row[2];
+        uint32_t *const par = sh.in.par[wave];
+        auto later = [&](int by) { return tile + by * kStep < tend ? tile + by * kStep : tile; };
+        if (tile < tend) {
+            id0 = entry(lo_key + tile * kTile);
+            id1 = entry(lo_key + tile * kTile + 16);
+            next0 = entry(lo_key + later(1) * kTile);
+            next1 = entry(lo_key + later(1) * kTile + 16);
+            rows_of(tile, id0, id1, row);
+            load_values(row, T);
+            load_keys(row, T);
+        }
         // Queries: the lane's row of each tile of 16, its 8 dimensions of every 32.
         half8_t qf[NT][ND][2];
         float qsum[NT][ND], kappa[NT];
@@ -351,8 +439,8 @@ __global__ __launch_bounds__(kSplitThreads, NT * ND > 4 ? 1 : 2) void attend_spl
 #pragma unroll
         for (int x = 0; x < NT; ++x) {
             const int r = 16 * x + col;
-            const int j = r < rows ? r / g.G : 0, hq = h * g.G + (r < rows ? r % g.G : 0);
-            const uint16_t *q = a.q + (int64_t)(s.first + j) * a.q_stride + (int64_t)hq * D + 16 * grp;
+            const int j = r < rows ? (int)(r * g.inv_G >> 16) : 0, hq = h * g.G + (r < rows ? r - j * g.G : 0);
+            const uint16_t *q = a.q + (int64_t)(s.first + j) * a.q_stride + (hq * D + 16 * grp);
             u32x4_t raw[ND][2];
             uint32_t most = 0;  // of the magnitudes' bits
 #pragma unroll
@@ -417,69 +505,7 @@ __global__ __launch_bounds__(kSplitThreads, NT * ND > 4 ? 1 : 2) void attend_spl
             }
         }
 
-        // Scalar loads: a vector load here would wait for the codes on the way.
-        const scalar_int *table = (const scalar_int *)(a.table + b * a.table_pages);
-        const int last_page = (s.len - 1) >> g.page_shift;
-        auto entry = [&](int key) -> int {
-            const int p = key >> g.page_shift;
-            return table[p < last_page ? p : last_page];
-        };
-        // Where the lane's dwords of the scales and zeros lie.
-        const uint32_t *par_base[ND];
-        bool par_second[ND];
-#pragma unroll
-        for (int d = 0; d < ND; ++d) {
-            const int c = lane + 64 * d, plane = c / (16 * ND), in = c - plane * 16 * ND;
-            const uint16_t *pp = plane == 0 ? a.cache.k_scales : plane == 1 ? a.cache.k_zeros : plane == 2 ? a.cache.v_scales : a.cache.v_zeros;
-            par_second[d] = in >= 8 * ND;
-            par_base[d] = reinterpret_cast<const uint32_t *>(pp) + (in >= 8 * ND ? in - 8 * ND : in);
-        }
-        auto rows_of = [&](int tile, int id0, int id1, int64_t (&row)[2]) {
-            const int key = lo_key + tile * kTile;
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                const int id = t ? id1 : id0;
-                row[t] = ((int64_t)((uint32_t)id < (uint32_t)pages ? id : 0) * heads + h) * page + ((key + 16 * t) & (page - 1));
-            }
-        };
-        auto load_keys = [&](const int64_t (&row)[2], Tile<ND> &T) {
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                const uint8_t *kc = a.cache.k_codes + row[t] * (D / 2) + (col * (D / 2) + 8 * grp);
-#pragma unroll
-                for (int d = 0; d < ND; ++d) T.k[t][d] = *reinterpret_cast<const u32x2_t *>(kc + 32 * d);
-            }
-        };
-        auto load_values = [&](const int64_t (&row)[2], Tile<ND> &T) {
-#pragma unroll
-            for (int d = 0; d < ND; ++d) {
-                const int c = lane + 64 * d;
-                const bool t = c >= 32 * ND;
-                T.v[d] = *reinterpret_cast<const u32x4_t *>(a.cache.v_codes + (t ? row[1] : row[0]) * (D / 2) +
-                                                            (t ? c - 32 * ND : c) * 16);
-                T.par[d] = par_base[d][(par_second[d] ? row[1] : row[0]) * ND / 2];
-            }
-        };
-
-        // The loads of the next tile are made in the last round too (of the
-        // same tile), so that no wait has to hold for both cases.
-        const int tend = s.len > 0 ? t1 : t0;
-        int tile = t0 + wave;
-        Tile<ND> T;
-        int id0 = -1, id1 = -1, next0 = -1, next1 = -1;  // table entries of this tile and the next
-        int64_t row[2];
-        uint32_t *const par = sh.in.par[wave];
-        auto later = [&](int by) { return tile + by * kSplitWaves < tend ? tile + by * kSplitWaves : tile; };
-        if (tile < tend) {
-            id0 = entry(lo_key + tile * kTile);
-            id1 = entry(lo_key + tile * kTile + 16);
-            next0 = entry(lo_key + later(1) * kTile);
-            next1 = entry(lo_key + later(1) * kTile + 16);
-            rows_of(tile, id0, id1, row);
-            load_values(row, T);
-            load_keys(row, T);
-        }
-        for (; tile < tend; tile += kSplitWaves) {
+        for (; tile < tend; tile += kStep) {
             const bool ok[2] = {(uint32_t)id0 < (uint32_t)pages && lo_key + tile * kTile < s.len,
                                 (uint32_t)id1 < (uint32_t)pages && lo_key + tile * kTile + 16 < s.len};
             const int key = lo_key + tile * kTile;
@@ -650,86 +676,109 @@ __global__ __launch_bounds__(kSplitThreads, NT * ND > 4 ? 1 : 2) void attend_spl
                 }
         }
 
-        // The four waves' results, 16 rows at a time.  A row's weights stand
-        // relative to 2^ref.
+        // Results, 16 rows at a time.  A row's weights stand relative to 2^ref.
         const bool whole = t0 == 0 && t1 == nt;
-        const int64_t slot = 2 * w + (i == begin ? 0 : 1);
-        if (!whole && t1 == nt && tid == 0) {
-            // The last piece: it names the others for the joining.
-            const int64_t first = shares.at(row_start);
-            g.ends[w] = End{(int)first, shares.start(first) == row_start ? 0 : 1, s.first, rows, h};
+        if (!DIRECT && t1 == nt && lane == 0) {
+            const int64_t first = whole ? w : shares.at(row_start);
+            g.pieces[b * heads + h] = Pieces{(int)first, (int)w, shares.start(first) == row_start ? 0 : 1};
         }
 #pragma unroll
         for (int x = 0; x < NT; ++x) {
             if (16 * x >= rows) break;
-            const float sum = sum4(l[x]);
-            const float ref = -nk[x];
-            __syncthreads();
-            if (grp == 0) {
-                sh.ref[wave][col] = ref;
-                sh.sum[wave][col] = sum;
-            }
+            float sum = sum4(l[x]), ref = -nk[x], z[ND];
 #pragma unroll
-            for (int d = 0; d < ND; ++d) {
-                const float z = sum4(zs[x][d]);
+            for (int d = 0; d < ND; ++d) z[d] = sum4(zs[x][d]);
+            const int r = 16 * x + col, j = (int)(r * g.inv_G >> 16);
+            const int64_t at_row = (int64_t)(s.first + j) * a.q_heads + (h * g.G + r - j * g.G);
+            if constexpr (!DIRECT) {
+                if (r >= rows) continue;
+                const int64_t at_part = (2 * w + (i == begin ? 0 : 1)) * g.max_rows + r;
+                const float f = !whole ? 1.0f : sum == 0 ? 0.0f : 1.0f / sum;
 #pragma unroll
-                for (int y = 0; y < 4; ++y) {
-                    float4_t v;
+                for (int d = 0; d < ND; ++d)
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) v[r] = fmaf(o[x][d][y][r], 0x1p20f, -z);
-                    *reinterpret_cast<float4_t *>(&sh.o[wave][col][64 * d + 16 * y + 4 * grp]) = v;
+                    for (int y = 0; y < 4; ++y) {
+                        float4_t v;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) v[e] = whole && sum == 0 ? 0.0f : fmaf(o[x][d][y][e], 0x1p20f, -z[d]) * f;
+                        const int at_d = 64 * d + 16 * y + 4 * grp;
+                        if (whole) store4(a, at_row * D + at_d, v);
+                        else *reinterpret_cast<float4_t *>(g.part + at_part * D + at_d) = v;
+                    }
+                if (grp == 0) {
+                    if (!whole) *reinterpret_cast<float2 *>(g.part_sums + at_part * 2) = make_float2(ref, sum);
+                    else if (a.lse)
+                        a.lse[at_row] = sum == 0 ? -INFINITY : (ref + __builtin_amdgcn_logf(sum)) * 0.693147180559945f;
                 }
-            }
-            __syncthreads();
-            for (int e = tid; e < 16 * D; e += kSplitThreads) {
-                const int c = e / D, d = e - c * D, r = 16 * x + c;
-                if (r >= rows) break;
-                float top = -INFINITY;
+            } else {
+                __syncthreads();
+                if (grp == 0) {
+                    sh.out.ref[wave][col] = ref;
+                    sh.out.sum[wave][col] = sum;
+                }
 #pragma unroll
-                for (int y = 0; y < kSplitWaves; ++y)
-                    if (sh.sum[y][c] != 0) top = fmaxf(top, sh.ref[y][c]);
-                float lt = 0, ot = 0;
+                for (int d = 0; d < ND; ++d)
 #pragma unroll
-                for (int y = 0; y < kSplitWaves; ++y)
-                    if (sh.sum[y][c] != 0) {
-                        const float f = __builtin_amdgcn_exp2f(sh.ref[y][c] - top);
-                        lt = fmaf(f, sh.sum[y][c], lt);
-                        ot = fmaf(f, sh.o[y][c][d], ot);
+                    for (int y = 0; y < 4; ++y) {
+                        float4_t v;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) v[e] = fmaf(o[x][d][y][e], 0x1p20f, -z[d]);
+                        *reinterpret_cast<float4_t *>(&sh.out.o[wave][col][64 * d + 16 * y + 4 * grp]) = v;
                     }
-                if (whole) {
-                    const int64_t t = s.first + r / g.G, hq = (int64_t)h * g.G + r % g.G;
-                    const float out = lt == 0 ? 0.0f : ot / lt;
-                    const int64_t at_out = (t * a.q_heads + hq) * D + d;
-                    if (a.bf16) static_cast<__bf16 *>(a.out)[at_out] = (__bf16)out;
-                    else static_cast<float *>(a.out)[at_out] = out;
-                    if (a.lse && d == 0)
-                        a.lse[t * a.q_heads + hq] = lt == 0 ? -INFINITY : (top + __builtin_amdgcn_logf(lt)) * 0.693147180559945f;
-                } else {
-                    g.part[(slot * g.max_rows + r) * D + d] = ot;
-                    if (d == 0) {
-                        g.part_sums[(slot * g.max_rows + r) * 2] = top;
-                        g.part_sums[(slot * g.max_rows + r) * 2 + 1] = lt;
+                __syncthreads();
+                for (int e = tid; e < 16 * D / 4; e += kSplitThreads) {
+                    const int c = e / (D / 4), d = e % (D / 4) * 4, rr = 16 * x + c;
+                    if (rr >= rows) break;
+                    float top = -INFINITY;
+#pragma unroll
+                    for (int y = 0; y < kSplitWaves; ++y)
+                        if (sh.out.sum[y][c] != 0) top = fmaxf(top, sh.out.ref[y][c]);
+                    float lt = 0;
+                    float4_t ot = {0, 0, 0, 0};
+#pragma unroll
+                    for (int y = 0; y < kSplitWaves; ++y) {
+                        const float part = sh.out.sum[y][c];
+                        const float4_t v = *reinterpret_cast<const float4_t *>(&sh.out.o[y][c][d]);
+                        if (part != 0) {
+                            const float f = __builtin_amdgcn_exp2f(sh.out.ref[y][c] - top);
+                            lt = fmaf(f, part, lt);
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) ot[q] = fmaf(f, v[q], ot[q]);
+                        }
                     }
+                    const int jj = (int)(rr * g.inv_G >> 16);
+                    const int64_t to = (int64_t)(s.first + jj) * a.q_heads + (h * g.G + rr - jj * g.G);
+                    const float f = lt == 0 ? 0.0f : 1.0f / lt;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) ot[q] = lt == 0 ? 0.0f : ot[q] * f;
+                    store4(a, to * D + d, ot);
+                    if (a.lse && d == 0) a.lse[to] = lt == 0 ? -INFINITY : (top + __builtin_amdgcn_logf(lt)) * 0.693147180559945f;
                 }
             }
         }
-        __syncthreads();
+        if (DIRECT) return;
         i = row_start + t1;
     }
 }
 
-// Joins the pieces of the rows that end with workgroup blockIdx.x, a workgroup
-// per row: 16 ND lanes a piece, the pieces dealt to groups of lanes.
+// Joins the pieces of a (sequence, key head), a workgroup per row: 16 ND lanes
+// a piece, the pieces dealt to groups of lanes.
 template <int ND>
 __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs g) {
     constexpr int D = ND * 64, kLanes = 16 * ND, kGroups = 256 / kLanes;
     __shared__ float4_t so[kGroups][kLanes];
     __shared__ float ss[kGroups];
     const CacheAttend &a = g.a;
-    const int w1 = (int)blockIdx.x, r = (int)blockIdx.y, tid = (int)threadIdx.x;
-    const End e = g.ends[w1];
-    if (e.first < 0 || r >= e.rows) return;
-    const int pieces = w1 - e.first + 1;
+    const int r = (int)blockIdx.y, tid = (int)threadIdx.x, heads = (int)a.cache.heads;
+    const int64_t b = blockIdx.x / heads;
+    const int h = (int)(blockIdx.x - b * heads);
+    const Sequence s = sequence_uniform(a, b);
+    int lo_key;
+    const int n = s.n < a.max_q ? s.n : (int)a.max_q;
+    if (tiles_of(g, s, &lo_key) == 0 || r >= n * g.G) return;
+    const Pieces e = g.pieces[blockIdx.x];
+    if (e.first == e.last) return;
+    const int pieces = e.last - e.first + 1;
     const float *sums = g.part_sums + 2 * r;
     auto slot = [&](int p) { return (int64_t)(2 * (e.first + p) + (p == 0 ? e.second : 0)) * g.max_rows; };
     float top = -INFINITY;
@@ -764,7 +813,7 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs g) {
         const float4_t v = so[p][c];
         ot += v;
     }
-    const int64_t t = e.token + r / g.G, hq = (int64_t)e.h * g.G + r % g.G;
+    const int64_t t = s.first + r / g.G, hq = (int64_t)h * g.G + r % g.G;
     float4_t v;
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = lt == 0 ? 0.0f : ot[i] / lt;
@@ -1277,11 +1326,17 @@ static int split_limit(int64_t D) { return D <= 128 ? 64 : 32; }
 
 struct AttendPlan {
     int64_t split_rows;  // the most rows of a sequence in the split kernel
+    int waves;           // its waves
     bool tiles;          // whether the tile kernel runs
     int64_t row_tiles;   // its tiles of rows at most
     int parts;           // workgroups the keys of one are dealt to
     size_t floats;         // workspace
 };
+
+// Tiles of 16 rows that the split kernel's accumulators are made for, and its
+// waves: those that 256 compute units hold at once.
+static int split_tiles(int nd, int64_t rows) { return rows <= 16 ? 1 : nd <= 2 && rows > 32 ? 4 : 2; }
+static int split_waves(int nd, int64_t rows) { return 256 * kSplitWaves * split_occupancy(nd, split_tiles(nd, rows)); }
 
 static AttendPlan attend_plan(int64_t T, int64_t q_heads, int64_t heads, int64_t D, int64_t B, int64_t max_q) {
     AttendPlan p = {};
@@ -1289,7 +1344,8 @@ static AttendPlan attend_plan(int64_t T, int64_t q_heads, int64_t heads, int64_t
     const int64_t q = max_q < T ? max_q : T;
     p.tiles = q * G > limit;
     p.split_rows = p.tiles ? limit : q * G;
-    p.floats = (size_t)(2 * kSplitGroups) * p.split_rows * (D + 2) + kSplitGroups * sizeof(End) / sizeof(float);
+    p.waves = split_waves((int)(D / 64), p.split_rows);
+    p.floats = (size_t)(2 * p.waves) * p.split_rows * (D + 2) + (size_t)(B * heads) * (sizeof(Pieces) / sizeof(float));
     if (p.tiles) {
         // Sequences that have more rows than the limit, and their tiles.
         const int64_t most = T * G / (limit + 1);
@@ -1317,9 +1373,10 @@ size_t attend_ws_bytes(int64_t T, int64_t q_heads, int64_t heads, int64_t D, int
 
 template <int ND, bool DIRECT>
 static const void *split_kernel(int64_t rows) {
-    if (rows <= 16) return reinterpret_cast<const void *>(&attend_split_kernel<ND, 1, DIRECT>);
+    const int nt = split_tiles(ND, rows);
+    if (nt == 1) return reinterpret_cast<const void *>(&attend_split_kernel<ND, 1, DIRECT>);
     if constexpr (ND <= 2) {
-        if (rows > 32) return reinterpret_cast<const void *>(&attend_split_kernel<ND, 4, DIRECT>);
+        if (nt == 4) return reinterpret_cast<const void *>(&attend_split_kernel<ND, 4, DIRECT>);
     }
     return reinterpret_cast<const void *>(&attend_split_kernel<ND, 2, DIRECT>);
 }
@@ -1334,17 +1391,19 @@ static hipError_t launch_attend(AttendArgs &g, const AttendPlan &p, float *works
     void *args[] = {&g};
     g.max_rows = (int)p.split_rows;
     g.part = workspace;
-    g.part_sums = g.part + (size_t)(2 * kSplitGroups) * p.split_rows * a.cache.D;
-    g.ends = reinterpret_cast<End *>(g.part_sums + (size_t)(2 * kSplitGroups) * p.split_rows * 2);
+    g.part_sums = g.part + (size_t)(2 * p.waves) * p.split_rows * a.cache.D;
+    g.pieces = reinterpret_cast<Pieces *>(g.part_sums + (size_t)(2 * p.waves) * p.split_rows * 2);
+    g.waves = p.waves;
     hipError_t e;
     if (a.table_pages * a.cache.page <= kDirectKeys) {
         e = hipLaunchKernel(split_kernel<ND, true>(p.split_rows), dim3((unsigned)(a.B * a.cache.heads)), dim3(kSplitThreads), args, 0,
                             stream);
     } else {
-        e = hipLaunchKernel(split_kernel<ND, false>(p.split_rows), dim3(kSplitGroups), dim3(kSplitThreads), args, 0, stream);
+        e = hipLaunchKernel(split_kernel<ND, false>(p.split_rows), dim3((unsigned)(p.waves / kSplitWaves)), dim3(kSplitThreads), args,
+                            0, stream);
         if (e != hipSuccess) return e;
-        e = hipLaunchKernel(reinterpret_cast<const void *>(&attend_join_kernel<ND>), dim3(kSplitGroups, (unsigned)p.split_rows),
-                            dim3(256), args, 0, stream);
+        e = hipLaunchKernel(reinterpret_cast<const void *>(&attend_join_kernel<ND>),
+                            dim3((unsigned)(a.B * a.cache.heads), (unsigned)p.split_rows), dim3(256), args, 0, stream);
     }
     if (e != hipSuccess || !p.tiles) return e;
     g.row_tiles = p.row_tiles;
@@ -1364,6 +1423,7 @@ hipError_t launch_cache_attend(const CacheAttend &a, void *workspace, hipStream_
     if (a.cache.pages == 0) g.a.table_pages = 0;  // no key can be seen
     g.page_shift = __builtin_ctzll((unsigned long long)a.cache.page);
     g.G = (int)(a.q_heads / a.cache.heads);
+    g.inv_G = (65536 + g.G - 1) / g.G;
     g.limit = split_limit(a.cache.D);
     const AttendPlan p = attend_plan(a.T, a.q_heads, a.cache.heads, a.cache.D, a.B, a.max_q);
     float *ws = static_cast<float *>(workspace);
