@@ -23,8 +23,7 @@ typedef __attribute__((address_space(4))) int32_t scalar_int;  // read-only: uni
 // several waves; first == last: it was not.
 struct Pieces {
     int first, last;  // the waves of the first and the last piece
-    int second;       // whether the first is its wave's second slot
-};
+};  // A wave's slots: 2 w for a piece that goes on, 2 w + 1 for one that begins.
 
 typedef __attribute__((address_space(4))) int32_t scalar_int;  // read-only: uniform loads are scalar
 
@@ -128,11 +127,16 @@ __device__ __forceinline__ Sequence sequence_uniform(const CacheAttend &a, int64
 constexpr int kTile = 32;        // keys a wave takes at a time
 constexpr int kSplitWaves = 4;
 constexpr int kSplitThreads = 64 * kSplitWaves;
-constexpr int kMinTiles = 3;       // tiles a wave should have at least
+constexpr int kMinTiles = 2;       // tiles a wave should have at least, beside kBegin
+// What beginning a piece costs a wave, in tiles: its tables, queries and first
+// codes arrive one after the other (5 us where a further tile takes 0.85; 6 units instead of 3 took 3 us more where waves have
+// few tiles, and nothing less elsewhere).
+constexpr int kBegin = 3;
 constexpr int kHeadroom = 6;       // powers of two that weights may pass 1 by
 
 // Tiles of one key head of a sequence (one at least where it has rows, so
-// that rows without keys are written).
+// that rows without keys are written).  In the list that is dealt to the waves
+// it has kBegin units and one for each tile.
 __device__ __forceinline__ int tiles_of(const AttendArgs &g, const Sequence &s, int *lo_key) {
     const CacheAttend &a = g.a;
     int lo = 0;
@@ -154,7 +158,7 @@ struct Shares {
     int64_t each, more, workers;
     __device__ __forceinline__ Shares(int64_t total, int waves) {
         workers = waves;
-        if (total <= (int64_t)waves * kMinTiles) workers = ((uint32_t)total + kMinTiles - 1) / kMinTiles;
+        if (total <= (int64_t)waves * (kBegin + kMinTiles)) workers = ((uint32_t)total + kBegin + kMinTiles - 1) / (kBegin + kMinTiles);
         each = (uint64_t)total >> 32 ? total / workers : (int64_t)((uint32_t)total / (uint32_t)workers);
         more = total - each * workers;
     }
@@ -176,11 +180,11 @@ __device__ __forceinline__ int64_t scan_sequences(int64_t B, int64_t *sums, Coun
     int64_t before = 0;
     for (int64_t b0 = 0; b0 < B; b0 += THREADS) {
         const int64_t b = b0 + tid;
-        const int64_t t = b < B ? count(b) : 0;
-        int64_t x = t;
+        const uint32_t t = b < B ? count(b) : 0;  // below 2^26
+        uint32_t x = t;
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) {
-            const int64_t y = __shfl_up(x, d);
+            const uint32_t y = __shfl_up(x, d);
             if ((tid & 63) >= d) x += y;
         }
         if ((tid & 63) == 63) sums[wave] = x;
@@ -191,7 +195,7 @@ __device__ __forceinline__ int64_t scan_sequences(int64_t B, int64_t *sums, Coun
             if (w < wave) off += sums[w];
             all += sums[w];
         }
-        if (b < B) found(b, off + x - t, t);
+        if (b < B) found(b, off + x - t, (int64_t)t);
         before += all;
         __syncthreads();
     }
@@ -317,7 +321,8 @@ __global__ __launch_bounds__(kSplitThreads, split_occupancy(ND, NT)) void attend
     } else {
         auto count = [&](int64_t x) {
             int lo;
-            return (int64_t)tiles_of(g, sequence_at(a, x), &lo);
+            const int t = tiles_of(g, sequence_at(a, x), &lo);
+            return t > 0 ? (uint32_t)t + kBegin : 0u;
         };
         total = heads * scan_sequences<kSplitThreads>(
                             a.B, sh.sums, count, [&](int64_t x, int64_t before, int64_t t) { one_b = x; one_at = before; one_t = t; });
@@ -354,18 +359,26 @@ __global__ __launch_bounds__(kSplitThreads, split_occupancy(ND, NT)) void attend
         const int nt = tiles_of(g, s, &lo_key);
         if (DIRECT) {
             if (nt == 0) return;
-        } else if (i >= at + (int64_t)nt * heads) {
-            at += (int64_t)nt * heads;
+        } else if (nt == 0 || i >= at + (int64_t)(nt + kBegin) * heads) {
+            if (nt > 0) at += (int64_t)(nt + kBegin) * heads;
             ++b;
             continue;
         }
-        // (i - at < nt heads, at most 2^25 2^10.)
-        const int64_t ahead = i - at;
-        const int h = DIRECT ? (int)(w % heads)
-                             : (int)((uint64_t)ahead >> 32 ? ahead / nt : (int64_t)((uint32_t)ahead / (uint32_t)nt));
-        const int64_t row_start = DIRECT ? 0 : at + (int64_t)h * nt;
-        const int t0 = DIRECT ? 0 : (int)(i - row_start);
-        const int t1 = DIRECT ? nt : (int)(end - row_start < nt ? end - row_start : nt);
+        int h, t0 = 0, t1 = nt;
+        int64_t row_start = 0;
+        if (DIRECT) {
+            h = (int)(w % heads);
+        } else {
+            const int64_t ahead = i - at;
+            const int units = nt + kBegin;
+            h = (int)((uint64_t)ahead >> 32 ? ahead / units : (int64_t)((uint32_t)ahead / (uint32_t)units));
+            row_start = at + (int64_t)h * units;
+            t0 = (int)(i - row_start) - kBegin;
+            t1 = (int)(end - row_start < units ? end - row_start : units) - kBegin;
+            i = row_start + t1 + kBegin;
+            if (t1 <= 0) continue;
+            if (t0 < 0) t0 = 0;
+        }
         const int n = s.n < a.max_q ? s.n : (int)a.max_q;
         const int rows = n * g.G;
 
@@ -509,6 +522,18 @@ __global__ __launch_bounds__(kSplitThreads, split_occupancy(ND, NT)) void attend
             const bool ok[2] = {(uint32_t)id0 < (uint32_t)pages && lo_key + tile * kTile < s.len,
                                 (uint32_t)id1 < (uint32_t)pages && lo_key + tile * kTile + 16 < s.len};
             const int key = lo_key + tile * kTile;
+            const bool edge = !ok[0] || !ok[1] || key + kTile > s.len;
+            if (__builtin_expect(edge, 0)) {
+                // Keys that no row sees may hold anything: scales and zeros of 0.
+                asm volatile("");  // (a branch, not selects)
+#pragma unroll
+                for (int d = 0; d < ND; ++d) {
+                    const int c = lane + 64 * d, in = c % (16 * ND), t = in >= 8 * ND, y = 2 * (in - t * 8 * ND);
+                    const bool page_ok = t ? ok[1] : ok[0];
+                    if (!page_ok || key + 16 * t + y / ND >= s.len) T.par[d] &= 0xFFFF0000u;
+                    if (!page_ok || key + 16 * t + (y + 1) / ND >= s.len) T.par[d] &= 0x0000FFFFu;
+                }
+            }
             uint8_t *vl = sh.in.v[wave];
 #pragma unroll
             for (int d = 0; d < ND; ++d) {
@@ -548,12 +573,6 @@ __global__ __launch_bounds__(kSplitThreads, split_occupancy(ND, NT)) void attend
                 }
             }
             load_keys(row, T);
-            uint32_t vs[2][2 * ND], vz[2][2 * ND];
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                read_par<ND>(par, kValueScales, t, grp, vs[t]);
-                read_par<ND>(par, kValueZeros, t, grp, vz[t]);
-            }
             const bool masked = key + kTile - 1 > all_to || key < all_from || !ok[0] || !ok[1];
             if (__builtin_expect(masked, 0)) {
                 asm volatile("");  // (a branch, not selects)
@@ -565,24 +584,17 @@ __global__ __launch_bounds__(kSplitThreads, split_occupancy(ND, NT)) void attend
 #pragma unroll
                         for (int x = 0; x < NT; ++x)
                             if (!ok[t] || k > seen_to[x] || k < seen_from[x]) S[x][t][r] = -INFINITY;
-                        // A key that no row sees may hold anything.
-                        if (!ok[t] || k >= s.len) {
-#pragma unroll
-                            for (int d = 0; d < ND; ++d) {
-                                const int y = r * ND + d;
-                                const uint32_t keep = y & 1 ? 0x0000FFFFu : 0xFFFF0000u;
-                                vs[t][y >> 1] &= keep;
-                                vz[t][y >> 1] &= keep;
-                            }
-                        }
                     }
             }
             // Whether a maximum has grown too far, or a value scale.
             uint32_t top_bits = 0;
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
+            for (int t = 0; t < 2; ++t) {
+                uint32_t vs[2 * ND];
+                read_par<ND>(par, kValueScales, t, grp, vs);
 #pragma unroll
-                for (int y = 0; y < 2 * ND; ++y) top_bits = pk_max(top_bits, vs[t][y]);
+                for (int y = 0; y < 2 * ND; ++y) top_bits = pk_max(top_bits, vs[y]);
+            }
             bool grown = half_max(top_bits) > limit_bits;
             float tmax[NT];
 #pragma unroll
@@ -594,21 +606,26 @@ __global__ __launch_bounds__(kSplitThreads, split_occupancy(ND, NT)) void attend
             if (__any(grown)) {
                 uint32_t fin = 0;
 #pragma unroll
-                for (int t = 0; t < 2; ++t)
+                for (int t = 0; t < 2; ++t) {
+                    uint32_t vs[2 * ND];
+                    read_par<ND>(par, kValueScales, t, grp, vs);
 #pragma unroll
                     for (int y = 0; y < 4 * ND; ++y) {
-                        const uint32_t v = (vs[t][y >> 1] >> (16 * (y & 1))) & 0xFFFF;
+                        const uint32_t v = (vs[y >> 1] >> (16 * (y & 1))) & 0xFFFF;
                         fin = v < 0x7C00u && v > fin ? v : fin;
                         // A scale that is not finite makes the block NaN in the
                         // rows that see the key, and does not reach the others.
                         if (v >= 0x7C00u) {
-                            vs[t][y >> 1] &= y & 1 ? 0x0000FFFFu : 0xFFFF0000u;
-                            vz[t][y >> 1] &= y & 1 ? 0x0000FFFFu : 0xFFFF0000u;
+                            uint16_t *at = reinterpret_cast<uint16_t *>(par + (kValueScales * 2 + t) * 8 * ND + grp * 2 * ND) + y;
+                            at[0] = 0;
+                            at[2 * 16 * ND] = 0;  // its zero, a plane further
 #pragma unroll
                             for (int x = 0; x < NT; ++x)
                                 if (S[x][t][y / ND] != -INFINITY) zs[x][y % ND] = NAN;
                         }
                     }
+                }
+                wave_fence();
                 fin = wave_max_u32(fin);
                 // Below 2^e: the exponent of the next power of two.
                 const int e = (int)(fin >> 10) == 0 ? -14 : (int)(fin >> 10) - 14;
@@ -638,25 +655,23 @@ __global__ __launch_bounds__(kSplitThreads, split_occupancy(ND, NT)) void attend
             // Weights, and the operands of the second product.
             half8_t pf[NT][ND];
 #pragma unroll
-            for (int x = 0; x < NT; ++x) {
-                float p[2][4];
+            for (int t = 0; t < 2; ++t) {
+                uint32_t vs[2 * ND], vz[2 * ND];
+                read_par<ND>(par, kValueScales, t, grp, vs);
+                read_par<ND>(par, kValueZeros, t, grp, vz);
 #pragma unroll
-                for (int t = 0; t < 2; ++t)
+                for (int x = 0; x < NT; ++x)
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
-                        p[t][r] = __builtin_amdgcn_exp2f(fmaf(S[x][t][r], kappa[x], nk[x]));
-                        l[x] += p[t][r];
-                    }
+                        const float p = __builtin_amdgcn_exp2f(fmaf(S[x][t][r], kappa[x], nk[x]));
+                        l[x] += p;
 #pragma unroll
-                for (int d = 0; d < ND; ++d)
-#pragma unroll
-                    for (int t = 0; t < 2; ++t)
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) {
-                            const _Float16 w16 = (_Float16)(p[t][r] * half_at(vs[t], r * ND + d));
+                        for (int d = 0; d < ND; ++d) {
+                            const _Float16 w16 = (_Float16)(p * half_at(vs, r * ND + d));
                             pf[x][d][2 * r + t] = w16;
-                            zs[x][d] = fmaf((float)w16, half_at(vz[t], r * ND + d), zs[x][d]);
+                            zs[x][d] = fmaf((float)w16, half_at(vz, r * ND + d), zs[x][d]);
                         }
+                    }
             }
             // Values: each group of 16 lanes turns its 8 keys (4 of each 16) by 32 dimensions.
             const int vkey = ((lane & 7) < 4 ? 0 : 16) + 4 * grp + (lane & 3);
@@ -679,8 +694,7 @@ __global__ __launch_bounds__(kSplitThreads, split_occupancy(ND, NT)) void attend
         // Results, 16 rows at a time.  A row's weights stand relative to 2^ref.
         const bool whole = t0 == 0 && t1 == nt;
         if (!DIRECT && t1 == nt && lane == 0) {
-            const int64_t first = whole ? w : shares.at(row_start);
-            g.pieces[b * heads + h] = Pieces{(int)first, (int)w, shares.start(first) == row_start ? 0 : 1};
+            g.pieces[b * heads + h] = Pieces{(int)(whole ? w : shares.at(row_start + kBegin)), (int)w};
         }
 #pragma unroll
         for (int x = 0; x < NT; ++x) {
@@ -692,7 +706,7 @@ __global__ __launch_bounds__(kSplitThreads, split_occupancy(ND, NT)) void attend
             const int64_t at_row = (int64_t)(s.first + j) * a.q_heads + (h * g.G + r - j * g.G);
             if constexpr (!DIRECT) {
                 if (r >= rows) continue;
-                const int64_t at_part = (2 * w + (i == begin ? 0 : 1)) * g.max_rows + r;
+                const int64_t at_part = (2 * w + (t0 == 0 ? 1 : 0)) * g.max_rows + r;
                 const float f = !whole ? 1.0f : sum == 0 ? 0.0f : 1.0f / sum;
 #pragma unroll
                 for (int d = 0; d < ND; ++d)
@@ -757,19 +771,17 @@ __global__ __launch_bounds__(kSplitThreads, split_occupancy(ND, NT)) void attend
             }
         }
         if (DIRECT) return;
-        i = row_start + t1;
     }
 }
 
-// Joins the pieces of a (sequence, key head), a workgroup per row: 16 ND lanes
-// a piece, the pieces dealt to groups of lanes.
-template <int ND>
+// Joins the pieces of a (sequence, key head): a workgroup per row and block of
+// 64 dimensions, 16 lanes a piece, the pieces dealt to 16 groups of lanes.
 __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs g) {
-    constexpr int D = ND * 64, kLanes = 16 * ND, kGroups = 256 / kLanes;
+    constexpr int kLanes = 16, kGroups = 16;
     __shared__ float4_t so[kGroups][kLanes];
     __shared__ float ss[kGroups];
     const CacheAttend &a = g.a;
-    const int r = (int)blockIdx.y, tid = (int)threadIdx.x, heads = (int)a.cache.heads;
+    const int r = (int)blockIdx.y, tid = (int)threadIdx.x, heads = (int)a.cache.heads, D = (int)a.cache.D;
     const int64_t b = blockIdx.x / heads;
     const int h = (int)(blockIdx.x - b * heads);
     const Sequence s = sequence_uniform(a, b);
@@ -779,46 +791,47 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs g) {
     const Pieces e = g.pieces[blockIdx.x];
     if (e.first == e.last) return;
     const int pieces = e.last - e.first + 1;
-    const float *sums = g.part_sums + 2 * r;
-    auto slot = [&](int p) { return (int64_t)(2 * (e.first + p) + (p == 0 ? e.second : 0)) * g.max_rows; };
+    const float2 *sums = reinterpret_cast<const float2 *>(g.part_sums) + r;
+    auto slot = [&](int p) { return (int64_t)(2 * (e.first + p) + (p == 0 ? 1 : 0)) * g.max_rows; };
     float top = -INFINITY;
     for (int p = tid & 63; p < pieces; p += 64) {
-        const float *q = sums + 2 * slot(p);
-        if (q[1] != 0) top = fmaxf(top, q[0]);
+        const float2 q = sums[slot(p)];
+        if (q.y != 0) top = fmaxf(top, q.x);
     }
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
-    const int c = tid % kLanes, gr = tid / kLanes;
+    const int c = tid % kLanes, gr = tid / kLanes, d = (int)blockIdx.z * 64 + 4 * c;
     float4_t ot = {0, 0, 0, 0};
     float lt = 0;
-    if (gr < kGroups)
-        for (int p = gr; p < pieces; p += kGroups) {
-            const int64_t x = slot(p) + r;
-            const float2 q = *reinterpret_cast<const float2 *>(g.part_sums + 2 * x);
-            const float4_t v = *reinterpret_cast<const float4_t *>(g.part + x * D + 4 * c);
-            const float f = q.y != 0 ? __builtin_amdgcn_exp2f(q.x - top) : 0.0f;
-            if (q.y != 0) lt = fmaf(f, q.y, lt);
+    const float *part = g.part + (int64_t)r * D + d;
+#pragma unroll 4
+    for (int p = gr; p < pieces; p += kGroups) {
+        const int64_t x = slot(p);
+        const float2 q = sums[x];
+        const float4_t v = *reinterpret_cast<const float4_t *>(part + x * D);
+        const bool any = q.y != 0;
+        const float f = any ? __builtin_amdgcn_exp2f(q.x - top) : 0.0f;
+        lt = any ? fmaf(f, q.y, lt) : lt;
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (q.y != 0) ot[i] = fmaf(f, v[i], ot[i]);
-        }
-    if (gr < kGroups) {
-        so[gr][c] = ot;
-        if (c == 0) ss[gr] = lt;
+        for (int i = 0; i < 4; ++i) ot[i] = any ? fmaf(f, v[i], ot[i]) : ot[i];
     }
+    so[gr][c] = ot;
+    if (c == 0) ss[gr] = lt;
     __syncthreads();
     if (tid >= kLanes) return;
+#pragma unroll
     for (int p = 1; p < kGroups; ++p) {
         lt += ss[p];
         const float4_t v = so[p][c];
         ot += v;
     }
-    const int64_t t = s.first + r / g.G, hq = (int64_t)h * g.G + r % g.G;
+    const int j = (int)(r * g.inv_G >> 16);
+    const int64_t at = (int64_t)(s.first + j) * a.q_heads + (h * g.G + r - j * g.G);
     float4_t v;
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = lt == 0 ? 0.0f : ot[i] / lt;
-    store4(a, (t * a.q_heads + hq) * D + 4 * c, v);
-    if (a.lse && c == 0) a.lse[t * a.q_heads + hq] = lt == 0 ? -INFINITY : (top + __builtin_amdgcn_logf(lt)) * 0.693147180559945f;
+    store4(a, at * D + d, v);
+    if (a.lse && d == 0) a.lse[at] = lt == 0 ? -INFINITY : (top + __builtin_amdgcn_logf(lt)) * 0.693147180559945f;
 }
 
 // ---------------------------------------------------------------------------
@@ -870,7 +883,7 @@ __device__ __forceinline__ bool find_row_tile(const AttendArgs &g, int64_t index
         a.B, sums,
         [&](int64_t b) {
             int64_t rows;
-            return (int64_t)row_tiles_of(g, sequence_at(a, b), &rows);
+            return (uint32_t)row_tiles_of(g, sequence_at(a, b), &rows);
         },
         [&](int64_t b, int64_t before, int64_t t) {
             if (index >= before && index < before + t) {
@@ -1381,9 +1394,12 @@ static const void *split_kernel(int64_t rows) {
     return reinterpret_cast<const void *>(&attend_split_kernel<ND, 2, DIRECT>);
 }
 
-// Tables that hold at most this many keys a sequence: a workgroup for each
-// (sequence, key head), which needs no plan and no joining.
-constexpr int64_t kDirectKeys = 512;
+// Where no token can see more keys than this (by the table, or the window): a
+// workgroup for each (sequence, key head), which needs no plan and no joining.
+// 64 sequences of up to 1000 keys and 8 heads 20 us instead of 31, of up to
+// 2000 keys 30 instead of 36; 2 heads of one sequence on 1000 keys 13 instead
+// of 18, but on 2000 21 instead of 16: there the keys need more waves.
+static bool direct(int64_t keys, int64_t items) { return keys <= 1024 || (keys <= 2048 && items >= 512); }
 
 template <int ND>
 static hipError_t launch_attend(AttendArgs &g, const AttendPlan &p, float *workspace, hipStream_t stream) {
@@ -1395,15 +1411,17 @@ static hipError_t launch_attend(AttendArgs &g, const AttendPlan &p, float *works
     g.pieces = reinterpret_cast<Pieces *>(g.part_sums + (size_t)(2 * p.waves) * p.split_rows * 2);
     g.waves = p.waves;
     hipError_t e;
-    if (a.table_pages * a.cache.page <= kDirectKeys) {
+    int64_t most = a.table_pages * a.cache.page;
+    if (a.window > 0 && a.window + a.max_q < most) most = a.window + a.max_q;
+    if (direct(most, a.B * a.cache.heads)) {
         e = hipLaunchKernel(split_kernel<ND, true>(p.split_rows), dim3((unsigned)(a.B * a.cache.heads)), dim3(kSplitThreads), args, 0,
                             stream);
     } else {
         e = hipLaunchKernel(split_kernel<ND, false>(p.split_rows), dim3((unsigned)(p.waves / kSplitWaves)), dim3(kSplitThreads), args,
                             0, stream);
         if (e != hipSuccess) return e;
-        e = hipLaunchKernel(reinterpret_cast<const void *>(&attend_join_kernel<ND>),
-                            dim3((unsigned)(a.B * a.cache.heads), (unsigned)p.split_rows), dim3(256), args, 0, stream);
+        e = hipLaunchKernel(reinterpret_cast<const void *>(&attend_join_kernel),
+                            dim3((unsigned)(a.B * a.cache.heads), (unsigned)p.split_rows, ND), dim3(256), args, 0, stream);
     }
     if (e != hipSuccess || !p.tiles) return e;
     g.row_tiles = p.row_tiles;
