@@ -1029,77 +1029,88 @@ __global__ __launch_bounds__(kTileThreads, 1) void attend_tile_kernel(AttendArgs
         return id >= 0 && id < pages ? id : -1;
     };
 
-    // What the thread decodes: pieces of 32 codes, keys' before values'.
+    // What the thread decodes: pieces of 32 codes, keys' before values'.  Loads
+    // are made without conditions, their values looked at where they are used:
+    // a wait then never holds for loads that came after.
     u32x4_t raw[kLoads];
     uint32_t raw_s[kLoads], raw_z[kLoads];
-    int raw_id[kLoads];
-    bool hidden = false;
+    int next_id[kLoads];     // the table's entries for the next load
+    bool raw_ok[kLoads], raw_hidden[kLoads];
+    const int last_page = (s.len - 1) >> g.page_shift;
+    auto is_value = [&](int i) { return wave * 64 + kTileThreads * i >= kUnits; };
+    auto is_piece = [&](int i) { return wave * 64 + kTileThreads * i < 2 * kUnits; };
+    auto key_of = [&](int i, int tile) {
+        const int in = (tid + kTileThreads * i) % kUnits;
+        return rt.lo + (tile < t1 ? tile : t1 - 1) * kKeys + in / (2 * ND);
+    };
     auto ids = [&](int tile) {
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
-            const int u = tid + kTileThreads * i, in = u % kUnits;
-            raw_id[i] = u < 2 * kUnits ? page_at(rt.lo + tile * kKeys + in / (2 * ND)) : -1;
+            const int p = key_of(i, tile) >> g.page_shift;
+            next_id[i] = table[p < last_page ? p : last_page];
         }
     };
     auto load = [&](int tile) {
-        hidden = false;
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
-            const int u = tid + kTileThreads * i, in = u % kUnits, piece = in % (2 * ND);
-            const bool value = u >= kUnits;  // the same for a wave
-            const int key = rt.lo + tile * kKeys + in / (2 * ND);
-            raw_s[i] = raw_z[i] = 0;
-            raw[i] = u32x4_t{0, 0, 0, 0};
-            hidden = hidden || (raw_id[i] < 0 && u < 2 * kUnits && key < s.len);
-            if (raw_id[i] >= 0) {
-                const int64_t row = ((int64_t)raw_id[i] * heads + h) * page + (key & (page - 1));
-                raw[i] = *reinterpret_cast<const u32x4_t *>((value ? a.cache.v_codes : a.cache.k_codes) + row * (D / 2) + piece * 16);
-                raw_s[i] = (value ? a.cache.v_scales : a.cache.k_scales)[row * ND + piece / 2];
-                raw_z[i] = (value ? a.cache.v_zeros : a.cache.k_zeros)[row * ND + piece / 2];
-            }
+            const int piece = (tid + kTileThreads * i) % (2 * ND), key = key_of(i, tile);
+            const bool value = is_value(i), page_ok = (uint32_t)next_id[i] < (uint32_t)pages;
+            raw_ok[i] = page_ok && key < s.len;
+            raw_hidden[i] = !page_ok && key < s.len;
+            const int64_t row = ((int64_t)(page_ok ? next_id[i] : 0) * heads + h) * page + (key & (page - 1));
+            raw[i] = *reinterpret_cast<const u32x4_t *>((value ? a.cache.v_codes : a.cache.k_codes) + row * (D / 2) + piece * 16);
+            raw_s[i] = (value ? a.cache.v_scales : a.cache.k_scales)[row * ND + piece / 2];
+            raw_z[i] = (value ? a.cache.v_zeros : a.cache.k_zeros)[row * ND + piece / 2];
         }
     };
     auto publish = [&](int tile) {
         TileNews &n = news[tile % 3];
-        if (__any(hidden) && lane == 0) atomicOr(&n.wild, (uint32_t)kHidden);
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
-            const int u = tid + kTileThreads * i;
-            const bool value = u >= kUnits;
-            const bool fin = raw_s[i] < 0x7C00u;
-            const uint32_t top = wave_max_u32(fin ? raw_s[i] : 0);
-            const bool wild = value && __any(!fin);
-            if (lane == 0 && u < 2 * kUnits) {
+            if (!is_piece(i)) break;
+            const bool value = is_value(i), fin = !raw_ok[i] || raw_s[i] < 0x7C00u;
+            const uint32_t top = wave_max_u32(raw_ok[i] && fin ? raw_s[i] : 0);
+            const uint32_t wild = (value && __any(!fin) ? (uint32_t)kWild : 0u) | (__any(raw_hidden[i]) ? (uint32_t)kHidden : 0u);
+            if (lane == 0) {
                 atomicMax(value ? &n.value_scale : &n.key_scale, top);
-                if (wild) atomicOr(&n.wild, (uint32_t)kWild);
+                if (wild) atomicOr(&n.wild, wild);
             }
         }
     };
     auto decode = [&](int buf, int ek, int ev) {
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
-            const int u = tid + kTileThreads * i, in = u % kUnits, piece = in % (2 * ND), key = in / (2 * ND);
-            const bool value = u >= kUnits;
-            if (u >= 2 * kUnits) break;
-            uint32_t sb = raw_s[i];
+            if (!is_piece(i)) break;
+            const int in = (tid + kTileThreads * i) % kUnits, piece = in % (2 * ND), key = in / (2 * ND);
+            const bool value = is_value(i);
+            uint32_t sb = raw_ok[i] ? raw_s[i] : 0;
             if (value && sb >= 0x7C00u) sb = 0;  // (rows that see it are made NaN below)
             const _Float16 sc = (_Float16)ldexpf(f16_bits_to_f32(sb), -(value ? ev : ek));
-            const _Float16 of = (_Float16)(-1024.0f - f16_bits_to_f32(raw_z[i]));
+            const _Float16 of = (_Float16)(-1024.0f - (raw_ok[i] ? f16_bits_to_f32(raw_z[i]) : 0.0f));
             const half2_t s2 = {sc, sc}, o2 = {of, of};
             // The 4 pieces of 16 bytes are written in an order that depends on
             // the lane, so that neighbours' do not meet in a bank.
             const int turn = piece & 3;
-            uint32_t w0 = raw[i].x, w1 = raw[i].y, w2 = raw[i].z, w3 = raw[i].w, x;
-            if (turn & 1) { x = w0; w0 = w1; w1 = w2; w2 = w3; w3 = x; }
-            if (turn & 2) { x = w0; w0 = w2; w2 = x; x = w1; w1 = w3; w3 = x; }
+            uint32_t w0 = raw[i].x, w1 = raw[i].y, w2 = raw[i].z, w3 = raw[i].w;
+            {
+                const bool t1 = turn & 1, t2 = turn & 2;
+                const uint32_t x0 = t1 ? w1 : w0, x1 = t1 ? w2 : w1, x2 = t1 ? w3 : w2, x3 = t1 ? w0 : w3;
+                w0 = t2 ? x2 : x0;
+                w1 = t2 ? x3 : x1;
+                w2 = t2 ? x0 : x2;
+                w3 = t2 ? x1 : x3;
+            }
             const uint32_t w[4] = {w0, w1, w2, w3};
             uint16_t *row = (value ? sv[buf] : sk[buf]) + key * D;
             const int swap = value ? value_turn(key) : key_turn(key);
+            if (value) {
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const int at = (4 * piece + ((c + turn) & 3)) ^ swap;
-                const u32x4_t v = value ? decode8<true>(w[c], o2, s2) : decode8<false>(w[c], o2, s2);
-                *reinterpret_cast<u32x4_t *>(row + at * 8) = v;
+                for (int c = 0; c < 4; ++c)
+                    *reinterpret_cast<u32x4_t *>(row + ((4 * piece + ((c + turn) & 3)) ^ swap) * 8) = decode8<true>(w[c], o2, s2);
+            } else {
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    *reinterpret_cast<u32x4_t *>(row + ((4 * piece + ((c + turn) & 3)) ^ swap) * 8) = decode8<false>(w[c], o2, s2);
             }
         }
     };
@@ -1128,12 +1139,10 @@ __global__ __launch_bounds__(kTileThreads, 1) void attend_tile_kernel(AttendArgs
             wild_next = __builtin_amdgcn_readfirstlane(n.wild);
         }
         decode(t0 & 1, ek_next, ev_next);
-        if (t0 + 1 < t1) {
-            ids(t0 + 1);
-            load(t0 + 1);
-            publish(t0 + 1);
-        }
-        if (t0 + 2 < t1) ids(t0 + 2);
+        ids(t0 + 1);
+        load(t0 + 1);
+        ids(t0 + 2);
+        publish(t0 + 1);
     }
     for (int tile = t0; tile < t1; ++tile) {
         __syncthreads();
@@ -1155,9 +1164,9 @@ __global__ __launch_bounds__(kTileThreads, 1) void attend_tile_kernel(AttendArgs
             ev_next = e2 > ev ? e2 : ev;
             decode((tile + 1) & 1, ek_next, ev_next);
             if (tid == 0) news[tile % 3] = TileNews{0, 0, 0};  // (read before this barrier, written after the next)
-            if (tile + 2 < t1) load(tile + 2);
-            if (tile + 3 < t1) ids(tile + 3);
         }
+        load(tile + 2);
+        ids(tile + 3);
         const int key0 = rt.lo + tile * kKeys;
         if (key0 <= some_to && key0 + kKeys - 1 >= some_from) {
             const uint16_t *kb = sk[tile & 1], *vb = sv[tile & 1];
@@ -1251,7 +1260,7 @@ __global__ __launch_bounds__(kTileThreads, 1) void attend_tile_kernel(AttendArgs
                 }
             }
         }
-        if (tile + 2 < t1) publish(tile + 2);
+        publish(tile + 2);
     }
 
     // Results.
