@@ -855,7 +855,7 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs g) {
 constexpr int kRowTile = 256;
 constexpr int kTileWaves = 8;
 constexpr int kTileThreads = 64 * kTileWaves;
-constexpr int kKeys = 64;
+constexpr int kKeyTile = 64;     // keys that parts are counted in
 constexpr int kMinKeyTiles = 8;  // tiles of keys a part should have
 constexpr float kTop = 9;        // a weight of 1 is 2^9
 
@@ -903,43 +903,32 @@ __device__ __forceinline__ bool find_row_tile(const AttendArgs &g, int64_t index
     r.hi = a.causal ? last_pos + 1 : r.s.len;
     if (r.hi < 0) r.hi = 0;
     const int64_t lo = a.window > 0 ? (int64_t)first_pos - a.window + 1 : 0;
-    r.lo = lo > 0 ? (int)(lo < r.hi ? lo : r.hi) & ~(kKeys - 1) : 0;
-    const int nt = (r.hi - r.lo + kKeys - 1) / kKeys;
+    r.lo = lo > 0 ? (int)(lo < r.hi ? lo : r.hi) & ~(kKeyTile - 1) : 0;
+    const int nt = (r.hi - r.lo + kKeyTile - 1) / kKeyTile;
     const int most = (nt + kMinKeyTiles - 1) / kMinKeyTiles;
     r.parts = most < g.parts ? (most < 1 ? 1 : most) : g.parts;
     return true;
 }
 
-// The pieces of 16 bytes of a row of LDS are dealt so that neither 8 keys at
-// one piece (reads of keys) nor 4 keys at two pieces (transposing reads of
-// values) meet in a bank.
+// Where a piece of 16 bytes of a row of LDS lies: dealt so that neither 8 keys
+// at one piece (reads of keys), nor 4 keys at two pieces (transposing reads of
+// values), nor the c-th pieces of 4 neighbours of two keys (writes) meet in a
+// bank.
 __device__ __forceinline__ int key_turn(int key) { return key & 7; }
-__device__ __forceinline__ int value_turn(int key) { return ((key & 3) << 1) | ((key >> 2) & 1); }
+__device__ __forceinline__ int value_turn(int key) { return ((key & 1) << 2) | (key & 2) | ((key >> 2) & 1); }
+__device__ __forceinline__ int place(int piece, int turn) { return piece ^ ((piece >> 2) & 3) ^ turn; }
 
 typedef short short4_t __attribute__((ext_vector_type(4)));
 
-// (code - zero) scale of 8 codes in fp16, in natural order if NATURAL, else 0 4 1 5 2 6 3 7.
-template <bool NATURAL>
-__device__ __forceinline__ u32x4_t decode8(uint32_t w, half2_t off, half2_t s) {
-    uint32_t r[4] = {(w & 0x000F000Fu) | 0x64006400u,  // 1024 + code
-                     ((w >> 4) & 0x000F000Fu) | 0x64006400u, ((w >> 8) & 0x000F000Fu) | 0x64006400u,
-                     ((w >> 12) & 0x000F000Fu) | 0x64006400u};
+// (code - zero) scale of 8 codes in fp16, in the order 0 4 1 5 2 6 3 7; `magic`
+// in a register, since an instruction takes one constant.
+__device__ __forceinline__ u32x4_t decode8(uint32_t w, half2_t off, half2_t s, uint32_t mask, uint32_t magic) {
+    const uint32_t r[4] = {(w & mask) | magic, ((w >> 4) & mask) | magic, ((w >> 8) & mask) | magic, ((w >> 12) & mask) | magic};
     u32x4_t o;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const half2_t h = (__builtin_bit_cast(half2_t, r[i]) + off) * s;
-        r[i] = __builtin_bit_cast(uint32_t, h);
-    }
-    if constexpr (NATURAL) {
-        o[0] = __builtin_amdgcn_perm(r[1], r[0], 0x05040100u);
-        o[1] = __builtin_amdgcn_perm(r[3], r[2], 0x05040100u);
-        o[2] = __builtin_amdgcn_perm(r[1], r[0], 0x07060302u);
-        o[3] = __builtin_amdgcn_perm(r[3], r[2], 0x07060302u);
-    } else {
-        o[0] = r[0];
-        o[1] = r[1];
-        o[2] = r[2];
-        o[3] = r[3];
+        o[i] = __builtin_bit_cast(uint32_t, h);
     }
     return o;
 }
@@ -949,16 +938,21 @@ __device__ __forceinline__ int exponent_above(uint32_t bits) {
     return bits == 0 ? -24 : bits < 0x400u ? -14 : (int)(bits >> 10) - 14;
 }
 
+// The bits of the largest fp16 below 2^e.
+__device__ __forceinline__ int below(int e) { return e <= -14 ? (e < -14 ? 0 : 0x3FF) : ((e + 15) << 10) - 1; }
+
 struct TileNews {
-    uint32_t key_scale, value_scale;  // the largest finite scales (bits) of a tile
+    uint32_t key_scale, value_scale;  // the largest finite scales (bits) that pass the exponents in use
     uint32_t wild;                    // kWild, kHidden
 };
 enum { kWild = 1, kHidden = 2 };  // some scale of a value is not finite; some page of the table is not one
 
-template <int ND>
+// KB: blocks of 32 keys a tile (with 192 and 256 dimensions one: the scores of
+// two would not stay in registers beside the sums).
+template <int ND, int KB>
 __global__ __launch_bounds__(kTileThreads, 1) void attend_tile_kernel(AttendArgs g) {
-    constexpr int D = ND * 64;
-    constexpr int kUnits = 128 * ND;                 // pieces of 16 bytes of codes of a tile of keys
+    constexpr int D = ND * 64, kKeys = 32 * KB;
+    constexpr int kUnits = kKeys * 2 * ND;           // pieces of 16 bytes of codes of a tile of keys
     constexpr int kLoads = (2 * kUnits + kTileThreads - 1) / kTileThreads;
     __shared__ __attribute__((aligned(16))) uint16_t sk[2][kKeys * D];
     __shared__ __attribute__((aligned(16))) uint16_t sv[2][kKeys * D];
@@ -986,30 +980,31 @@ __global__ __launch_bounds__(kTileThreads, 1) void attend_tile_kernel(AttendArgs
     half8_t qf[ND * 4];
     float kappa;
     {
-        const uint16_t *q = a.q + (int64_t)(s.first + j) * a.q_stride + (int64_t)hq * D + 8 * half;
-        float v[ND * 4][8], top = 0;
+        const uint16_t *q = a.q + (int64_t)(s.first + j) * a.q_stride + (hq * D + 8 * half);
+        u32x4_t raw[ND * 4];
+        uint32_t most = 0;
 #pragma unroll
         for (int d = 0; d < ND * 4; ++d) {
-            const u32x4_t raw = *reinterpret_cast<const u32x4_t *>(q + 16 * d);
+            raw[d] = *reinterpret_cast<const u32x4_t *>(q + 16 * d);
 #pragma unroll
             for (int y = 0; y < 4; ++y) {
-                const uint32_t p = raw[y];
-                v[d][2 * y] = __builtin_bit_cast(float, p << 16);
-                v[d][2 * y + 1] = __builtin_bit_cast(float, p & 0xFFFF0000u);
-            }
-#pragma unroll
-            for (int y = 0; y < 8; ++y) {
-                const float m = fabsf(v[d][y]);
-                if (m < INFINITY) top = fmaxf(top, m);
+                const uint32_t p = raw[d][y];
+                most = pk_max(most, p & 0x7FFF7FFFu);
             }
         }
-        top = fmaxf(top, __shfl_xor(top, 32));
-        const int ex = top > 0 ? 10 - (int)__builtin_amdgcn_frexp_expf(top) : 0;  // the largest to 2^9 .. 2^10
+        most = half_max(pk_max(most, (uint32_t)__shfl_xor((int)most, 32)));
+        const int ex = live ? 136 - (int)(most >> 7) : -300;  // the largest to 2^9 .. 2^10
         kappa = ldexpf(a.scale * 1.44269504088896f, -ex);
 #pragma unroll
         for (int d = 0; d < ND * 4; ++d)
 #pragma unroll
-            for (int y = 0; y < 8; ++y) qf[d][y] = (_Float16)(live ? ldexpf(v[d][(y & 1) * 4 + (y >> 1)], ex) : 0.0f);
+            for (int y = 0; y < 4; ++y) {
+                // Codes come in the order 0 4 1 5 2 6 3 7.
+                const uint32_t p = raw[d][y];
+                const int to = 2 * y < 4 ? 4 * y : 4 * y - 7;
+                qf[d][to] = (_Float16)ldexpf(__builtin_bit_cast(float, p << 16), ex);
+                qf[d][to + 2] = (_Float16)ldexpf(__builtin_bit_cast(float, p & 0xFFFF0000u), ex);
+            }
     }
     const int pos = s.len - s.n + j;
     const int seen_to = live ? (a.causal ? pos : s.len - 1) : -1;
@@ -1032,10 +1027,13 @@ __global__ __launch_bounds__(kTileThreads, 1) void attend_tile_kernel(AttendArgs
     // What the thread decodes: pieces of 32 codes, keys' before values'.  Loads
     // are made without conditions, their values looked at where they are used:
     // a wait then never holds for loads that came after.
-    u32x4_t raw[kLoads];
-    uint32_t raw_s[kLoads], raw_z[kLoads];
-    int next_id[kLoads];     // the table's entries for the next load
-    bool raw_ok[kLoads], raw_hidden[kLoads];
+    struct Raw {
+        u32x4_t codes;
+        uint32_t scale, zero;
+        bool ok, hidden;
+    };
+    Raw raw[kLoads], coming[kLoads];  // of the tile to decode, and of the next
+    int next_id[kLoads];              // the table's entries for the load after
     const int last_page = (s.len - 1) >> g.page_shift;
     auto is_value = [&](int i) { return wave * 64 + kTileThreads * i >= kUnits; };
     auto is_piece = [&](int i) { return wave * 64 + kTileThreads * i < 2 * kUnits; };
@@ -1055,63 +1053,60 @@ __global__ __launch_bounds__(kTileThreads, 1) void attend_tile_kernel(AttendArgs
         for (int i = 0; i < kLoads; ++i) {
             const int piece = (tid + kTileThreads * i) % (2 * ND), key = key_of(i, tile);
             const bool value = is_value(i), page_ok = (uint32_t)next_id[i] < (uint32_t)pages;
-            raw_ok[i] = page_ok && key < s.len;
-            raw_hidden[i] = !page_ok && key < s.len;
+            Raw &c = coming[i];
+            c.ok = page_ok && key < s.len;
+            c.hidden = !page_ok && key < s.len;
             const int64_t row = ((int64_t)(page_ok ? next_id[i] : 0) * heads + h) * page + (key & (page - 1));
-            raw[i] = *reinterpret_cast<const u32x4_t *>((value ? a.cache.v_codes : a.cache.k_codes) + row * (D / 2) + piece * 16);
-            raw_s[i] = (value ? a.cache.v_scales : a.cache.k_scales)[row * ND + piece / 2];
-            raw_z[i] = (value ? a.cache.v_zeros : a.cache.k_zeros)[row * ND + piece / 2];
+            c.codes = *reinterpret_cast<const u32x4_t *>((value ? a.cache.v_codes : a.cache.k_codes) + row * (D / 2) + piece * 16);
+            c.scale = (value ? a.cache.v_scales : a.cache.k_scales)[row * ND + piece / 2];
+            c.zero = (value ? a.cache.v_zeros : a.cache.k_zeros)[row * ND + piece / 2];
         }
     };
-    auto publish = [&](int tile) {
+    auto take = [&] {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) raw[i] = coming[i];
+    };
+    // Tells of scales that pass the exponents in use, and of what is rare.
+    auto publish = [&](int tile, int ek, int ev) {
         TileNews &n = news[tile % 3];
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
             if (!is_piece(i)) break;
-            const bool value = is_value(i), fin = !raw_ok[i] || raw_s[i] < 0x7C00u;
-            const uint32_t top = wave_max_u32(raw_ok[i] && fin ? raw_s[i] : 0);
-            const uint32_t wild = (value && __any(!fin) ? (uint32_t)kWild : 0u) | (__any(raw_hidden[i]) ? (uint32_t)kHidden : 0u);
-            if (lane == 0) {
-                atomicMax(value ? &n.value_scale : &n.key_scale, top);
-                if (wild) atomicOr(&n.wild, wild);
+            const Raw &c = coming[i];
+            const bool value = is_value(i);
+            const uint32_t bits = c.ok ? c.scale : 0;
+            if (__any((int)bits > below(value ? ev : ek) || c.hidden)) {
+                const bool fin = bits < 0x7C00u;
+                const uint32_t top = wave_max_u32(fin ? bits : 0);
+                const uint32_t wild =
+                    (value && __any(!fin) ? (uint32_t)kWild : 0u) | (__any(c.hidden) ? (uint32_t)kHidden : 0u);
+                if (lane == 0) {
+                    atomicMax(value ? &n.value_scale : &n.key_scale, top);
+                    if (wild) atomicOr(&n.wild, wild);
+                }
             }
         }
     };
+    uint32_t mask = 0x000F000Fu, magic = 0x64006400u;  // 1024 + code
+    asm volatile("" : "+s"(mask), "+v"(magic));
     auto decode = [&](int buf, int ek, int ev) {
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
             if (!is_piece(i)) break;
             const int in = (tid + kTileThreads * i) % kUnits, piece = in % (2 * ND), key = in / (2 * ND);
             const bool value = is_value(i);
-            uint32_t sb = raw_ok[i] ? raw_s[i] : 0;
+            const Raw &c0 = raw[i];
+            uint32_t sb = c0.ok ? c0.scale : 0;
             if (value && sb >= 0x7C00u) sb = 0;  // (rows that see it are made NaN below)
             const _Float16 sc = (_Float16)ldexpf(f16_bits_to_f32(sb), -(value ? ev : ek));
-            const _Float16 of = (_Float16)(-1024.0f - (raw_ok[i] ? f16_bits_to_f32(raw_z[i]) : 0.0f));
+            const _Float16 of = (_Float16)(-1024.0f - (c0.ok ? f16_bits_to_f32(c0.zero) : 0.0f));
             const half2_t s2 = {sc, sc}, o2 = {of, of};
-            // The 4 pieces of 16 bytes are written in an order that depends on
-            // the lane, so that neighbours' do not meet in a bank.
-            const int turn = piece & 3;
-            uint32_t w0 = raw[i].x, w1 = raw[i].y, w2 = raw[i].z, w3 = raw[i].w;
-            {
-                const bool t1 = turn & 1, t2 = turn & 2;
-                const uint32_t x0 = t1 ? w1 : w0, x1 = t1 ? w2 : w1, x2 = t1 ? w3 : w2, x3 = t1 ? w0 : w3;
-                w0 = t2 ? x2 : x0;
-                w1 = t2 ? x3 : x1;
-                w2 = t2 ? x0 : x2;
-                w3 = t2 ? x1 : x3;
-            }
-            const uint32_t w[4] = {w0, w1, w2, w3};
+            const uint32_t w[4] = {c0.codes.x, c0.codes.y, c0.codes.z, c0.codes.w};
             uint16_t *row = (value ? sv[buf] : sk[buf]) + key * D;
-            const int swap = value ? value_turn(key) : key_turn(key);
-            if (value) {
+            const int turn = value ? value_turn(key) : key_turn(key);
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    *reinterpret_cast<u32x4_t *>(row + ((4 * piece + ((c + turn) & 3)) ^ swap) * 8) = decode8<true>(w[c], o2, s2);
-            } else {
-#pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    *reinterpret_cast<u32x4_t *>(row + ((4 * piece + ((c + turn) & 3)) ^ swap) * 8) = decode8<false>(w[c], o2, s2);
-            }
+            for (int c = 0; c < 4; ++c)
+                *reinterpret_cast<u32x4_t *>(row + place(4 * piece + c, turn) * 8) = decode8(w[c], o2, s2, mask, magic);
         }
     };
 
@@ -1130,7 +1125,7 @@ __global__ __launch_bounds__(kTileThreads, 1) void attend_tile_kernel(AttendArgs
         ids(t0);
         load(t0);
         __syncthreads();
-        publish(t0);
+        publish(t0, -24, -24);
         __syncthreads();
         {
             const TileNews n = news[t0 % 3];
@@ -1138,11 +1133,12 @@ __global__ __launch_bounds__(kTileThreads, 1) void attend_tile_kernel(AttendArgs
             ev_next = __builtin_amdgcn_readfirstlane(exponent_above(n.value_scale));
             wild_next = __builtin_amdgcn_readfirstlane(n.wild);
         }
+        take();
         decode(t0 & 1, ek_next, ev_next);
         ids(t0 + 1);
         load(t0 + 1);
         ids(t0 + 2);
-        publish(t0 + 1);
+        publish(t0 + 1, ek_next, ev_next);
     }
     for (int tile = t0; tile < t1; ++tile) {
         __syncthreads();
@@ -1155,38 +1151,40 @@ __global__ __launch_bounds__(kTileThreads, 1) void attend_tile_kernel(AttendArgs
 #pragma unroll
             for (int y = 0; y < 2 * ND; ++y) o[y] *= f;
         }
-        if (tile + 1 < t1) {
+        {
             const TileNews n = news[(tile + 1) % 3];
             const int e1 = __builtin_amdgcn_readfirstlane(exponent_above(n.key_scale));
             const int e2 = __builtin_amdgcn_readfirstlane(exponent_above(n.value_scale));
             wild_next = __builtin_amdgcn_readfirstlane(n.wild);
             ek_next = e1 > ek ? e1 : ek;
             ev_next = e2 > ev ? e2 : ev;
-            decode((tile + 1) & 1, ek_next, ev_next);
-            if (tid == 0) news[tile % 3] = TileNews{0, 0, 0};  // (read before this barrier, written after the next)
         }
+        if (tid == 0) news[tile % 3] = TileNews{0, 0, 0};  // (read before this barrier, written after the next)
+        take();
         load(tile + 2);
         ids(tile + 3);
+        if (tile + 1 < t1) decode((tile + 1) & 1, ek_next, ev_next);
         const int key0 = rt.lo + tile * kKeys;
         if (key0 <= some_to && key0 + kKeys - 1 >= some_from) {
             const uint16_t *kb = sk[tile & 1], *vb = sv[tile & 1];
-            float16_t S[2];
+            float16_t S[KB];
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
+            for (int x = 0; x < KB; ++x)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) S[x][i] = 0;
 #pragma unroll
-                for (int d = 0; d < ND * 4; ++d) {
-                    const u32x4_t k = *reinterpret_cast<const u32x4_t *>(kb + (32 * x + col) * D + ((2 * d + half) ^ key_turn(col)) * 8);
+            for (int d = 0; d < ND * 4; ++d)
+#pragma unroll
+                for (int x = 0; x < KB; ++x) {
+                    const u32x4_t k = *reinterpret_cast<const u32x4_t *>(kb + (32 * x + col) * D + ((2 * d ^ ((d >> 1) & 3)) ^ half ^ key_turn(col)) * 8);
                     S[x] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(half8_t, k), qf[d], S[x], 0, 0, 0);
                 }
-            }
             const float kap = ldexpf(kappa, ek);
             if (key0 + kKeys - 1 > all_to || key0 < all_from || (wild & kHidden)) {
                 uint64_t shown = ~0ull;
                 if (wild & kHidden) shown = __ballot(page_at(key0 + lane) >= 0);
 #pragma unroll
-                for (int x = 0; x < 2; ++x)
+                for (int x = 0; x < KB; ++x)
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
                         const int key = key0 + 32 * x + 8 * (i / 4) + 4 * half + (i & 3);
@@ -1195,7 +1193,7 @@ __global__ __launch_bounds__(kTileThreads, 1) void attend_tile_kernel(AttendArgs
             }
             float tm = S[0][0];
 #pragma unroll
-            for (int x = 0; x < 2; ++x)
+            for (int x = 0; x < KB; ++x)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) tm = fmaxf(tm, S[x][i]);
             if (__any(fmaf(tm, kap, ck) > kTop + kHeadroom)) {
@@ -1209,9 +1207,9 @@ __global__ __launch_bounds__(kTileThreads, 1) void attend_tile_kernel(AttendArgs
 #pragma unroll
                 for (int y = 0; y < 2 * ND; ++y) o[y] *= fade;
             }
-            half8_t pf[2][2];
+            half8_t pf[KB][2];
 #pragma unroll
-            for (int x = 0; x < 2; ++x)
+            for (int x = 0; x < KB; ++x)
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
                     u32x4_t w;
@@ -1228,20 +1226,19 @@ __global__ __launch_bounds__(kTileThreads, 1) void attend_tile_kernel(AttendArgs
             const int gk = 4 * half + ((lane & 15) >> 2);               // the key of 8 that the lane's address names
             const int gd = ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1);   // its piece of a block of 32 dimensions
 #pragma unroll
-            for (int y = 0; y < 2 * ND; ++y) {
-                const uint16_t *va = vb + gk * D + ((4 * y + gd) ^ value_turn(gk)) * 8 + (lane & 1) * 4;
+            for (int x = 0; x < KB; ++x)
 #pragma unroll
-                for (int x = 0; x < 2; ++x)
+                for (int z = 0; z < 2; ++z)
 #pragma unroll
-                    for (int z = 0; z < 2; ++z) {
+                    for (int y = 0; y < 2 * ND; ++y) {
                         typedef __attribute__((address_space(3))) short4_t lds_short4;
+                        typedef short short8_t __attribute__((ext_vector_type(8)));
+                        const uint16_t *va = vb + gk * D + ((4 * y ^ (y & 3)) ^ gd ^ value_turn(gk)) * 8 + (lane & 1) * 4;
                         const short4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_short4 *)(va + (32 * x + 16 * z) * D));
                         const short4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_short4 *)(va + (32 * x + 16 * z + 8) * D));
-                        typedef short short8_t __attribute__((ext_vector_type(8)));
                         const short8_t v8 = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
                         o[y] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(half8_t, v8), pf[x][z], o[y], 0, 0, 0);
                     }
-            }
             if (wild & kWild) {
                 // Rows that see a value whose scale is not finite.
                 for (int k = 0; k < kKeys; ++k) {
@@ -1260,11 +1257,23 @@ __global__ __launch_bounds__(kTileThreads, 1) void attend_tile_kernel(AttendArgs
                 }
             }
         }
-        publish(tile + 2);
+        publish(tile + 2, ek_next, ev_next);
     }
 
-    // Results.
+    // Results.  Of 8 dimensions the lane has 0 4 1 5 (2 6 3 7 in the other half
+    // of the wave): exchanged, it has 0 1 2 3 (4 5 6 7).
     const float sum = l + __shfl_xor(l, 32), ref = -nk;
+#pragma unroll
+    for (int y = 0; y < 2 * ND; ++y)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float a0 = o[y][4 * i], a1 = o[y][4 * i + 1], a2 = o[y][4 * i + 2], a3 = o[y][4 * i + 3];
+            const float b0 = __shfl_xor(half ? a0 : a1, 32), b1 = __shfl_xor(half ? a2 : a3, 32);
+            o[y][4 * i] = half ? b0 : a0;
+            o[y][4 * i + 1] = half ? b1 : a2;
+            o[y][4 * i + 2] = half ? a1 : b0;
+            o[y][4 * i + 3] = half ? a3 : b1;
+        }
     if (!live) return;
     const int64_t t = s.first + j;
     if (rt.parts == 1) {
@@ -1437,7 +1446,7 @@ static hipError_t launch_attend(AttendArgs &g, const AttendPlan &p, float *works
     g.parts = p.parts;
     const int64_t n = p.row_tiles * a.cache.heads;
     g.part_sums = g.part + (size_t)n * p.parts * kRowTile * a.cache.D;
-    e = hipLaunchKernel(reinterpret_cast<const void *>(&attend_tile_kernel<ND>), dim3((unsigned)(n * p.parts)),
+    e = hipLaunchKernel(reinterpret_cast<const void *>(&attend_tile_kernel<ND, ND <= 2 ? 2 : 1>), dim3((unsigned)(n * p.parts)),
                         dim3(kTileThreads), args, 0, stream);
     if (e != hipSuccess || p.parts == 1) return e;
     return hipLaunchKernel(reinterpret_cast<const void *>(&attend_tile_join_kernel<ND>), dim3((unsigned)n, kRowTile / 16), dim3(256),
