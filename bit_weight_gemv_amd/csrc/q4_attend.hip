@@ -17,6 +17,11 @@ namespace q4 {
 typedef _Float16 half8_t __attribute__((ext_vector_type(8)));
 typedef int int2_t __attribute__((ext_vector_type(2)));
 
+// A tile of rows of the tile kernel, for the joining: parts is 0 where it has none.
+struct TileRows {
+    int first, row0, rows, parts;
+};
+
 typedef __attribute__((address_space(4))) int32_t scalar_int;  // read-only: uniform loads are scalar
 
 // Where the pieces of a (sequence, key head) lie that the split kernel dealt to
@@ -46,8 +51,10 @@ struct AttendArgs {
     float *part_sums;
     Pieces *pieces;     // split kernel: [sequence][key head]
     int waves;          // its waves at most
+    TileRows *tile_rows;  // tile kernel: [tile of rows]
     int64_t row_tiles;  // tile kernel: tiles of rows at most
     int parts;          // workgroups the keys of one are dealt to at most
+    int part_tiles;     // tiles of kKeyTile keys a part should have
 };
 
 // A sequence as a kernel sees it, every value within its bounds.
@@ -496,7 +503,10 @@ __global__ __launch_bounds__(kSplitThreads, split_occupancy(ND, NT)) void attend
             seen_to[x] = r < rows ? (a.causal ? pos : s.len - 1) : -1;
             seen_from[x] = a.window > 0 ? pos - (int)(a.window < 0x7fffffff ? a.window : 0x7fffffff) + 1 : 0;
         }
-        // Keys that all rows see: tiles within need no mask.
+        // The first key that some row sees, and keys that all rows see: tiles
+        // within need no mask.
+        const int64_t low = a.window > 0 ? (int64_t)s.len - s.n - a.window + 1 : 0;
+        const int low_key = low > 0 ? (int)(low < s.len ? low : s.len) : 0;
         const int all_to = a.causal ? s.len - s.n : s.len - 1;
         const int64_t all_from = a.window > 0 ? (int64_t)s.len - s.n + (n - 1) - a.window + 1 : 0;
 
@@ -522,7 +532,7 @@ __global__ __launch_bounds__(kSplitThreads, split_occupancy(ND, NT)) void attend
             const bool ok[2] = {(uint32_t)id0 < (uint32_t)pages && lo_key + tile * kTile < s.len,
                                 (uint32_t)id1 < (uint32_t)pages && lo_key + tile * kTile + 16 < s.len};
             const int key = lo_key + tile * kTile;
-            const bool edge = !ok[0] || !ok[1] || key + kTile > s.len;
+            const bool edge = !ok[0] || !ok[1] || key + kTile > s.len || key < low_key;
             if (__builtin_expect(edge, 0)) {
                 // Keys that no row sees may hold anything: scales and zeros of 0.
                 asm volatile("");  // (a branch, not selects)
@@ -530,8 +540,9 @@ __global__ __launch_bounds__(kSplitThreads, split_occupancy(ND, NT)) void attend
                 for (int d = 0; d < ND; ++d) {
                     const int c = lane + 64 * d, in = c % (16 * ND), t = in >= 8 * ND, y = 2 * (in - t * 8 * ND);
                     const bool page_ok = t ? ok[1] : ok[0];
-                    if (!page_ok || key + 16 * t + y / ND >= s.len) T.par[d] &= 0xFFFF0000u;
-                    if (!page_ok || key + 16 * t + (y + 1) / ND >= s.len) T.par[d] &= 0x0000FFFFu;
+                    const int k0 = key + 16 * t + y / ND, k1 = key + 16 * t + (y + 1) / ND;
+                    if (!page_ok || k0 >= s.len || k0 < low_key) T.par[d] &= 0xFFFF0000u;
+                    if (!page_ok || k1 >= s.len || k1 < low_key) T.par[d] &= 0x0000FFFFu;
                 }
             }
             uint8_t *vl = sh.in.v[wave];
@@ -845,8 +856,9 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs g) {
 // stands; V is turned by the transposing 16-bit LDS read.
 // 2^E is above every scale of the keys so far (of the values': the sums are
 // rescaled when it grows), so that a decoded value is rounded by 2^-11 of
-// itself and none passes fp16.  The sum of a row's weights is that of the
-// rounded weights.
+// itself and none passes fp16.  The sum of a row's weights is that of the fp32
+// weights: with the sum of the rounded ones, one instruction for two of them,
+// lse was off by up to 2^-11.
 //
 // Where the rows are few for the card, the keys of a tile of rows are dealt to
 // several workgroups, whose results a second launch joins.
@@ -863,7 +875,8 @@ struct RowTile {
     int64_t b;
     Sequence s;
     int row0, rows;   // first row, rows of the sequence
-    int lo, hi;       // keys that some row of the tile sees: lo (a multiple of 64) .. hi - 1
+    int low, hi;      // keys that some row of the tile sees: low .. hi - 1
+    int lo;           // low, down to a multiple of 64
     int parts;        // workgroups its keys are dealt to
 };
 
@@ -903,9 +916,10 @@ __device__ __forceinline__ bool find_row_tile(const AttendArgs &g, int64_t index
     r.hi = a.causal ? last_pos + 1 : r.s.len;
     if (r.hi < 0) r.hi = 0;
     const int64_t lo = a.window > 0 ? (int64_t)first_pos - a.window + 1 : 0;
-    r.lo = lo > 0 ? (int)(lo < r.hi ? lo : r.hi) & ~(kKeyTile - 1) : 0;
+    r.low = lo > 0 ? (int)(lo < r.hi ? lo : r.hi) : 0;
+    r.lo = r.low & ~(kKeyTile - 1);
     const int nt = (r.hi - r.lo + kKeyTile - 1) / kKeyTile;
-    const int most = (nt + kMinKeyTiles - 1) / kMinKeyTiles;
+    const int most = (nt + g.part_tiles - 1) / g.part_tiles;
     r.parts = most < g.parts ? (most < 1 ? 1 : most) : g.parts;
     return true;
 }
@@ -962,13 +976,18 @@ __global__ __launch_bounds__(kTileThreads, 1) void attend_tile_kernel(AttendArgs
     const int tid = (int)threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int col = lane & 31, half = lane >> 5;
     const int heads = (int)a.cache.heads, page = (int)a.cache.page, pages = (int)a.cache.pages;
-    // The last tiles of rows see the most keys: they begin first.
-    const int64_t per = (int64_t)heads * g.parts;
-    const int64_t index = g.row_tiles - 1 - blockIdx.x / per;
-    const int part = (int)(blockIdx.x % per) / heads, h = (int)(blockIdx.x % heads);
+    // The last tiles of rows see the most keys: they begin first, and all first
+    // parts before the second ones (workgroups go to the card's dies and their
+    // quarters strictly in turn: a tile's parts side by side, of which short
+    // tiles have only the first, would leave some without work).
+    const int64_t items = g.row_tiles * heads;
+    const int part = (int)(blockIdx.x / items), h = (int)(blockIdx.x % heads);
+    const int64_t index = g.row_tiles - 1 - (blockIdx.x - part * items) / heads;
     RowTile rt;
-    if (!find_row_tile<kTileThreads>(g, index, sums, found, rt)) return;
-    if (part >= rt.parts) return;
+    const bool valid = find_row_tile<kTileThreads>(g, index, sums, found, rt);
+    if (part == 0 && h == 0 && tid == 0)
+        g.tile_rows[index] = valid ? TileRows{rt.s.first, rt.row0, rt.rows, rt.parts} : TileRows{0, 0, 0, 0};
+    if (!valid || part >= rt.parts) return;
     const Sequence s = rt.s;
     const int nt_all = (rt.hi - rt.lo + kKeys - 1) / kKeys;
     const int t0 = (int)((int64_t)nt_all * part / rt.parts), t1 = (int)((int64_t)nt_all * (part + 1) / rt.parts);
@@ -1054,7 +1073,7 @@ __global__ __launch_bounds__(kTileThreads, 1) void attend_tile_kernel(AttendArgs
             const int piece = (tid + kTileThreads * i) % (2 * ND), key = key_of(i, tile);
             const bool value = is_value(i), page_ok = (uint32_t)next_id[i] < (uint32_t)pages;
             Raw &c = coming[i];
-            c.ok = page_ok && key < s.len;
+            c.ok = page_ok && key >= rt.low && key < rt.hi;  // (others may hold anything)
             c.hidden = !page_ok && key < s.len;
             const int64_t row = ((int64_t)(page_ok ? next_id[i] : 0) * heads + h) * page + (key & (page - 1));
             c.codes = *reinterpret_cast<const u32x4_t *>((value ? a.cache.v_codes : a.cache.k_codes) + row * (D / 2) + piece * 16);
@@ -1217,8 +1236,8 @@ __global__ __launch_bounds__(kTileThreads, 1) void attend_tile_kernel(AttendArgs
                     for (int i = 0; i < 4; ++i) {
                         const float pa = __builtin_amdgcn_exp2f(fmaf(S[x][8 * y + 2 * i], kap, nk));
                         const float pb = __builtin_amdgcn_exp2f(fmaf(S[x][8 * y + 2 * i + 1], kap, nk));
-                        const half2_t p2 = __builtin_bit_cast(half2_t, __builtin_amdgcn_cvt_pkrtz(pa, pb));
-                        l = __builtin_amdgcn_fdot2(p2, half2_t{1, 1}, l, false);
+                        const half2_t p2 = {(_Float16)pa, (_Float16)pb};
+                        l += pa + pb;
                         w[i] = __builtin_bit_cast(uint32_t, p2);
                     }
                     pf[x][y] = __builtin_bit_cast(half8_t, w);
@@ -1310,39 +1329,55 @@ __global__ __launch_bounds__(kTileThreads, 1) void attend_tile_kernel(AttendArgs
     }
 }
 
-// Joins the parts of a tile of rows, 16 rows a workgroup.
+// Joins the parts of a tile of rows: 4 dimensions of a row a lane.
 template <int ND>
 __global__ __launch_bounds__(256) void attend_tile_join_kernel(AttendArgs g) {
-    constexpr int D = ND * 64;
-    __shared__ int64_t sums[4], found[2];
+    constexpr int D = ND * 64, kRows = 256 / (16 * ND);  // rows at a time, 4 times
     const CacheAttend &a = g.a;
     const int heads = (int)a.cache.heads, h = (int)(blockIdx.x % heads);
     const int64_t index = blockIdx.x / heads;
-    RowTile rt;
-    if (!find_row_tile<256>(g, index, sums, found, rt) || rt.parts == 1) return;
-    for (int e = (int)threadIdx.x; e < 16 * D / 4; e += 256) {
-        const int c = (int)blockIdx.y * 16 + e / (D / 4), d = e % (D / 4) * 4, r = rt.row0 + c;
-        if (r >= rt.rows) break;
+    const scalar_int *desc = (const scalar_int *)(g.tile_rows + index);
+    const int first = desc[0], row0 = desc[1], rows = desc[2], parts = desc[3];
+    if (parts < 2) return;
+    const int c0 = (int)threadIdx.x / (D / 4), d = (int)threadIdx.x % (D / 4) * 4;
+    if (c0 >= kRows) return;
+    for (int c = (int)blockIdx.y * 4 * kRows + c0; c < ((int)blockIdx.y + 1) * 4 * kRows && c < kRowTile && row0 + c < rows; c += kRows) {
+        const int r = row0 + c;
         const int64_t slot0 = (index * heads + h) * g.parts * kRowTile + c;
-        float top = -INFINITY;
-        for (int p = 0; p < rt.parts; ++p) {
-            const float *q = g.part_sums + (slot0 + (int64_t)p * kRowTile) * 2;
-            if (q[1] != 0) top = fmaxf(top, q[0]);
-        }
-        float lt = 0;
+        const float2 *sums = reinterpret_cast<const float2 *>(g.part_sums) + slot0;
+        const float *part = g.part + slot0 * D + d;
+        float top = -INFINITY, lt = 0;
         float4_t ot = {0, 0, 0, 0};
-        for (int p = 0; p < rt.parts; ++p) {
-            const int64_t slot = slot0 + (int64_t)p * kRowTile;
-            const float *q = g.part_sums + slot * 2;
-            if (q[1] != 0) {
-                const float f = __builtin_amdgcn_exp2f(q[0] - top);
-                lt = fmaf(f, q[1], lt);
-                const float4_t v = *reinterpret_cast<const float4_t *>(g.part + slot * D + d);
+        // Four parts at a time; one past the last counts for nothing.
+        for (int p0 = 0; p0 < parts; p0 += 4) {
+            float2 q[4];
+            float4_t v[4];
+            float most = top;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) ot[i] = fmaf(f, v[i], ot[i]);
+            for (int i = 0; i < 4; ++i) {
+                const int64_t p = (int64_t)(p0 + i < parts ? p0 + i : 0) * kRowTile;
+                q[i] = sums[p];
+                v[i] = *reinterpret_cast<const float4_t *>(part + p * D);
+                if (p0 + i >= parts) q[i].y = 0;
+                if (q[i].y != 0) most = fmaxf(most, q[i].x);
+            }
+            const float fade = top == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(top - most);
+            if (top != -INFINITY) {
+                lt *= fade;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) ot[e] *= fade;
+            }
+            top = most;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (q[i].y == 0) continue;
+                const float f = __builtin_amdgcn_exp2f(q[i].x - top);
+                lt = fmaf(f, q[i].y, lt);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) ot[e] = fmaf(f, v[i][e], ot[e]);
             }
         }
-        const int64_t t = rt.s.first + r / g.G, hq = (int64_t)h * g.G + r % g.G;
+        const int64_t t = first + r / g.G, hq = (int64_t)h * g.G + r % g.G;
         float4_t v;
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i] = lt == 0 ? 0.0f : ot[i] / lt;
@@ -1358,7 +1393,8 @@ static int split_limit(int64_t D) { return D <= 128 ? 64 : 32; }
 struct AttendPlan {
     int64_t split_rows;  // the most rows of a sequence in the split kernel
     int waves;           // its waves
-    bool tiles;          // whether the tile kernel runs
+    bool split, tiles;   // whether the split kernel runs, and the tile kernel
+    int limit;           // the most rows of a sequence that are the split kernel's
     int64_t row_tiles;   // its tiles of rows at most
     int parts;           // workgroups the keys of one are dealt to
     size_t floats;         // workspace
@@ -1374,12 +1410,14 @@ static AttendPlan attend_plan(int64_t T, int64_t q_heads, int64_t heads, int64_t
     const int64_t G = q_heads / heads, limit = split_limit(D);
     const int64_t q = max_q < T ? max_q : T;
     p.tiles = q * G > limit;
+    p.split = !p.tiles || B > 1;  // (one sequence that may be long: the tile kernel takes it as it comes)
+    p.limit = p.split ? (int)limit : 0;
     p.split_rows = p.tiles ? limit : q * G;
     p.waves = split_waves((int)(D / 64), p.split_rows);
-    p.floats = (size_t)(2 * p.waves) * p.split_rows * (D + 2) + (size_t)(B * heads) * (sizeof(Pieces) / sizeof(float));
+    if (p.split) p.floats = (size_t)(2 * p.waves) * p.split_rows * (D + 2) + (size_t)(B * heads) * (sizeof(Pieces) / sizeof(float));
     if (p.tiles) {
-        // Sequences that have more rows than the limit, and their tiles.
-        const int64_t most = T * G / (limit + 1);
+        // Sequences of more rows than the limit, and their tiles.
+        const int64_t most = T * G / (p.limit + 1);
         p.row_tiles = T * G / kRowTile + (B < most ? B : most);
         // Parts: as few rounds of the card's 256 compute units for a tile of
         // rows as possible, a part costing 4 in 100 for the joining.
@@ -1392,7 +1430,8 @@ static AttendPlan attend_plan(int64_t T, int64_t q_heads, int64_t heads, int64_t
                 p.parts = parts;
             }
         }
-        const size_t f = p.parts == 1 ? 0 : (size_t)n * p.parts * kRowTile * (D + 2);
+        const size_t f = (size_t)p.row_tiles * (sizeof(TileRows) / sizeof(float)) +
+                         (p.parts == 1 ? 0 : (size_t)n * p.parts * kRowTile * (D + 2));
         if (f > p.floats) p.floats = f;
     }
     return p;
@@ -1423,34 +1462,43 @@ template <int ND>
 static hipError_t launch_attend(AttendArgs &g, const AttendPlan &p, float *workspace, hipStream_t stream) {
     const CacheAttend &a = g.a;
     void *args[] = {&g};
-    g.max_rows = (int)p.split_rows;
-    g.part = workspace;
-    g.part_sums = g.part + (size_t)(2 * p.waves) * p.split_rows * a.cache.D;
-    g.pieces = reinterpret_cast<Pieces *>(g.part_sums + (size_t)(2 * p.waves) * p.split_rows * 2);
-    g.waves = p.waves;
-    hipError_t e;
-    int64_t most = a.table_pages * a.cache.page;
-    if (a.window > 0 && a.window + a.max_q < most) most = a.window + a.max_q;
-    if (direct(most, a.B * a.cache.heads)) {
-        e = hipLaunchKernel(split_kernel<ND, true>(p.split_rows), dim3((unsigned)(a.B * a.cache.heads)), dim3(kSplitThreads), args, 0,
-                            stream);
-    } else {
-        e = hipLaunchKernel(split_kernel<ND, false>(p.split_rows), dim3((unsigned)(p.waves / kSplitWaves)), dim3(kSplitThreads), args,
-                            0, stream);
-        if (e != hipSuccess) return e;
-        e = hipLaunchKernel(reinterpret_cast<const void *>(&attend_join_kernel),
-                            dim3((unsigned)(a.B * a.cache.heads), (unsigned)p.split_rows, ND), dim3(256), args, 0, stream);
+    hipError_t e = hipSuccess;
+    if (p.split) {
+        g.max_rows = (int)p.split_rows;
+        g.part = workspace;
+        g.part_sums = g.part + (size_t)(2 * p.waves) * p.split_rows * a.cache.D;
+        g.pieces = reinterpret_cast<Pieces *>(g.part_sums + (size_t)(2 * p.waves) * p.split_rows * 2);
+        g.waves = p.waves;
+        int64_t most = a.table_pages * a.cache.page;
+        if (a.window > 0 && a.window + a.max_q < most) most = a.window + a.max_q;
+        if (direct(most, a.B * a.cache.heads)) {
+            e = hipLaunchKernel(split_kernel<ND, true>(p.split_rows), dim3((unsigned)(a.B * a.cache.heads)), dim3(kSplitThreads), args,
+                                0, stream);
+        } else {
+            e = hipLaunchKernel(split_kernel<ND, false>(p.split_rows), dim3((unsigned)(p.waves / kSplitWaves)), dim3(kSplitThreads),
+                                args, 0, stream);
+            if (e != hipSuccess) return e;
+            e = hipLaunchKernel(reinterpret_cast<const void *>(&attend_join_kernel),
+                                dim3((unsigned)(a.B * a.cache.heads), (unsigned)p.split_rows, ND), dim3(256), args, 0, stream);
+        }
     }
     if (e != hipSuccess || !p.tiles) return e;
     g.row_tiles = p.row_tiles;
     g.parts = p.parts;
+    // Parts in proportion to the keys, the longest that the table holds in all.
+    const int64_t longest = (a.table_pages * a.cache.page + kKeyTile - 1) / kKeyTile;
+    g.part_tiles = (int)((longest + p.parts - 1) / p.parts);
+    if (g.part_tiles < kMinKeyTiles) g.part_tiles = kMinKeyTiles;
     const int64_t n = p.row_tiles * a.cache.heads;
+    g.tile_rows = reinterpret_cast<TileRows *>(workspace);
+    g.part = workspace + (size_t)p.row_tiles * (sizeof(TileRows) / sizeof(float));
     g.part_sums = g.part + (size_t)n * p.parts * kRowTile * a.cache.D;
     e = hipLaunchKernel(reinterpret_cast<const void *>(&attend_tile_kernel<ND, ND <= 2 ? 2 : 1>), dim3((unsigned)(n * p.parts)),
                         dim3(kTileThreads), args, 0, stream);
     if (e != hipSuccess || p.parts == 1) return e;
-    return hipLaunchKernel(reinterpret_cast<const void *>(&attend_tile_join_kernel<ND>), dim3((unsigned)n, kRowTile / 16), dim3(256),
-                           args, 0, stream);
+    constexpr int kJoinRows = 4 * (256 / (16 * ND));
+    return hipLaunchKernel(reinterpret_cast<const void *>(&attend_tile_join_kernel<ND>),
+                           dim3((unsigned)n, (kRowTile + kJoinRows - 1) / kJoinRows), dim3(256), args, 0, stream);
 }
 
 hipError_t launch_cache_attend(const CacheAttend &a, void *workspace, hipStream_t stream) {
@@ -1460,8 +1508,8 @@ hipError_t launch_cache_attend(const CacheAttend &a, void *workspace, hipStream_
     g.page_shift = __builtin_ctzll((unsigned long long)a.cache.page);
     g.G = (int)(a.q_heads / a.cache.heads);
     g.inv_G = (65536 + g.G - 1) / g.G;
-    g.limit = split_limit(a.cache.D);
     const AttendPlan p = attend_plan(a.T, a.q_heads, a.cache.heads, a.cache.D, a.B, a.max_q);
+    g.limit = p.limit;
     float *ws = static_cast<float *>(workspace);
     switch (a.cache.D / 64) {
         case 1: return launch_attend<1>(g, p, ws, stream);

@@ -214,3 +214,219 @@ def test_attend(env, i, mode):
             dtype="float32" if mode == "window" else "bfloat16")
     if mode == "causal" and all(n == 1 for n in new):
         b.check(env, "tokens", tokens=True, scale=0.37)
+
+
+def test_empty_sequences_and_tokens_of_none(env):
+    """Sequences without keys or tokens, tokens before the first and behind the
+    last sequence, tokens past max_q: zeros and -infinity where a token sees
+    nothing, what was there where it belongs to none."""
+    torch, q4, dev = env
+    for G, D in ((2, 64), (40, 128)):
+        b = Batch(env, [0, 40, 3, 0, 90], [3, 4, 9, 0, 6], 2, G, D, 16, 7)
+        T = b.q.shape[0]
+        offsets = torch.tensor([2, 3, 7, 16, 16, T - 1], dtype=torch.int32, device=dev)
+        for dtype in (torch.bfloat16, torch.float32):
+            out = torch.full((T, 2 * G, D), 7.0, dtype=dtype, device=dev)
+            lse = torch.full((T, 2 * G), 5.0, device=dev)
+            q4.q4_cache_attend(*b.dev, q_offsets=offsets, max_q=8, out=out, lse=lse)
+            o, bound, l, lb, touched = ref.attend(b.q.astype(np.float64), b.planes, b.table, b.lens, offsets.cpu().numpy(),
+                                                  out_bf16=dtype == torch.bfloat16)
+            touched[7 + 8] = False          # the ninth token of its sequence
+            kept = torch.from_numpy(~touched).to(dev)
+            assert (out[kept] == 7).all() and (lse[kept] == 5).all() and int(kept.sum()) == 4
+            at = np.flatnonzero(touched)
+            within(out[at], o[at], bound[at], "out")
+            within(lse[at], l[at], lb[at], "lse")
+            empty = np.isinf(l[at, 0])
+            assert empty.sum() >= 7 and (out[at][empty] == 0).all()
+
+
+def test_pages_of_none_are_hidden(env):
+    torch, q4, dev = env
+    for new in ([1, 1, 1], [3, 1, 2], [70, 1, 40]):
+        b = Batch(env, [100, 77, 200], new, 2, 4, 128, 16, 11)
+        rng = np.random.default_rng(3)
+        table = b.table.copy()
+        for row in table:
+            row[rng.integers(0, 4, 2)] = rng.choice([-1, 1 << 30, -2 ** 31, len(b.planes["k_codes"])], 2)
+        b.table = table
+        b.dev = b.dev[:2] + (torch.from_numpy(table).to(dev), b.dev[3])
+        b.check(env, f"hidden {new}")
+        b.check(env, f"hidden {new}", causal=False)
+    # A sequence all of whose pages are hidden.
+    b = Batch(env, [40, 700], [2, 1], 1, 2, 64, 16, 12)
+    b.table[:] = -1
+    b.dev = b.dev[:2] + (torch.from_numpy(b.table).to(dev), b.dev[3])
+    out, lse = b.check(env, "all hidden")
+    assert (out == 0).all() and torch.isinf(lse).all()
+
+
+def _rows_of(b, seq, keys):
+    page = b.planes["k_codes"].shape[2]
+    return b.table[seq, np.asarray(keys) // page], np.asarray(keys) % page
+
+
+@pytest.mark.parametrize("new", [[1, 1], [4, 1], [80, 1], [60, 30]])
+@pytest.mark.parametrize("slack", [1, 40])
+def test_what_a_token_does_not_see_does_not_reach_it(env, new, slack):
+    """NaN, infinities and the largest scales in keys behind a token, before its
+    window, behind the last key and in the slots of other sequences."""
+    torch, q4, dev = env
+    heads, G, D, page = 2, 4, 128, 16
+    b = Batch(env, [170, 99], new, heads, G, D, page, 21, slack=slack)
+    planes = {n: p.copy() for n, p in b.planes.items()}
+    used = set()
+    for s in range(2):
+        ids, at = _rows_of(b, s, np.arange(b.lens[s]))
+        used |= set(zip(ids.tolist(), at.tolist()))
+    for p in range(planes["k_codes"].shape[0]):
+        for i in range(page):
+            if (p, i) not in used:
+                for n in PLANES:
+                    planes[n][p, :, i] = 255 if "codes" in n else np.nan
+    # The clean results, then bad keys that the window or the causal mask hides.
+    window = 50
+    clean, lse0 = b.check(env, "clean", window=window)
+    lowest = [int(b.lens[s]) - new[s] - window for s in range(2)]
+    bad = {0: [k for k in (0, 5, lowest[0]) if 0 <= k <= lowest[0]], 1: [k for k in (1, lowest[1]) if 0 <= k <= lowest[1]]}
+    for s, keys in bad.items():
+        for k, v in zip(keys, (np.nan, np.inf, 65504)):
+            ids, at = _rows_of(b, s, [k])
+            for n in ("k_scales", "v_scales"):
+                planes[n][ids[0], :, at[0]] = v
+    b.dev = (b.dev[0], to_cache(env, planes)) + b.dev[2:]
+    out, lse = q4.q4_cache_attend(*b.dev, q_offsets=b.offsets_dev, max_q=b.max_q, window=window, return_lse=True)
+    assert torch.equal(out, clean) and torch.equal(lse, lse0)
+
+
+@pytest.mark.parametrize("new", [[1, 1], [5, 1], [80, 1]])
+@pytest.mark.parametrize("side", ["k", "v"])
+def test_not_finite_values_reach_the_tokens_that_see_them(env, new, side):
+    """A NaN scale in one block of one key: of a value, the outputs of that block
+    in the tokens and heads that see it are NaN; of a key, all of them; the
+    others keep their bits."""
+    torch, q4, dev = env
+    heads, G, D, page = 2, 4, 128, 16
+    b = Batch(env, [170, 99], new, heads, G, D, page, 31)
+    clean, _ = b.check(env, "clean")
+    for bits in (0x7E00, 0x7C00):
+        planes = {n: p.copy() for n, p in b.planes.items()}
+        key = 170 - max(1, new[0] // 2)       # about half of the tokens see it
+        ids, at = _rows_of(b, 0, [key])
+        planes[side + "_scales"].view(np.uint16)[ids[0], 1, at[0], 1] = bits
+        planes[side + "_codes"][ids[0], 1, at[0]] = 0x9C
+        planes[side + "_zeros"][ids[0], 1, at[0]] = 0
+        cache = to_cache(env, planes)
+        out = q4.q4_cache_attend(b.dev[0], cache, *b.dev[2:], q_offsets=b.offsets_dev, max_q=b.max_q).float()
+        sees = np.zeros(b.q.shape[0], bool)
+        sees[:new[0]] = 170 - new[0] + np.arange(new[0]) >= key
+        assert sees.any()
+        got = out.cpu().numpy()
+        if bits == 0x7E00 or side == "v":
+            part = got[sees][:, G:, 64:] if side == "v" else got[sees][:, G:]
+            assert np.isnan(part).all()
+        keep = np.ones(got.shape, bool)
+        keep[np.ix_(sees, range(G, 2 * G), range(64, 128) if side == "v" else range(128))] = False
+        if new[0] == 1 or side == "k":
+            # (The other block of that key's value is what it was: only codes changed.)
+            pass
+        if side == "v":
+            keep[np.ix_(sees, range(G, 2 * G))] = False
+        assert np.array_equal(got[keep], clean.float().cpu().numpy()[keep])
+
+
+def test_queries_that_are_not_finite_stay_with_their_rows(env):
+    torch, q4, dev = env
+    for new in ([1, 2], [40, 30]):
+        b = Batch(env, [80, 60], new, 2, 4, 64, 16, 41)
+        clean, _ = b.check(env, "clean")
+        q = b.dev[0].clone()
+        q[1, 3, 7] = float("nan")
+        q[0, 5, 60] = float("inf")
+        out = q4.q4_cache_attend(q, *b.dev[1:], q_offsets=b.offsets_dev, max_q=b.max_q)
+        assert torch.isnan(out[1, 3]).all() and torch.isnan(out[0, 5]).all()
+        same = torch.ones(out.shape[:2], dtype=torch.bool, device=dev)
+        same[1, 3] = same[0, 5] = False
+        assert torch.equal(out[same], clean[same])
+        # A row of zeros weighs all its keys alike; the largest and smallest queries.
+        q = b.dev[0].clone()
+        q[0, 0] = 0
+        q[0, 1] *= 1e-30
+        q[1, 2] *= 2e4
+        b.q = q.float().cpu().numpy()
+        b.dev = (q,) + b.dev[1:]
+        b.check(env, "zero, tiny and large queries")
+
+
+@pytest.mark.parametrize("new", [[1, 1, 1], [64, 1, 40]])
+def test_scales_from_tiny_to_huge(env, new):
+    """Scales that grow along the keys (the running exponents move), subnormal
+    ones, zeros, and values near the end of fp16."""
+    torch, q4, dev = env
+    b = Batch(env, [300, 130, 64], new, 2, 2, 128, 16, 51)
+    rng = np.random.default_rng(8)
+    for s, (lo, hi) in enumerate(((-22, 3), (3, -20), (-24, -24))):
+        n = int(b.lens[s])
+        ids, at = _rows_of(b, s, np.arange(n))
+        e = np.linspace(lo, hi, n)[:, None, None] + rng.integers(-1, 2, (n, 2, 2))
+        b.planes["v_scales"][ids, :, at] = (2.0 ** np.clip(e, -24, 15) * rng.uniform(1, 1.9, e.shape)).astype(np.float16)
+        b.planes["k_scales"][ids, :, at] = (2.0 ** np.clip(-np.abs(e) / 2, -24, 0)).astype(np.float16)
+    b.planes["v_scales"][b.table[0, 0], 0, 3] = 0
+    b.dev = (b.dev[0], to_cache(env, b.planes)) + b.dev[2:]
+    b.check(env, "scales", dtype="float32")
+    ids, at = _rows_of(b, 0, np.arange(290, 300))
+    b.planes["v_scales"][ids, :, at] = 4300.0      # times up to 15: past 64000
+    b.dev = (b.dev[0], to_cache(env, b.planes)) + b.dev[2:]
+    b.check(env, "large values", dtype="float32")
+
+
+def test_one_page_for_many_and_the_same_page_twice(env):
+    """A shared prefix: sequences whose tables name the same pages, one page in
+    several places of a table."""
+    torch, q4, dev = env
+    b = Batch(env, [200, 150, 90], [1, 40, 3], 2, 3, 64, 16, 61)
+    b.table[1, :5] = b.table[0, :5]
+    b.table[2, :5] = b.table[0, 2]
+    b.dev = b.dev[:2] + (torch.from_numpy(b.table).to(dev), b.dev[3])
+    b.check(env, "shared pages")
+
+
+def test_long_context_and_many_sequences(env):
+    """More tiles than waves, more sequences than a workgroup has threads."""
+    torch, q4, dev = env
+    rng = np.random.default_rng(71)
+    lens = rng.integers(0, 40, 700)
+    lens[::97] = 400
+    b = Batch(env, lens, rng.integers(0, 3, 700), 1, 2, 64, 16, 72, slack=120)
+    b.check(env, "700 sequences")
+    b = Batch(env, [9000, 5, 2111], [1, 1, 1], 3, 3, 64, 32, 73, sharp=2.0)
+    b.check(env, "long")
+    b = Batch(env, [2500, 400], [150, 90], 1, 4, 64, 32, 74)
+    b.check(env, "parts", dtype="float32")
+
+
+def test_strided_queries_and_given_outputs(env):
+    torch, q4, dev = env
+    b = Batch(env, [50, 70], [2, 40], 2, 4, 64, 16, 81)
+    T = b.q.shape[0]
+    wide = torch.full((T, 12, 64), float("nan"), dtype=torch.bfloat16, device=dev)
+    wide[:, 2:10] = b.dev[0]
+    first, _ = b.check(env, "dense")
+    out = torch.empty((T, 8, 64), dtype=torch.bfloat16, device=dev)
+    need = q4.q4_cache_attend_ws_bytes(T, 8, 2, 64, 2, b.max_q)
+    ws = torch.full((need,), 0xFF, dtype=torch.uint8, device=dev)
+    got = q4.q4_cache_attend(wide[:, 2:10], *b.dev[1:], q_offsets=b.offsets_dev, max_q=b.max_q, out=out, workspace=ws)
+    assert got is out and torch.equal(out, first)
+    with pytest.raises(q4.Q4Error):
+        q4.q4_cache_attend(wide[:, 2:10], *b.dev[1:], q_offsets=b.offsets_dev, max_q=b.max_q, out=out, workspace=ws[:-16])
+
+
+def test_the_same_bits_on_every_call(env):
+    torch, q4, dev = env
+    for new, lens in (([1, 1], [5000, 300]), ([200, 60], [3000, 60])):
+        b = Batch(env, lens, new, 2, 4, 128, 16, 91)
+        run = lambda: q4.q4_cache_attend(*b.dev, q_offsets=b.offsets_dev, max_q=b.max_q, out_dtype=torch.float32, return_lse=True)  # noqa: E731
+        o, l = run()
+        for _ in range(3):
+            o2, l2 = run()
+            assert torch.equal(o, o2) and torch.equal(l, l2)
