@@ -70,9 +70,10 @@ typedef struct {
  *   q: NULL, or the queries [T][q_heads][D] of in_type with q_stride as k;
  *     rotated like the keys into q_out, bf16 bits [T][q_heads][D], 16-byte
  *     aligned (every token's, whatever its slot).
- * Angles, rotations and the decisions of the packing are in 64 bits: the
- * packed row is that of the exact formula (but for decisions that 2^-50 of
- * the values would turn), q_out is within half a bf16 step (and 2^-24) of it.
+ * Angles, the keys' rotation and the decisions of the packing are in 64 bits:
+ * the packed row is that of the exact formula (but for decisions that 2^-50 of
+ * the values would turn).  Queries are turned in fp32: q_out is within half a
+ * bf16 step of a value that is within 2^-22 f (|x1| + |x2|) of the exact one.
  * A block of 64 values that holds a NaN or an infinity, or whose scale
  * rounds to an infinity, is written as NaN (scale NaN, codes and zero 0).
  * No output may overlap an input or another output.  T == 0 is a no-op.

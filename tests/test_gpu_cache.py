@@ -97,7 +97,16 @@ def test_append_is_the_formula_bit_for_bit(env, T, heads, qh, D, page, rot, inte
         assert same.all(), (n, int((~same).sum()))
     if qh:
         w = ref.rotate(x[:, :qh], pos, freq, inter, 1.25)
-        within(q, w, (2.0 ** -8 + 2.0 ** -24) * np.abs(w) + 1e-37, "rotated q")
+        # Two rounded products and a sum of fp32 factors, then half a bf16 step.
+        pairs = np.abs(ref.rotate(np.abs(x[:, :qh]), 0 * pos, freq, inter, 1.0)).astype(np.float64)
+        half = rot // 2
+        if inter:
+            pairs[..., 0:rot:2] = pairs[..., 1:rot:2] = pairs[..., 0:rot:2] + pairs[..., 1:rot:2]
+        else:
+            pairs[..., :half] = pairs[..., half:rot] = pairs[..., :half] + pairs[..., half:rot]
+        pairs[..., rot:] = 0
+        e = 2.0 ** -22 * 1.25 * pairs
+        within(q, w, 2.0 ** -8 * (np.abs(w) + e) + e + 1e-37, "rotated q")
     else:
         assert q is None
 
@@ -128,7 +137,8 @@ def test_append_blocks_that_are_not_finite(env):
 
 @pytest.mark.parametrize("n,heads,D,page,dtype", [(1, 1, 64, 16, "bfloat16"), (37, 12, 64, 32, "float32"),
                                                   (100, 8, 128, 64, "bfloat16"), (9, 3, 192, 16, "float32"),
-                                                  (300, 2, 256, 128, "bfloat16")])
+                                                  (300, 2, 256, 128, "bfloat16"), (4099, 9, 64, 16, "bfloat16"),
+                                                  (5000, 8, 192, 32, "float32")])
 def test_read_is_the_rows(env, n, heads, D, page, dtype):
     torch, q4, dev = env
     rng = np.random.default_rng(n)
