@@ -1397,13 +1397,37 @@ struct AttendPlan {
     int limit;           // the most rows of a sequence that are the split kernel's
     int64_t row_tiles;   // its tiles of rows at most
     int parts;           // workgroups the keys of one are dealt to
-    size_t floats;         // workspace
+    int prompt_parts;    // the same where there is no long prefix
+    size_t floats;       // workspace
 };
 
 // Tiles of 16 rows that the split kernel's accumulators are made for, and its
 // waves: those that 256 compute units hold at once.
 static int split_tiles(int nd, int64_t rows) { return rows <= 16 ? 1 : nd <= 2 && rows > 32 ? 4 : 2; }
 static int split_waves(int nd, int64_t rows) { return 256 * kSplitWaves * split_occupancy(nd, split_tiles(nd, rows)); }
+
+// Workgroups that the keys of each of n tiles of rows are dealt to, each one
+// more costing 4 in 100 for the joining.  Behind a long prefix all tiles see
+// about as many keys: as few rounds of the 256 compute units for each key as
+// possible (512 tokens behind 32488 and 8 key heads: 3 parts 405 us, 5 parts
+// 480; 64 tokens: 16 parts 103 us, 8 parts 163).  In a prompt they see half as
+// many as the last one on average: the parts of that one should take no longer
+// than the card does with all (4096 tokens and 2 key heads: 3 parts 150 us, 2
+// parts 138).
+static int key_parts(int64_t n, bool prompt) {
+    int best_parts = 1;
+    double best = 0;
+    for (int parts = 1; parts <= 32 && (parts == 1 || n * parts <= 1024); ++parts) {
+        double cost = (double)((n * parts + 255) / 256) / parts;
+        if (prompt) cost = 1.0 / parts > n / 512.0 ? 1.0 / parts : n / 512.0;
+        cost *= 1 + 0.04 * (parts - 1);
+        if (parts == 1 || cost < best) {
+            best = cost;
+            best_parts = parts;
+        }
+    }
+    return best_parts;
+}
 
 static AttendPlan attend_plan(int64_t T, int64_t q_heads, int64_t heads, int64_t D, int64_t B, int64_t max_q) {
     AttendPlan p = {};
@@ -1418,20 +1442,13 @@ static AttendPlan attend_plan(int64_t T, int64_t q_heads, int64_t heads, int64_t
     if (p.tiles) {
         // Sequences of more rows than the limit, and their tiles.
         const int64_t most = T * G / (p.limit + 1);
-        p.row_tiles = T * G / kRowTile + (B < most ? B : most);
-        // Parts: as few rounds of the card's 256 compute units for a tile of
-        // rows as possible, a part costing 4 in 100 for the joining.
+        p.row_tiles = (T * G + (B < most ? B : most) * (kRowTile - 1)) / kRowTile;
         const int64_t n = p.row_tiles * heads;
-        double best = 0;
-        for (int parts = 1; parts <= 8 && (parts == 1 || n * parts <= 1024); ++parts) {
-            const double cost = (double)((n * parts + 255) / 256) / parts * (1 + 0.04 * (parts - 1));
-            if (parts == 1 || cost < best) {
-                best = cost;
-                p.parts = parts;
-            }
-        }
+        p.parts = key_parts(n, false);
+        p.prompt_parts = key_parts(n, true);
+        const int64_t parts = p.parts > p.prompt_parts ? p.parts : p.prompt_parts;
         const size_t f = (size_t)p.row_tiles * (sizeof(TileRows) / sizeof(float)) +
-                         (p.parts == 1 ? 0 : (size_t)n * p.parts * kRowTile * (D + 2));
+                         (parts == 1 ? 0 : (size_t)(n * parts) * kRowTile * (D + 2));
         if (f > p.floats) p.floats = f;
     }
     return p;
@@ -1484,18 +1501,20 @@ static hipError_t launch_attend(AttendArgs &g, const AttendPlan &p, float *works
     }
     if (e != hipSuccess || !p.tiles) return e;
     g.row_tiles = p.row_tiles;
-    g.parts = p.parts;
+    const int64_t keys = a.table_pages * a.cache.page;
+    const int parts = 2 * a.max_q >= keys && a.causal ? p.prompt_parts : p.parts;
+    g.parts = parts;
     // Parts in proportion to the keys, the longest that the table holds in all.
-    const int64_t longest = (a.table_pages * a.cache.page + kKeyTile - 1) / kKeyTile;
-    g.part_tiles = (int)((longest + p.parts - 1) / p.parts);
+    const int64_t longest = (keys + kKeyTile - 1) / kKeyTile;
+    g.part_tiles = (int)((longest + parts - 1) / parts);
     if (g.part_tiles < kMinKeyTiles) g.part_tiles = kMinKeyTiles;
     const int64_t n = p.row_tiles * a.cache.heads;
     g.tile_rows = reinterpret_cast<TileRows *>(workspace);
     g.part = workspace + (size_t)p.row_tiles * (sizeof(TileRows) / sizeof(float));
-    g.part_sums = g.part + (size_t)n * p.parts * kRowTile * a.cache.D;
-    e = hipLaunchKernel(reinterpret_cast<const void *>(&attend_tile_kernel<ND, ND <= 2 ? 2 : 1>), dim3((unsigned)(n * p.parts)),
+    g.part_sums = g.part + (size_t)n * parts * kRowTile * a.cache.D;
+    e = hipLaunchKernel(reinterpret_cast<const void *>(&attend_tile_kernel<ND, ND <= 2 ? 2 : 1>), dim3((unsigned)(n * parts)),
                         dim3(kTileThreads), args, 0, stream);
-    if (e != hipSuccess || p.parts == 1) return e;
+    if (e != hipSuccess || parts == 1) return e;
     constexpr int kJoinRows = 4 * (256 / (16 * ND));
     return hipLaunchKernel(reinterpret_cast<const void *>(&attend_tile_join_kernel<ND>),
                            dim3((unsigned)n, (kRowTile + kJoinRows - 1) / kJoinRows), dim3(256), args, 0, stream);
