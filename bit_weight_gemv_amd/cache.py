@@ -88,12 +88,10 @@ def _tokens(t, name, D, dtype, device):
     if t.device != device:
         raise ValueError(f"{name} must be on {device}, got {t.device}")
     T, heads, _ = t.shape
-    if T == 0:
-        return heads * D
     stride, head, one = t.stride()
     if one != 1 or (heads > 1 and head != D):
         raise ValueError(f"{name}: a token's heads must be contiguous")
-    return stride if T > 1 else max(stride, heads * D)
+    return stride if T > 1 else heads * D
 
 
 def q4_cache_append(cache, k, v, slots, positions=None, inv_freq=None, interleaved=False, amplitude=1.0, q=None, q_out=None,

@@ -30,16 +30,6 @@ struct Pieces {
     int first, last;  // the waves of the first and the last piece
 };  // A wave's slots: 2 w for a piece that goes on, 2 w + 1 for one that begins.
 
-typedef __attribute__((address_space(4))) int32_t scalar_int;  // read-only: uniform loads are scalar
-
-// What a workgroup of the split kernel leaves for the joining: the rows whose
-// last piece it holds.
-struct End {
-    int first;   // the workgroup of the first piece; -1: nothing to join
-    int second;  // whether that is its second slot
-    int token, rows, h;
-};
-
 struct AttendArgs {
     CacheAttend a;
     int page_shift;
@@ -53,8 +43,8 @@ struct AttendArgs {
     int waves;          // its waves at most
     TileRows *tile_rows;  // tile kernel: [tile of rows]
     int64_t row_tiles;  // tile kernel: tiles of rows at most
-    int parts;          // workgroups the keys of one are dealt to at most
-    int part_tiles;     // tiles of kKeyTile keys a part should have
+    int parts;          // workgroups the keys of one are dealt to at most,
+    int prefix_parts, prompt_parts;  // behind a long prefix, and without one
 };
 
 // A sequence as a kernel sees it, every value within its bounds.
@@ -136,8 +126,9 @@ constexpr int kSplitWaves = 4;
 constexpr int kSplitThreads = 64 * kSplitWaves;
 constexpr int kMinTiles = 2;       // tiles a wave should have at least, beside kBegin
 // What beginning a piece costs a wave, in tiles: its tables, queries and first
-// codes arrive one after the other (5 us where a further tile takes 0.85; 6 units instead of 3 took 3 us more where waves have
-// few tiles, and nothing less elsewhere).
+// codes arrive one after the other (5 us where a further tile takes 0.85; 6
+// units instead of 3 took 3 us more where waves have few tiles, and nothing
+// less elsewhere).
 constexpr int kBegin = 3;
 constexpr int kHeadroom = 6;       // powers of two that weights may pass 1 by
 
@@ -197,7 +188,9 @@ __device__ __forceinline__ int64_t scan_sequences(int64_t B, int64_t *sums, Coun
         if ((tid & 63) == 63) sums[wave] = x;
         __syncthreads();
         int64_t off = before, all = 0;
-#pragma unroll
+        // (Unrolled, 8 waves' sums cost the tile kernel scalar registers, and one
+        // vector register to spill them: D = 256 413 us instead of 363.)
+#pragma unroll(THREADS > 256 ? 1 : THREADS / 64)
         for (int w = 0; w < THREADS / 64; ++w) {
             if (w < wave) off += sums[w];
             all += sums[w];
@@ -501,7 +494,7 @@ __global__ __launch_bounds__(kSplitThreads, split_occupancy(ND, NT)) void attend
             }
             const int pos = s.len - s.n + j;
             seen_to[x] = r < rows ? (a.causal ? pos : s.len - 1) : -1;
-            seen_from[x] = a.window > 0 ? pos - (int)(a.window < 0x7fffffff ? a.window : 0x7fffffff) + 1 : 0;
+            seen_from[x] = a.window > 0 ? pos - (int)a.window + 1 : 0;
         }
         // The first key that some row sees, and keys that all rows see: tiles
         // within need no mask.
@@ -889,14 +882,25 @@ __device__ __forceinline__ int row_tiles_of(const AttendArgs &g, const Sequence 
 // The index-th tile of rows; false past the last.
 template <int THREADS>
 __device__ __forceinline__ bool find_row_tile(const AttendArgs &g, int64_t index, int64_t *sums, int64_t *found,
-                                              RowTile &r) {
+                                              int *longest, RowTile &r) {
     const CacheAttend &a = g.a;
-    if (threadIdx.x == 0) found[0] = -1;
+    if (threadIdx.x == 0) {
+        found[0] = -1;
+        longest[0] = longest[1] = 0;
+    }
+    int most_keys = 0, most_before = 0;  // of the thread's sequences: keys that a tile of rows sees, and those before the new
     scan_sequences<THREADS>(
         a.B, sums,
         [&](int64_t b) {
             int64_t rows;
-            return (uint32_t)row_tiles_of(g, sequence_at(a, b), &rows);
+            const Sequence s = sequence_at(a, b);
+            const uint32_t t = (uint32_t)row_tiles_of(g, s, &rows);
+            if (t > 0) {
+                const int seen = a.window > 0 ? (int)a.window + kRowTile / g.G : s.len;
+                most_keys = max(most_keys, min(seen, s.len));
+                most_before = max(most_before, min(seen, s.len - s.n));
+            }
+            return t;
         },
         [&](int64_t b, int64_t before, int64_t t) {
             if (index >= before && index < before + t) {
@@ -904,6 +908,11 @@ __device__ __forceinline__ bool find_row_tile(const AttendArgs &g, int64_t index
                 found[1] = index - before;
             }
         });
+    if (g.parts > 1) {
+        if (most_keys > 0) atomicMax(longest, most_keys);
+        if (most_before > 0) atomicMax(longest + 1, most_before);
+        __syncthreads();
+    }
     r.b = uniform64(found[0]);
     if (r.b < 0) return false;
     r.s = sequence_at(a, r.b);
@@ -919,8 +928,20 @@ __device__ __forceinline__ bool find_row_tile(const AttendArgs &g, int64_t index
     r.low = lo > 0 ? (int)(lo < r.hi ? lo : r.hi) : 0;
     r.lo = r.low & ~(kKeyTile - 1);
     const int nt = (r.hi - r.lo + kKeyTile - 1) / kKeyTile;
-    const int most = (nt + g.part_tiles - 1) / g.part_tiles;
-    r.parts = most < g.parts ? (most < 1 ? 1 : most) : g.parts;
+    r.parts = 1;
+    if (g.parts > 1) {
+        // In proportion to the keys, the most that any tile of rows sees in all:
+        // by the lengths, since a table may be far wider (512 tokens behind
+        // 32488 in a table for 131072 397 us; by the table's width, which gives
+        // them one part, 1114).  Prompts in such a table pay for workgroups that
+        // find nothing to do (2048 tokens 100 us instead of 89).
+        const int keys = __builtin_amdgcn_readfirstlane(longest[0]), before = __builtin_amdgcn_readfirstlane(longest[1]);
+        const int parts = before <= keys / 2 ? g.prompt_parts : g.prefix_parts;
+        int each = (keys + kKeyTile * parts - 1) / (kKeyTile * parts);
+        each = each < kMinKeyTiles ? kMinKeyTiles : each;
+        const int most = (nt + each - 1) / each;
+        r.parts = most < parts ? (most < 1 ? 1 : most) : parts;
+    }
     return true;
 }
 
@@ -971,6 +992,7 @@ __global__ __launch_bounds__(kTileThreads, 1) void attend_tile_kernel(AttendArgs
     __shared__ __attribute__((aligned(16))) uint16_t sk[2][kKeys * D];
     __shared__ __attribute__((aligned(16))) uint16_t sv[2][kKeys * D];
     __shared__ int64_t sums[kTileWaves], found[2];
+    __shared__ int longest[2];
     __shared__ TileNews news[3];
     const CacheAttend &a = g.a;
     const int tid = (int)threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -984,7 +1006,7 @@ __global__ __launch_bounds__(kTileThreads, 1) void attend_tile_kernel(AttendArgs
     const int part = (int)(blockIdx.x / items), h = (int)(blockIdx.x % heads);
     const int64_t index = g.row_tiles - 1 - (blockIdx.x - part * items) / heads;
     RowTile rt;
-    const bool valid = find_row_tile<kTileThreads>(g, index, sums, found, rt);
+    const bool valid = find_row_tile<kTileThreads>(g, index, sums, found, longest, rt);
     if (part == 0 && h == 0 && tid == 0)
         g.tile_rows[index] = valid ? TileRows{rt.s.first, rt.row0, rt.rows, rt.parts} : TileRows{0, 0, 0, 0};
     if (!valid || part >= rt.parts) return;
@@ -1502,12 +1524,11 @@ static hipError_t launch_attend(AttendArgs &g, const AttendPlan &p, float *works
     if (e != hipSuccess || !p.tiles) return e;
     g.row_tiles = p.row_tiles;
     const int64_t keys = a.table_pages * a.cache.page;
-    const int parts = 2 * a.max_q >= keys && a.causal ? p.prompt_parts : p.parts;
+    // Whether there is a long prefix the lengths say, and sometimes the table.
+    g.prompt_parts = a.causal ? p.prompt_parts : p.parts;
+    g.prefix_parts = 2 * a.max_q >= keys ? g.prompt_parts : p.parts;
+    const int parts = g.prompt_parts > g.prefix_parts ? g.prompt_parts : g.prefix_parts;
     g.parts = parts;
-    // Parts in proportion to the keys, the longest that the table holds in all.
-    const int64_t longest = (keys + kKeyTile - 1) / kKeyTile;
-    g.part_tiles = (int)((longest + parts - 1) / parts);
-    if (g.part_tiles < kMinKeyTiles) g.part_tiles = kMinKeyTiles;
     const int64_t n = p.row_tiles * a.cache.heads;
     g.tile_rows = reinterpret_cast<TileRows *>(workspace);
     g.part = workspace + (size_t)p.row_tiles * (sizeof(TileRows) / sizeof(float));
@@ -1524,6 +1545,7 @@ hipError_t launch_cache_attend(const CacheAttend &a, void *workspace, hipStream_
     AttendArgs g = {};
     g.a = a;
     if (a.cache.pages == 0) g.a.table_pages = 0;  // no key can be seen
+    if (a.window > g.a.table_pages * a.cache.page) g.a.window = 0;  // it reaches past the first key everywhere
     g.page_shift = __builtin_ctzll((unsigned long long)a.cache.page);
     g.G = (int)(a.q_heads / a.cache.heads);
     g.inv_G = (65536 + g.G - 1) / g.G;

@@ -52,8 +52,8 @@ Range strided(const void *p, int64_t T, int64_t stride, int64_t width, uint64_t 
 
 bool attend_shape_ok(int64_t T, int64_t q_heads, int64_t heads, int64_t D, int64_t B, int64_t max_q) {
     return T >= 0 && T <= kMost && heads >= 1 && heads <= Q4_CACHE_MAX_HEADS && q_heads >= 1 &&
-           q_heads <= Q4_CACHE_MAX_HEADS && q_heads % heads == 0 && T * q_heads <= kMostRows && d_ok(D) && B >= 0 && B <= kMost && B * heads <= kMost && max_q >= 1 &&
-           max_q <= kMost;
+           q_heads <= Q4_CACHE_MAX_HEADS && q_heads % heads == 0 && T * q_heads <= kMostRows && d_ok(D) && B >= 0 &&
+           B <= kMost && B * heads <= kMost && max_q >= 1 && max_q <= kMost;
 }
 
 }  // namespace

@@ -56,8 +56,8 @@ typedef struct {
  * q4_cache_append -- for every token t < T with 0 <= slots[t] < pages * page:
  * the keys k[t] (rotated) and values v[t] of all heads, packed by the rule of
  * q4_pack_affine, written to the rows of that slot.  Another slot (-1 for
- * padding) is skipped.  The slots of one call are distinct; of tokens with
- * the same slot, each block of 64 values is that of one of them.
+ * padding) is skipped.  The slots of one call are distinct: what the rows of
+ * a slot given twice hold is unspecified (other rows are not affected).
  *   k, v: [T][heads][D] of in_type (Q4_OUT_F32 or Q4_OUT_BF16), 16-byte
  *     aligned; a token's heads are contiguous, tokens k_stride and v_stride
  *     elements apart (>= heads * D, a multiple of 16 bytes).
