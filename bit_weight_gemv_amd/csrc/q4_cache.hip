@@ -267,9 +267,12 @@ hipError_t launch_cache_append(const CacheAppend &a, hipStream_t stream) {
     g.lanes = (int)(a.cache.D / 8);
     g.tasks = (int)((2 * a.cache.heads + a.q_heads) * g.lanes);
     // A workgroup per token where the tokens fill the card, else one for
-    // every 256 lanes of work.
+    // every 256 lanes of work (which makes the sines again in each).  Appended
+    // and read back, 40 + 8 heads of 128: 256 tokens 9.3 us against 8.5 split,
+    // 512 tokens 10.6 against 11.7, 8191 tokens 59 against 102; 16 + 2 heads:
+    // 512 tokens 8.6 against 8.3, 1024 tokens 9.5 against 11.2.
     const int rounds = (g.tasks + kAppendThreads - 1) / kAppendThreads;
-    g.parts = a.T >= 1024 ? 1 : rounds;
+    g.parts = a.T * rounds >= 1536 ? 1 : rounds;
     void *args[] = {&g};
     return hipLaunchKernel(a.bf16 ? reinterpret_cast<const void *>(&cache_append_kernel<true>)
                                   : reinterpret_cast<const void *>(&cache_append_kernel<false>),
