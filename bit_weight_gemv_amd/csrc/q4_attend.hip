@@ -848,13 +848,13 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs g) {
 //
 // Bound by the matrix cores and the exponentials.  A workgroup of 8 waves takes
 // 256 rows of one key head (32 a wave) and walks the keys 64 at a time: they
-// are decoded once, by all waves, into LDS as fp16 (c - zero) scale 2^-E, one
-// buffer ahead of the one in use, so that a tile costs one barrier.  32 x 32 x
-// 16 products: S^T = K Q^T, whose result is the operand of O^T = V^T P^T as it
-// stands; V is turned by the transposing 16-bit LDS read.
-// 2^E is above every scale of the keys so far (of the values': the sums are
-// rescaled when it grows), so that a decoded value is rounded by 2^-11 of
-// itself and none passes fp16.  The sum of a row's weights is that of the fp32
+// are decoded once, by all waves, into LDS as fp16, one buffer ahead of the one
+// in use, so that a tile costs one barrier.  32 x 32 x 16 products: S^T = K Q^T,
+// whose result is the operand of O^T = V^T P^T as it stands; V is turned by the
+// transposing 16-bit LDS read.
+// They become (c - zero) scale 2^-E, rounded by 2^-11 of themselves; 2^E is
+// above every scale so far (of the values': the sums are rescaled when it
+// grows), so that none passes fp16.  The sum of a row's weights is that of the fp32
 // weights: with the sum of the rounded ones, one instruction for two of them,
 // lse was off by up to 2^-11.
 //
@@ -994,13 +994,21 @@ enum { kWild = 1, kHidden = 2 };  // some scale of a value is not finite; some p
 
 // KB: blocks of 32 keys a tile (with 192 and 256 dimensions one: the scores of
 // two would not stay in registers beside the sums).
-template <int ND, int KB>
+// EXACT: keys enter as c - zero and a score is multiplied behind each block of
+// 64 by its scale over that of the next, so that it has the precision of fp32.
+// For calls that ask for lse, which is fp32: from keys rounded to fp16 it was
+// off by 3e-5 of itself, and is by 6e-8.  out, of weights and values in fp16,
+// gains nothing that a bf16 shows, and EXACT costs (512 tokens behind 32488 472
+// us instead of 405, prompts of 8191 219 instead of 190, with D = 64 145
+// instead of 135, with 256 508 instead of 364).
+template <int ND, int KB, bool EXACT>
 __global__ __launch_bounds__(kTileThreads, 1) void attend_tile_kernel(AttendArgs g) {
     constexpr int D = ND * 64, kKeys = 32 * KB;
     constexpr int kUnits = kKeys * 2 * ND;           // pieces of 16 bytes of codes of a tile of keys
     constexpr int kLoads = (2 * kUnits + kTileThreads - 1) / kTileThreads;
     __shared__ __attribute__((aligned(16))) uint16_t sk[2][kKeys * D];
     __shared__ __attribute__((aligned(16))) uint16_t sv[2][kKeys * D];
+    __shared__ __attribute__((aligned(16))) float key_scales[2][EXACT ? ND * kKeys : 1];
     __shared__ int64_t sums[kTileWaves], found[2];
     __shared__ int longest[2];
     __shared__ TileNews news[3];
@@ -1081,6 +1089,7 @@ __global__ __launch_bounds__(kTileThreads, 1) void attend_tile_kernel(AttendArgs
     struct Raw {
         u32x4_t codes;
         uint32_t scale, zero;
+        uint32_t after;  // EXACT: the scale of a key's next block
         bool ok, hidden;
     };
     Raw raw[kLoads], coming[kLoads];  // of the tile to decode, and of the next
@@ -1111,6 +1120,7 @@ __global__ __launch_bounds__(kTileThreads, 1) void attend_tile_kernel(AttendArgs
             c.codes = *reinterpret_cast<const u32x4_t *>((value ? a.cache.v_codes : a.cache.k_codes) + row * (D / 2) + piece * 16);
             c.scale = (value ? a.cache.v_scales : a.cache.k_scales)[row * ND + piece / 2];
             c.zero = (value ? a.cache.v_zeros : a.cache.k_zeros)[row * ND + piece / 2];
+            if (EXACT && ND > 1) c.after = a.cache.k_scales[row * ND + (piece / 2 + 1 < ND ? piece / 2 + 1 : piece / 2)];
         }
     };
     auto take = [&] {
@@ -1125,7 +1135,7 @@ __global__ __launch_bounds__(kTileThreads, 1) void attend_tile_kernel(AttendArgs
             if (!is_piece(i)) break;
             const Raw &c = coming[i];
             const bool value = is_value(i);
-            const uint32_t bits = c.ok ? c.scale : 0;
+            const uint32_t bits = c.ok && (value || !EXACT) ? c.scale : 0;
             if (__any((int)bits > below(value ? ev : ek) || c.hidden)) {
                 const bool fin = bits < 0x7C00u;
                 const uint32_t top = wave_max_u32(fin ? bits : 0);
@@ -1148,8 +1158,14 @@ __global__ __launch_bounds__(kTileThreads, 1) void attend_tile_kernel(AttendArgs
             const bool value = is_value(i);
             const Raw &c0 = raw[i];
             uint32_t sb = c0.ok ? c0.scale : 0;
+            if (EXACT && !value) {
+                // A scale of 0 (codes of 0) as 2^-24: it divides the one before.
+                const float own = f16_bits_to_f32(sb > 0 ? sb : 1u), after = f16_bits_to_f32(c0.ok && c0.after > 0 ? c0.after : 1u);
+                if (!(piece & 1)) key_scales[buf][piece / 2 * kKeys + key] = piece / 2 + 1 < ND ? own * __builtin_amdgcn_rcpf(after) : own;
+                sb = sb > 0 ? 0x3C00u : 0u;
+            }
             if (value && sb >= 0x7C00u) sb = 0;  // (rows that see it are made NaN below)
-            const _Float16 sc = (_Float16)ldexpf(f16_bits_to_f32(sb), -(value ? ev : ek));
+            const _Float16 sc = (_Float16)ldexpf(f16_bits_to_f32(sb), -(value ? ev : EXACT ? 0 : ek));
             const _Float16 of = (_Float16)(-1024.0f - (c0.ok ? f16_bits_to_f32(c0.zero) : 0.0f));
             const half2_t s2 = {sc, sc}, o2 = {of, of};
             const uint32_t w[4] = {c0.codes.x, c0.codes.y, c0.codes.z, c0.codes.w};
@@ -1224,13 +1240,26 @@ __global__ __launch_bounds__(kTileThreads, 1) void attend_tile_kernel(AttendArgs
 #pragma unroll
                 for (int i = 0; i < 16; ++i) S[x][i] = 0;
 #pragma unroll
-            for (int d = 0; d < ND * 4; ++d)
+            for (int d = 0; d < ND * 4; ++d) {
 #pragma unroll
                 for (int x = 0; x < KB; ++x) {
                     const u32x4_t k = *reinterpret_cast<const u32x4_t *>(kb + (32 * x + col) * D + ((2 * d ^ ((d >> 1) & 3)) ^ half ^ key_turn(col)) * 8);
                     S[x] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(half8_t, k), qf[d], S[x], 0, 0, 0);
                 }
-            const float kap = ldexpf(kappa, ek);
+                if (EXACT && (d & 3) == 3) {
+                    // Behind a block its scale, over that of the next block.
+                    const float *ks = key_scales[tile & 1] + d / 4 * kKeys + 4 * half;
+#pragma unroll
+                    for (int x = 0; x < KB; ++x)
+#pragma unroll
+                        for (int g = 0; g < 4; ++g) {
+                            const float4_t sc = *reinterpret_cast<const float4_t *>(ks + 32 * x + 8 * g);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) S[x][4 * g + i] *= sc[i];
+                        }
+                }
+            }
+            const float kap = EXACT ? kappa : ldexpf(kappa, ek);
             if (key0 + kKeys - 1 > all_to || key0 < all_from || (wild & kHidden)) {
                 uint64_t shown = ~0ull;
                 if (wild & kHidden) shown = __ballot(page_at(key0 + lane) >= 0);
@@ -1543,8 +1572,10 @@ static hipError_t launch_attend(AttendArgs &g, const AttendPlan &p, float *works
     g.tile_rows = reinterpret_cast<TileRows *>(workspace);
     g.part = workspace + (size_t)p.row_tiles * (sizeof(TileRows) / sizeof(float));
     g.part_sums = g.part + (size_t)n * parts * kRowTile * a.cache.D;
-    e = hipLaunchKernel(reinterpret_cast<const void *>(&attend_tile_kernel<ND, ND <= 2 ? 2 : 1>), dim3((unsigned)(n * parts)),
-                        dim3(kTileThreads), args, 0, stream);
+    constexpr int KB = ND <= 2 ? 2 : 1;
+    e = hipLaunchKernel(a.lse ? reinterpret_cast<const void *>(&attend_tile_kernel<ND, KB, true>)
+                              : reinterpret_cast<const void *>(&attend_tile_kernel<ND, KB, false>),
+                        dim3((unsigned)(n * parts)), dim3(kTileThreads), args, 0, stream);
     if (e != hipSuccess || parts == 1) return e;
     constexpr int kJoinRows = 4 * (256 / (16 * ND));
     return hipLaunchKernel(reinterpret_cast<const void *>(&attend_tile_join_kernel<ND>),

@@ -106,7 +106,10 @@ int q4_cache_read(const q4_cache *cache, const int32_t *slots, int64_t n,
  * A token that sees no key, or only scores of -infinity, gets zeros and an
  * lse of -infinity.  Keys that a token does not see never reach its output,
  * whatever they hold; a NaN or an infinity that it sees does, as in the
- * formula.
+ * formula.  Weights, and in prompts decoded values, are rounded to fp16 (2^-11
+ * each); keys are exact where there are few tokens or lse is asked for, and
+ * rounded to fp16 otherwise, so that the bits of out may differ between calls
+ * with lse and without.  lse has the precision of fp32.
  *   q: bf16 bits [T][q_heads][D], 16-byte aligned, tokens q_stride elements
  *     apart (>= q_heads * D, a multiple of 8).  q_heads is a multiple of
  *     heads.

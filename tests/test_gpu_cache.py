@@ -183,14 +183,16 @@ class Batch:
 
     def check(self, env, what, causal=True, window=0, scale=None, dtype="bfloat16", tokens=False, **kw):
         torch, q4, dev = env
-        got, lse = q4.q4_cache_attend(*self.dev, q_offsets=None if tokens else self.offsets_dev,
-                                      max_q=None if tokens else self.max_q, causal=causal, window=window, scale=scale,
-                                      out_dtype=getattr(torch, dtype), return_lse=True, **kw)
+        kw = dict(q_offsets=None if tokens else self.offsets_dev, max_q=None if tokens else self.max_q, causal=causal,
+                  window=window, scale=scale, out_dtype=getattr(torch, dtype), **kw)
+        got, lse = q4.q4_cache_attend(*self.dev, return_lse=True, **kw)
+        self.plain = q4.q4_cache_attend(*self.dev, **kw)  # (keys of prompts are rounded where no lse is asked for)
         torch.cuda.synchronize()
         out, bound, l, lb, touched = ref.attend(self.q.astype(np.float64), self.planes, self.table, self.lens, self.offsets,
                                                 causal, window, scale, dtype == "bfloat16")
         assert touched.all()
         within(got, out, bound, what + " out")
+        within(self.plain, out, bound, what + " out alone")
         within(lse, l, lb, what + " lse")
         return got, lse
 
@@ -307,18 +309,27 @@ def test_what_a_token_does_not_see_does_not_reach_it(env, new, slack):
     b.dev = (b.dev[0], to_cache(env, planes)) + b.dev[2:]
     out, lse = q4.q4_cache_attend(*b.dev, q_offsets=b.offsets_dev, max_q=b.max_q, window=window, return_lse=True)
     assert torch.equal(out, clean) and torch.equal(lse, lse0)
+    out = q4.q4_cache_attend(*b.dev, q_offsets=b.offsets_dev, max_q=b.max_q, window=window)
+    assert torch.equal(out, b.plain)
 
 
 @pytest.mark.parametrize("new", [[1, 1], [5, 1], [80, 1]])
 @pytest.mark.parametrize("side", ["k", "v"])
-def test_not_finite_values_reach_the_tokens_that_see_them(env, new, side):
+@pytest.mark.parametrize("with_lse", [False, True])
+def test_not_finite_values_reach_the_tokens_that_see_them(env, new, side, with_lse):
     """A NaN scale in one block of one key: of a value, the outputs of that block
     in the tokens and heads that see it are NaN; of a key, all of them; the
     others keep their bits."""
     torch, q4, dev = env
     heads, G, D, page = 2, 4, 128, 16
     b = Batch(env, [170, 99], new, heads, G, D, page, 31)
-    clean, _ = b.check(env, "clean")
+    b.check(env, "clean")
+
+    def attend(cache):
+        out = q4.q4_cache_attend(b.dev[0], cache, *b.dev[2:], q_offsets=b.offsets_dev, max_q=b.max_q, return_lse=with_lse)
+        return out[0] if with_lse else out
+
+    clean = attend(b.cache)
     for bits in (0x7E00, 0x7C00):
         planes = {n: p.copy() for n, p in b.planes.items()}
         key = 170 - max(1, new[0] // 2)       # about half of the tokens see it
@@ -327,7 +338,7 @@ def test_not_finite_values_reach_the_tokens_that_see_them(env, new, side):
         planes[side + "_codes"][ids[0], 1, at[0]] = 0x9C
         planes[side + "_zeros"][ids[0], 1, at[0]] = 0
         cache = to_cache(env, planes)
-        out = q4.q4_cache_attend(b.dev[0], cache, *b.dev[2:], q_offsets=b.offsets_dev, max_q=b.max_q).float()
+        out = attend(cache).float()
         sees = np.zeros(b.q.shape[0], bool)
         sees[:new[0]] = 170 - new[0] + np.arange(new[0]) >= key
         assert sees.any()
@@ -349,7 +360,8 @@ def test_queries_that_are_not_finite_stay_with_their_rows(env):
     torch, q4, dev = env
     for new in ([1, 2], [40, 30]):
         b = Batch(env, [80, 60], new, 2, 4, 64, 16, 41)
-        clean, _ = b.check(env, "clean")
+        b.check(env, "clean")
+        clean = b.plain
         q = b.dev[0].clone()
         q[1, 3, 7] = float("nan")
         q[0, 5, 60] = float("inf")
@@ -425,7 +437,8 @@ def test_strided_queries_and_given_outputs(env):
     out = torch.empty((T, 8, 64), dtype=torch.bfloat16, device=dev)
     need = q4.q4_cache_attend_ws_bytes(T, 8, 2, 64, 2, b.max_q)
     ws = torch.full((need,), 0xFF, dtype=torch.uint8, device=dev)
-    got = q4.q4_cache_attend(wide[:, 2:10], *b.dev[1:], q_offsets=b.offsets_dev, max_q=b.max_q, out=out, workspace=ws)
+    got = q4.q4_cache_attend(wide[:, 2:10], *b.dev[1:], q_offsets=b.offsets_dev, max_q=b.max_q, out=out, workspace=ws,
+                             lse=torch.empty((T, 8), device=dev))
     assert got is out and torch.equal(out, first)
     with pytest.raises(q4.Q4Error):
         q4.q4_cache_attend(wide[:, 2:10], *b.dev[1:], q_offsets=b.offsets_dev, max_q=b.max_q, out=out, workspace=ws[:-16])

@@ -77,3 +77,29 @@ def test_one_token_of_a_larger_tensor(env):
     lens = torch.tensor([18], dtype=torch.int32, device=dev)
     out = [q4.q4_cache_attend(t, caches[0], table, lens) for t in (part, part.contiguous())]
     assert torch.equal(*out)
+
+
+@pytest.mark.parametrize("lens,new,G,D", [([700, 333], [300, 90], 4, 128), ([500], [200], 1, 64), ([400], [66], 5, 192),
+                                          ([300, 900], [130, 100], 2, 256), ([2000, 64], [1, 5], 7, 128)])
+def test_lse_has_the_precision_of_its_type(env, lens, new, G, D):
+    """lse is fp32, and so are its scores: keys enter the products exactly.  A
+    score's D products and ND scaled sums are added in fp32, every step rounded
+    by 2^-24 of at most sum |q| |code - zero| scale, doubled where zero points
+    are subtracted behind (30 for 15), with 2^-24 for each product that a
+    matrix core aligns: 2 (2 D + 16) 2^-24 of 30 sum |q| scale bounds every
+    score; the sum of the weights adds (keys + 16) 2^-24, the exponent and the
+    logarithm 2^-22 of the largest score and 1.  Of independent roundings the
+    2-norm over all rows stays below half of 2e-5 of the norm of lse."""
+    torch, q4, dev = env
+    b = Batch(env, lens, new, 2, G, D, 16, 300 + D, sharp=2.0)
+    _, lse = q4.q4_cache_attend(*b.dev, q_offsets=b.offsets_dev, max_q=b.max_q, return_lse=True)
+    got = lse.cpu().numpy().astype(np.float64)
+    _, _, want, _, _ = ref.attend(b.q.astype(np.float64), b.planes, b.table, b.lens, b.offsets)
+    assert np.isfinite(want).all()
+    # The largest block sums of |q| times scales 0.5 at most.
+    most = 30 * 0.5 * np.abs(b.q.astype(np.float64)).sum(-1) * D ** -0.5
+    bound = 2 * (2 * D + 16) * 2.0 ** -24 * most + (max(lens) + 16) * 2.0 ** -24 + 2.0 ** -22 * (most + 1)
+    assert (np.abs(got - want) <= bound).all()
+    rel = np.linalg.norm(got - want) / np.linalg.norm(want)
+    print(f"{lens} {new} D {D}: lse off by {rel:.2g} (2-norm), {np.abs(got - want).max():.2g} at most", flush=True)
+    assert rel < 1e-5
