@@ -3,6 +3,7 @@
 // For a row (a token's query head) with scores s_i = scale q . k_i over the
 // keys it sees: out = sum p_i v_i / sum p_i, p_i = 2^(c (s_i - m)), c = log2 e.
 // One pass over the keys, with the running maximum m; sums are fp32.
+#include <float.h>
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -35,6 +36,8 @@ struct AttendArgs {
     int page_shift;
     int G;            // query heads a key head
     uint32_t inv_G;   // 2^16 / G, rounded up: r inv_G / 2^16 is r / G for r < 64, G <= 64
+    float c;          // scale log2 e = c 2^c_exp, c from 1/2 to 1
+    int c_exp;
     int limit;        // the split kernel takes sequences of at most this many rows
     int max_rows;     // rows a partial result is kept for
     float *part;      // partial results: [slot][max_rows][D], then (ref, sum) pairs
@@ -46,6 +49,25 @@ struct AttendArgs {
     int parts;          // workgroups the keys of one are dealt to at most,
     int prefix_parts, prompt_parts;  // behind a long prefix, and without one
 };
+
+// A row of q enters the products times 2^ex, its largest magnitude (of these
+// bf16 bits) 2^top to 2^(top + 1) then; kappa = scale log2 e 2^(shift - ex)
+// makes exponents of 2 of the scores.  kappa times 2^low stays a normal number
+// (a masked score is -infinity, and -infinity times 0 a NaN), so that rows of
+// zeros, and rows so small that no score reaches 2^-90, get a smaller ex; and
+// kappa times 2^high stays finite, so that scores of 0 stay 0.
+struct RowScale {
+    int ex;
+    float kappa;
+};
+template <int TOP, int SHIFT, int LOW, int HIGH>
+__device__ __forceinline__ RowScale row_scale(float c, int c_exp, uint32_t most, bool live) {
+    const int most_ex = c_exp + SHIFT + LOW + 125;
+    int ex = live ? 127 + TOP - (int)(most >> 7) : -300;
+    ex = ex < most_ex ? ex : most_ex;
+    const int k = c_exp + SHIFT - ex;
+    return RowScale{ex, ldexpf(c, k < 127 - HIGH ? k : 127 - HIGH)};
+}
 
 // A sequence as a kernel sees it, every value within its bounds.
 struct Sequence {
@@ -472,8 +494,9 @@ __global__ __launch_bounds__(kSplitThreads, split_occupancy(ND, NT)) void attend
                 }
             // The row's largest to 2^14 .. 2^15 (a row with an infinity has no
             // finite result, whatever its other values become).
-            const int ex = r < rows ? 141 - (int)(half_max4(most) >> 7) : -300;
-            kappa[x] = ldexpf(a.scale * 1.44269504088896f, 20 - ex);
+            const RowScale rs = row_scale<14, 20, 0, 0>(g.c, g.c_exp, half_max4(most), r < rows);
+            const int ex = rs.ex;
+            kappa[x] = rs.kappa;
             const uint32_t one = 0x00100010u;  // the code 1, twice
             const half8_t ones = __builtin_bit_cast(half8_t, u32x4_t{one, one, one, one});
 #pragma unroll
@@ -1052,8 +1075,9 @@ __global__ __launch_bounds__(kTileThreads, 1) void attend_tile_kernel(AttendArgs
             }
         }
         most = half_max(pk_max(most, (uint32_t)__shfl_xor((int)most, 32)));
-        const int ex = live ? 136 - (int)(most >> 7) : -300;  // the largest to 2^9 .. 2^10
-        kappa = ldexpf(a.scale * 1.44269504088896f, -ex);
+        const RowScale rs = row_scale<9, 0, -24, 16>(g.c, g.c_exp, most, live);  // (the keys' exponent is from -24 to 16)
+        const int ex = rs.ex;
+        kappa = rs.kappa;
 #pragma unroll
         for (int d = 0; d < ND * 4; ++d)
 #pragma unroll
@@ -1590,6 +1614,8 @@ hipError_t launch_cache_attend(const CacheAttend &a, void *workspace, hipStream_
     g.page_shift = __builtin_ctzll((unsigned long long)a.cache.page);
     g.G = (int)(a.q_heads / a.cache.heads);
     g.inv_G = (65536 + g.G - 1) / g.G;
+    const float c = a.scale * 1.44269504088896f;
+    g.c = frexpf(c < FLT_MAX ? c : FLT_MAX, &g.c_exp);
     const AttendPlan p = attend_plan(a.T, a.q_heads, a.cache.heads, a.cache.D, a.B, a.max_q);
     g.limit = p.limit;
     float *ws = static_cast<float *>(workspace);
