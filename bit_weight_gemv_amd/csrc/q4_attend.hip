@@ -875,9 +875,11 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs g) {
 // in use, so that a tile costs one barrier.  32 x 32 x 16 products: S^T = K Q^T,
 // whose result is the operand of O^T = V^T P^T as it stands; V is turned by the
 // transposing 16-bit LDS read.
-// They become (c - zero) scale 2^-E, rounded by 2^-11 of themselves; 2^E is
-// above every scale so far (of the values': the sums are rescaled when it
-// grows), so that none passes fp16.  The sum of a row's weights is that of the fp32
+// They become (c - zero) scale 2^-E, with 2^E for keys and one for values such
+// that all scales are from 2^(E - 14) to 2^E: normal numbers in fp16, each rounded
+// by 2^-11 of itself, whatever the largest scale of the tile is and whoever
+// sees it (with 2^E above the largest scale alone, one of 65504 that a row did
+// not even see left 0 of its values of scale 0.001).  The sum of a row's weights is that of the fp32
 // weights: with the sum of the rounded ones, one instruction for two of them,
 // lse was off by up to 2^-11.
 //
@@ -1009,11 +1011,24 @@ __device__ __forceinline__ int exponent_above(uint32_t bits) {
 // The bits of the largest fp16 below 2^e.
 __device__ __forceinline__ int below(int e) { return e <= -14 ? (e < -14 ? 0 : 0x3FF) : ((e + 15) << 10) - 1; }
 
-struct TileNews {
-    uint32_t key_scale, value_scale;  // the largest finite scales (bits) that pass the exponents in use
-    uint32_t wild;                    // kWild, kHidden
+// A tile's scales from 2^(e - 14) to 2^e are normal in fp16 under 2^-e, so that
+// keys and values are rounded by 2^-11 of themselves.  The bits of the smallest:
+constexpr int kSpan = 14;
+__device__ __forceinline__ uint32_t from(int e) {
+    return e <= kSpan - 24 ? 1 : e < kSpan - 14 ? 1u << (e - kSpan + 24) : (uint32_t)(e - kSpan + 15) << 10;
+}
+// Whether a scale of these bits is neither 0 nor in those of exponent e.
+__device__ __forceinline__ bool outside(uint32_t bits, int e) {
+    return bits != 0 && bits - from(e) >= (uint32_t)(below(e) + 1) - from(e);
+}
+
+struct TileScales {
+    uint32_t key_top, key_bottom, value_top, value_bottom;  // bits of the largest finite scale, 0x7C00 less the smallest but 0
+    uint32_t wild;                                          // kWild, kHidden
 };
-enum { kWild = 1, kHidden = 2 };  // some scale of a value is not finite; some page of the table is not one
+// Some scale of a value is not finite; some page of the table is not one; some
+// scale is outside of the exponents in use.
+enum { kWild = 1, kHidden = 2, kOutside = 4 };
 
 // KB: blocks of 32 keys a tile (with 192 and 256 dimensions one: the scores of
 // two would not stay in registers beside the sums).
@@ -1021,36 +1036,47 @@ enum { kWild = 1, kHidden = 2 };  // some scale of a value is not finite; some p
 // 64 by its scale over that of the next, so that it has the precision of fp32.
 // For calls that ask for lse, which is fp32: from keys rounded to fp16 it was
 // off by 3e-5 of itself, and is by 6e-8.  out, of weights and values in fp16,
-// gains nothing that a bf16 shows, and EXACT costs (512 tokens behind 32488 472
-// us instead of 405, prompts of 8191 219 instead of 190, with D = 64 145
-// instead of 135, with 256 508 instead of 364).
-template <int ND, int KB, bool EXACT>
-__global__ __launch_bounds__(kTileThreads, 1) void attend_tile_kernel(AttendArgs g) {
+// gains nothing that a bf16 shows, and EXACT costs (512 tokens behind 32488 481
+// us instead of 394, prompts of 8191 213 instead of 173, with D = 64 141
+// instead of 124, with 256 531 instead of 394).
+// FAR: keys as in EXACT, and values in as many powers of two as a tile of keys
+// needs (14 at a time), a tile after the other: right for whatever scales a
+// cache may hold, and twice as slow (512 tokens behind 32488: 394 us; begun
+// again under other powers of two, for one value scale 128 times the others,
+// 486; FAR for one that is 2^18 times the others 780, for scales from 2^-20 to
+// 1 everywhere 1050).
+enum TileMode { kRounded, kExact, kFar };
+
+template <int ND, int KB>
+struct TileShared {
+    uint16_t sk[2][32 * KB * ND * 64], sv[2][32 * KB * ND * 64];
+    float key_scales[2][ND * 32 * KB];
+    int64_t sums[kTileWaves], found[2];
+    int longest[2];
+    uint32_t news[3];  // of a tile: kWild, kHidden, kOutside
+    TileScales scales;
+};
+
+// A tile of rows over its part of the keys.  Keys and values are under one
+// power of two each: that of the first tile of keys, or of all.  kAgain, and
+// nothing written, where the first tile's does not hold for a later one;
+// kTooFar, where none does (FAR: neither).
+enum TileEnd { kDone, kAgain, kTooFar };
+template <int ND, int KB, TileMode MODE>
+__device__ __forceinline__ TileEnd attend_tile(const AttendArgs &g, TileShared<ND, KB> &sh, const RowTile &rt, int64_t index, int h,
+                                               int part, bool all, int tid) {
     constexpr int D = ND * 64, kKeys = 32 * KB;
     constexpr int kUnits = kKeys * 2 * ND;           // pieces of 16 bytes of codes of a tile of keys
     constexpr int kLoads = (2 * kUnits + kTileThreads - 1) / kTileThreads;
-    __shared__ __attribute__((aligned(16))) uint16_t sk[2][kKeys * D];
-    __shared__ __attribute__((aligned(16))) uint16_t sv[2][kKeys * D];
-    __shared__ __attribute__((aligned(16))) float key_scales[2][EXACT ? ND * kKeys : 1];
-    __shared__ int64_t sums[kTileWaves], found[2];
-    __shared__ int longest[2];
-    __shared__ TileNews news[3];
+    constexpr bool EXACT = MODE != kRounded;
+    auto &sk = sh.sk, &sv = sh.sv;
+    auto &key_scales = sh.key_scales;
+    auto &news = sh.news;
+    auto &scales = sh.scales;
     const CacheAttend &a = g.a;
-    const int tid = (int)threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int col = lane & 31, half = lane >> 5;
     const int heads = (int)a.cache.heads, page = (int)a.cache.page, pages = (int)a.cache.pages;
-    // The last tiles of rows see the most keys: they begin first, and all first
-    // parts before the second ones (workgroups go to the card's dies and their
-    // quarters strictly in turn: a tile's parts side by side, of which short
-    // tiles have only the first, would leave some without work).
-    const int64_t items = g.row_tiles * heads;
-    const int part = (int)(blockIdx.x / items), h = (int)(blockIdx.x % heads);
-    const int64_t index = g.row_tiles - 1 - (blockIdx.x - part * items) / heads;
-    RowTile rt;
-    const bool valid = find_row_tile<kTileThreads>(g, index, sums, found, longest, rt);
-    if (part == 0 && h == 0 && tid == 0)
-        g.tile_rows[index] = valid ? TileRows{rt.s.first, rt.row0, rt.rows, rt.parts} : TileRows{0, 0, 0, 0};
-    if (!valid || part >= rt.parts) return;
     const Sequence s = rt.s;
     const int nt_all = (rt.hi - rt.lo + kKeys - 1) / kKeys;
     const int t0 = (int)((int64_t)nt_all * part / rt.parts), t1 = (int)((int64_t)nt_all * (part + 1) / rt.parts);
@@ -1151,29 +1177,85 @@ __global__ __launch_bounds__(kTileThreads, 1) void attend_tile_kernel(AttendArgs
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) raw[i] = coming[i];
     };
-    // Tells of scales that pass the exponents in use, and of what is rare.
+    // Tells of finite scales outside of the exponents in use, and of what is rare.
     auto publish = [&](int tile, int ek, int ev) {
-        TileNews &n = news[tile % 3];
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
             if (!is_piece(i)) break;
             const Raw &c = coming[i];
             const bool value = is_value(i);
             const uint32_t bits = c.ok && (value || !EXACT) ? c.scale : 0;
-            if (__any((int)bits > below(value ? ev : ek) || c.hidden)) {
+            if (__any(outside(bits, value ? ev : ek) || c.hidden)) {
                 const bool fin = bits < 0x7C00u;
-                const uint32_t top = wave_max_u32(fin ? bits : 0);
-                const uint32_t wild =
-                    (value && __any(!fin) ? (uint32_t)kWild : 0u) | (__any(c.hidden) ? (uint32_t)kHidden : 0u);
-                if (lane == 0) {
-                    atomicMax(value ? &n.value_scale : &n.key_scale, top);
-                    if (wild) atomicOr(&n.wild, wild);
-                }
+                const uint32_t rare = (__any(fin && outside(bits, value ? ev : ek)) ? (uint32_t)kOutside : 0u) |
+                                      (value && __any(!fin) ? (uint32_t)kWild : 0u) | (__any(c.hidden) ? (uint32_t)kHidden : 0u);
+                if (lane == 0) atomicOr(&news[tile % 3], rare);
             }
         }
     };
+    // The exponents that all finite scales of the tiles t .. end - 1 are within,
+    // in the middle, so that larger and smaller ones later on are within
+    // too; and what is rare in the last of them (which stays in `coming`).
+    // False where one exponent is not enough.
+    auto survey = [&](int t, int end, int &ek, int &ev, uint32_t &wild) -> bool {
+        uint32_t top[kLoads] = {}, bottom[kLoads] = {}, rare = 0;
+        if (tid == 0) scales = TileScales{0, 0, 0, 0, 0};
+        for (; t < end; ++t) {
+            ids(t);
+            load(t);
+            rare = 0;
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) {
+                if (!is_piece(i)) break;
+                const Raw &c = coming[i];
+                const bool value = is_value(i);
+                const uint32_t bits = c.ok && (value || !EXACT) ? c.scale : 0;
+                const bool fin = bits > 0 && bits < 0x7C00u;
+                top[i] = max(top[i], fin ? bits : 0);
+                bottom[i] = max(bottom[i], fin ? 0x7C00u - bits : 0);
+                rare |= (value && bits >= 0x7C00u ? (uint32_t)kWild : 0u) | (c.hidden ? (uint32_t)kHidden : 0u);
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            if (!is_piece(i)) break;
+            const bool value = is_value(i);
+            const uint32_t x = wave_max_u32(top[i]), y = wave_max_u32(bottom[i]);
+            if (lane == 0) {
+                atomicMax(value ? &scales.value_top : &scales.key_top, x);
+                atomicMax(value ? &scales.value_bottom : &scales.key_bottom, y);
+            }
+        }
+        if (rare) atomicOr(&scales.wild, rare);
+        __syncthreads();
+        const TileScales n = scales;
+        wild = __builtin_amdgcn_readfirstlane(n.wild);
+        auto fit = [&](uint32_t x, uint32_t y, int &e) {
+            x = __builtin_amdgcn_readfirstlane(x);
+            y = 0x7C00u - (uint32_t)__builtin_amdgcn_readfirstlane(y);
+            e = exponent_above(x);
+            const int most = x == 0 ? -24 : kSpan + (y < 0x400u ? 7 - __builtin_clz(y) : (int)(y >> 10) - 15);  // y is 2^(most - 14) at least
+            const bool within = e <= most;
+            e = min(e + (within ? (most - e + 1) / 2 : 0), 16);
+            return within;
+        };
+        const bool keys = fit(n.key_top, n.key_bottom, ek), values = fit(n.value_top, n.value_bottom, ev);
+        return keys && values;
+    };
     uint32_t mask = 0x000F000Fu, magic = 0x64006400u;  // 1024 + code
     asm volatile("" : "+s"(mask), "+v"(magic));
+    // 32 codes in fp16, times sc.
+    auto put = [&](const Raw &c0, bool value, int buf, int key, int piece, _Float16 sc) {
+        const _Float16 of = (_Float16)(-1024.0f - (c0.ok ? f16_bits_to_f32(c0.zero) : 0.0f));
+        const half2_t s2 = {sc, sc}, o2 = {of, of};
+        const uint32_t w[4] = {c0.codes.x, c0.codes.y, c0.codes.z, c0.codes.w};
+        uint16_t *row = (value ? sv[buf] : sk[buf]) + key * D;
+        const int turn = value ? value_turn(key) : key_turn(key);
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+            *reinterpret_cast<u32x4_t *>(row + place(4 * piece + c, turn) * 8) = decode8(w[c], o2, s2, mask, magic);
+    };
     auto decode = [&](int buf, int ek, int ev) {
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
@@ -1189,15 +1271,7 @@ __global__ __launch_bounds__(kTileThreads, 1) void attend_tile_kernel(AttendArgs
                 sb = sb > 0 ? 0x3C00u : 0u;
             }
             if (value && sb >= 0x7C00u) sb = 0;  // (rows that see it are made NaN below)
-            const _Float16 sc = (_Float16)ldexpf(f16_bits_to_f32(sb), -(value ? ev : EXACT ? 0 : ek));
-            const _Float16 of = (_Float16)(-1024.0f - (c0.ok ? f16_bits_to_f32(c0.zero) : 0.0f));
-            const half2_t s2 = {sc, sc}, o2 = {of, of};
-            const uint32_t w[4] = {c0.codes.x, c0.codes.y, c0.codes.z, c0.codes.w};
-            uint16_t *row = (value ? sv[buf] : sk[buf]) + key * D;
-            const int turn = value ? value_turn(key) : key_turn(key);
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-                *reinterpret_cast<u32x4_t *>(row + place(4 * piece + c, turn) * 8) = decode8(w[c], o2, s2, mask, magic);
+            put(c0, value, buf, key, piece, (_Float16)ldexpf(f16_bits_to_f32(sb), -(value ? ev : EXACT ? 0 : ek)));
         }
     };
 
@@ -1207,161 +1281,210 @@ __global__ __launch_bounds__(kTileThreads, 1) void attend_tile_kernel(AttendArgs
 #pragma unroll
         for (int i = 0; i < 16; ++i) o[y][i] = 0;
     float top = -INFINITY, nk = kTop, ck = INFINITY, l = 0;
-    int ek = -24, ev = -24;      // of the tile in use
-    int ek_next = -24, ev_next = -24;
+    int ek = -24, ev = -24;
     uint32_t wild = 0, wild_next = 0;
 
-    if (t0 < t1) {
-        if (tid < 3) news[tid] = TileNews{0, 0, 0};
-        ids(t0);
-        load(t0);
-        __syncthreads();
-        publish(t0, -24, -24);
-        __syncthreads();
-        {
-            const TileNews n = news[t0 % 3];
-            ek_next = __builtin_amdgcn_readfirstlane(exponent_above(n.key_scale));
-            ev_next = __builtin_amdgcn_readfirstlane(exponent_above(n.value_scale));
-            wild_next = __builtin_amdgcn_readfirstlane(n.wild);
-        }
-        take();
-        decode(t0 & 1, ek_next, ev_next);
-        ids(t0 + 1);
-        load(t0 + 1);
-        ids(t0 + 2);
-        publish(t0 + 1, ek_next, ev_next);
-    }
-    for (int tile = t0; tile < t1; ++tile) {
-        __syncthreads();
-        // This tile is in LDS, the next one in registers.
-        ek = ek_next;
-        wild = wild_next;
-        if (ev_next != ev) {
-            const float f = exp2i(ev - ev_next);
-            ev = ev_next;
+    // A tile in the buffers: its scores, their weights, and the values' sums.
+    auto scores = [&](int buf, float16_t(&S)[KB]) {
+        const uint16_t *kb = sk[buf];
 #pragma unroll
-            for (int y = 0; y < 2 * ND; ++y) o[y] *= f;
-        }
-        {
-            const TileNews n = news[(tile + 1) % 3];
-            const int e1 = __builtin_amdgcn_readfirstlane(exponent_above(n.key_scale));
-            const int e2 = __builtin_amdgcn_readfirstlane(exponent_above(n.value_scale));
-            wild_next = __builtin_amdgcn_readfirstlane(n.wild);
-            ek_next = e1 > ek ? e1 : ek;
-            ev_next = e2 > ev ? e2 : ev;
-        }
-        if (tid == 0) news[tile % 3] = TileNews{0, 0, 0};  // (read before this barrier, written after the next)
-        take();
-        load(tile + 2);
-        ids(tile + 3);
-        if (tile + 1 < t1) decode((tile + 1) & 1, ek_next, ev_next);
-        const int key0 = rt.lo + tile * kKeys;
-        if (key0 <= some_to && key0 + kKeys - 1 >= some_from) {
-            const uint16_t *kb = sk[tile & 1], *vb = sv[tile & 1];
-            float16_t S[KB];
+        for (int x = 0; x < KB; ++x)
 #pragma unroll
-            for (int x = 0; x < KB; ++x)
+            for (int i = 0; i < 16; ++i) S[x][i] = 0;
 #pragma unroll
-                for (int i = 0; i < 16; ++i) S[x][i] = 0;
+        for (int d = 0; d < ND * 4; ++d) {
 #pragma unroll
-            for (int d = 0; d < ND * 4; ++d) {
-#pragma unroll
-                for (int x = 0; x < KB; ++x) {
-                    const u32x4_t k = *reinterpret_cast<const u32x4_t *>(kb + (32 * x + col) * D + ((2 * d ^ ((d >> 1) & 3)) ^ half ^ key_turn(col)) * 8);
-                    S[x] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(half8_t, k), qf[d], S[x], 0, 0, 0);
-                }
-                if (EXACT && (d & 3) == 3) {
-                    // Behind a block its scale, over that of the next block.
-                    const float *ks = key_scales[tile & 1] + d / 4 * kKeys + 4 * half;
-#pragma unroll
-                    for (int x = 0; x < KB; ++x)
-#pragma unroll
-                        for (int g = 0; g < 4; ++g) {
-                            const float4_t sc = *reinterpret_cast<const float4_t *>(ks + 32 * x + 8 * g);
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) S[x][4 * g + i] *= sc[i];
-                        }
-                }
+            for (int x = 0; x < KB; ++x) {
+                const u32x4_t k = *reinterpret_cast<const u32x4_t *>(kb + (32 * x + col) * D + ((2 * d ^ ((d >> 1) & 3)) ^ half ^ key_turn(col)) * 8);
+                S[x] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(half8_t, k), qf[d], S[x], 0, 0, 0);
             }
-            const float kap = EXACT ? kappa : ldexpf(kappa, ek);
-            if (key0 + kKeys - 1 > all_to || key0 < all_from || (wild & kHidden)) {
-                uint64_t shown = ~0ull;
-                if (wild & kHidden) shown = __ballot(page_at(key0 + lane) >= 0);
+            if (EXACT && (d & 3) == 3) {
+                // Behind a block its scale, over that of the next block.
+                const float *ks = key_scales[buf] + d / 4 * kKeys + 4 * half;
 #pragma unroll
                 for (int x = 0; x < KB; ++x)
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const int key = key0 + 32 * x + 8 * (i / 4) + 4 * half + (i & 3);
-                        if (key > seen_to || key < seen_from || !(shown >> (key - key0) & 1)) S[x][i] = -INFINITY;
+                    for (int g = 0; g < 4; ++g) {
+                        const float4_t sc = *reinterpret_cast<const float4_t *>(ks + 32 * x + 8 * g);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) S[x][4 * g + i] *= sc[i];
                     }
             }
-            float tm = S[0][0];
+        }
+    };
+    auto weights = [&](int key0, float kap, float16_t(&S)[KB], half8_t(&pf)[KB][2]) {
+        if (key0 + kKeys - 1 > all_to || key0 < all_from || (wild & kHidden)) {
+            uint64_t shown = ~0ull;
+            if (wild & kHidden) shown = __ballot(page_at(key0 + lane) >= 0);
 #pragma unroll
             for (int x = 0; x < KB; ++x)
 #pragma unroll
-                for (int i = 0; i < 16; ++i) tm = fmaxf(tm, S[x][i]);
-            if (__any(fmaf(tm, kap, ck) > kTop + kHeadroom)) {
-                const float m = fmaxf(top, fmaxf(tm, __shfl_xor(tm, 32)) * kap);
-                const float kn = m == -INFINITY ? kTop : kTop - m;
-                const float fade = top == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(kn - nk);
-                top = m;
-                nk = kn;
-                ck = m == -INFINITY ? INFINITY : kn;
-                l *= fade;
-#pragma unroll
-                for (int y = 0; y < 2 * ND; ++y) o[y] *= fade;
-            }
-            half8_t pf[KB][2];
-#pragma unroll
-            for (int x = 0; x < KB; ++x)
-#pragma unroll
-                for (int y = 0; y < 2; ++y) {
-                    u32x4_t w;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float pa = __builtin_amdgcn_exp2f(fmaf(S[x][8 * y + 2 * i], kap, nk));
-                        const float pb = __builtin_amdgcn_exp2f(fmaf(S[x][8 * y + 2 * i + 1], kap, nk));
-                        const half2_t p2 = {(_Float16)pa, (_Float16)pb};
-                        l += pa + pb;
-                        w[i] = __builtin_bit_cast(uint32_t, p2);
-                    }
-                    pf[x][y] = __builtin_bit_cast(half8_t, w);
+                for (int i = 0; i < 16; ++i) {
+                    const int key = key0 + 32 * x + 8 * (i / 4) + 4 * half + (i & 3);
+                    if (key > seen_to || key < seen_from || !(shown >> (key - key0) & 1)) S[x][i] = -INFINITY;
                 }
-            const int gk = 4 * half + ((lane & 15) >> 2);               // the key of 8 that the lane's address names
-            const int gd = ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1);   // its piece of a block of 32 dimensions
+        }
+        float tm = S[0][0];
 #pragma unroll
-            for (int x = 0; x < KB; ++x)
+        for (int x = 0; x < KB; ++x)
 #pragma unroll
-                for (int z = 0; z < 2; ++z)
+            for (int i = 0; i < 16; ++i) tm = fmaxf(tm, S[x][i]);
+        if (__any(fmaf(tm, kap, ck) > kTop + kHeadroom)) {
+            const float m = fmaxf(top, fmaxf(tm, __shfl_xor(tm, 32)) * kap);
+            const float kn = m == -INFINITY ? kTop : kTop - m;
+            const float fade = top == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(kn - nk);
+            top = m;
+            nk = kn;
+            ck = m == -INFINITY ? INFINITY : kn;
+            l *= fade;
 #pragma unroll
-                    for (int y = 0; y < 2 * ND; ++y) {
-                        typedef __attribute__((address_space(3))) short4_t lds_short4;
-                        typedef short short8_t __attribute__((ext_vector_type(8)));
-                        const uint16_t *va = vb + gk * D + ((4 * y ^ (y & 3)) ^ gd ^ value_turn(gk)) * 8 + (lane & 1) * 4;
-                        const short4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_short4 *)(va + (32 * x + 16 * z) * D));
-                        const short4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_short4 *)(va + (32 * x + 16 * z + 8) * D));
-                        const short8_t v8 = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-                        o[y] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(half8_t, v8), pf[x][z], o[y], 0, 0, 0);
-                    }
-            if (wild & kWild) {
-                // Rows that see a value whose scale is not finite.
-                for (int k = 0; k < kKeys; ++k) {
-                    const int key = key0 + k, id = page_at(key);
-                    if (id < 0) continue;
-                    const int64_t row = ((int64_t)id * heads + h) * page + (key & (page - 1));
+            for (int y = 0; y < 2 * ND; ++y) o[y] *= fade;
+        }
 #pragma unroll
-                    for (int d = 0; d < ND; ++d) {
-                        const float bad = a.cache.v_scales[row * ND + d] >= 0x7C00u && key <= seen_to && key >= seen_from ? NAN : 0.0f;
+        for (int x = 0; x < KB; ++x)
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            o[2 * d][i] += bad;
-                            o[2 * d + 1][i] += bad;
-                        }
-                    }
+            for (int y = 0; y < 2; ++y) {
+                u32x4_t w;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float pa = __builtin_amdgcn_exp2f(fmaf(S[x][8 * y + 2 * i], kap, nk));
+                    const float pb = __builtin_amdgcn_exp2f(fmaf(S[x][8 * y + 2 * i + 1], kap, nk));
+                    const half2_t p2 = {(_Float16)pa, (_Float16)pb};
+                    l += pa + pb;
+                    w[i] = __builtin_bit_cast(uint32_t, p2);
+                }
+                pf[x][y] = __builtin_bit_cast(half8_t, w);
+            }
+    };
+    auto add_values = [&](int buf, const half8_t(&pf)[KB][2]) {
+        const uint16_t *vb = sv[buf];
+        const int gk = 4 * half + ((lane & 15) >> 2);               // the key of 8 that the lane's address names
+        const int gd = ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1);   // its piece of a block of 32 dimensions
+#pragma unroll
+        for (int x = 0; x < KB; ++x)
+#pragma unroll
+            for (int z = 0; z < 2; ++z)
+#pragma unroll
+                for (int y = 0; y < 2 * ND; ++y) {
+                    typedef __attribute__((address_space(3))) short4_t lds_short4;
+                    typedef short short8_t __attribute__((ext_vector_type(8)));
+                    const uint16_t *va = vb + gk * D + ((4 * y ^ (y & 3)) ^ gd ^ value_turn(gk)) * 8 + (lane & 1) * 4;
+                    const short4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_short4 *)(va + (32 * x + 16 * z) * D));
+                    const short4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_short4 *)(va + (32 * x + 16 * z + 8) * D));
+                    const short8_t v8 = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+                    o[y] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(half8_t, v8), pf[x][z], o[y], 0, 0, 0);
+                }
+    };
+    // Rows that see a value whose scale is not finite.
+    auto infect = [&](int key0) {
+        for (int k = 0; k < kKeys; ++k) {
+            const int key = key0 + k, id = page_at(key);
+            if (id < 0) continue;
+            const int64_t row = ((int64_t)id * heads + h) * page + (key & (page - 1));
+#pragma unroll
+            for (int d = 0; d < ND; ++d) {
+                const float bad = a.cache.v_scales[row * ND + d] >= 0x7C00u && key <= seen_to && key >= seen_from ? NAN : 0.0f;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    o[2 * d][i] += bad;
+                    o[2 * d + 1][i] += bad;
                 }
             }
         }
-        publish(tile + 2, ek_next, ev_next);
+    };
+    // o is in units of 2^ev.
+    auto rescale = [&](int to) {
+        const float f = exp2i(ev - to);
+        ev = to;
+#pragma unroll
+        for (int y = 0; y < 2 * ND; ++y) o[y] *= f;
+    };
+
+    if constexpr (MODE != kFar) {
+        if (t0 < t1) {
+            if (tid < 3) news[tid] = 0;
+            if (!survey(t0, all ? t1 : t0 + 1, ek, ev, wild_next)) return kTooFar;
+            if (all) {
+                ids(t0);
+                load(t0);
+                wild_next = kWild | kHidden;  // (of the last tile, not this one: looked for)
+            }
+            take();
+            decode(t0 & 1, ek, ev);
+            ids(t0 + 1);
+            load(t0 + 1);
+            ids(t0 + 2);
+            publish(t0 + 1, ek, ev);
+        }
+        for (int tile = t0; tile < t1; ++tile) {
+            __syncthreads();
+            // This tile is in LDS, the next one in registers.
+            wild = wild_next;
+            wild_next = __builtin_amdgcn_readfirstlane(news[(tile + 1) % 3]);
+            if (wild_next & kOutside) return kAgain;
+            if (tid == 0) news[tile % 3] = 0;  // (read before this barrier, written after the next)
+            take();
+            load(tile + 2);
+            ids(tile + 3);
+            if (tile + 1 < t1) decode((tile + 1) & 1, ek, ev);
+            const int key0 = rt.lo + tile * kKeys;
+            if (key0 <= some_to && key0 + kKeys - 1 >= some_from) {
+                float16_t S[KB];
+                half8_t pf[KB][2];
+                scores(tile & 1, S);
+                weights(key0, EXACT ? kappa : ldexpf(kappa, ek), S, pf);
+                add_values(tile & 1, pf);
+                if (wild & kWild) infect(key0);
+            }
+            publish(tile + 2, ek, ev);
+        }
+    } else {
+        for (int tile = t0; tile < t1; ++tile) {
+            __syncthreads();
+            int e;
+            const bool one = survey(tile, tile + 1, ek, e, wild);
+            if (!one) e = kSpan - 26;  // values below 2^-12, then 2^2, then 2^16
+            const int key0 = rt.lo + tile * kKeys;
+            const bool seen = key0 <= some_to && key0 + kKeys - 1 >= some_from;
+            auto decode_values = [&](int e) {
+#pragma unroll
+                for (int i = 0; i < kLoads; ++i) {
+                    if (!is_piece(i) || !is_value(i)) continue;
+                    const int in = (tid + kTileThreads * i) % kUnits;
+                    const uint32_t sb = coming[i].ok && coming[i].scale < 0x7C00u && !outside(coming[i].scale, e) ? coming[i].scale : 0;
+                    put(coming[i], true, 0, in / (2 * ND), in % (2 * ND), (_Float16)ldexpf(f16_bits_to_f32(sb), -e));
+                }
+            };
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) {
+                if (!is_piece(i) || is_value(i)) continue;
+                const int in = (tid + kTileThreads * i) % kUnits, piece = in % (2 * ND), key = in / (2 * ND);
+                const uint32_t sb = coming[i].ok ? coming[i].scale : 0;
+                if (!(piece & 1)) key_scales[1][piece / 2 * kKeys + key] = f16_bits_to_f32(sb > 0 ? sb : 1u);
+                put(coming[i], false, 0, key, piece, (_Float16)(sb > 0 ? 1.0f : 0.0f));
+            }
+            decode_values(e);
+            __syncthreads();
+            for (int i = tid; i < ND * kKeys; i += kTileThreads)
+                key_scales[0][i] = key_scales[1][i] / (i + kKeys < ND * kKeys ? key_scales[1][i + kKeys] : 1.0f);
+            __syncthreads();
+            half8_t pf[KB][2];
+            if (seen) {
+                float16_t S[KB];
+                scores(0, S);
+                weights(key0, kappa, S, pf);
+            }
+            for (;;) {
+                rescale(e);
+                if (seen) add_values(0, pf);
+                e += kSpan;
+                if (one || e > 16) break;
+                __syncthreads();
+                decode_values(e);
+                __syncthreads();
+            }
+            if (seen && (wild & kWild)) infect(key0);
+        }
     }
 
     // Results.  Of 8 dimensions the lane has 0 4 1 5 (2 6 3 7 in the other half
@@ -1378,7 +1501,7 @@ __global__ __launch_bounds__(kTileThreads, 1) void attend_tile_kernel(AttendArgs
             o[y][4 * i + 2] = half ? a1 : b0;
             o[y][4 * i + 3] = half ? a3 : b1;
         }
-    if (!live) return;
+    if (!live) return kDone;
     const int64_t t = s.first + j;
     if (rt.parts == 1) {
         const float f = sum == 0 ? 0.0f : exp2i(ev) / sum;
@@ -1412,6 +1535,36 @@ __global__ __launch_bounds__(kTileThreads, 1) void attend_tile_kernel(AttendArgs
             g.part_sums[slot * 2 + 1] = sum;
         }
     }
+    return kDone;
+}
+
+template <int ND, int KB, bool EXACT>
+__global__ __launch_bounds__(kTileThreads, 1) void attend_tile_kernel(AttendArgs g) {
+    __shared__ __attribute__((aligned(16))) TileShared<ND, KB> sh;
+    int tid = (int)threadIdx.x;
+    const int heads = (int)g.a.cache.heads;
+    // The last tiles of rows see the most keys: they begin first, and all first
+    // parts before the second ones (workgroups go to the card's dies and their
+    // quarters strictly in turn: a tile's parts side by side, of which short
+    // tiles have only the first, would leave some without work).
+    const int64_t items = g.row_tiles * heads;
+    const int part = (int)(blockIdx.x / items), h = (int)(blockIdx.x % heads);
+    const int64_t index = g.row_tiles - 1 - (blockIdx.x - part * items) / heads;
+    RowTile rt;
+    const bool valid = find_row_tile<kTileThreads>(g, index, sh.sums, sh.found, sh.longest, rt);
+    if (part == 0 && h == 0 && tid == 0)
+        g.tile_rows[index] = valid ? TileRows{rt.s.first, rt.row0, rt.rows, rt.parts} : TileRows{0, 0, 0, 0};
+    if (!valid || part >= rt.parts) return;
+    // (What is made of an opaque tid is not kept in registers for the next run.)
+    for (bool all = false;; all = true) {
+        asm volatile("" : "+v"(tid));
+        const TileEnd end = attend_tile<ND, KB, EXACT ? kExact : kRounded>(g, sh, rt, index, h, part, all, tid);
+        if (end == kDone) return;
+        __syncthreads();
+        if (end == kTooFar || all) break;
+    }
+    asm volatile("" : "+v"(tid));
+    attend_tile<ND, KB, kFar>(g, sh, rt, index, h, part, false, tid);
 }
 
 // Joins the parts of a tile of rows: 4 dimensions of a row a lane.
