@@ -132,9 +132,16 @@ __device__ __forceinline__ Sequence sequence_uniform(const CacheAttend &a, int64
 //   s = sum_b scale_b (sum_d q_d c_d - zero_b Q_b),
 // and p' = p scale_b for the second product, whose zero points are
 // subtracted at the end as the sum of p' zero_b.
-// p' enters as fp16 (2^-11, random): scaled by 2^F so that the largest value
-// scale of the keys so far, times a weight of 1, is 2^9; when the maximum
-// grows by less than 2^6 nothing is rescaled.
+// p' enters as fp16 (2^-11, random): scaled by 2^F so that a value scale of 2^E,
+// times a weight of 1, is 2^9; when the maximum grows by less than 2^6 nothing is
+// rescaled.  All value scales of a tile are from 2^(E - 10) to 2^E, so that what fp16
+// loses of a weight (2^-25) is 2^-24 of the largest one with its own block's
+// scale, whatever the other blocks' and keys' are, seen or not.  E moves up and
+// down with them, and a tile whose scales are further apart is taken more than
+// once: with E above all scales so far, values of scale 0.0015 beside others of
+// 65504, seen or not, were off by 1.4e-3 of themselves and those of 2^-14 by 0.03,
+// now by 2.6e-4.  (64 decode tokens over scales from 2^-20 to 1: 175 us, over
+// scales within 2^10 75.)
 //
 // The work is the list of all tiles of 32 keys of all (sequence, key head),
 // dealt evenly to a fixed number of waves, whatever the lengths: each finds its
@@ -156,6 +163,7 @@ constexpr int kMinTiles = 2;       // tiles a wave should have at least, beside 
 // less elsewhere).
 constexpr int kBegin = 3;
 constexpr int kHeadroom = 6;       // powers of two that weights may pass 1 by
+constexpr int kSplitSpan = 10;     // powers of two that the value scales of a tile may lie within
 
 // Tiles of one key head of a sequence (one at least where it has rows, so
 // that rows without keys are written).  In the list that is dealt to the waves
@@ -243,7 +251,23 @@ __device__ __forceinline__ float max4(float v) {
 __device__ __forceinline__ uint32_t pk_max(uint32_t a, uint32_t b) {
     return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2_t, a), __builtin_bit_cast(u16x2_t, b)));
 }
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp_u32(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, true);
+}
+__device__ __forceinline__ uint32_t pk_sub(uint32_t a, uint32_t b) {
+    return __builtin_bit_cast(uint32_t, (u16x2_t)(__builtin_bit_cast(u16x2_t, a) - __builtin_bit_cast(u16x2_t, b)));
+}
 __device__ __forceinline__ uint32_t half_max(uint32_t v) { return (v >> 16) > (v & 0xFFFF) ? v >> 16 : v & 0xFFFF; }
+// The larger of pairs of 16-bit integers over the wave.
+__device__ __forceinline__ uint32_t wave_pk_max(uint32_t v) {
+    v = pk_max(v, dpp_u32<kDppQuadXor1>(v));
+    v = pk_max(v, dpp_u32<kDppQuadXor2>(v));
+    v = pk_max(v, dpp_u32<kDppRowHalfMirror>(v));
+    v = pk_max(v, dpp_u32<kDppRowMirror>(v));
+    v = pk_max(v, (uint32_t)__builtin_amdgcn_ds_swizzle((int)v, 0x401F));
+    return (uint32_t)__builtin_amdgcn_readfirstlane((int)pk_max(v, (uint32_t)__shfl_xor((int)v, 32)));
+}
 // The largest 16-bit integer over lanes l, l ^ 16, l ^ 32, l ^ 48.
 __device__ __forceinline__ uint32_t half_max4(uint32_t v) {
     v = pk_max(v, (uint32_t)__builtin_amdgcn_ds_swizzle((int)v, 0x401F));
@@ -305,14 +329,48 @@ __device__ __forceinline__ void read_par(const uint32_t *lds, int plane, int t, 
     }
 }
 
+// The exponent e with a finite fp16 of these bits below 2^e.
+__device__ __forceinline__ int exponent_above(uint32_t bits) {
+    return bits == 0 ? -24 : bits < 0x400u ? -14 : (int)(bits >> 10) - 14;
+}
+// The exponent e with a finite fp16 of these bits (not 0) at 2^e or above.
+__device__ __forceinline__ int exponent_of(uint32_t bits) {
+    return bits < 0x400u ? 7 - __builtin_clz(bits) : (int)(bits >> 10) - 15;
+}
+
+// Scales from 2^(e - SPAN) to 2^e, and 0, are within exponent e (-24: only 0).
+// The bits of the smallest, and of the one past the largest.
+template <int SPAN>
+__device__ __forceinline__ uint32_t from(int e) {
+    const int f = e - SPAN;
+    return f <= -24 ? 1 : f < -14 ? 1u << (f + 24) : (uint32_t)(f + 15) << 10;
+}
+__device__ __forceinline__ uint32_t past(int e) { return e < -14 ? 1 : (uint32_t)(e + 15) << 10; }
+template <int SPAN>
+__device__ __forceinline__ bool outside(uint32_t bits, int e) {
+    return bits != 0 && bits - from<SPAN>(e) >= past(e) - from<SPAN>(e);
+}
+
+// The exponent that scales from `least` to `top` (bits; 0: none) are within, in
+// the middle, so that larger and smaller ones later on are too; false, and
+// that of the largest, where there is none.
+template <int SPAN>
+__device__ __forceinline__ bool fit(uint32_t top, uint32_t least, int *e) {
+    const int lo = exponent_above(top), hi = top == 0 ? lo : SPAN + exponent_of(least);
+    const int mid = lo + (hi > lo ? (hi - lo + 1) / 2 : 0);
+    *e = mid < 16 ? mid : 16;
+    return lo <= hi;
+}
+
 // Workgroups a compute unit: what the registers allow.
 constexpr int split_occupancy(int ND, int NT) { return NT * ND <= 2 ? 3 : NT * ND <= 4 ? 2 : 1; }
 
-template <int ND, bool DIRECT>
+template <int ND, int NT, bool DIRECT>
 struct SplitShared {
     struct In {
         uint8_t v[kSplitWaves][kTile * ND * 32];
         uint32_t par[kSplitWaves][64 * ND];
+        float kept[kSplitWaves][2 * NT][64];
     };
     struct Out {  // of the waves that share a (sequence, key head)
         float o[kSplitWaves][16][ND * 64 + 4];
@@ -330,7 +388,7 @@ struct SplitShared {
 template <int ND, int NT, bool DIRECT>
 __global__ __launch_bounds__(kSplitThreads, split_occupancy(ND, NT)) void attend_split_kernel(AttendArgs g) {
     constexpr int D = ND * 64;
-    __shared__ __attribute__((aligned(16))) SplitShared<ND, DIRECT> sh;
+    __shared__ __attribute__((aligned(16))) SplitShared<ND, NT, DIRECT> sh;
     const CacheAttend &a = g.a;
     const int tid = (int)threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int col = lane & 15, grp = lane >> 4;
@@ -413,6 +471,10 @@ __global__ __launch_bounds__(kSplitThreads, split_occupancy(ND, NT)) void attend
         auto entry = [&](int key) -> int {
             const int p = key >> g.page_shift;
             return table[p < last_page ? p : last_page];
+        };
+        // Whether the lane's d-th dword of the scales and zeros is of values' scales.
+        auto has_scales = [&](int d) {
+            return 64 * d < 48 * ND && 64 * d + 63 >= 32 * ND && (lane + 64 * d) / (16 * ND) == kValueScales;
         };
         // Where the lane's dwords of the scales and zeros lie.
         const uint32_t *par_base[ND];
@@ -531,8 +593,11 @@ __global__ __launch_bounds__(kSplitThreads, split_occupancy(ND, NT)) void attend
 
         float m[NT], l[NT], nk[NT], ck[NT], zs[NT][ND];
         float4_t o[NT][ND][4];
-        int E = -24;                   // value scales so far are below 2^E
-        uint32_t limit_bits = 0;       // the largest fp16 below
+        // The value scales of a tile are within E: two of them less low2 are at
+        // most span2.  (Begun with 0, which holds for values of common sizes.)
+        int E = 0;
+        uint32_t low2 = from<kSplitSpan>(0) * 0x10001u, span2 = (past(0) - 1 - from<kSplitSpan>(0)) * 0x10001u;
+        uint32_t cut = 0x7C00u;        // a tile that is taken again: scales from here on have been
 #pragma unroll
         for (int x = 0; x < NT; ++x) {
             m[x] = -INFINITY;
@@ -547,22 +612,69 @@ __global__ __launch_bounds__(kSplitThreads, split_occupancy(ND, NT)) void attend
             }
         }
 
-        for (; tile < tend; tile += kStep) {
+        for (int step = 0; tile < tend; tile += step) {
             const bool ok[2] = {(uint32_t)id0 < (uint32_t)pages && lo_key + tile * kTile < s.len,
                                 (uint32_t)id1 < (uint32_t)pages && lo_key + tile * kTile + 16 < s.len};
             const int key = lo_key + tile * kTile;
             const bool edge = !ok[0] || !ok[1] || key + kTile > s.len || key < low_key;
             if (__builtin_expect(edge, 0)) {
-                // Keys that no row sees may hold anything: scales and zeros of 0.
+                // Keys that no row sees may hold anything: scales and zeros of 0,
+                // value scales (whose weights are 0) within E.
                 asm volatile("");  // (a branch, not selects)
 #pragma unroll
                 for (int d = 0; d < ND; ++d) {
                     const int c = lane + 64 * d, in = c % (16 * ND), t = in >= 8 * ND, y = 2 * (in - t * 8 * ND);
                     const bool page_ok = t ? ok[1] : ok[0];
                     const int k0 = key + 16 * t + y / ND, k1 = key + 16 * t + (y + 1) / ND;
-                    if (!page_ok || k0 >= s.len || k0 < low_key) T.par[d] &= 0xFFFF0000u;
-                    if (!page_ok || k1 >= s.len || k1 < low_key) T.par[d] &= 0x0000FFFFu;
+                    const uint32_t fill = has_scales(d) ? low2 : 0;
+                    if (!page_ok || k0 >= s.len || k0 < low_key) T.par[d] = (T.par[d] & 0xFFFF0000u) | (fill & 0xFFFF);
+                    if (!page_ok || k1 >= s.len || k1 < low_key) T.par[d] = (T.par[d] & 0xFFFF) | (fill & 0xFFFF0000u);
                 }
+            }
+            // Value scales that are not within E.
+            bool odd = false;
+#pragma unroll
+            for (int d = 0; d < ND; ++d) odd = odd || (has_scales(d) && pk_max(pk_sub(T.par[d], low2), span2) != span2);
+            const bool repeated = cut < 0x7C00u;
+            bool again = false, grown = false;
+            int next_E = E;
+            if (__any(odd) || repeated) {
+                asm volatile("");  // (a branch, not selects)
+                uint32_t top = 0, low = 0;  // the largest of those that are left, 0x7C00 less the smallest
+#pragma unroll
+                for (int d = 0; d < ND; ++d)
+#pragma unroll
+                    for (int i = 0; i < 32; i += 16) {
+                        const uint32_t v = has_scales(d) ? (T.par[d] >> i) & 0xFFFF : 0;
+                        top = v < cut && v > top ? v : top;
+                        low = v > 0 && v < cut && 0x7C00u - v > low ? 0x7C00u - v : low;
+                        grown = grown || (v >= 0x7C00u && !repeated);
+                    }
+                top = wave_pk_max(top << 16 | low);
+                low = 0x7C00u - (top & 0xFFFF);
+                top >>= 16;
+                if (top > 0 && (outside<kSplitSpan>(top, E) || outside<kSplitSpan>(low, E))) again = !fit<kSplitSpan>(top, low, &next_E);
+                grown = grown || next_E != E;
+                if (again || repeated) {
+                    // No exponent holds for the tile: it is taken once for each
+                    // that it needs, the largest first, with other scales 0.
+                    const uint32_t lo = from<kSplitSpan>(next_E), hi = past(next_E) < cut ? past(next_E) : cut;
+#pragma unroll
+                    for (int d = 0; d < ND; ++d)
+#pragma unroll
+                        for (int i = 0; i < 32; i += 16) {
+                            const uint32_t v = (T.par[d] >> i) & 0xFFFF;
+                            if (has_scales(d) && !(v >= lo && v < hi) && (repeated || v < 0x7C00u)) T.par[d] &= ~(0xFFFFu << i);
+                        }
+                    if (repeated) {  // its weights are summed already
+#pragma unroll
+                        for (int x = 0; x < NT; ++x) {
+                            sh.in.kept[wave][2 * x][lane] = l[x];
+                            sh.in.kept[wave][2 * x + 1][lane] = nk[x];
+                        }
+                    }
+                }
+                cut = again ? from<kSplitSpan>(next_E) : 0x7C00u;
             }
             uint8_t *vl = sh.in.v[wave];
 #pragma unroll
@@ -571,12 +683,15 @@ __global__ __launch_bounds__(kSplitThreads, split_occupancy(ND, NT)) void attend
                 par[lane + 64 * d] = T.par[d];
             }
             wave_fence();
-            id0 = next0;
-            id1 = next1;
-            rows_of(later(1), id0, id1, row);
+            if (!again) {
+                id0 = next0;
+                id1 = next1;
+            }
+            const int to = again ? tile : later(1), then = again ? later(1) : later(2);
+            rows_of(to, id0, id1, row);
             load_values(row, T);
-            next0 = entry(lo_key + later(2) * kTile);
-            next1 = entry(lo_key + later(2) * kTile + 16);
+            next0 = entry(lo_key + then * kTile);
+            next1 = entry(lo_key + then * kTile + 16);
 
             // Scores.
             float S[NT][2][4];
@@ -603,6 +718,7 @@ __global__ __launch_bounds__(kSplitThreads, split_occupancy(ND, NT)) void attend
                 }
             }
             load_keys(row, T);
+            step = again ? 0 : kStep;
             const bool masked = key + kTile - 1 > all_to || key < all_from || !ok[0] || !ok[1];
             if (__builtin_expect(masked, 0)) {
                 asm volatile("");  // (a branch, not selects)
@@ -616,16 +732,7 @@ __global__ __launch_bounds__(kSplitThreads, split_occupancy(ND, NT)) void attend
                             if (!ok[t] || k > seen_to[x] || k < seen_from[x]) S[x][t][r] = -INFINITY;
                     }
             }
-            // Whether a maximum has grown too far, or a value scale.
-            uint32_t top_bits = 0;
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                uint32_t vs[2 * ND];
-                read_par<ND>(par, kValueScales, t, grp, vs);
-#pragma unroll
-                for (int y = 0; y < 2 * ND; ++y) top_bits = pk_max(top_bits, vs[y]);
-            }
-            bool grown = half_max(top_bits) > limit_bits;
+            // Whether a maximum has grown too far.
             float tmax[NT];
 #pragma unroll
             for (int x = 0; x < NT; ++x) {
@@ -634,7 +741,6 @@ __global__ __launch_bounds__(kSplitThreads, split_occupancy(ND, NT)) void attend
                 grown = grown || fmaf(tmax[x], kappa[x], ck[x]) > (float)(9 - E + kHeadroom);
             }
             if (__any(grown)) {
-                uint32_t fin = 0;
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
                     uint32_t vs[2 * ND];
@@ -642,7 +748,6 @@ __global__ __launch_bounds__(kSplitThreads, split_occupancy(ND, NT)) void attend
 #pragma unroll
                     for (int y = 0; y < 4 * ND; ++y) {
                         const uint32_t v = (vs[y >> 1] >> (16 * (y & 1))) & 0xFFFF;
-                        fin = v < 0x7C00u && v > fin ? v : fin;
                         // A scale that is not finite makes the block NaN in the
                         // rows that see the key, and does not reach the others.
                         if (v >= 0x7C00u) {
@@ -656,13 +761,10 @@ __global__ __launch_bounds__(kSplitThreads, split_occupancy(ND, NT)) void attend
                     }
                 }
                 wave_fence();
-                fin = wave_max_u32(fin);
-                // Below 2^e: the exponent of the next power of two.
-                const int e = (int)(fin >> 10) == 0 ? -14 : (int)(fin >> 10) - 14;
-                if (fin > 0 && e > E) {
-                    E = e;
-                    limit_bits = (uint32_t)(e + 15) << 10;
-                    limit_bits -= 1;
+                if (next_E != E) {
+                    E = next_E;
+                    low2 = from<kSplitSpan>(E) * 0x10001u;
+                    span2 = (past(E) - 1 - from<kSplitSpan>(E)) * 0x10001u;
                 }
                 const float F = (float)(9 - E);
 #pragma unroll
@@ -719,6 +821,11 @@ __global__ __launch_bounds__(kSplitThreads, split_occupancy(ND, NT)) void attend
                         o[x][d][2 * y + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, pf[x][d], o[x][d][2 * y + 1], 0, 0, 0);
                     }
                 }
+            if (repeated) {
+#pragma unroll
+                for (int x = 0; x < NT; ++x)
+                    l[x] = sh.in.kept[wave][2 * x][lane] * __builtin_amdgcn_exp2f(nk[x] - sh.in.kept[wave][2 * x + 1][lane]);
+            }
         }
 
         // Results, 16 rows at a time.  A row's weights stand relative to 2^ref.
@@ -878,8 +985,8 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs g) {
 // They become (c - zero) scale 2^-E, with 2^E for keys and one for values such
 // that all scales are from 2^(E - 14) to 2^E: normal numbers in fp16, each rounded
 // by 2^-11 of itself, whatever the largest scale of the tile is and whoever
-// sees it (with 2^E above the largest scale alone, one of 65504 that a row did
-// not even see left 0 of its values of scale 0.001).  The sum of a row's weights is that of the fp32
+// sees it (with 2^E above the largest scale alone, values of scale 0.0015 beside
+// others of 65504, seen or not, were off by 0.8 of themselves, now by 3e-4).  The sum of a row's weights is that of the fp32
 // weights: with the sum of the rounded ones, one instruction for two of them,
 // lse was off by up to 2^-11.
 //
@@ -1003,24 +1110,9 @@ __device__ __forceinline__ u32x4_t decode8(uint32_t w, half2_t off, half2_t s, u
     return o;
 }
 
-// The exponent e with a finite fp16 of these bits below 2^e.
-__device__ __forceinline__ int exponent_above(uint32_t bits) {
-    return bits == 0 ? -24 : bits < 0x400u ? -14 : (int)(bits >> 10) - 14;
-}
-
-// The bits of the largest fp16 below 2^e.
-__device__ __forceinline__ int below(int e) { return e <= -14 ? (e < -14 ? 0 : 0x3FF) : ((e + 15) << 10) - 1; }
-
 // A tile's scales from 2^(e - 14) to 2^e are normal in fp16 under 2^-e, so that
-// keys and values are rounded by 2^-11 of themselves.  The bits of the smallest:
+// keys and values are rounded by 2^-11 of themselves.
 constexpr int kSpan = 14;
-__device__ __forceinline__ uint32_t from(int e) {
-    return e <= kSpan - 24 ? 1 : e < kSpan - 14 ? 1u << (e - kSpan + 24) : (uint32_t)(e - kSpan + 15) << 10;
-}
-// Whether a scale of these bits is neither 0 nor in those of exponent e.
-__device__ __forceinline__ bool outside(uint32_t bits, int e) {
-    return bits != 0 && bits - from(e) >= (uint32_t)(below(e) + 1) - from(e);
-}
 
 struct TileScales {
     uint32_t key_top, key_bottom, value_top, value_bottom;  // bits of the largest finite scale, 0x7C00 less the smallest but 0
@@ -1185,9 +1277,9 @@ __device__ __forceinline__ TileEnd attend_tile(const AttendArgs &g, TileShared<N
             const Raw &c = coming[i];
             const bool value = is_value(i);
             const uint32_t bits = c.ok && (value || !EXACT) ? c.scale : 0;
-            if (__any(outside(bits, value ? ev : ek) || c.hidden)) {
+            if (__any(outside<kSpan>(bits, value ? ev : ek) || c.hidden)) {
                 const bool fin = bits < 0x7C00u;
-                const uint32_t rare = (__any(fin && outside(bits, value ? ev : ek)) ? (uint32_t)kOutside : 0u) |
+                const uint32_t rare = (__any(fin && outside<kSpan>(bits, value ? ev : ek)) ? (uint32_t)kOutside : 0u) |
                                       (value && __any(!fin) ? (uint32_t)kWild : 0u) | (__any(c.hidden) ? (uint32_t)kHidden : 0u);
                 if (lane == 0) atomicOr(&news[tile % 3], rare);
             }
@@ -1231,16 +1323,9 @@ __device__ __forceinline__ TileEnd attend_tile(const AttendArgs &g, TileShared<N
         __syncthreads();
         const TileScales n = scales;
         wild = __builtin_amdgcn_readfirstlane(n.wild);
-        auto fit = [&](uint32_t x, uint32_t y, int &e) {
-            x = __builtin_amdgcn_readfirstlane(x);
-            y = 0x7C00u - (uint32_t)__builtin_amdgcn_readfirstlane(y);
-            e = exponent_above(x);
-            const int most = x == 0 ? -24 : kSpan + (y < 0x400u ? 7 - __builtin_clz(y) : (int)(y >> 10) - 15);  // y is 2^(most - 14) at least
-            const bool within = e <= most;
-            e = min(e + (within ? (most - e + 1) / 2 : 0), 16);
-            return within;
-        };
-        const bool keys = fit(n.key_top, n.key_bottom, ek), values = fit(n.value_top, n.value_bottom, ev);
+        auto bits = [](uint32_t x) { return (uint32_t)__builtin_amdgcn_readfirstlane(x); };
+        const bool keys = fit<kSpan>(bits(n.key_top), 0x7C00u - bits(n.key_bottom), &ek);
+        const bool values = fit<kSpan>(bits(n.value_top), 0x7C00u - bits(n.value_bottom), &ev);
         return keys && values;
     };
     uint32_t mask = 0x000F000Fu, magic = 0x64006400u;  // 1024 + code
@@ -1451,7 +1536,7 @@ __device__ __forceinline__ TileEnd attend_tile(const AttendArgs &g, TileShared<N
                 for (int i = 0; i < kLoads; ++i) {
                     if (!is_piece(i) || !is_value(i)) continue;
                     const int in = (tid + kTileThreads * i) % kUnits;
-                    const uint32_t sb = coming[i].ok && coming[i].scale < 0x7C00u && !outside(coming[i].scale, e) ? coming[i].scale : 0;
+                    const uint32_t sb = coming[i].ok && coming[i].scale < 0x7C00u && !outside<kSpan>(coming[i].scale, e) ? coming[i].scale : 0;
                     put(coming[i], true, 0, in / (2 * ND), in % (2 * ND), (_Float16)ldexpf(f16_bits_to_f32(sb), -e));
                 }
             };

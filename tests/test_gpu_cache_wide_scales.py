@@ -37,6 +37,13 @@ SHAPES = [  # lens, new tokens, heads, G, D
     ([400, 130], [120, 50], 1, 2, 192),
     ([1200], [50], 1, 1, 256),               # keys dealt to several workgroups
     ([2600, 700], [150, 300], 1, 2, 128),
+    ([170, 99], [80, 1], 2, 4, 128),
+    ([170, 99], [5, 1], 2, 4, 128),          # drafts: rows of a tile of keys see different ones
+    ([700, 90], [7, 5], 1, 2, 192),
+    ([2100, 40], [4, 3], 1, 3, 64),
+    ([700, 90], [9, 3], 1, 7, 128),
+    ([600, 1500], [8, 2], 1, 4, 256),
+    ([400, 300], [30, 2], 1, 2, 64),
 ]
 
 
@@ -81,7 +88,8 @@ def test_scales_of_every_size_side_by_side(env, i, low, high):
     b.check(env, f"scales {low} to {high}", dtype="float32", window=33)
 
 
-@pytest.mark.parametrize("lens,new,heads,G,D", SHAPES)
+@pytest.mark.parametrize("lens,new,heads,G,D", SHAPES + [
+    ([300, 200, 90], [1, 1, 1], 2, 8, 128), ([4000, 9], [1, 1], 1, 5, 256), ([5000, 100], [1, 1], 2, 2, 128)])
 def test_blocks_of_a_row_far_apart(env, lens, new, heads, G, D):
     """The first block's values 2^16 to 2^30 times the last one's: every block's
     outputs within its own bound, in keys alike and in one key of 37."""
@@ -97,7 +105,8 @@ def test_blocks_of_a_row_far_apart(env, lens, new, heads, G, D):
 
 
 @pytest.mark.parametrize("lens,new,heads,G,D", [([900, 300], [90, 80], 1, 2, 128), ([700], [300], 2, 2, 64),
-                                                ([1100], [40], 1, 2, 256)])
+                                                ([1100], [40], 1, 2, 256), ([1500, 40], [6, 2], 2, 2, 64),
+                                                ([1100], [1], 1, 4, 128), ([1100], [9], 1, 7, 128)])
 def test_stretches_of_large_and_small_values(env, lens, new, heads, G, D):
     """Tiles of large values, of small ones and of both in turn: what has been
     summed is carried from one power of two to the next, up and down."""
@@ -115,7 +124,7 @@ def test_stretches_of_large_and_small_values(env, lens, new, heads, G, D):
     b.check(env, "stretches", dtype="float32", causal=False)
 
 
-@pytest.mark.parametrize("new", [[80, 50]])
+@pytest.mark.parametrize("new", [[80, 50], [80, 1], [4, 1], [1, 1]])
 def test_large_values_of_no_weight(env, new):
     """A seen key of the largest value scale whose weight is far below what its
     output would notice, and outputs from small values beside it."""
@@ -134,3 +143,28 @@ def test_large_values_of_no_weight(env, new):
     renew(env, b)
     out, _ = b.check(env, "no weight", dtype="float32")
     assert out[:new[0]].abs().max() < 0.1
+
+
+@pytest.mark.parametrize("lens,new,heads,G,D", SHAPES)
+def test_not_finite_among_scales_far_apart(env, lens, new, heads, G, D):
+    """A NaN scale of one block of one value in a tile of scales far apart: its
+    block is NaN in the rows that see it, all else within the bound."""
+    b = batch(env, lens, new, heads, G, D, 950 + D, 2.0 ** -20, 2.0 ** 6, slack=80)
+    bad = lens[0] - max(1, new[0] // 2)
+    ids, at = _rows_of(b, 0, [bad])
+    scale = b.planes["v_scales"][ids[0], :, at[0], -1].copy()
+    b.planes["v_scales"][ids[0], :, at[0], -1] = np.nan
+    renew(env, b)
+    torch, q4, dev = env
+    o2 = q4.q4_cache_attend(*b.dev, q_offsets=b.offsets_dev, max_q=b.max_q, out_dtype=torch.float32)
+    o1, _ = q4.q4_cache_attend(*b.dev, q_offsets=b.offsets_dev, max_q=b.max_q, out_dtype=torch.float32, return_lse=True)
+    b.planes["v_scales"][ids[0], :, at[0], -1] = scale
+    want, bound, _, _, _ = ref.attend(b.q.astype(np.float64), b.planes, b.table, b.lens, b.offsets, out_bf16=False)
+    sees = np.zeros(b.q.shape[0], bool)
+    sees[:new[0]] = lens[0] - new[0] + np.arange(new[0]) >= bad
+    for got in (o1, o2):
+        g = got.cpu().numpy()
+        assert np.isnan(g[sees][..., D - 64:]).all() and np.isfinite(g[~sees]).all()
+        within(got[torch.from_numpy(~sees).to(dev)], want[~sees], bound[~sees], "rows that do not see it")
+        if D > 64:
+            within(got[torch.from_numpy(sees).to(dev)][..., :D - 64], want[sees][..., :D - 64], bound[sees][..., :D - 64], "its other blocks")
