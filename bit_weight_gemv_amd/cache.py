@@ -72,6 +72,8 @@ class KVCache:
 def q4_cache_new(pages: int, heads: int, page: int, D: int, device) -> KVCache:
     """An uninitialised cache of pages * page positions."""
     torch = _base.torch_module()
+    if D <= 0 or D % 64:
+        raise ValueError("D must be a positive multiple of 64")
     planes = []
     for _ in range(2):
         planes.append(torch.empty((pages, heads, page, D // 2), dtype=torch.uint8, device=device))
