@@ -143,22 +143,29 @@ def q4_cache_append(cache, k, v, slots, positions=None, inv_freq=None, interleav
     return q_out
 
 
-def q4_cache_read(cache, slots, out_dtype=None, k_out=None, v_out=None, stream=None):
+def q4_cache_read(cache, slots, out_dtype=None, k_out=None, v_out=None, stream=None, keys=True, values=True):
     """(keys, values) [n, heads, D] of the slots int32 [n], in bf16 or fp32;
-    a slot outside the cache reads as zeros."""
+    a slot outside the cache reads as zeros.  keys or values False: not read,
+    and None in its place."""
     torch = _base.torch_module()
     dev = cache.device
     _base.check(slots, "slots", torch.int32, dev)
     n = slots.numel()
+    if not (keys or values):
+        raise ValueError("neither keys nor values to read")
+    if (k_out is not None and not keys) or (v_out is not None and not values):
+        raise ValueError("an output of what is not read")
     if out_dtype is None:
         out_dtype = k_out.dtype if k_out is not None else v_out.dtype if v_out is not None else torch.bfloat16
     kind = _base.out_type(out_dtype, "out_dtype")
     shape = (n, cache.heads, cache.D)
     with _base.on(dev, stream) as st:
-        k_out = st.output(k_out, shape, out_dtype, "k_out")
-        v_out = st.output(v_out, shape, out_dtype, "v_out")
-        r = _base.function("q4_cache_read", _ARGS)(cache.pointer, slots.data_ptr(), n, kind, k_out.data_ptr(),
-                                                   v_out.data_ptr(), st.handle)
+        if keys:
+            k_out = st.output(k_out, shape, out_dtype, "k_out")
+        if values:
+            v_out = st.output(v_out, shape, out_dtype, "v_out")
+        r = _base.function("q4_cache_read", _ARGS)(cache.pointer, slots.data_ptr(), n, kind, k_out.data_ptr() if keys else None,
+                                                   v_out.data_ptr() if values else None, st.handle)
     _base.raise_for(r, "q4_cache_read")
     return k_out, v_out
 
