@@ -40,9 +40,10 @@ extern "C" {
  * of page p for head h; slot p * page + i names that position in all heads.
  *   codes: uint8 [pages][heads][page][D/2], 16-byte aligned;
  *   scales, zeros: fp16 bits [pages][heads][page][D/64], 16-byte aligned.
- * A value is (code - zero) * scale.  Zeros are integers from 0 to 15 (what
- * q4_cache_append and q4_pack_affine write; for others the results of
- * q4_cache_attend are unspecified).  pages * page < 2^31.
+ * A value is (code - zero) * scale.  For q4_cache_attend zeros are integers
+ * from 0 to 15 and scales positive or 0, not -0 (what q4_cache_append and
+ * q4_pack_affine write), or NaN for a block that is; a token that sees a key
+ * of other ones has unspecified results.  pages * page < 2^31.
  */
 typedef struct {
     uint8_t *k_codes;
@@ -105,11 +106,16 @@ int q4_cache_read(const q4_cache *cache, const int32_t *slots, int64_t n,
  *   lse = ln sum_i exp(s_i).
  * A token that sees no key, or only scores of -infinity, gets zeros and an
  * lse of -infinity.  Keys that a token does not see never reach its output,
- * whatever they hold; a NaN or an infinity that it sees does, as in the
- * formula.  Weights, and in prompts decoded values, are rounded to fp16 (2^-11
- * each); keys are exact where there are few tokens or lse is asked for, and
- * rounded to fp16 otherwise, so that the bits of out may differ between calls
- * with lse and without.  lse has the precision of fp32.
+ * whatever they hold; a NaN that it sees does, as in the formula: of a value
+ * in the outputs of its block, of a key in all.  (The bits of its sums may
+ * differ with what other tokens of the call see.)  A row of q that holds a NaN
+ * or an infinity and sees a key gets NaN, or what the formula gives.  Weights,
+ * and in prompts decoded values, are rounded to fp16 (2^-11 each, of themselves:
+ * whatever other blocks and keys hold); keys are exact where there are few
+ * tokens or lse is asked for, and rounded to fp16 otherwise, so that the bits
+ * of out may differ between calls with lse and without.  lse has the precision
+ * of fp32.  Scores are below 2^24 in magnitude (fp32 does not hold the
+ * differences of larger ones, whose rows are unspecified).
  *   q: bf16 bits [T][q_heads][D], 16-byte aligned, tokens q_stride elements
  *     apart (>= q_heads * D, a multiple of 8).  q_heads is a multiple of
  *     heads.
@@ -121,7 +127,7 @@ int q4_cache_read(const q4_cache *cache, const int32_t *slots, int64_t n,
  *   max_q: at most this many new tokens belong to one sequence (with
  *     q_offsets NULL: 1); tokens of a sequence past it keep what out and lse
  *     held.  It chooses the kernels and their grids.
- *   scale: finite and positive.  window >= 0, 0 where causal == 0.
+ *   scale: finite and positive, whatever the size.  window >= 0, 0 where causal == 0.
  *   out: [T][q_heads][D] of out_type (Q4_OUT_F32 or Q4_OUT_BF16), 16-byte
  *     aligned.  lse: fp32 [T][q_heads], 4-byte aligned, or NULL.
  *   workspace: q4_cache_attend_ws_bytes(...) bytes, 16-byte aligned; calls
