@@ -54,7 +54,7 @@ struct AttendArgs {
 // bf16 bits) 2^top to 2^(top + 1) then; kappa = scale log2 e 2^(shift - ex)
 // makes exponents of 2 of the scores.  kappa times 2^low stays a normal number
 // (a masked score is -infinity, and -infinity times 0 a NaN), so that rows of
-// zeros, and rows so small that no score reaches 2^-90, get a smaller ex; and
+// zeros, and rows so small that no score reaches 2^-60, get a smaller ex; and
 // kappa times 2^high stays finite, so that scores of 0 stay 0.
 struct RowScale {
     int ex;
@@ -148,8 +148,8 @@ __device__ __forceinline__ Sequence sequence_uniform(const CacheAttend &a, int64
 // share from the lengths.  What a wave begins and does not end, or ends and did
 // not begin, goes to the workspace, and a second launch joins the pieces in
 // order (the same bits on every call).  64 tokens on up to 8192 ragged keys, 40
-// + 8 heads of 128: 67 us, 4.2 TB/s, and 8 for the joining (dealt by
-// workgroups instead of waves 115 in all; a copy of the same bytes 64).  Vector
+// + 8 heads of 128: 66 us, 4.2 TB/s, and 9 for the joining (a kernel trace;
+// dealt by workgroups instead of waves 115 in all; a copy of the same bytes 64).  Vector
 // instructions are under way for two thirds of the cycles, products for 0.11.
 // ---------------------------------------------------------------------------
 
@@ -986,17 +986,19 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs g) {
 // that all scales are from 2^(E - 14) to 2^E: normal numbers in fp16, each rounded
 // by 2^-11 of itself, whatever the largest scale of the tile is and whoever
 // sees it (with 2^E above the largest scale alone, values of scale 0.0015 beside
-// others of 65504, seen or not, were off by 0.8 of themselves, now by 3e-4).  The sum of a row's weights is that of the fp32
-// weights: with the sum of the rounded ones, one instruction for two of them,
-// lse was off by up to 2^-11.
+// others of 65504, seen or not, were off by 0.8 of themselves, now by 3e-4).
+// The sum of a row's weights is that of the fp32 weights: with the sum of the
+// rounded ones, one instruction for two of them, lse was off by up to 2^-11.
 //
 // Where the rows are few for the card, the keys of a tile of rows are dealt to
 // several workgroups, whose results a second launch joins.
-// 512 tokens behind 32488, 40 + 8 heads of 128: 403 us, 850 TFLOP/s (a large
-// library product makes 1153); prompts of 8191 tokens, 16 + 2 heads, 165.  A tile of
-// 64 keys costs about 5000 cycles: QK 1190, PV 770, decoding 1230, maximum and
-// softmax 1040, barrier and exponents 950, overlapped only in part by the two
-// waves of a SIMD.  256 rows: with 128 the decoding would weigh twice.
+// 512 tokens behind 32488, 40 + 8 heads of 128: 393 to 397 us, 865 TFLOP/s (a
+// large library product makes 1153); prompts of 8191 tokens, 16 + 2 heads, 171 to
+// 175, of which 9 are the kernels of few rows (calls in a replayed graph).  A
+// tile of 64 keys cost about 5000 cycles while it told of its largest scales (3 in
+// 100 more than now): QK 1190, PV 770, decoding 1230, maximum and softmax 1040,
+// barrier and exponents 950, overlapped only in part by the two waves of a
+// SIMD.  256 rows: with 128 the decoding would weigh twice.
 // ---------------------------------------------------------------------------
 
 constexpr int kRowTile = 256;
@@ -1074,9 +1076,8 @@ __device__ __forceinline__ bool find_row_tile(const AttendArgs &g, int64_t index
     if (g.parts > 1) {
         // In proportion to the keys, the most that any tile of rows sees in all:
         // by the lengths, since a table may be far wider (512 tokens behind
-        // 32488 in a table for 131072 397 us; by the table's width, which gives
-        // them one part, 1114).  Prompts in such a table pay for workgroups that
-        // find nothing to do (2048 tokens 100 us instead of 89).
+        // 32488 in a table for 131072 394 us as in one for 33000; in one part,
+        // as by that width, 1031).
         const int keys = __builtin_amdgcn_readfirstlane(longest[0]), before = __builtin_amdgcn_readfirstlane(longest[1]);
         const int parts = before <= keys / 2 ? g.prompt_parts : g.prefix_parts;
         int each = (keys + kKeyTile * parts - 1) / (kKeyTile * parts);
@@ -1128,9 +1129,9 @@ enum { kWild = 1, kHidden = 2, kOutside = 4 };
 // 64 by its scale over that of the next, so that it has the precision of fp32.
 // For calls that ask for lse, which is fp32: from keys rounded to fp16 it was
 // off by 3e-5 of itself, and is by 6e-8.  out, of weights and values in fp16,
-// gains nothing that a bf16 shows, and EXACT costs (512 tokens behind 32488 481
-// us instead of 394, prompts of 8191 213 instead of 173, with D = 64 141
-// instead of 124, with 256 531 instead of 394).
+// gains nothing that a bf16 shows, and EXACT costs (512 tokens behind 32488 484
+// us instead of 394, prompts of 8191 214 instead of 173, with D = 64 141
+// instead of 123, with 256 507 instead of 374).
 // FAR: keys as in EXACT, and values in as many powers of two as a tile of keys
 // needs (14 at a time), a tile after the other: right for whatever scales a
 // cache may hold, and twice as slow (512 tokens behind 32488: 394 us; begun
@@ -1623,6 +1624,15 @@ __device__ __forceinline__ TileEnd attend_tile(const AttendArgs &g, TileShared<N
     return kDone;
 }
 
+// FAR as a call, for D = 256: inlined, it had the loop of the others keep more in
+// scratch memory (prompts of 8191 tokens 393 us instead of 374, with lse 534
+// instead of 507; with D = 128 it is the better: 172 instead of 173, 214 instead of 217).
+template <int ND, int KB>
+__device__ __attribute__((noinline)) void attend_tile_far(AttendArgs g, TileShared<ND, KB> *sh, RowTile rt, int64_t index, int h,
+                                                          int part) {
+    attend_tile<ND, KB, kFar>(g, *sh, rt, index, h, part, false, (int)threadIdx.x);
+}
+
 template <int ND, int KB, bool EXACT>
 __global__ __launch_bounds__(kTileThreads, 1) void attend_tile_kernel(AttendArgs g) {
     __shared__ __attribute__((aligned(16))) TileShared<ND, KB> sh;
@@ -1648,8 +1658,12 @@ __global__ __launch_bounds__(kTileThreads, 1) void attend_tile_kernel(AttendArgs
         __syncthreads();
         if (end == kTooFar || all) break;
     }
-    asm volatile("" : "+v"(tid));
-    attend_tile<ND, KB, kFar>(g, sh, rt, index, h, part, false, tid);
+    if constexpr (ND == 4) {
+        attend_tile_far<ND, KB>(g, &sh, rt, index, h, part);
+    } else {
+        asm volatile("" : "+v"(tid));
+        attend_tile<ND, KB, kFar>(g, sh, rt, index, h, part, false, tid);
+    }
 }
 
 // Joins the parts of a tile of rows: 4 dimensions of a row a lane.
@@ -1732,11 +1746,11 @@ static int split_waves(int nd, int64_t rows) { return 256 * kSplitWaves * split_
 // Workgroups that the keys of each of n tiles of rows are dealt to, each one
 // more costing 4 in 100 for the joining.  Behind a long prefix all tiles see
 // about as many keys: as few rounds of the 256 compute units for each key as
-// possible (512 tokens behind 32488 and 8 key heads: 3 parts 405 us, 5 parts
-// 480; 64 tokens: 16 parts 103 us, 8 parts 163).  In a prompt they see half as
+// possible (512 tokens behind 32488 and 8 key heads: 3 parts 393 us, 5 parts
+// 467; 64 tokens: 16 parts 97 us, 8 parts 154).  In a prompt they see half as
 // many as the last one on average: the parts of that one should take no longer
 // than the card does with all (4096 tokens and 2 key heads: 3 parts 150 us, 2
-// parts 138).
+// parts 135).
 static int key_parts(int64_t n, bool prompt) {
     int best_parts = 1;
     double best = 0;
