@@ -126,7 +126,8 @@ int q4_cache_read(const q4_cache *cache, const int32_t *slots, int64_t n,
  *     every sequence keep what out and lse held.
  *   max_q: at most this many new tokens belong to one sequence (with
  *     q_offsets NULL: 1); tokens of a sequence past it keep what out and lse
- *     held.  It chooses the kernels and their grids.
+ *     held.  It chooses the kernels and their grids: single tokens beside
+ *     longer rows are faster in a call of their own.
  *   scale: finite and positive, whatever the size.  window >= 0, 0 where causal == 0.
  *   out: [T][q_heads][D] of out_type (Q4_OUT_F32 or Q4_OUT_BF16), 16-byte
  *     aligned.  lse: fp32 [T][q_heads], 4-byte aligned, or NULL.
