@@ -40,7 +40,7 @@ def batch(env, i, key_scales):
 
 
 @pytest.mark.parametrize("i", range(len(SHAPES)))
-@pytest.mark.parametrize("scale", [1e-38, 1e-30, 1e-12, 0.01, None, 1.0])
+@pytest.mark.parametrize("scale", [1e-45, 1e-38, 1e-30, 1e-12, 0.01, None, 1.0])
 @pytest.mark.parametrize("window", [0, 21])
 def test_rows_of_zeros_take_the_mean_of_what_they_see(env, i, scale, window):
     for what, scales in (("zero and tiny keys", (0.0, 2.0 ** -14, 2.0 ** -20)),

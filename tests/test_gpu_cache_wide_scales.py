@@ -168,3 +168,62 @@ def test_not_finite_among_scales_far_apart(env, lens, new, heads, G, D):
         within(got[torch.from_numpy(~sees).to(dev)], want[~sees], bound[~sees], "rows that do not see it")
         if D > 64:
             within(got[torch.from_numpy(sees).to(dev)][..., :D - 64], want[sees][..., :D - 64], bound[sees][..., :D - 64], "its other blocks")
+
+
+@pytest.mark.parametrize("lens,new,heads,G,D", [([900, 300], [90, 80], 1, 2, 128), ([300, 170], [1, 1], 2, 4, 128), ([2100, 40], [4, 3], 1, 3, 64),
+                                                ([400], [60], 1, 1, 256)])
+def test_captured_calls_as_the_scales_grow_apart(env, lens, new, heads, G, D):
+    """One captured call, replayed as the cache's scales change in place: close
+    together, one far from the others, far apart everywhere, all zero."""
+    torch, q4, dev = env
+    b = renew(env, batch(env, lens, new, heads, G, D, 970 + D, 0.1, 0.5, slack=80))
+    rng = np.random.default_rng(4)
+    out = torch.empty(b.q.shape, dtype=torch.float32, device=dev)
+    lse = torch.empty(b.q.shape[:2], device=dev)
+    need = q4.q4_cache_attend_ws_bytes(b.q.shape[0], heads * G, heads, D, len(lens), b.max_q)
+    ws = torch.empty(need, dtype=torch.uint8, device=dev)
+    kw = dict(q_offsets=b.offsets_dev, max_q=b.max_q)
+
+    def both(o, l):
+        q4.q4_cache_attend(*b.dev, out=o, workspace=ws, **kw)
+        q4.q4_cache_attend(*b.dev, out=torch.empty_like(o), lse=l, workspace=ws, **kw)
+
+    both(out, lse)
+    torch.cuda.synchronize()
+    g, st = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(st):
+        with torch.cuda.graph(g, stream=st):
+            both(out, lse)
+    torch.cuda.synchronize()
+    shape = b.planes["v_scales"].shape
+    steps = [logarithmic(rng, 0.1, 0.5, shape) for _ in range(4)]
+    ids, at = _rows_of(b, 0, [37])
+    steps[1][ids[0], :, at[0]] = 65504
+    steps[2] = logarithmic(rng, 2.0 ** -24, 2.0 ** 10, shape)
+    steps[3][:] = 0
+    for n, scales in enumerate(steps + steps[:1]):
+        b.planes["v_scales"] = scales
+        b.cache = b.dev[1]
+        b.cache.v_scales.copy_(torch.from_numpy(scales))
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        eager, eager_lse = torch.empty_like(out), torch.empty_like(lse)
+        both(eager, eager_lse)
+        assert torch.equal(out, eager) and torch.equal(lse, eager_lse), n
+        want, bound, l, lb, _ = ref.attend(b.q.astype(np.float64), b.planes, b.table, b.lens, b.offsets, out_bf16=False)
+        within(out, want, bound, f"replay {n}")
+        within(lse, l, lb, f"replay {n} lse")
+
+
+@pytest.mark.parametrize("lens,new,heads,G,D", SHAPES)
+def test_hidden_pages_among_scales_far_apart(env, lens, new, heads, G, D):
+    torch, q4, dev = env
+    b = batch(env, lens, new, heads, G, D, 990 + D, 2.0 ** -20, 2.0 ** 10, slack=80)
+    for row in b.table:
+        row[1:6:2] = (-1, len(b.planes["k_codes"]), 2 ** 31 - 1)
+    renew(env, b)
+    b.dev = b.dev[:2] + (torch.from_numpy(b.table).to(dev), b.dev[3])
+    b.check(env, "hidden", dtype="float32")
+    b.check(env, "hidden", dtype="float32", window=50)
