@@ -185,8 +185,10 @@ def q4_cache_attend(q, cache, table, lens, q_offsets=None, max_q=None, causal=Tr
     tokens that a sequence has (T where none is given).  A token sees the keys
     up to its own position (causal), the last `window` of them if window > 0.
     scale: 1 / sqrt(D) where none is given.  Returns out [T, q_heads, D] (bf16
-    or fp32), with return_lse (out, lse fp32 [T, q_heads]); prompts are slower
-    with lse, whose scores are kept in fp32's precision."""
+    or fp32; weights are rounded by 2^-11 for both), with return_lse (out, lse
+    fp32 [T, q_heads]); prompts are slower with lse, whose scores are kept in
+    fp32's precision.  Single tokens beside longer rows are faster in a call of
+    their own."""
     torch = _base.torch_module()
     dev, D = cache.device, cache.D
     qs = _tokens(q, "q", D, torch.bfloat16, dev)
