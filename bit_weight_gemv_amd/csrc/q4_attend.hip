@@ -1135,9 +1135,9 @@ enum { kWild = 1, kHidden = 2, kOutside = 4 };
 // FAR: keys as in EXACT, and values in as many powers of two as a tile of keys
 // needs (14 at a time), a tile after the other: right for whatever scales a
 // cache may hold, and twice as slow (512 tokens behind 32488: 394 us; begun
-// again under other powers of two, for one value scale 128 times the others,
-// 486; FAR for one that is 2^18 times the others 780, for scales from 2^-20 to
-// 1 everywhere 1050).
+// again under other powers of two, for one value scale 2^11 times the others,
+// 490; FAR for one that is 2^18 times the others 783, for scales from 2^-20 to
+// 1 everywhere 1055).
 enum TileMode { kRounded, kExact, kFar };
 
 template <int ND, int KB>

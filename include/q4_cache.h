@@ -114,8 +114,8 @@ int q4_cache_read(const q4_cache *cache, const int32_t *slots, int64_t n,
  * whatever other blocks and keys hold), in fp32 outputs too; keys are exact
  * where there are few tokens or lse is asked for, and rounded to fp16 otherwise,
  * so that the bits of out may differ between calls with lse and without.  lse
- * has the precision of fp32.  Scores are below 2^24 in magnitude (fp32 does not hold the
- * differences of larger ones, whose rows are unspecified).
+ * has the precision of fp32.  Scores are below 2^24 in magnitude (fp32 does not
+ * hold the differences of larger ones, whose rows are unspecified).
  *   q: bf16 bits [T][q_heads][D], 16-byte aligned, tokens q_stride elements
  *     apart (>= q_heads * D, a multiple of 8).  q_heads is a multiple of
  *     heads.
