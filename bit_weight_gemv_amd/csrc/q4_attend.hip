@@ -255,8 +255,10 @@ template <int CTRL>
 __device__ __forceinline__ uint32_t dpp_u32(uint32_t v) {
     return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, true);
 }
-__device__ __forceinline__ uint32_t pk_sub(uint32_t a, uint32_t b) {
-    return __builtin_bit_cast(uint32_t, (u16x2_t)(__builtin_bit_cast(u16x2_t, a) - __builtin_bit_cast(u16x2_t, b)));
+// Each of two 16-bit integers less that of b, and 0 where it is 0.
+__device__ __forceinline__ uint32_t pk_sub_but_0(uint32_t a, uint32_t b) {
+    const u16x2_t x = __builtin_bit_cast(u16x2_t, a), one = {1, 1};
+    return __builtin_bit_cast(uint32_t, (u16x2_t)(x - __builtin_elementwise_min(x, one) * __builtin_bit_cast(u16x2_t, b)));
 }
 __device__ __forceinline__ uint32_t half_max(uint32_t v) { return (v >> 16) > (v & 0xFFFF) ? v >> 16 : v & 0xFFFF; }
 // The larger of pairs of 16-bit integers over the wave.
@@ -618,23 +620,21 @@ __global__ __launch_bounds__(kSplitThreads, split_occupancy(ND, NT)) void attend
             const int key = lo_key + tile * kTile;
             const bool edge = !ok[0] || !ok[1] || key + kTile > s.len || key < low_key;
             if (__builtin_expect(edge, 0)) {
-                // Keys that no row sees may hold anything: scales and zeros of 0,
-                // value scales (whose weights are 0) within E.
+                // Keys that no row sees may hold anything: scales and zeros of 0.
                 asm volatile("");  // (a branch, not selects)
 #pragma unroll
                 for (int d = 0; d < ND; ++d) {
                     const int c = lane + 64 * d, in = c % (16 * ND), t = in >= 8 * ND, y = 2 * (in - t * 8 * ND);
                     const bool page_ok = t ? ok[1] : ok[0];
                     const int k0 = key + 16 * t + y / ND, k1 = key + 16 * t + (y + 1) / ND;
-                    const uint32_t fill = has_scales(d) ? low2 : 0;
-                    if (!page_ok || k0 >= s.len || k0 < low_key) T.par[d] = (T.par[d] & 0xFFFF0000u) | (fill & 0xFFFF);
-                    if (!page_ok || k1 >= s.len || k1 < low_key) T.par[d] = (T.par[d] & 0xFFFF) | (fill & 0xFFFF0000u);
+                    if (!page_ok || k0 >= s.len || k0 < low_key) T.par[d] &= 0xFFFF0000u;
+                    if (!page_ok || k1 >= s.len || k1 < low_key) T.par[d] &= 0x0000FFFFu;
                 }
             }
-            // Value scales that are not within E.
+            // Value scales that are not within E (0 is: blocks of padded heads).
             bool odd = false;
 #pragma unroll
-            for (int d = 0; d < ND; ++d) odd = odd || (has_scales(d) && pk_max(pk_sub(T.par[d], low2), span2) != span2);
+            for (int d = 0; d < ND; ++d) odd = odd || (has_scales(d) && pk_max(pk_sub_but_0(T.par[d], low2), span2) != span2);
             const bool repeated = cut < 0x7C00u;
             bool again = false, grown = false;
             int next_E = E;
