@@ -1131,7 +1131,7 @@ enum { kWild = 1, kHidden = 2, kOutside = 4 };
 // off by 3e-5 of itself, and is by 6e-8.  out, of weights and values in fp16,
 // gains nothing that a bf16 shows, and EXACT costs (512 tokens behind 32488 484
 // us instead of 394, prompts of 8191 214 instead of 173, with D = 64 141
-// instead of 123, with 256 507 instead of 374).
+// instead of 123, with 256 533 instead of 393).
 // FAR: keys as in EXACT, and values in as many powers of two as a tile of keys
 // needs (14 at a time), a tile after the other: right for whatever scales a
 // cache may hold, and twice as slow (512 tokens behind 32488: 394 us; begun
@@ -1624,15 +1624,6 @@ __device__ __forceinline__ TileEnd attend_tile(const AttendArgs &g, TileShared<N
     return kDone;
 }
 
-// FAR as a call, for D = 256: inlined, it had the loop of the others keep more in
-// scratch memory (prompts of 8191 tokens 393 us instead of 374, with lse 534
-// instead of 507; with D = 128 it is the better: 172 instead of 173, 214 instead of 217).
-template <int ND, int KB>
-__device__ __attribute__((noinline)) void attend_tile_far(AttendArgs g, TileShared<ND, KB> *sh, RowTile rt, int64_t index, int h,
-                                                          int part) {
-    attend_tile<ND, KB, kFar>(g, *sh, rt, index, h, part, false, (int)threadIdx.x);
-}
-
 template <int ND, int KB, bool EXACT>
 __global__ __launch_bounds__(kTileThreads, 1) void attend_tile_kernel(AttendArgs g) {
     __shared__ __attribute__((aligned(16))) TileShared<ND, KB> sh;
@@ -1658,12 +1649,10 @@ __global__ __launch_bounds__(kTileThreads, 1) void attend_tile_kernel(AttendArgs
         __syncthreads();
         if (end == kTooFar || all) break;
     }
-    if constexpr (ND == 4) {
-        attend_tile_far<ND, KB>(g, &sh, rt, index, h, part);
-    } else {
-        asm volatile("" : "+v"(tid));
-        attend_tile<ND, KB, kFar>(g, sh, rt, index, h, part, false, tid);
-    }
+    // (As a call that is not inlined it took 612 MB of scratch memory where D = 256
+    // instead of 109, for 376 us instead of 393.)
+    asm volatile("" : "+v"(tid));
+    attend_tile<ND, KB, kFar>(g, sh, rt, index, h, part, false, tid);
 }
 
 // Joins the parts of a tile of rows: 4 dimensions of a row a lane.
